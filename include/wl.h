@@ -285,6 +285,139 @@ wl_status wl_stack_decode(wl_stack stack, const void *x, void *stream);
 void wl_stack_destroy(wl_stack stack);
 
 /*
+ * Decoder-layer operators around the projections
+ * ----------------------------------------------
+ * The pages' models are decoders: between the Q/K/V and the O projection sit
+ * rotary positions, a key/value cache and attention, and between the blocks
+ * norms and the residual stream.  The pages leave these to the serving
+ * framework; the entry points below are this library's own.
+ *
+ * A paged cache holds, per page, kv head and slot, one row of `dim` codes of
+ * k and one of v, and one fp32 scale for each row; a value is code * scale.
+ *   WL_CACHE_E4M3: 8-bit floats (4 exponent, 3 mantissa bits, no infinity);
+ *     the scale is the smallest power of two 2^e, e >= -126, with
+ *     max|row| <= 448 * 2^e (1 for a row of zeros).  A power of two loses
+ *     nothing against max/448: the codes keep their 4 significant bits.
+ *   WL_CACHE_BF16: codes are the values rounded to bf16, the scale is 1.
+ *   A row with a NaN or an infinity is stored as codes 0 and scale NaN: all of
+ *     it reads back as NaN, and only queries that see it become NaN.
+ */
+typedef enum { WL_CACHE_E4M3 = 0, WL_CACHE_BF16 = 1 } wl_cache_format;
+
+typedef struct {
+    void *k, *v;              /* [pages, kv_heads, page_size, dim], 1 or 2 bytes per code, 16-byte aligned */
+    float *k_scale, *v_scale; /* [pages, kv_heads, page_size] */
+    int64_t pages, kv_heads, page_size, dim;
+    wl_cache_format format;
+} wl_cache;
+
+/*
+ * The sequences of a call, in device memory: sequence b holds len[b] positions
+ * in the cache, and the call is about its next count[b] <= n ones (count NULL:
+ * n each).  Cache position j of sequence b lies in page
+ * pages[b * max_pages + j / page_size], slot j % page_size.  The kernels check
+ * what they read: counts are clamped to [0, n], lengths to [0, max_pages *
+ * page_size]; a position past the table or with a page outside [0, cache.pages)
+ * is not written, reads as zero, is seen by no query, and is reported by
+ * wl_device_status() as WL_ERR_INVALID_ARG.
+ */
+typedef struct {
+    const int32_t *pages; /* [batch, max_pages] */
+    const int32_t *len;   /* [batch] */
+    const int32_t *count; /* [batch] or NULL */
+    int64_t batch, max_pages, n;
+} wl_seqs;
+
+/*
+ * Rotary positions.  Pair i of a head turns by position * phase[i] * 2^-64
+ * turns (the product wraps at one turn, so the angle of any position is exact
+ * to 2^-32 turn); cos and sin are multiplied by amplitude.  Pairs are
+ * (i, i + rot/2), or (2i, 2i + 1) if interleaved; dims >= rot are not changed.
+ */
+typedef struct {
+    const uint64_t *phase; /* device, [rot/2] */
+    int64_t rot;           /* even, 0 <= rot <= dim; 0: no rotation */
+    int32_t interleaved;
+    float amplitude;
+} wl_rope;
+
+typedef enum {
+    WL_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot) radians per position */
+    WL_ROPE_LINEAR = 1, /* f_i / factor: positions interpolated */
+    WL_ROPE_BASE = 2,   /* base * factor^(rot/(rot-2)): the slowest pair is interpolated, the fastest kept */
+    WL_ROPE_RAMP = 3    /* between both, by how often a pair turns in orig_len positions: >= fast turns kept, <= slow
+                           turns interpolated; amplitude 0.1 ln(factor) + 1 (the YaRN method, Peng et al. 2023) */
+} wl_rope_scaling;
+
+/*
+ * wl_rope_phases -- fills phase[rot/2] and *amplitude in HOST memory (copy the
+ * table to the device for wl_rope).  factor >= 1; orig_len, fast and slow are
+ * read by WL_ROPE_RAMP only (orig_len >= 1, fast > slow > 0).  Host-only.
+ */
+wl_status wl_rope_phases(int64_t rot, double base, wl_rope_scaling scaling, double factor, double orig_len,
+                         double fast, double slow, uint64_t *phase, float *amplitude);
+
+/*
+ * wl_rope_append -- what follows wl_qkv_fused, in one launch: q_out = rotated
+ * q (bf16), and k (rotated) and v written to the cache at positions len[b] ..
+ * len[b] + count[b] - 1, quantised from the fp32 rotated values.
+ * q [batch*n, q_heads*dim], k and v [batch*n, kv_heads*dim] of type xdt (bf16
+ * or fp32), token (b, i) in row b*n + i, rows q_stride, k_stride, v_stride
+ * elements apart; q_out bf16 contiguous; rows i >= count[b] of q_out are zero.
+ * positions [batch*n] int32: the rotary position of each token (NULL: len[b] +
+ * i; a drafted tree gives len[b] + depth).  q and q_out may both be NULL: only
+ * the cache is written.
+ * Limits: dim a multiple of 16, 16 <= dim <= 256; strides multiples of 8;
+ * q, k, v, q_out 16-byte aligned.
+ */
+wl_status wl_rope_append(const void *q, const void *k, const void *v, void *q_out, int64_t q_heads, int64_t q_stride,
+                         int64_t k_stride, int64_t v_stride, wl_out_dtype xdt, const int32_t *positions, wl_rope rope,
+                         wl_cache cache, wl_seqs seqs, void *stream);
+
+/*
+ * wl_cache_read -- k_out and v_out [batch, n, kv_heads, dim] (type dt): the
+ * values at positions len[b] + i for i < count[b], zero beyond.  e4m3 values
+ * are exact in either type but for over- or underflow of the type's range.
+ */
+wl_status wl_cache_read(wl_cache cache, wl_seqs seqs, void *k_out, void *v_out, wl_out_dtype dt, void *stream);
+
+/*
+ * wl_tree_attention -- attention of the 1 <= n <= 64 newest tokens of each
+ * sequence (their k and v already in the cache at len[b] + i) over its cache:
+ * token i sees the len[b] positions before them and those new tokens j with
+ * bit j of mask[b*n + i] set (its ancestors and itself in a drafted tree).
+ * mask NULL: token i sees new tokens 0..i, so n = 1 is plain decoding and a
+ * prompt goes through in chunks of 64.  Softmax of scale * q.k in fp32; query
+ * head h reads kv head h / (q_heads / kv_heads).  A token that sees nothing,
+ * and rows i >= count[b], give zeros.
+ * q and out bf16 [batch, n, q_heads, dim], contiguous, 16-byte aligned.
+ * workspace: wl_tree_attention_workspace_bytes(...) bytes (0 for invalid
+ * sizes), 256-byte aligned, contents need no initialisation; calls that share
+ * it must not overlap in time.
+ */
+size_t wl_tree_attention_workspace_bytes(int64_t batch, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim);
+
+wl_status wl_tree_attention(const void *q, int64_t q_heads, const uint64_t *mask, float scale, wl_cache cache,
+                            wl_seqs seqs, void *out, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * wl_norm_residual -- what lies between two blocks, in one launch:
+ *     u  = y, or rms(y) * (w_offset + w_post)      (w_post NULL: y itself)
+ *     x' = alpha * x + beta * gate * u             (gate NULL: 1; y NULL: x' = alpha * x)
+ *     h  = rms(x') * (w_offset + w_pre)            (h NULL: not formed)
+ * with rms(a) = a / sqrt(mean(a^2) + eps), all in fp32; h takes x' before its
+ * rounding to x_out.  y and gate [T, H] of type ydt (gate rows gate_stride
+ * elements apart, 0: one row for all tokens), x and x_out [T, H] of type xdt
+ * (x_out may be x itself; it may be NULL if y is), h [T, H] of type hdt,
+ * w_post and w_pre [H] fp32.
+ * Limits: T >= 1, H a multiple of 8, 8 <= H <= 16384; everything 16-byte aligned.
+ */
+wl_status wl_norm_residual(const void *y, const void *gate, int64_t gate_stride, const void *x, const float *w_post,
+                           const float *w_pre, void *x_out, void *h, int64_t T, int64_t H, float alpha, float beta,
+                           float eps, float w_offset, wl_out_dtype ydt, wl_out_dtype xdt, wl_out_dtype hdt,
+                           void *stream);
+
+/*
  * wl_band_of_layer -- which of the G shared W0 blocks layer `layer` of an
  * L-layer stack uses: floor(layer * G / L) (contiguous bands).  G = L is the
  * passthrough point (one W0 per layer, "Set the fast path on NVIDIA"); G = 1
@@ -296,8 +429,9 @@ int64_t wl_band_of_layer(int64_t layer, int64_t L, int64_t G);
 /*
  * wl_device_status -- synchronise `stream`, then read and clear the device
  * status word of the current device.  Returns WL_ERR_TIMEOUT if a bounded
- * wait in a kernel of this library gave up since the last read, WL_ERR_CUDA
- * if the synchronisation failed, else WL_OK.
+ * wait in a kernel of this library gave up since the last read,
+ * WL_ERR_INVALID_ARG if a kernel met a cache position without a valid page,
+ * WL_ERR_CUDA if the synchronisation failed, else WL_OK.
  */
 wl_status wl_device_status(void *stream);
 

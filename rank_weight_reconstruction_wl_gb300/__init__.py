@@ -25,6 +25,8 @@ __all__ = [
     "wl_mlp_geglu_fused", "wl_mlp_geglu_fused_noalloc", "wl_materialize", "wl_decompose_band", "decompose",
     "wl_band_of_layer", "wl_device_status",
     "wl_last_error", "wl_version", "wl_selftest_wait", "WLStack", "EXPORTED_SYMBOLS", "WL_OK", "WL_ERR_INVALID_ARG",
+    "KVCache", "CacheSeqs", "RopeTable", "wl_rope_append", "wl_cache_read", "wl_tree_attention",
+    "wl_tree_attention_workspace_bytes", "wl_norm_residual",
     "WL_ERR_UNSUPPORTED", "WL_ERR_CUDA", "WL_ERR_TIMEOUT", "WL_ERR_WORKSPACE", "WL_ERR_INTERNAL", "WL_MAX_RANK",
 ]
 
@@ -41,7 +43,8 @@ STATUS_NAMES = {0: "WL_OK", 1: "WL_ERR_INVALID_ARG", 2: "WL_ERR_UNSUPPORTED", 3:
 EXPORTED_SYMBOLS = ("wl_linear", "wl_qkv_fused", "wl_linear_f32", "wl_qkv_fused_f32", "wl_decompose_workspace_bytes",
                     "wl_decompose_band", "wl_mlp_workspace_bytes", "wl_mlp_geglu_fused",
                     "wl_mlp_geglu_fused_noalloc", "wl_materialize", "wl_stack_create", "wl_stack_decode",
-                    "wl_stack_destroy", "wl_band_of_layer", "wl_device_status", "wl_last_error", "wl_version", "wl_selftest_wait")
+                    "wl_stack_destroy", "wl_rope_phases", "wl_rope_append", "wl_cache_read",
+                    "wl_tree_attention_workspace_bytes", "wl_tree_attention", "wl_norm_residual", "wl_band_of_layer", "wl_device_status", "wl_last_error", "wl_version", "wl_selftest_wait")
 
 
 class WLError(RuntimeError):
@@ -66,6 +69,19 @@ class _Layer(C.Structure):
 
 class _LayerOut(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("yq", "yk", "yv", "yo", "ym")]
+
+
+class _Cache(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, C.c_int64) for n in ("pages", "kv_heads", "page_size", "dim")] + [("format", C.c_int)])
+
+
+class _Seqs(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("pages", "len", "count")] + [(n, C.c_int64) for n in ("batch", "max_pages", "n")]
+
+
+class _Rope(C.Structure):
+    _fields_ = [("phase", C.c_void_p), ("rot", C.c_int64), ("interleaved", C.c_int32), ("amplitude", C.c_float)]
 
 
 _lock = threading.Lock()
@@ -118,6 +134,20 @@ def lib():
         L.wl_stack_decode.restype = st
         L.wl_stack_destroy.argtypes = [vp]
         L.wl_stack_destroy.restype = None
+        f64, f32 = C.c_double, C.c_float
+        L.wl_rope_phases.argtypes = [i64, f64, C.c_int, f64, f64, f64, f64, C.POINTER(C.c_uint64), C.POINTER(f32)]
+        L.wl_rope_phases.restype = st
+        L.wl_rope_append.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, C.c_int, vp, _Rope, _Cache, _Seqs, vp]
+        L.wl_rope_append.restype = st
+        L.wl_cache_read.argtypes = [_Cache, _Seqs, vp, vp, C.c_int, vp]
+        L.wl_cache_read.restype = st
+        L.wl_tree_attention_workspace_bytes.argtypes = [i64] * 5
+        L.wl_tree_attention_workspace_bytes.restype = C.c_size_t
+        L.wl_tree_attention.argtypes = [vp, i64, vp, f32, _Cache, _Seqs, vp, vp, C.c_size_t, vp]
+        L.wl_tree_attention.restype = st
+        L.wl_norm_residual.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, f32, f32, f32, f32, C.c_int, C.c_int,
+                                       C.c_int, vp]
+        L.wl_norm_residual.restype = st
         L.wl_band_of_layer.argtypes = [i64, i64, i64]
         L.wl_band_of_layer.restype = i64
         L.wl_device_status.argtypes = [vp]
@@ -464,6 +494,263 @@ class WLStack:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------- decoder-layer operators --
+class RopeTable:
+    """Rotary table: ``phases`` [rot/2] int64 on the GPU (turns per position in
+    units of 2^-64 turn), the pair layout and the amplitude of cos and sin."""
+
+    SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+
+    def __init__(self, phases: torch.Tensor, interleaved: bool = False, amplitude: float = 1.0):
+        _need(phases, "phases", torch.int64)
+        self.phases, self.interleaved, self.amplitude = phases, bool(interleaved), float(amplitude)
+        self.rot = 2 * phases.numel()
+        self._c = _Rope(phases.data_ptr(), self.rot, int(self.interleaved), self.amplitude)
+
+    @classmethod
+    def make(cls, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+             orig_len: float = 0.0, fast: float = 32.0, slow: float = 1.0, device="cuda") -> "RopeTable":
+        """The table of wl_rope_phases, copied to the device.  scaling: "none",
+        "linear" (f/factor), "base" (a larger base) or "ramp" (both, by how
+        often a pair turns in orig_len positions)."""
+        phases, amplitude = rope_phases(rot, base, scaling, factor, orig_len, fast, slow)
+        return cls(phases.to(device), interleaved, amplitude)
+
+
+def rope_phases(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0,
+                fast: float = 32.0, slow: float = 1.0):
+    """(phases [rot/2] int64 on the host, amplitude) of wl_rope_phases."""
+    if scaling not in RopeTable.SCALINGS:
+        raise ValueError(f"unknown rotary scaling {scaling!r}")
+    ph = (C.c_uint64 * max(1, int(rot) // 2))()
+    amp = C.c_float()
+    _check(lib().wl_rope_phases(int(rot), base, RopeTable.SCALINGS[scaling], factor, orig_len, fast, slow, ph, C.byref(amp)))
+    return torch.tensor([C.c_int64(v).value for v in ph[:int(rot) // 2]], dtype=torch.int64), amp.value
+
+
+class KVCache:
+    """A paged key/value cache: k, v [pages, kv_heads, page_size, dim]
+    (float8_e4m3fn or bfloat16 codes) and fp32 row scales k_scale, v_scale
+    [pages, kv_heads, page_size]; a value is code * scale."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a tensor [pages, kv_heads, page_size, dim]")
+        if k.dtype not in (torch.float8_e4m3fn, torch.bfloat16):
+            raise TypeError(f"a cache holds float8_e4m3fn or bfloat16, got {k.dtype}")
+        _need(k, "k", k.dtype)
+        _need(v, "v", k.dtype, k.shape)
+        _need(k_scale, "k_scale", torch.float32, k.shape[:3])
+        _need(v_scale, "v_scale", torch.float32, k.shape[:3])
+        if not (k.device == v.device == k_scale.device == v_scale.device):
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.pages, self.kv_heads, self.page_size, self.dim = (int(n) for n in k.shape)
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages, self.kv_heads,
+                         self.page_size, self.dim, 0 if k.dtype == torch.float8_e4m3fn else 1)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int, dim: int, dtype=torch.float8_e4m3fn, device="cuda") -> "KVCache":
+        """A cache of unwritten pages."""
+        shape = (pages, kv_heads, page_size, dim)
+        if dtype not in (torch.float8_e4m3fn, torch.bfloat16):
+            raise TypeError(f"a cache holds float8_e4m3fn or bfloat16, got {dtype}")
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        ks, vs = (torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+class CacheSeqs:
+    """The sequences of a call: pages [batch, max_pages] int32 (page of each run
+    of page_size positions), len [batch] int32 (positions already in the
+    cache), n new positions each, or count[b] <= n of them (int32).  All on the
+    GPU and read when the kernels run, so they may change between calls."""
+
+    def __init__(self, pages: torch.Tensor, len: torch.Tensor, n: int, count: torch.Tensor | None = None):
+        _need(pages, "pages", torch.int32)
+        if pages.dim() != 2:
+            raise ValueError("pages must be [batch, max_pages]")
+        B = int(pages.shape[0])
+        _need(len, "len", torch.int32, (B,))
+        if count is not None:
+            _need(count, "count", torch.int32, (B,))
+        self.pages, self.len, self.n, self.count, self.batch = pages, len, int(n), count, B
+        self.tokens = B * self.n
+        self._c = _Seqs(pages.data_ptr(), len.data_ptr(), None if count is None else count.data_ptr(), B,
+                        int(pages.shape[1]), self.n)
+
+
+def _token_rows(t, name: str, dtype, tokens: int, width: int) -> int:
+    """Row stride in elements of a tensor of `tokens` rows of `width` elements:
+    [tokens, width], [tokens, heads, dim] or [batch, n, heads, dim], rows any
+    one distance apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != tokens * width:
+        raise ValueError(f"{name} must hold {tokens} rows of {width} elements, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return width
+    sh, sd = t.shape, t.stride()
+    lead = 2 if t.dim() == 4 else 1
+    run = 1  # the trailing dimensions are one run of `width` elements
+    for n, st in zip(reversed(sh[lead:]), reversed(sd[lead:])):
+        if n > 1 and st != run:
+            raise ValueError(f"{name}: each token's row must be contiguous")
+        run *= n
+    if run != width or t.dim() not in (2, 3, 4):
+        raise ValueError(f"{name} must be [tokens, heads*dim], [tokens, heads, dim] or [batch, n, heads, dim]")
+    if lead == 2 and sh[0] > 1 and sh[1] > 1 and sd[0] != sh[1] * sd[1]:
+        raise ValueError(f"{name}: all token rows must be the same distance apart")
+    return int(sd[lead - 1]) if sh[lead - 1] > 1 else int(sd[0]) if lead == 2 and sh[0] > 1 else width
+
+
+class _on:
+    """Makes `device` the current one for a call (nothing to do where it is)."""
+
+    def __init__(self, device):
+        self.device, self.back = device, None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, seqs: CacheSeqs, q_out=None, stream=None):
+    """Rotates q and k and writes k and v to the cache, quantised, at positions
+    len[b] .. len[b] + count[b] - 1; returns q_out, the rotated q as bf16 (None
+    where q is None).  q, k, v: the outputs of wl_qkv_fused, or any bf16 or
+    fp32 tensors of batch * n token rows (_token_rows).  positions: int32
+    [batch, n], or None for len[b] + i.  rope None: no rotation."""
+    dt = k.dtype
+    code = _ydt(dt)
+    tokens, kvw = seqs.tokens, cache.kv_heads * cache.dim
+    ks, vs = _token_rows(k, "k", dt, tokens, kvw), _token_rows(v, "v", dt, tokens, kvw)
+    heads, qs = 0, 0
+    if q is not None:
+        heads = q.numel() // (tokens * cache.dim)
+        qs = _token_rows(q, "q", dt, tokens, heads * cache.dim)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _need(q_out, "q_out", torch.bfloat16, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if positions is not None:
+        _need(positions, "positions", torch.int32)
+        if positions.numel() != tokens:
+            raise ValueError(f"positions must hold batch * n = {tokens} numbers, got {tuple(positions.shape)}")
+    with _on(cache.device):
+        _check(lib().wl_rope_append(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), heads, qs, ks, vs, code, _ptr(positions),
+                                    rope._c if rope is not None else _Rope(None, 0, 0, 1.0), cache._c, seqs._c,
+                                    _stream(stream, cache.device)))
+    return q_out
+
+
+def wl_cache_read(cache: KVCache, seqs: CacheSeqs, dt=torch.bfloat16, outs=None, stream=None):
+    """The cache's values at positions len[b] + i, i < count[b] (zeros beyond):
+    (k, v) [batch, n, kv_heads, dim] as bf16 or fp32."""
+    code = _ydt(dt)
+    shape = (seqs.batch, seqs.n, cache.kv_heads, cache.dim)
+    if outs is None:
+        outs = tuple(torch.empty(shape, dtype=_tdt(code), device=cache.device) for _ in range(2))
+    for o, name in zip(outs, ("k_out", "v_out")):
+        _need(o, name, _tdt(code), shape)
+    with _on(cache.device):
+        _check(lib().wl_cache_read(cache._c, seqs._c, outs[0].data_ptr(), outs[1].data_ptr(), code, _stream(stream, cache.device)))
+    return tuple(outs)
+
+
+def wl_tree_attention_workspace_bytes(batch, n, q_heads, kv_heads, dim) -> int:
+    return int(lib().wl_tree_attention_workspace_bytes(batch, n, q_heads, kv_heads, dim))
+
+
+def wl_tree_attention(q, cache: KVCache, seqs: CacheSeqs, mask=None, scale: float | None = None, out=None, workspace=None,
+                      stream=None):
+    """Attention of the n newest tokens of each sequence over its cache; token i
+    sees the len[b] positions before them and the new tokens j with bit j of
+    mask[b, i] (int64; None: 0..i).  q bf16 [batch, n, q_heads, dim] (or
+    [batch * n, q_heads * dim]) -> out of the same shape.  scale defaults to
+    dim ** -0.5.  workspace: at least wl_tree_attention_workspace_bytes() bytes,
+    256-byte aligned; by default allocated for the call."""
+    tokens = seqs.tokens
+    heads = q.numel() // (tokens * cache.dim)
+    _need(q, "q", torch.bfloat16)
+    if heads * tokens * cache.dim != q.numel():
+        raise ValueError(f"q must hold batch * n = {tokens} rows of heads * {cache.dim} elements, got {tuple(q.shape)}")
+    if mask is not None:
+        _need(mask, "mask", torch.int64)
+        if mask.numel() != tokens:
+            raise ValueError(f"mask must hold batch * n = {tokens} words, got {tuple(mask.shape)}")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, q.shape)
+    with _on(cache.device):
+        st = _stream(stream, cache.device)
+        if workspace is None:
+            # of the call's own stream, so that the allocator hands it on only after the call
+            nb = lib().wl_tree_attention_workspace_bytes(seqs.batch, seqs.n, heads, cache.kv_heads, cache.dim)
+            if stream is None:
+                workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=cache.device)
+            else:
+                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), cache.device)
+                with torch.cuda.stream(s):
+                    workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=cache.device)
+        _check(lib().wl_tree_attention(q.data_ptr(), heads, _ptr(mask), scale if scale is not None else cache.dim ** -0.5,
+                                       cache._c, seqs._c, out.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), st))
+    return out
+
+
+def wl_norm_residual(y, x, w_post=None, w_pre=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                     w_offset: float = 0.0, x_out=None, h_dt=torch.bfloat16, h=None, stream=None):
+    """x' = alpha x + beta gate (rms(y) (w_offset + w_post)) and h = rms(x')
+    (w_offset + w_pre): the norm after one block, its gate, the residual and the
+    norm before the next, in one launch.  y [T, H] or None; gate [T, H], or [H]
+    or [1, H] for all tokens, of y's type; w_post, w_pre fp32 [H] or None (no
+    norm after the block; no h).  Returns (x', h); x_out may be x (in place)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [T, H]")
+    T, H = x.shape
+    xc = _ydt(x.dtype)
+    _need(x, "x", x.dtype)
+    yc, gs = xc, 0
+    if y is not None:
+        yc = _ydt(y.dtype)
+        _need(y, "y", y.dtype, (T, H))
+    if gate is not None:
+        if y is None:
+            raise ValueError("gate needs y")
+        _need(gate, "gate", y.dtype)
+        if gate.numel() != H and tuple(gate.shape) != (T, H):
+            raise ValueError(f"gate must be [{T}, {H}], [1, {H}] or [{H}], got {tuple(gate.shape)}")
+        gs = H if gate.numel() != H else 0
+    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if w is not None:
+            _need(w, name, torch.float32, (H,))
+    if x_out is None and (y is not None or alpha != 1.0):
+        x_out = torch.empty_like(x)
+    if x_out is not None:
+        _need(x_out, "x_out", x.dtype, (T, H))
+    hc = _ydt(h_dt)
+    if w_pre is not None and h is None:
+        h = torch.empty(T, H, dtype=_tdt(hc), device=x.device)
+    if h is not None:
+        _need(h, "h", _tdt(hc), (T, H))
+    with _on(x.device):
+        _check(lib().wl_norm_residual(_ptr(y), _ptr(gate), gs, x.data_ptr(), _ptr(w_post), _ptr(w_pre), _ptr(x_out), _ptr(h), T,
+                                      H, alpha, beta, eps, w_offset, yc, xc, hc, _stream(stream, x.device)))
+    return (x if x_out is None else x_out), h
 
 
 def wl_band_of_layer(layer: int, L: int, G: int) -> int:

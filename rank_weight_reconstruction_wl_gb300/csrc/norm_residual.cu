@@ -1,0 +1,146 @@
+// norm_residual.cu -- norm after a block, gate, residual update and norm
+// before the next block, in one pass over the row.
+//
+//     u  = y  or  y / rms(y) * (w_offset + w_post)
+//     x' = alpha x + beta gate u
+//     h  = x' / rms(x') * (w_offset + w_pre),   rms(a) = sqrt(mean a^2 + eps)
+//
+// One CTA per token.  The row stays in registers between the two sums of
+// squares, so y and x are read once and x' and h written once.
+#include "cache_row.cuh"
+
+namespace wl {
+
+struct NormArgs {
+    const void *y, *gate, *x;
+    const float *w_post, *w_pre;
+    void *x_out, *h;
+    int64_t gate_stride;
+    int H;
+    float alpha, beta, eps, w_offset;
+};
+
+// Sum over the CTA; every thread gets the same value (fixed order).
+__device__ __forceinline__ float block_sum(float v, float *red)
+{
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
+    return s;
+}
+
+// V: chunks of 8 elements per thread.
+template <typename Y, typename X, typename O, int V>
+__global__ void norm_residual_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float red[2][32];
+    const int nchunk = a.H / 8;
+    const int64_t row = (int64_t)blockIdx.x * a.H;
+    float u[V][8], x[V][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < nchunk) {
+            load8(static_cast<const X *>(a.x) + row + c * 8, x[i]);
+            if (a.y) load8(static_cast<const Y *>(a.y) + row + c * 8, u[i]);
+        }
+    }
+    if (a.y) {
+        float f = a.beta;
+        if (a.w_post) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (threadIdx.x + i * blockDim.x < nchunk)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss += u[i][j] * u[i][j];
+            f *= rsqrtf(block_sum(ss, red[0]) / (float)a.H + a.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c < nchunk) {
+                float w[8], g[8];
+                if (a.w_post) {
+                    load8(a.w_post + c * 8, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[i][j] *= a.w_offset + w[j];
+                }
+                if (a.gate) {
+                    load8(static_cast<const Y *>(a.gate) + blockIdx.x * a.gate_stride + c * 8, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[i][j] *= g[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[i][j] = a.alpha * x[i][j] + f * u[i][j];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i][j] *= a.alpha;
+    }
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < nchunk) {
+            if (a.x_out) store8(static_cast<X *>(a.x_out) + row + c * 8, x[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += x[i][j] * x[i][j];
+        }
+    }
+    if (!a.h) return;
+    const float f = rsqrtf(block_sum(ss, red[1]) / (float)a.H + a.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < nchunk) {
+            float w[8];
+            load8(a.w_pre + c * 8, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i][j] *= f * (a.w_offset + w[j]);
+            store8(static_cast<O *>(a.h) + row + c * 8, x[i]);
+        }
+    }
+}
+
+template <typename Y, typename X, typename O>
+static void norm_launch(const NormArgs &a, int64_t T, cudaStream_t st)
+{
+    const int nchunk = a.H / 8;
+    const int V = nchunk <= 256 ? 1 : nchunk <= 512 ? 2 : nchunk <= 1024 ? 4 : 8;
+    const int threads = ((nchunk + V - 1) / V + 31) / 32 * 32;
+    const unsigned grid = (unsigned)T;
+    switch (V) {
+    case 1: norm_residual_kernel<Y, X, O, 1><<<grid, threads, 0, st>>>(a); break;
+    case 2: norm_residual_kernel<Y, X, O, 2><<<grid, threads, 0, st>>>(a); break;
+    case 4: norm_residual_kernel<Y, X, O, 4><<<grid, threads, 0, st>>>(a); break;
+    default: norm_residual_kernel<Y, X, O, 8><<<grid, threads, 0, st>>>(a); break;
+    }
+}
+
+wl_status launch_norm_residual(const void *y, const void *gate, int64_t gate_stride, const void *x, const float *w_post,
+                               const float *w_pre, void *x_out, void *h, int64_t T, int64_t H, float alpha, float beta,
+                               float eps, float w_offset, int ydt, int xdt, int hdt, cudaStream_t st)
+{
+    const NormArgs a{y, gate, x, w_post, w_pre, x_out, h, gate_stride, (int)H, alpha, beta, eps, w_offset};
+    const int kind = (ydt == WL_OUT_F32 ? 4 : 0) + (xdt == WL_OUT_F32 ? 2 : 0) + (hdt == WL_OUT_F32 ? 1 : 0);
+    switch (kind) {
+    case 0: norm_launch<bf16, bf16, bf16>(a, T, st); break;
+    case 1: norm_launch<bf16, bf16, float>(a, T, st); break;
+    case 2: norm_launch<bf16, float, bf16>(a, T, st); break;
+    case 3: norm_launch<bf16, float, float>(a, T, st); break;
+    case 4: norm_launch<float, bf16, bf16>(a, T, st); break;
+    case 5: norm_launch<float, bf16, float>(a, T, st); break;
+    case 6: norm_launch<float, float, bf16>(a, T, st); break;
+    default: norm_launch<float, float, float>(a, T, st); break;
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_norm_residual launch");
+}
+
+}  // namespace wl

@@ -345,6 +345,8 @@ wl_status wl_device_status(void *stream)
                         (word & kWaitRingFull) ? " ring-full" : "",
                         (word & kWaitRingEmpty) ? " ring-empty" : "",
                         (word & kWaitExchange) ? " cluster-exchange" : "");
+        if (word & kStatusPage)
+            return fail(WL_ERR_INVALID_ARG, "a kernel met a cache position without a valid page");
     }
     return WL_OK;
 }

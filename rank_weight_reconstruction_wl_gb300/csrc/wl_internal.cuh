@@ -41,6 +41,7 @@ constexpr unsigned kWaitRingFull = 2u;    // consumer waiting for a loaded ring 
 constexpr unsigned kWaitRingEmpty = 4u;   // producer waiting for a free ring stage
 constexpr unsigned kWaitExchange = 8u;    // waiting for cluster peers' (or other CTAs') partial sums
 constexpr unsigned kWaitDrain = 16u;      // a CTA that gave up could not confirm its copies in flight had landed
+constexpr unsigned kStatusPage = 32u;     // a cache position without a valid page was met and skipped
 
 // Upper bound of every spin-wait in this library, in SM clock cycles: 4e9
 // cycles is 2 s at 2 GHz (longer at lower clocks).  A wait that runs longer
@@ -141,6 +142,20 @@ constexpr int kDecompMaxK = 160;
 size_t decompose_workspace_bytes(int64_t out, int64_t in, int64_t r, int64_t p);
 wl_status launch_decompose(const bf16 *const *W, int n, int out, int in, int r, int p, int iters, const float *omega,
                            bf16 *W0, float *s, bf16 *U, bf16 *V, void *ws, size_t ws_bytes, cudaStream_t st);
+
+// Decoder-layer operators (rope_cache.cu, tree_attention.cu, norm_residual.cu)
+constexpr int kMaxTree = 64;
+wl_status launch_rope_append(const void *q, const void *k, const void *v, bf16 *q_out, int64_t q_heads, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int xdt, const int32_t *positions, const wl_rope &rope,
+                             const wl_cache &cache, const wl_seqs &seqs, const DeviceInfo *di, cudaStream_t st);
+wl_status launch_cache_read(const wl_cache &cache, const wl_seqs &seqs, void *k_out, void *v_out, int dt,
+                            const DeviceInfo *di, cudaStream_t st);
+size_t tree_attention_workspace_bytes(int64_t batch, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim);
+wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *mask, float scale, const wl_cache &cache,
+                                const wl_seqs &seqs, bf16 *out, void *ws, const DeviceInfo *di, cudaStream_t st);
+wl_status launch_norm_residual(const void *y, const void *gate, int64_t gate_stride, const void *x, const float *w_post,
+                               const float *w_pre, void *x_out, void *h, int64_t T, int64_t H, float alpha, float beta,
+                               float eps, float w_offset, int ydt, int xdt, int hdt, cudaStream_t st);
 
 wl_status launch_materialize(const bf16 *W0, const float *s, const bf16 *U,
                              const bf16 *V, void *W_eff, int64_t out, int64_t in,
