@@ -50,6 +50,7 @@ struct TaArgs {
     float2 *ml;    // [2 * ctas][RT] reference and sum of each row
     int4 *desc;    // [ctas] unit that CTA c begins and others finish: sequence, unit, last CTA (sequence -1: none)
     int q_heads, group, rtiles;
+    uint32_t group_inv;  // ceil(2^32 / group), 0 for 1
     float scale;
     CacheArgs c;
 };
@@ -66,16 +67,22 @@ struct TaShape {
     static constexpr int QB = N * ROWB;
     static constexpr int PW = 2 * RT;                // bytes of a position's weights
     static constexpr int PB = kTaTile * PW;
-    static constexpr int MISC = 2048;
-    static constexpr int ROOM = (232448 - 1024 - MISC - QB - 2 * PB) / SLOT;
-    static constexpr int SLOTS = ROOM < 12 ? ROOM : 12;
-    static constexpr int SMEM = 1024 + MISC + QB + 2 * PB + SLOTS * SLOT;
+    static constexpr int MISC = 3072;
+    static constexpr int ROOM = (232448 - MISC - QB - 2 * PB) / SLOT;
+    static constexpr int SLOTS = ROOM < 10 ? ROOM : 10;
+    static constexpr int SMEM = MISC + QB + 2 * PB + SLOTS * SLOT;
     static constexpr int MT = DP / 128;              // M tiles of the second product
-    static constexpr int COLS = (2 + MT) * N <= 64 ? 64 : (2 + MT) * N <= 128 ? 128 : (2 + MT) * N <= 256 ? 256 : 512;
+    static constexpr bool PP = RT <= 32;             // each softmax warpgroup has tiles and sums of its own
+    static constexpr int USED = (2 + (PP ? 2 : 1) * MT) * N;  // two score buffers, the sums
+    static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
     static constexpr int KSTEP = 32 / ES;            // contraction elements per MMA: 32 bytes of a K-major row
-    static constexpr int CW = RT / 2;                // columns per softmax warpgroup
+    static constexpr int CW = PP ? RT : RT / 2;      // columns per softmax thread
+    // Exponents of weights: the limit, and how far below it a moved reference
+    // puts the largest weight.  e4m3 ends at 448, so the limit is 2^8, and the
+    // gap is precision lost for fewer moves; bf16 has range to spare.
+    static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f;
     static constexpr int SWP = PW == 128 ? 2 : PW == 64 ? 4 : 6;  // swizzle code of the weights' rows
-    static_assert(SLOTS >= 4 && SMEM <= 232448 && (2 + MT) * N <= 512, "tile shape");
+    static_assert(SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
 };
 
 // ---------------------------------------------------------------- helpers --
@@ -120,22 +127,27 @@ __device__ __forceinline__ void tmem_wait16(uint32_t *r)
                  : "memory");
 }
 
-// CW consecutive columns of this thread's lane, waited for.
-template <int CW>
-__device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&v)[CW])
+// C (a multiple of 16) consecutive columns of this thread's lane: the load,
+// and the wait that makes the registers valid (one wait covers all loads).
+template <int C>
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[C])
 {
-    uint32_t r[CW];
-    if constexpr (CW == 8) {
-        tmem_ld8_nw(taddr, r);
-        tmem_wait_ld8(r);
-    } else {
 #pragma unroll
-        for (int i = 0; i < CW; i += 16) tmem_ld16_nw(taddr + i, r + i);
+    for (int i = 0; i < C; i += 16) tmem_ld16_nw(taddr + i, r + i);
+}
+template <int C>
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[C])
+{
 #pragma unroll
-        for (int i = 0; i < CW; i += 16) tmem_wait16(r + i);
-    }
-#pragma unroll
-    for (int i = 0; i < CW; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < C; i += 16) tmem_wait16(r + i);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -143,6 +155,53 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Pairs of fp32 numbers in one register pair, with the packed operations.
+__device__ __forceinline__ uint64_t f2(float lo, float hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ uint64_t u2(uint32_t lo, uint32_t hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two halves as e4m3 codes.
+__device__ __forceinline__ uint32_t half2_e4m3(__half2 h)
+{
+    uint16_t v;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(v) : "r"(*reinterpret_cast<const uint32_t *>(&h)));
+    return v;
 }
 
 // Barrier `id` of `n` threads that also tells whether any of them brought true.
@@ -210,6 +269,10 @@ __device__ __forceinline__ void ta_drain(uint64_t *bar, unsigned *status)
         }
     }
 }
+
+// New token of row g of a kv head: g / group.  g < 64 group and group <= 4096,
+// so the product with the rounded-up reciprocal is exact.
+__device__ __forceinline__ int ta_token(const TaArgs &a, int g) { return a.group == 1 ? g : (int)__umulhi((uint32_t)g, a.group_inv); }
 
 // ------------------------------------------------------------------ range --
 // Walks a CTA's range of the tiles of all units, unit by unit.
@@ -289,17 +352,23 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
     using Z = TaShape<kE4M3, DP, RT>;
     constexpr int N = Z::N, CW = Z::CW, SLOTS = Z::SLOTS;
     extern __shared__ __align__(1024) char smem_raw[];
-    char *smem = smem_raw + ((1024u - (s32(smem_raw) & 1023u)) & 1023u);
+    // The whole limit is used, so there is no room to align by hand.
+    if (s32(smem_raw) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(a.c.status, kStatusAlign);
+        return;
+    }
+    char *smem = smem_raw;
     char *sq = smem, *sp = sq + Z::QB, *ring = sp + 2 * Z::PB, *misc = ring + SLOTS * Z::SLOT;
     uint64_t *smask = reinterpret_cast<uint64_t *>(misc);            // [RT]
     float *red = reinterpret_cast<float *>(misc + 512);              // [2][4][32]
-    float *qmax = reinterpret_cast<float *>(misc + 2016);            // [8]
+    float *nms = reinterpret_cast<float *>(misc + 1792);             // [2][32] minus the references of the columns
+    uint64_t *ptrs = reinterpret_cast<uint64_t *>(misc + 2048);      // [4][32] rows of a tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc + 1536);
     uint64_t *full = bars, *empty = full + SLOTS, *s_full = empty + SLOTS, *s_empty = s_full + 2, *p_full = s_full + 4,
              *pv_done = s_full + 6, *q_ready = s_full + 8, *drain = s_full + 9;
     uint32_t *tmem_hold = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_hold + 1);
-    static_assert((2 * 12 + 11) * 8 <= 2016 - 1536, "barriers");
+    static_assert((2 * SLOTS + 11) * 8 <= 1792 - 1536, "barriers");
 
     const CacheArgs &c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -312,8 +381,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], 8);
-            mbar_init(&p_full[i], 8);
+            mbar_init(&s_empty[i], Z::PP ? 4 : 8);
+            mbar_init(&p_full[i], Z::PP ? 4 : 8);
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(q_ready, 8);
@@ -342,6 +411,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         const int pw = warp - 12;
         constexpr int LPR = Z::SLOTROW / 16, RPP = 32 / LPR;  // lanes per row, rows per pass
         const int ch = lane % LPR, sub = lane / LPR;
+        const char **tab = reinterpret_cast<const char **>(ptrs + pw * 32);
+        const uint32_t to = (uint32_t)((ch >> 3) * (kTaTile * 128) + (pw * 32 + sub) * 128);
+        const uint32_t sw = (uint32_t)(((ch & 7) ^ sub) << 4);  // the row's low bits are sub and those of the pass
         int item = 0;
         auto place = [&](int j, int total, int hk) -> int64_t {
             if (j >= total) return -1;
@@ -350,22 +422,24 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             return row;
         };
         auto copy = [&](const char *base, int64_t row) {
+            __syncwarp();
+            tab[lane] = row >= 0 ? base + row * (c.dim * Z::ES) : nullptr;
+            __syncwarp();
 #pragma unroll
             for (int s = 0; s < Z::NS; ++s, ++item) {
                 const int slot = item % SLOTS;
                 ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
                 if (*abort_flag) continue;
-                const uint32_t dst = s32(ring + slot * Z::SLOT);
+                const uint32_t dst = s32(ring + slot * Z::SLOT) + to;
                 const int col = s * Z::SLOTROW + ch * 16;
                 const bool in = col < c.dim * Z::ES;
 #pragma unroll
                 for (int p = 0; p < 32 / RPP; ++p) {
-                    const int r = p * RPP + sub, t = pw * 32 + r;
-                    const int64_t at = __shfl_sync(0xffffffffu, row, r);
-                    const bool ok = in && at >= 0;
-                    const char *src = ok ? base + at * (c.dim * Z::ES) + col : base;
-                    const uint32_t d = dst + (uint32_t)((ch >> 3) * (kTaTile * 128) + t * 128 + (((ch & 7) ^ (t & 7)) << 4));
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(ok ? 16 : 0) : "memory");
+                    const char *src = tab[p * RPP + sub];
+                    const bool ok = in && src != nullptr;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     dst + p * (RPP * 128) + (sw ^ (((p * RPP) & 7) << 4))),
+                                 "l"(ok ? src + col : base), "r"(ok ? 16 : 0));
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(&full[slot])) : "memory");
             }
@@ -444,7 +518,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     for (int m = 0; m < MS; ++m)
 #pragma unroll
                         for (int k = 0; k < kTaTile / Z::KSTEP; ++k)
-                            mma(ocol + (s * MS + m) * N,
+                            mma(ocol + ((Z::PP ? (i & 1) * Z::MT : 0) + s * MS + m) * N,
                                 ta_desc(av + m * Z::ES * (kTaTile * 128) + k * Z::KSTEP * 128, kTaTile * 128, 1024, 2),
                                 ta_desc(pb + k * Z::KSTEP * Z::PW, 8 * Z::PW, 8 * Z::PW, Z::SWP), kIdPV, (first && k == 0) ? 0u : 1u);
                     umma_commit(&empty[slot]);
@@ -457,9 +531,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 tc_fence_after();
                 for (int t = w.tile; t < t1; ++t, ++it) {
                     scores(it);
-                    if (t > w.tile) values(it - 1, (t - 1 - w.tile) % kTaFlush == 0);
+                    if (t > w.tile) values(it - 1, (t - 1 - w.tile) % kTaFlush < (Z::PP ? 2 : 1));
                 }
-                values(it - 1, (t1 - 1 - w.tile) % kTaFlush == 0);
+                values(it - 1, (t1 - 1 - w.tile) % kTaFlush < (Z::PP ? 2 : 1));
                 ++seg;
                 ta_next(w, c, units);
             }
@@ -469,50 +543,57 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax
-        // Warpgroup wg takes columns wg * CW ..; a thread is one position of
-        // a tile (lane of S^T) and, at the end, one dim of each M tile.
+        // A thread is one position of a tile (lane of S^T).  RT = 64: both
+        // warpgroups work on every tile, half the columns each.  RT <= 32:
+        // warpgroup wg takes the tiles of buffer wg, all columns, with sums
+        // and references of its own, so that two tiles are in hand at once.
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTaRegsSoftmax));
-        const int wg = warp >> 2, tk = threadIdx.x & 127, col0 = wg * CW;
+        const int wg = warp >> 2, tk = threadIdx.x & 127, col0 = Z::PP ? 0 : wg * CW;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         float *wred = red + wg * 128;
+        float *mine = reinterpret_cast<float *>(sp + wg * Z::PB);  // [4][CW] sums, [CW] references, when the buffer is idle
+        float *fac = reinterpret_cast<float *>(sp + 1024);         // [3][64] factors of both streams and of flushed sums
         int it = 0;
         if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
         while (w.left > 0) {
             const int t0 = w.tile, t1 = ta_end(w), total = w.cnt > 0 ? w.len + w.cnt : 0;
             const int hk = w.u / a.rtiles, row0 = (w.u - hk * a.rtiles) * RT, rows = min(RT, c.n * a.group - row0);
+            constexpr int STEP = Z::PP ? 2 : 1;
             // place and scales of this thread's position, loaded a tile ahead
             auto place = [&](int t) -> int64_t {
                 const int j = t * kTaTile + tk;
-                return j < total ? cache_row(c, w.b, hk, j) : -1;
+                return t < t1 && j < total ? cache_row(c, w.b, hk, j) : -1;
             };
-            int64_t at = place(t0), at1 = t0 + 1 < t1 ? place(t0 + 1) : -1;
+            const int tf = t0 + (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's first tile
+            int64_t at = place(tf), at1 = place(tf + STEP);
             float ks = at >= 0 ? __ldg(c.k_scale + at) : 0.0f, vs = at >= 0 ? __ldg(c.v_scale + at) : 1.0f;
-            bar_n<256>(3);  // both warpgroups are done with the previous segment's masks
+            // nm: minus the references of the columns (the same for all threads,
+            // so in shared memory), l: this position's sums, as pairs; unset:
+            // columns that have seen nothing yet and have no reference.
+            float *nm = nms + wg * 32;
+            uint64_t l[CW / 2];
+            uint32_t unset;
+            auto fresh = [&]() {
+                // a column beyond the rows never counts and never moves
+                if (tk < CW) nm[tk] = col0 + tk < rows ? 0.0f : kTaNone;
+#pragma unroll
+                for (int i = 0; i < CW / 2; ++i) l[i] = 0ull;
+                const int nc = min(max(rows - col0, 0), CW);
+                unset = nc == 32 ? ~0u : (1u << nc) - 1;
+            };
+            fresh();
             // ---- the segment's queries: rows of the B operand
             float qscale = a.scale * kLog2e;
             {
                 constexpr int CH = DP / 8, PER = RT * CH / 256;  // 8-element chunks of a row, per thread
-                uint4 qv[PER];
-                uint32_t amax = 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = threadIdx.x + i * 256, r = e / CH, d = (e % CH) * 8, g = row0 + r;
-                    qv[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows && d < c.dim && g / a.group < w.cnt) {
-                        const int64_t tok = (int64_t)w.b * c.n + g / a.group;
-                        qv[i] = *reinterpret_cast<const uint4 *>(a.q + (tok * a.q_heads + hk * a.group + g % a.group) * c.dim + d);
-                    }
-                    if (kE4M3) {
-                        const uint32_t u[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = u[j] & 0x7fffu, hi = (u[j] >> 16) & 0x7fffu;
-                            amax = max(amax, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                        }
-                    }
-                }
+                auto chunk = [&](int e) -> uint4 {
+                    const int r = e / CH, d = (e % CH) * 8, g = row0 + r, tok = ta_token(a, g);
+                    if (r >= rows || d >= c.dim || tok >= w.cnt) return make_uint4(0u, 0u, 0u, 0u);
+                    return *reinterpret_cast<const uint4 *>(
+                        a.q + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + (g - tok * a.group)) * c.dim + d);
+                };
                 if (threadIdx.x < RT) {
-                    const int g = row0 + threadIdx.x, i = g / a.group;
+                    const int g = row0 + threadIdx.x, i = ta_token(a, g);
                     uint64_t m = 0;
                     if ((int)threadIdx.x < rows && i < w.cnt) {
                         m = a.mask ? a.mask[(int64_t)w.b * c.n + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
@@ -523,20 +604,33 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 float up = 1.0f;
                 if (kE4M3) {
                     // one power of two brings the largest |q| of the tile into [128, 256)
+                    uint32_t amax = 0;
+#pragma unroll 2
+                    for (int i = 0; i < PER; ++i) {
+                        const uint4 v = chunk(threadIdx.x + i * 256);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = u[j] & 0x7fffu, hi = (u[j] >> 16) & 0x7fffu;
+                            amax = max(amax, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                        }
+                    }
                     amax = __reduce_max_sync(0xffffffffu, amax);
-                    if (lane == 0) qmax[warp] = __uint_as_float(amax << 16);
+                    if (lane == 0) red[warp] = __uint_as_float(amax << 16);
                     bar_n<256>(3);
                     float mx = 0.0f;
-                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, qmax[i]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[i]);
                     const int be = max((int)(__float_as_uint(mx) >> 23), 14);
                     up = __uint_as_float((uint32_t)(261 - be) << 23);  // 2^(134 - be)
                     qscale *= __uint_as_float((uint32_t)(be - 7) << 23);
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < PER; ++i) {
                     const int e = threadIdx.x + i * 256, r = e / CH, ck = e % CH;
+                    const uint4 v = chunk(e);
                     if (kE4M3) {
-                        const uint32_t u[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                         uint32_t hi[2] = {}, lo[2] = {};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -554,226 +648,267 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         *reinterpret_cast<uint2 *>(o + r * 128 + ((c16 ^ (r & 7)) << 4)) = make_uint2(hi[0], hi[1]);
                         *reinterpret_cast<uint2 *>(o + (RT + r) * 128 + ((c16 ^ (r & 7)) << 4)) = make_uint2(lo[0], lo[1]);
                     } else {
-                        *reinterpret_cast<uint4 *>(sq + (ck / 8) * (N * 128) + r * 128 + (((ck & 7) ^ (r & 7)) << 4)) = qv[i];
+                        *reinterpret_cast<uint4 *>(sq + (ck / 8) * (N * 128) + r * 128 + (((ck & 7) ^ (r & 7)) << 4)) = v;
                     }
                 }
                 fence_async_smem();
                 bar_n<256>(3);  // the masks too
                 if (lane == 0) mbar_arrive(q_ready);
             }
-            float m[CW], l[CW];
-#pragma unroll
-            for (int i = 0; i < CW; ++i) m[i] = kTaNone, l[i] = 0.0f;
             const int slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
             const bool whole = t0 == 0 && t1 == w.ntiles;
-            bool flushed = false;
+            bool flushed = false, some = false;  // some: this warpgroup has sums in tensor memory
             for (int t = t0; t < t1; ++t, ++it) {
-                const int j = t * kTaTile + tk;
-                const bool seen = at >= 0;
-                const float cs = ks * qscale, lv = log2f(vs), iv = vs == vs ? 1.0f / vs : 1.0f;
-                at = at1;
-                if (t + 1 < t1) {
+                if (!Z::PP || (it & 1) == wg) {
+                    const int j = t * kTaTile + tk;
+                    const bool seen = at >= 0;
+                    const bool bad = vs != vs;
+                    const float v1 = fmaxf(vs, 1.17549435e-38f);
+                    // log2 of the scale: exponent exact, 0 for the mantissa of a power of two
+                    const float lv = bad ? vs : (float)((int)(__float_as_uint(v1) >> 23) - 127) +
+                                               __log2f(__uint_as_float((__float_as_uint(v1) & 0x7fffffu) | 0x3f800000u));
+                    const float iv = bad ? 1.0f : __frcp_rn(v1);
+                    const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv), iv2 = f2(iv, iv);
+                    at = at1;
                     ks = at >= 0 ? __ldg(c.k_scale + at) : 0.0f;
                     vs = at >= 0 ? __ldg(c.v_scale + at) : 1.0f;
-                    at1 = t + 2 < t1 ? place(t + 2) : -1;
-                }
-                float x[CW];
-                ta_wait(&s_full[it & 1], (unsigned)((it >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                tc_fence_after();
-                const uint32_t sc = tmem + lanes + (it & 1) * N + col0;
-                tmem_cols<CW>(sc, x);
-                if (kE4M3) {
+                    at1 = place(t + 2 * STEP);
+                    ta_wait(&s_full[it & 1], (unsigned)((it >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                    tc_fence_after();
+                    const uint32_t sc = tmem + lanes + (it & 1) * N + col0;
+                    uint64_t y[CW / 2];
+                    {
+                        uint32_t x[CW], xl[kE4M3 ? CW : 16];
+                        tmem_get(sc, x);
+                        if (kE4M3) tmem_get(sc + RT, xl);
+                        tmem_got(x);
+                        if (kE4M3) tmem_got(xl);
+                        const uint64_t r32 = f2(0.03125f, 0.03125f);
 #pragma unroll
-                    for (int i = 0; i < CW; i += 8) {
-                        float lo[8];
-                        tmem_cols<8>(sc + RT + i, lo);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[i + k] = fmaf(lo[k], 0.03125f, x[i + k]);
+                        for (int i = 0; i < CW / 2; ++i) {
+                            y[i] = u2(x[2 * i], x[2 * i + 1]);
+                            if (kE4M3) y[i] = fma2(u2(xl[2 * i], xl[2 * i + 1]), r32, y[i]);
+                        }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[it & 1]);
-                float top = -INFINITY;
-                if (!seen) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[it & 1]);
+                    // y = x - m
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) x[i] = -INFINITY;
-                } else if (j < w.len) {
+                    for (int i = 0; i < CW / 2; ++i) y[i] = add2(fma2(y[i], cs2, lv2), *reinterpret_cast<const uint64_t *>(nm + 2 * i));
+                    if (__builtin_expect(!__all_sync(0xffffffffu, seen && j < w.len), 0)) {
+                        const int bit = j - w.len;
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) {
-                        x[i] = fmaf(x[i], cs, lv);
-                        top = fmaxf(top, x[i] - m[i]);
+                        for (int i = 0; i < CW / 2; ++i) {
+                            float p = f2_lo(y[i]), q = f2_hi(y[i]);
+                            if (!seen || (bit >= 0 && !((smask[col0 + 2 * i] >> bit) & 1))) p = -INFINITY;
+                            if (!seen || (bit >= 0 && !((smask[col0 + 2 * i + 1] >> bit) & 1))) q = -INFINITY;
+                            y[i] = f2(p, q);
+                        }
                     }
-                } else {
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) {
-                        x[i] = (smask[col0 + i] >> (j - w.len)) & 1 ? fmaf(x[i], cs, lv) : -INFINITY;
-                        top = fmaxf(top, x[i] - m[i]);
+                    for (int i = 0; i < CW / 2; ++i) top = max3(top, f2_lo(y[i]), f2_hi(y[i]));
+                    // Weights up to 2^kTop stay as they are; only a position
+                    // above that moves its column's reference, to kGap below.
+                    if (__builtin_expect(bar_or<128>(1 + wg, top > Z::kTop || unset), 0)) {
+                        {
+                            float v[CW];
+#pragma unroll
+                            for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(y[i]), v[2 * i + 1] = f2_hi(y[i]);
+                            const float cm = warp_columns<CW>(v, [](float p, float q) { return fmaxf(p, q); });
+                            if (lane < CW) wred[(warp & 3) * 32 + lane] = cm;
+                        }
+                        bar_n<128>(1 + wg);
+                        // one warp decides: how far each column's exponents move, the factor of its sums
+                        if (tk < 32) {
+                            const float mx = lane < CW ? fmaxf(fmaxf(wred[lane], wred[32 + lane]), fmaxf(wred[64 + lane], wred[96 + lane])) : -INFINITY;
+                            const bool first = (unset >> lane) & 1 && mx > -INFINITY, move = first || mx > Z::kTop;
+                            const uint32_t set = __ballot_sync(0xffffffffu, move);
+                            const float d = move ? Z::kTop - Z::kGap - mx : 0.0f;
+                            wred[lane] = d;
+                            if (move) nm[lane] += d;
+                            wred[32 + lane] = first ? 1.0f : ex2(d);  // nothing to scale in a first one: its sums are zero
+                            if (lane == 0) reinterpret_cast<uint32_t *>(wred)[64] = unset & ~set;
+                        }
+                        bar_n<128>(1 + wg);
+                        unset = reinterpret_cast<const uint32_t *>(wred)[64];
+#pragma unroll
+                        for (int i = 0; i < CW / 2; ++i) {
+                            const uint64_t d = *reinterpret_cast<const uint64_t *>(wred + 2 * i);
+                            y[i] = add2(y[i], d);
+                            l[i] = mul2(l[i], *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * i));
+                        }
+                        if (some) {
+                            const int before = it - STEP;
+                            ta_wait(&pv_done[before & 1], (unsigned)((before >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int p = 0; p < Z::MT * Z::PARTS; ++p) {
+                                const uint32_t ad = tmem + lanes + 2 * N + (Z::PP ? wg * Z::MT * N : 0) + p * RT + col0;
+                                uint32_t o[CW];
+                                tmem_get(ad, o);
+                                tmem_got(o);
+#pragma unroll
+                                for (int i = 0; i < CW / 2; ++i) {
+                                    const uint64_t v = mul2(u2(o[2 * i], o[2 * i + 1]), *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * i));
+                                    o[2 * i] = (uint32_t)v, o[2 * i + 1] = (uint32_t)(v >> 32);
+                                }
+#pragma unroll
+                                for (int i = 0; i < CW; i += 16) tmem_st16(ad + i, o + i);
+                            }
+                            tmem_wait_st();
+                        }
                     }
-                }
-                // Weights up to 2^8 are held as they are; only a position above
-                // that moves its row's reference (to 2^7 below it).
-                if (bar_or<128>(1 + wg, top > 8.0f)) {
+                    // weights: w = 2^(x - m) = p * v_scale
+                    if (it >= 2)
+                        ta_wait(&pv_done[it & 1], (unsigned)(((it - 2) >> 1) & 1), c.status, kWaitRingEmpty, abort_flag);
+                    char *pr = sp + (it & 1) * Z::PB;
+                    const uint32_t rowb = tk * Z::PW, sw = ((rowb >> 7) & (Z::PW / 16 - 1)) << 4;
 #pragma unroll
-                    for (int i = 0; i < CW; i += 8) {
-                        float y[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = x[i + k];
-                        const float cm = warp_columns<8>(y, [](float p, float q) { return fmaxf(p, q); });
-                        if (lane < 8) wred[(warp & 3) * 32 + i + lane] = cm;
-                    }
-                    bar_n<128>(1 + wg);
-                    const bool sums = (t - t0) % kTaFlush != 0;  // sums of earlier tiles are in tensor memory
-                    if (sums) {
-                        ta_wait(&pv_done[(it - 1) & 1], (unsigned)(((it - 1) >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                        tc_fence_after();
-                    }
-#pragma unroll
-                    for (int i = 0; i < CW; i += 8) {
-                        float f[8];
-                        bool any = false;
+                    for (int i = 0; i < CW; i += 16) {
+                        uint32_t hi[4], lo[4], bw[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float mx = fmaxf(fmaxf(wred[i + k], wred[32 + i + k]), fmaxf(wred[64 + i + k], wred[96 + i + k]));
-                            f[k] = 1.0f;
-                            if (mx - m[i + k] > 8.0f) {
-                                f[k] = ex2(m[i + k] - (mx - 7.0f));
-                                m[i + k] = mx - 7.0f;
-                                l[i + k] *= f[k];
-                                any = true;
+                            const float p = ex2(f2_lo(y[i / 2 + k])), q = ex2(f2_hi(y[i / 2 + k]));
+                            l[i / 2 + k] = fma2(f2(p, q), iv2, l[i / 2 + k]);
+                            if constexpr (kE4M3) {
+                                // 11 bits of the weight, cut into 4 + 4
+                                const __half2 h = __floats2half2_rn(p, q);
+                                const uint32_t c8 = half2_e4m3(h);
+                                const __half2_raw br = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c8, __NV_E4M3);
+                                const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2 *>(&br)), __float2half2_rn(32.0f));
+                                const uint32_t l8 = half2_e4m3(rest);
+                                if (k & 1) {
+                                    hi[k / 2] |= c8 << 16;
+                                    lo[k / 2] |= l8 << 16;
+                                } else {
+                                    hi[k / 2] = c8;
+                                    lo[k / 2] = l8;
+                                }
+                            } else {
+                                bw[k] = bf16x2_bits(p, q);
                             }
                         }
-                        if (!any || !sums) continue;
-#pragma unroll
-                        for (int p = 0; p < Z::MT * Z::PARTS; ++p) {
-                            const uint32_t ad = tmem + lanes + 2 * N + p * RT + col0 + i;
-                            float o[8];
-                            tmem_cols<8>(ad, o);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] *= f[k];
-                            tmem_st8(ad, o);
+                        if constexpr (kE4M3) {
+                            *reinterpret_cast<uint4 *>(pr + ((rowb + col0 + i) ^ sw)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4 *>(pr + ((rowb + RT + col0 + i) ^ sw)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        } else {
+                            *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + i)) ^ sw)) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+                            *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + i) + 16) ^ sw)) = make_uint4(bw[4], bw[5], bw[6], bw[7]);
                         }
                     }
-                    if (sums) tmem_wait_st();
-                    bar_n<128>(1 + wg);  // wred is free again
+                    some = true;
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[it & 1]);
                 }
-                // weights: w = 2^(x - m) = p * v_scale
-#pragma unroll
-                for (int i = 0; i < CW; ++i) {
-                    x[i] = ex2(x[i] - m[i]);
-                    l[i] = fmaf(x[i], iv, l[i]);
-                }
-                if (it >= 2)
-                    ta_wait(&pv_done[it & 1], (unsigned)(((it - 2) >> 1) & 1), c.status, kWaitRingEmpty, abort_flag);
-                char *pr = sp + (it & 1) * Z::PB;
-                const uint32_t rowb = tk * Z::PW, sw = ((rowb >> 7) & (Z::PW / 16 - 1)) << 4;
-                if constexpr (kE4M3) {
-                    uint32_t hi[CW / 4], lo[CW / 4];
-#pragma unroll
-                    for (int i = 0; i < CW / 4; ++i) {
-                        uint32_t hh[2], ll[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float p = x[4 * i + 2 * k], q = x[4 * i + 2 * k + 1];
-                            hh[k] = __nv_cvt_float2_to_fp8x2(make_float2(p, q), __NV_SATFINITE, __NV_E4M3);
-                            const float2 b = e4m3x2_f32(hh[k]);
-                            ll[k] = __nv_cvt_float2_to_fp8x2(make_float2((p - b.x) * 32.0f, (q - b.y) * 32.0f), __NV_SATFINITE, __NV_E4M3);
-                        }
-                        hi[i] = hh[0] | (hh[1] << 16);
-                        lo[i] = ll[0] | (ll[1] << 16);
-                    }
-                    if constexpr (CW == 8) {
-                        *reinterpret_cast<uint2 *>(pr + ((rowb + col0) ^ sw)) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2 *>(pr + ((rowb + RT + col0) ^ sw)) = make_uint2(lo[0], lo[1]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < CW / 16; ++i) {
-                            *reinterpret_cast<uint4 *>(pr + ((rowb + col0 + 16 * i) ^ sw)) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                            *reinterpret_cast<uint4 *>(pr + ((rowb + RT + col0 + 16 * i) ^ sw)) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < CW / 8; ++i)
-                        *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + 8 * i)) ^ sw)) =
-                            make_uint4(bf16x2_bits(x[8 * i], x[8 * i + 1]), bf16x2_bits(x[8 * i + 2], x[8 * i + 3]),
-                                       bf16x2_bits(x[8 * i + 4], x[8 * i + 5]), bf16x2_bits(x[8 * i + 6], x[8 * i + 7]));
-                }
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[it & 1]);
-
                 const bool last = t + 1 == t1;
                 if (!last && (t + 1 - t0) % kTaFlush != 0) continue;
                 // ---- the sums leave tensor memory
-                ta_wait(&pv_done[it & 1], (unsigned)((it >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                tc_fence_after();
-                const float ls = warp_columns<CW>(l, [](float p, float q) { return p + q; });
-                if (lane < CW) wred[(warp & 3) * 32 + lane] = ls;
-                bar_n<128>(1 + wg);
+                {
+                    const int own = it - (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's last tile, if it had one
+                    if (some) ta_wait(&pv_done[own & 1], (unsigned)((own >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                    tc_fence_after();
+                    float v[CW];
 #pragma unroll
-                for (int i = 0; i < CW; i += 8) {
-                    float f0[8], f1[8];  // factors of these sums and of those flushed before
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int r = col0 + i + k;
-                        float sum = (wred[i + k] + wred[32 + i + k]) + (wred[64 + i + k] + wred[96 + i + k]);
-                        float top_r = m[i + k];
-                        f0[k] = 1.0f, f1[k] = 0.0f;
+                    for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(l[i]), v[2 * i + 1] = f2_hi(l[i]);
+                    const float ls = warp_columns<CW>(v, [](float p, float q) { return p + q; });
+                    if (lane < CW) mine[(warp & 3) * CW + lane] = ls;
+                    if (tk < CW) mine[4 * CW + tk] = (unset >> tk) & 1 ? kTaNone : -nm[tk];
+                    bar_n<256>(3);
+                    float top_r = kTaNone, sum = 0.0f;
+                    if ((int)threadIdx.x < rows) {
+                        const int r = threadIdx.x;
+                        float f[3] = {1.0f, 0.0f, 0.0f};
+                        auto side = [&](int g, int col, float &mr, float &sr) {
+                            const float *o = reinterpret_cast<const float *>(sp + g * Z::PB);
+                            mr = o[4 * CW + col];
+                            sr = (o[col] + o[CW + col]) + (o[2 * CW + col] + o[3 * CW + col]);
+                        };
+                        if (Z::PP) {
+                            float m0, m1, s0, s1;
+                            side(0, r, m0, s0);
+                            side(1, r, m1, s1);
+                            top_r = fmaxf(m0, m1);
+                            f[0] = ex2(m0 - top_r);
+                            f[1] = ex2(m1 - top_r);
+                            sum = s0 * f[0] + s1 * f[1];
+                        } else {
+                            side(r / CW, r % CW, top_r, sum);
+                        }
                         if (flushed) {
                             const float2 o = a.ml[(int64_t)slot * RT + r];
-                            top_r = fmaxf(o.x, top_r);
-                            f0[k] = ex2(m[i + k] - top_r);
-                            f1[k] = ex2(o.x - top_r);
-                            sum = sum * f0[k] + o.y * f1[k];
+                            const float mm = fmaxf(o.x, top_r), g = ex2(top_r - mm);
+                            f[2] = ex2(o.x - mm);
+                            f[0] *= g, f[1] *= g;
+                            sum = sum * g + o.y * f[2];
+                            top_r = mm;
                         }
                         if (last && whole) {
                             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                            f0[k] *= inv, f1[k] *= inv;
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) f[k] *= inv;
+                        } else {
+                            a.ml[(int64_t)slot * RT + r] = make_float2(top_r, sum);
                         }
-                        m[i + k] = top_r;
-                        l[i + k] = sum;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) fac[k * 64 + r] = f[k];
                     }
+                    bar_n<256>(3);
+                    // which streams have sums: in a segment of one tile only one has
+                    const int blk = (t - t0) % kTaFlush;  // tiles since the last flush, less one
+                    const bool both = blk > 0;
+                    const int lone = it & 1;
+#pragma unroll 1
+                    for (int q = wg; q < (RT / 16) * Z::MT; q += 2) {
+                        const int i = (q % (RT / 16)) * 16, mt = q / (RT / 16), d = mt * 128 + tk;
+                        if (i >= rows) continue;
+                        float v[16] = {};
+                        const int g0 = Z::PP && !both ? lone : 0, g1 = Z::PP && both ? 2 : g0 + 1;
+#pragma unroll 1
+                        for (int g = g0; g < g1; ++g) {
+                            const uint32_t ad = tmem + lanes + 2 * N + (g * Z::MT + mt) * N + i;
+                            uint32_t o[16], ol[16];
+                            tmem_get(ad, o);
+                            if (kE4M3) tmem_get(ad + RT, ol);
+                            tmem_got(o);
+                            if (kE4M3) tmem_got(ol);
 #pragma unroll
-                    for (int mt = 0; mt < Z::MT; ++mt) {
-                        const int d = mt * 128 + tk;
-                        const uint32_t ad = tmem + lanes + 2 * N + mt * N + col0 + i;
-                        float o[8];
-                        tmem_cols<8>(ad, o);
-                        if (kE4M3) {
-                            float lo[8];
-                            tmem_cols<8>(ad + RT, lo);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = fmaf(lo[k], 0.03125f, o[k]);
+                            for (int k = 0; k < 16; ++k) {
+                                float x = __uint_as_float(o[k]);
+                                if (kE4M3) x = fmaf(__uint_as_float(ol[k]), 0.03125f, x);
+                                v[k] = fmaf(x, fac[g * 64 + i + k], v[k]);
+                            }
                         }
+                        if (d >= c.dim) continue;
+                        float *pd = a.part + ((int64_t)slot * RT + i) * DP + d;
+                        int tok = ta_token(a, row0 + i), gi = row0 + i - tok * a.group;
+                        bf16 *po = a.out + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + gi) * c.dim + d;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = col0 + i + k;
-                            if (r >= rows || d >= c.dim) continue;
-                            float *pd = a.part + ((int64_t)slot * RT + r) * DP + d;
-                            float v = o[k] * f0[k];
-                            if (flushed) v = fmaf(*pd, f1[k], v);
+                        for (int k = 0; k < 16; ++k) {
+                            if (i + k >= rows) break;
+                            if (flushed) v[k] = fmaf(pd[k * DP], fac[128 + i + k], v[k]);
                             if (last && whole) {
-                                const int g = row0 + r, tokn = g / a.group;
-                                a.out[(((int64_t)w.b * c.n + tokn) * a.q_heads + hk * a.group + g % a.group) * c.dim + d] =
-                                    __float2bfloat16_rn(tokn < w.cnt ? v : 0.0f);
+                                *po = __float2bfloat16_rn(tok < w.cnt ? v[k] : 0.0f);
+                                po += c.dim;
+                                if (++gi == a.group) {
+                                    gi = 0;
+                                    ++tok;
+                                    po += (int64_t)(a.q_heads - a.group) * c.dim;
+                                }
                             } else {
-                                *pd = v;
+                                pd[k * DP] = v[k];
                             }
                         }
                     }
+                    tc_fence_before();
+                    flushed = true;
+                    some = false;
+                    fresh();
+                    bar_n<256>(3);  // factors, masks and sums may be overwritten
                 }
-                bar_n<128>(1 + wg);  // every thread has read ml and wred
-                if (!(last && whole) && tk == 0) {
-#pragma unroll
-                    for (int i = 0; i < CW; ++i) a.ml[(int64_t)slot * RT + col0 + i] = make_float2(m[i], l[i]);
-                }
-                tc_fence_before();
-                bar_n<128>(1 + wg);
-                flushed = true;
-#pragma unroll
-                for (int i = 0; i < CW; ++i) m[i] = kTaNone, l[i] = 0.0f;
             }
             if (threadIdx.x == 0 && t0 == 0 && !whole) {
                 // unit ends at tile index e of all: CTA ceil(e * ctas / total) - 1 has its last tile
@@ -894,6 +1029,7 @@ wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *
     a.ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + ta_part_bytes(RT, DP));
     a.desc = reinterpret_cast<int4 *>(reinterpret_cast<char *>(a.ml) + ta_ml_bytes(RT));
     a.q_heads = (int)q_heads, a.group = group, a.rtiles = (int)((rows + RT - 1) / RT);
+    a.group_inv = group > 1 ? (uint32_t)(((1ull << 32) + group - 1) / group) : 0u;
     a.scale = scale;
     a.c = cache_args(cache, seqs, di->status);
     // at most one CTA per tile that the table can hold

@@ -345,6 +345,7 @@ wl_status wl_device_status(void *stream)
                         (word & kWaitRingFull) ? " ring-full" : "",
                         (word & kWaitRingEmpty) ? " ring-empty" : "",
                         (word & kWaitExchange) ? " cluster-exchange" : "");
+        if (word & kStatusAlign) return fail(WL_ERR_INTERNAL, "dynamic shared memory was not aligned as declared");
         if (word & kStatusPage)
             return fail(WL_ERR_INVALID_ARG, "a kernel met a cache position without a valid page");
     }

@@ -42,6 +42,7 @@ constexpr unsigned kWaitRingEmpty = 4u;   // producer waiting for a free ring st
 constexpr unsigned kWaitExchange = 8u;    // waiting for cluster peers' (or other CTAs') partial sums
 constexpr unsigned kWaitDrain = 16u;      // a CTA that gave up could not confirm its copies in flight had landed
 constexpr unsigned kStatusPage = 32u;     // a cache position without a valid page was met and skipped
+constexpr unsigned kStatusAlign = 64u;    // dynamic shared memory was not aligned as declared; the kernel did nothing
 
 // Upper bound of every spin-wait in this library, in SM clock cycles: 4e9
 // cycles is 2 s at 2 GHz (longer at lower clocks).  A wait that runs longer
