@@ -82,7 +82,7 @@ struct TaShape {
     // gap is precision lost for fewer moves; bf16 has range to spare.
     static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f;
     static constexpr int SWP = PW == 128 ? 2 : PW == 64 ? 4 : 6;  // swizzle code of the weights' rows
-    static_assert(SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
+    static_assert(2 * PB >= RT * DP * 2 && SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
 };
 
 // ---------------------------------------------------------------- helpers --
@@ -345,6 +345,21 @@ __device__ __forceinline__ void ta_next(TaWalk &w, const CacheArgs &c, int units
     }
 }
 
+// A position's place in the cache, in two steps so that neither waits for the
+// other's load: the table's page (-2 past the end, -1 past the table), then
+// the row of the codes and scales, ~0 where there is none.
+__device__ __forceinline__ int ta_page(const CacheArgs &c, int b, int j, int end)
+{
+    if (j >= end) return -2;
+    const int p = c.page_shift >= 0 ? j >> c.page_shift : j / c.page_size;
+    return p < c.max_pages ? __ldg(c.pages + (int64_t)b * c.max_pages + p) : -1;
+}
+__device__ __forceinline__ uint32_t ta_row(const CacheArgs &c, int page, int hk, int j)
+{
+    const int off = c.page_shift >= 0 ? j & (c.page_size - 1) : j % c.page_size;
+    return page < 0 || page >= c.npages ? ~0u : ((uint32_t)page * c.kv_heads + hk) * c.page_size + off;
+}
+
 // ------------------------------------------------------------------ kernel --
 template <bool kE4M3, int DP, int RT>
 __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __grid_constant__ TaArgs a)
@@ -362,7 +377,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
     uint64_t *smask = reinterpret_cast<uint64_t *>(misc);            // [RT]
     float *red = reinterpret_cast<float *>(misc + 512);              // [2][4][32]
     float *nms = reinterpret_cast<float *>(misc + 1792);             // [2][32] minus the references of the columns
-    uint64_t *ptrs = reinterpret_cast<uint64_t *>(misc + 2048);      // [4][32] rows of a tile
+    uint32_t *rowtab = reinterpret_cast<uint32_t *>(misc + 2048);    // [4][2][32] rows of two tiles
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc + 1536);
     uint64_t *full = bars, *empty = full + SLOTS, *s_full = empty + SLOTS, *s_empty = s_full + 2, *p_full = s_full + 4,
              *pv_done = s_full + 6, *q_ready = s_full + 8, *drain = s_full + 9;
@@ -411,50 +426,58 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         const int pw = warp - 12;
         constexpr int LPR = Z::SLOTROW / 16, RPP = 32 / LPR;  // lanes per row, rows per pass
         const int ch = lane % LPR, sub = lane / LPR;
-        const char **tab = reinterpret_cast<const char **>(ptrs + pw * 32);
+        uint32_t *tab = rowtab + pw * 64;  // rows of the even and odd tile
         const uint32_t to = (uint32_t)((ch >> 3) * (kTaTile * 128) + (pw * 32 + sub) * 128);
         const uint32_t sw = (uint32_t)(((ch & 7) ^ sub) << 4);  // the row's low bits are sub and those of the pass
+        const uint32_t rowb = (uint32_t)(c.dim * Z::ES);
         int item = 0;
-        auto place = [&](int j, int total, int hk) -> int64_t {
-            if (j >= total) return -1;
-            const int64_t row = cache_row(c, w.b, hk, j);
-            if (row < 0) atomicOr(c.status, kStatusPage);
-            return row;
-        };
-        auto copy = [&](const char *base, int64_t row) {
-            __syncwarp();
-            tab[lane] = row >= 0 ? base + row * (c.dim * Z::ES) : nullptr;
-            __syncwarp();
+        auto copy = [&](const char *base, const uint32_t *tb) {
 #pragma unroll
             for (int s = 0; s < Z::NS; ++s, ++item) {
                 const int slot = item % SLOTS;
-                ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
-                if (*abort_flag) continue;
                 const uint32_t dst = s32(ring + slot * Z::SLOT) + to;
-                const int col = s * Z::SLOTROW + ch * 16;
-                const bool in = col < c.dim * Z::ES;
+                const uint32_t col = s * Z::SLOTROW + ch * 16;
+                const bool in = col < rowb;
+                const char *src = in ? base + col : base;
+                uint32_t r[32 / RPP];
+#pragma unroll
+                for (int p = 0; p < 32 / RPP; ++p) r[p] = tb[p * RPP + sub];
+                ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
 #pragma unroll
                 for (int p = 0; p < 32 / RPP; ++p) {
-                    const char *src = tab[p * RPP + sub];
-                    const bool ok = in && src != nullptr;
+                    const bool ok = in && r[p] != ~0u;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                      dst + p * (RPP * 128) + (sw ^ (((p * RPP) & 7) << 4))),
-                                 "l"(ok ? src + col : base), "r"(ok ? 16 : 0));
+                                 "l"(src + (ok ? (uint64_t)r[p] * rowb : 0ull)), "r"(ok ? 16 : 0));
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(&full[slot])) : "memory");
             }
         };
         while (w.left > 0) {
-            const int t1 = ta_end(w), total = w.cnt > 0 ? w.len + w.cnt : 0, hk = w.u / a.rtiles;
-            int64_t prev = -1, next = place(w.tile * kTaTile + pw * 32 + lane, total, hk);
-            for (int t = w.tile; t < t1; ++t) {
-                const int64_t row = next;
-                if (t + 1 < t1) next = place((t + 1) * kTaTile + pw * 32 + lane, total, hk);
-                copy(c.k, row);
-                if (t > w.tile) copy(c.v, prev);
-                prev = row;
+            // Two tiles ahead the page of a row is loaded, one tile ahead it
+            // becomes a row: no copy waits for a lookup (4421 -> 6691 GB/s in
+            // isolation).
+            const int t1 = ta_end(w), hk = w.u / a.rtiles, end = min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile);
+            int j = w.tile * kTaTile + pw * 32 + lane;
+            auto place = [&](int pg, int j) -> uint32_t {
+                const uint32_t row = ta_row(c, pg, hk, j);
+                if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
+                return row;
+            };
+            int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
+            __syncwarp();
+            tab[(w.tile & 1) * 32 + lane] = place(pg, j);
+            __syncwarp();
+            for (int t = w.tile; t < t1; ++t, j += kTaTile) {
+                pg = pg1;
+                pg1 = ta_page(c, w.b, j + 2 * kTaTile, end);
+                copy(c.k, tab + (t & 1) * 32);
+                if (t > w.tile) copy(c.v, tab + ((t - 1) & 1) * 32);
+                __syncwarp();  // the table of tile t - 1 has been read
+                tab[((t + 1) & 1) * 32 + lane] = place(pg, j + kTaTile);
+                __syncwarp();
             }
-            copy(c.v, prev);
+            copy(c.v, tab + ((t1 - 1) & 1) * 32);
             ta_next(w, c, units);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -491,7 +514,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 for (int s = 0; s < Z::NS; ++s) {
                     int slot;
                     take(slot);
-                    if (*abort_flag) continue;
                     const uint32_t ak = br + slot * Z::SLOT;
 #pragma unroll
                     for (int k = 0; k < Z::SLOTROW / 32; ++k) {
@@ -511,7 +533,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 for (int s = 0; s < Z::NS; ++s) {
                     int slot;
                     take(slot);
-                    if (*abort_flag) continue;
                     const uint32_t av = br + slot * Z::SLOT;
                     constexpr int MS = Z::MT / Z::NS;  // M tiles of a slot
 #pragma unroll
@@ -559,14 +580,19 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             const int t0 = w.tile, t1 = ta_end(w), total = w.cnt > 0 ? w.len + w.cnt : 0;
             const int hk = w.u / a.rtiles, row0 = (w.u - hk * a.rtiles) * RT, rows = min(RT, c.n * a.group - row0);
             constexpr int STEP = Z::PP ? 2 : 1;
-            // place and scales of this thread's position, loaded a tile ahead
-            auto place = [&](int t) -> int64_t {
-                const int j = t * kTaTile + tk;
-                return t < t1 && j < total ? cache_row(c, w.b, hk, j) : -1;
-            };
+            // scales of this thread's position, loaded a tile ahead
             const int tf = t0 + (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's first tile
-            int64_t at = place(tf), at1 = place(tf + STEP);
-            float ks = at >= 0 ? __ldg(c.k_scale + at) : 0.0f, vs = at >= 0 ? __ldg(c.v_scale + at) : 1.0f;
+            const int end = min(total, t1 * kTaTile);
+            int pg1;
+            uint32_t at;
+            float ks, vs;
+            {
+                const int j = tf * kTaTile + tk;
+                at = ta_row(c, ta_page(c, w.b, j, end), hk, j);
+                pg1 = ta_page(c, w.b, j + STEP * kTaTile, end);
+                ks = at != ~0u ? __ldg(c.k_scale + at) : 0.0f;
+                vs = at != ~0u ? __ldg(c.v_scale + at) : 1.0f;
+            }
             // nm: minus the references of the columns (the same for all threads,
             // so in shared memory), l: this position's sums, as pairs; unset:
             // columns that have seen nothing yet and have no reference.
@@ -586,12 +612,19 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             float qscale = a.scale * kLog2e;
             {
                 constexpr int CH = DP / 8, PER = RT * CH / 256;  // 8-element chunks of a row, per thread
-                auto chunk = [&](int e) -> uint4 {
-                    const int r = e / CH, d = (e % CH) * 8, g = row0 + r, tok = ta_token(a, g);
-                    if (r >= rows || d >= c.dim || tok >= w.cnt) return make_uint4(0u, 0u, 0u, 0u);
-                    return *reinterpret_cast<const uint4 *>(
-                        a.q + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + (g - tok * a.group)) * c.dim + d);
-                };
+                // all of a thread's chunks are in flight at once; they wait in the idle weight buffers
+                uint4 *raw = reinterpret_cast<uint4 *>(sp) + threadIdx.x;
+                uint4 v[PER];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int e = threadIdx.x + i * 256, r = e / CH, d = (e % CH) * 8, g = row0 + r, tok = ta_token(a, g);
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows && d < c.dim && tok < w.cnt)
+                        v[i] = *reinterpret_cast<const uint4 *>(
+                            a.q + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + (g - tok * a.group)) * c.dim + d);
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) raw[i * 256] = v[i];
                 if (threadIdx.x < RT) {
                     const int g = row0 + threadIdx.x, i = ta_token(a, g);
                     uint64_t m = 0;
@@ -605,9 +638,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 if (kE4M3) {
                     // one power of two brings the largest |q| of the tile into [128, 256)
                     uint32_t amax = 0;
-#pragma unroll 2
+#pragma unroll 1
                     for (int i = 0; i < PER; ++i) {
-                        const uint4 v = chunk(threadIdx.x + i * 256);
+                        const uint4 v = raw[i * 256];
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -628,7 +661,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 #pragma unroll 1
                 for (int i = 0; i < PER; ++i) {
                     const int e = threadIdx.x + i * 256, r = e / CH, ck = e % CH;
-                    const uint4 v = chunk(e);
+                    const uint4 v = raw[i * 256];
                     if (kE4M3) {
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                         uint32_t hi[2] = {}, lo[2] = {};
@@ -661,7 +694,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             for (int t = t0; t < t1; ++t, ++it) {
                 if (!Z::PP || (it & 1) == wg) {
                     const int j = t * kTaTile + tk;
-                    const bool seen = at >= 0;
+                    const bool seen = at != ~0u;
                     const bool bad = vs != vs;
                     const float v1 = fmaxf(vs, 1.17549435e-38f);
                     // log2 of the scale: exponent exact, 0 for the mantissa of a power of two
@@ -669,10 +702,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                                                __log2f(__uint_as_float((__float_as_uint(v1) & 0x7fffffu) | 0x3f800000u));
                     const float iv = bad ? 1.0f : __frcp_rn(v1);
                     const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv), iv2 = f2(iv, iv);
-                    at = at1;
-                    ks = at >= 0 ? __ldg(c.k_scale + at) : 0.0f;
-                    vs = at >= 0 ? __ldg(c.v_scale + at) : 1.0f;
-                    at1 = place(t + 2 * STEP);
+                    at = ta_row(c, pg1, hk, j + STEP * kTaTile);
+                    ks = at != ~0u ? __ldg(c.k_scale + at) : 0.0f;
+                    vs = at != ~0u ? __ldg(c.v_scale + at) : 1.0f;
+                    pg1 = ta_page(c, w.b, j + 2 * STEP * kTaTile, end);
                     ta_wait(&s_full[it & 1], (unsigned)((it >> 1) & 1), c.status, kWaitRingFull, abort_flag);
                     tc_fence_after();
                     const uint32_t sc = tmem + lanes + (it & 1) * N + col0;
@@ -1023,6 +1056,8 @@ wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *
     const int group = (int)(q_heads / cache.kv_heads), DP = cache.dim <= 128 ? 128 : 256;
     const int64_t rows = seqs.n * group;
     const int RT = ta_rows(rows);
+    if (cache.pages * cache.kv_heads * cache.page_size >= (int64_t)0xffffffff)
+        return fail(WL_ERR_UNSUPPORTED, "wl_tree_attention: pages * kv_heads * page_size must be below 2^32 - 1");
     TaArgs a;
     a.q = q, a.mask = mask, a.out = out;
     a.part = static_cast<float *>(ws);
