@@ -27,7 +27,7 @@ struct TmapKey {
     uintptr_t base;
     int64_t inner, outer, ld;
     int box_inner, box_outer, swz;
-    int nblk;  // 0: 2D map; > 0: 3D view of nblk consecutive 64-column blocks per box
+    int nblk;  // 0: 2D map of bf16; -1: 2D map of bytes; > 0: 3D view of nblk consecutive 64-column blocks per box
     bool operator==(const TmapKey &o) const
     {
         return base == o.base && inner == o.inner && outer == o.outer && ld == o.ld &&
@@ -135,6 +135,36 @@ wl_status tmap_kblocks_bf16(const void *base, int64_t K, int64_t rows, int box_r
     if (r != CUDA_SUCCESS)
         return fail(WL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a k-block view of a [%lld, %lld] matrix", (int)r,
                     (long long)rows, (long long)K);
+    g_tmaps.emplace(key, m);
+    *out = m;
+    return WL_OK;
+}
+
+// Rows of row_bytes bytes (a multiple of 16) back to back; a box is box_rows
+// rows x 128 bytes with 128-byte swizzle, zeros past a row's end.
+wl_status tmap_rows_u8(const void *base, int64_t row_bytes, int64_t rows, int box_rows, CUtensorMap *out)
+{
+    std::lock_guard<std::mutex> lk(g_tmap_mu);
+    const wl_status es = load_encoder();
+    if (es != WL_OK) return es;
+    const TmapKey key{reinterpret_cast<uintptr_t>(base), row_bytes, rows, row_bytes, 128, box_rows, 128, -1};
+    auto it = g_tmaps.find(key);
+    if (it != g_tmaps.end()) {
+        *out = it->second;
+        return WL_OK;
+    }
+    if (g_tmaps.size() > 4096) g_tmaps.clear();
+    CUtensorMap m;
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(WL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld rows of %lld bytes", (int)r, (long long)rows,
+                    (long long)row_bytes);
     g_tmaps.emplace(key, m);
     *out = m;
     return WL_OK;

@@ -43,6 +43,8 @@ constexpr float kTaNone = -3.0e38f;  // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct TaArgs {
+    CUtensorMap kmap, vmap;  // the codes as [rows, row bytes], boxes of `box` rows x 128 bytes, zero past a row's end
+    int box;                 // rows of a box: a run of positions that lies in one page; 0: no box copies
     const bf16 *q;
     const uint64_t *mask;
     bf16 *out;
@@ -80,7 +82,7 @@ struct TaShape {
     // Exponents of weights: the limit, and how far below it a moved reference
     // puts the largest weight.  e4m3 ends at 448, so the limit is 2^8, and the
     // gap is precision lost for fewer moves; bf16 has range to spare.
-    static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f;
+    static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f, kNear = kE4M3 ? 2.0f : 0.0f;
     static constexpr int SWP = PW == 128 ? 2 : PW == 64 ? 4 : 6;  // swizzle code of the weights' rows
     static_assert(2 * PB >= RT * DP * 2 && SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
 };
@@ -141,13 +143,13 @@ __device__ __forceinline__ void tmem_got(uint32_t (&r)[C])
 #pragma unroll
     for (int i = 0; i < C; i += 16) tmem_wait16(r + i);
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+__device__ __forceinline__ void load16(const float *p, float (&v)[16])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 f = reinterpret_cast<const float4 *>(p)[i];
+        v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(&full[i], 128);
+            mbar_init(&full[i], a.box ? 1 : 4);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -419,68 +421,127 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 
     if (warp >= 12) {
         // ------------------------------------------------ cache loads
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRegsOther));
         // Ring items in the order the MMAs take them: K0, K1, V0, K2, V1, ...
-        // Warp pw holds rows 32 pw .. of a tile: a lane looks up one row's
-        // place, then the lanes of a row copy 16 bytes each.
-        const int pw = warp - 12;
-        constexpr int LPR = Z::SLOTROW / 16, RPP = 32 / LPR;  // lanes per row, rows per pass
-        const int ch = lane % LPR, sub = lane / LPR;
-        uint32_t *tab = rowtab + pw * 64;  // rows of the even and odd tile
-        const uint32_t to = (uint32_t)((ch >> 3) * (kTaTile * 128) + (pw * 32 + sub) * 128);
-        const uint32_t sw = (uint32_t)(((ch & 7) ^ sub) << 4);  // the row's low bits are sub and those of the pass
-        const uint32_t rowb = (uint32_t)(c.dim * Z::ES);
+        // Two tiles ahead a page is looked up, one tile ahead it becomes a
+        // row: no copy waits for a lookup.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRegsOther));
         int item = 0;
-        auto copy = [&](const char *base, const uint32_t *tb) {
+        if (a.box == 0) {
+            // 16-byte copies: warp pw takes rows 32 pw .. of a tile; zeros
+            // where there is no row
+            const int pw = warp - 12;
+            constexpr int LPR = Z::SLOTROW / 16, RPP = 32 / LPR;  // lanes per row, rows per pass
+            const int ch = lane % LPR, sub = lane / LPR;
+            uint32_t *tab = rowtab + pw * 64;  // rows of the even and odd tile
+            const uint32_t to = (uint32_t)((ch >> 3) * (kTaTile * 128) + (pw * 32 + sub) * 128);
+            const uint32_t sw = (uint32_t)(((ch & 7) ^ sub) << 4);  // the row's low bits are sub and those of the pass
+            const uint32_t rowb = (uint32_t)(c.dim * Z::ES);
+            auto copy = [&](const char *base, const uint32_t *tb) {
 #pragma unroll
-            for (int s = 0; s < Z::NS; ++s, ++item) {
-                const int slot = item % SLOTS;
-                const uint32_t dst = s32(ring + slot * Z::SLOT) + to;
-                const uint32_t col = s * Z::SLOTROW + ch * 16;
-                const bool in = col < rowb;
-                const char *src = in ? base + col : base;
-                uint32_t r[32 / RPP];
-#pragma unroll
-                for (int p = 0; p < 32 / RPP; ++p) r[p] = tb[p * RPP + sub];
-                ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
-#pragma unroll
-                for (int p = 0; p < 32 / RPP; ++p) {
-                    const bool ok = in && r[p] != ~0u;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                     dst + p * (RPP * 128) + (sw ^ (((p * RPP) & 7) << 4))),
-                                 "l"(src + (ok ? (uint64_t)r[p] * rowb : 0ull)), "r"(ok ? 16 : 0));
+                for (int s = 0; s < Z::NS; ++s, ++item) {
+                    const int slot = item % SLOTS;
+                    const uint32_t dst = s32(ring + slot * Z::SLOT) + to, col = s * Z::SLOTROW + ch * 16;
+                    const bool in = col < rowb;
+                    const char *src = in ? base + col : base;
+                    ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
+#pragma unroll 4
+                    for (int p = 0; p < 32 / RPP; ++p) {
+                        const uint32_t r = tb[p * RPP + sub];
+                        const bool ok = in && r != ~0u;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         dst + p * (RPP * 128) + (sw ^ (((p * RPP) & 7) << 4))),
+                                     "l"(src + (ok ? (uint64_t)r * rowb : 0ull)), "r"(ok ? 16 : 0));
+                    }
+                    cp_async_wait_all();
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[slot]);
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(&full[slot])) : "memory");
-            }
-        };
-        while (w.left > 0) {
-            // Two tiles ahead the page of a row is loaded, one tile ahead it
-            // becomes a row: no copy waits for a lookup (4421 -> 6691 GB/s in
-            // isolation).
-            const int t1 = ta_end(w), hk = w.u / a.rtiles, end = min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile);
-            int j = w.tile * kTaTile + pw * 32 + lane;
-            auto place = [&](int pg, int j) -> uint32_t {
-                const uint32_t row = ta_row(c, pg, hk, j);
-                if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
-                return row;
             };
-            int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
-            __syncwarp();
-            tab[(w.tile & 1) * 32 + lane] = place(pg, j);
-            __syncwarp();
-            for (int t = w.tile; t < t1; ++t, j += kTaTile) {
-                pg = pg1;
-                pg1 = ta_page(c, w.b, j + 2 * kTaTile, end);
-                copy(c.k, tab + (t & 1) * 32);
-                if (t > w.tile) copy(c.v, tab + ((t - 1) & 1) * 32);
-                __syncwarp();  // the table of tile t - 1 has been read
-                tab[((t + 1) & 1) * 32 + lane] = place(pg, j + kTaTile);
-                __syncwarp();
+            while (w.left > 0) {
+                const int t1 = ta_end(w), hk = w.u / a.rtiles, end = min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile);
+                int j = w.tile * kTaTile + pw * 32 + lane;
+                auto place = [&](int t, int pg, int j) {
+                    const uint32_t row = ta_row(c, pg, hk, j);
+                    if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
+                    __syncwarp();  // the tile that had this table has been issued
+                    tab[(t & 1) * 32 + lane] = row;
+                    __syncwarp();
+                };
+                int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
+                place(w.tile, pg, j);
+                for (int t = w.tile; t < t1; ++t, j += kTaTile) {
+                    pg = pg1;
+                    pg1 = ta_page(c, w.b, j + 2 * kTaTile, end);
+                    copy(c.k, tab + (t & 1) * 32);
+                    if (t > w.tile) copy(c.v, tab + ((t - 1) & 1) * 32);
+                    place(t + 1, pg, j + kTaTile);
+                }
+                copy(c.v, tab + ((t1 - 1) & 1) * 32);
+                ta_next(w, c, units);
             }
-            copy(c.v, tab + ((t1 - 1) & 1) * 32);
-            ta_next(w, c, units);
+        } else if (warp == 12) {
+            // Boxes: lane r looks up run r of a.box positions; one lane copies
+            // them all.  A run at the end brings what its page holds beyond;
+            // what no box brings stays as it was: scores there are masked,
+            // and the softmax warps zero those rows of V.
+            const int runs = kTaTile / a.box;
+            const uint32_t bytes = (uint32_t)(a.box * Z::SLOTROW);
+            auto copy = [&](const CUtensorMap *map, const uint32_t *tb, uint32_t have) {
+#pragma unroll
+                for (int s = 0; s < Z::NS; ++s, ++item) {
+                    const int slot = item % SLOTS;
+                    ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
+                    if (elect_one()) {
+                        mbar_expect_tx(&full[slot], (uint32_t)__popc(have) * bytes);
+                        char *dst = ring + slot * Z::SLOT;
+#pragma unroll 1
+                        for (int k = 0; k < runs; ++k, dst += a.box * 128) {
+                            const uint32_t row = tb[k];
+                            if (row == ~0u) continue;
+#pragma unroll
+                            for (int h = 0; h < Z::SLOTROW / 128; ++h)
+                                tma_load_2d(dst + h * (kTaTile * 128), map, s * Z::SLOTROW + h * 128, (int)row, &full[slot]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            };
+            while (w.left > 0) {
+                const int t1 = ta_end(w), hk = w.u / a.rtiles;
+                const int end = lane < runs ? min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile) : 0;
+                int j = w.tile * kTaTile + lane * a.box;
+                auto place = [&](int t, int pg, int j) -> uint32_t {
+                    const uint32_t row = ta_row(c, pg, hk, j);
+                    if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
+                    rowtab[(t & 1) * 32 + lane] = row;
+                    __syncwarp();
+                    return __ballot_sync(0xffffffffu, row != ~0u);
+                };
+                int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
+                uint32_t have = place(w.tile, pg, j), before = 0;
+                for (int t = w.tile; t < t1; ++t, j += kTaTile) {
+                    pg = pg1;
+                    pg1 = ta_page(c, w.b, j + 2 * kTaTile, end);
+                    copy(&a.kmap, rowtab + (t & 1) * 32, have);
+                    if (t > w.tile) copy(&a.vmap, rowtab + ((t - 1) & 1) * 32, before);
+                    before = have;
+                    have = place(t + 1, pg, j + kTaTile);
+                }
+                copy(&a.vmap, rowtab + ((t1 - 1) & 1) * 32, before);
+                ta_next(w, c, units);
+            }
+            // Boxes still in flight (only after a wait gave up) land before the CTA's shared memory goes.
+            const long long t0 = wait_clock();
+            for (int i = max(0, item - SLOTS); i < item; ++i)
+                while (!mbar_test(&full[i % SLOTS], (unsigned)((i / SLOTS) & 1))) {
+                    if (wait_clock() - t0 > kWaitLimitCycles) {
+                        atomicOr(c.status, kStatusTimeout | kWaitDrain);
+                        i = item;
+                        break;
+                    }
+                }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= 8) {
         // ------------------------------------------------ MMA issuer
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRegsOther));
@@ -503,7 +564,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             auto take = [&](int &slot) {
                 slot = item % SLOTS;
                 ta_wait(&full[slot], (unsigned)((item / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
-                fence_async_smem();  // the copies were ordinary shared-memory writes
                 ++item;
             };
             auto scores = [&](int i) {
@@ -574,7 +634,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         float *wred = red + wg * 128;
         float *mine = reinterpret_cast<float *>(sp + wg * Z::PB);  // [4][CW] sums, [CW] references, when the buffer is idle
         float *fac = reinterpret_cast<float *>(sp + 1024);         // [3][64] factors of both streams and of flushed sums
-        int it = 0;
+        int it = 0, items = 0;  // tiles and ring items of earlier segments
         if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
         while (w.left > 0) {
             const int t0 = w.tile, t1 = ta_end(w), total = w.cnt > 0 ? w.len + w.cnt : 0;
@@ -637,15 +697,19 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 float up = 1.0f;
                 if (kE4M3) {
                     // one power of two brings the largest |q| of the tile into [128, 256)
-                    uint32_t amax = 0;
-#pragma unroll 1
-                    for (int i = 0; i < PER; ++i) {
-                        const uint4 v = raw[i * 256];
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t two = 0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = u[j] & 0x7fffu, hi = (u[j] >> 16) & 0x7fffu;
-                            amax = max(amax, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                    for (int i = 0; i < PER; ++i)
+                        two = __vmaxu2(__vmaxu2(two, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu)),
+                                       __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+                    uint32_t amax = max(two & 0xffffu, two >> 16);
+                    if (__builtin_expect(amax >= 0x7f80u, 0)) {  // NaN or infinity: the largest of the others
+                        amax = 0;
+                        const uint16_t *e = reinterpret_cast<const uint16_t *>(raw);
+#pragma unroll 1
+                        for (int i = 0; i < PER * 8; ++i) {
+                            const uint32_t u = e[(i / 8) * 2048 + i % 8] & 0x7fffu;
+                            amax = max(amax, u < 0x7f80u ? u : 0u);
                         }
                     }
                     amax = __reduce_max_sync(0xffffffffu, amax);
@@ -658,7 +722,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     up = __uint_as_float((uint32_t)(261 - be) << 23);  // 2^(134 - be)
                     qscale *= __uint_as_float((uint32_t)(be - 7) << 23);
                 }
-#pragma unroll 1
+#pragma unroll 2
                 for (int i = 0; i < PER; ++i) {
                     const int e = threadIdx.x + i * 256, r = e / CH, ck = e % CH;
                     const uint4 v = raw[i * 256];
@@ -753,42 +817,54 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                             if (lane < CW) wred[(warp & 3) * 32 + lane] = cm;
                         }
                         bar_n<128>(1 + wg);
-                        // one warp decides: how far each column's exponents move, the factor of its sums
+                        // one warp decides: how far each column's exponents move
+                        // (also those about to reach the limit), the factor of its sums
                         if (tk < 32) {
                             const float mx = lane < CW ? fmaxf(fmaxf(wred[lane], wred[32 + lane]), fmaxf(wred[64 + lane], wred[96 + lane])) : -INFINITY;
-                            const bool first = (unset >> lane) & 1 && mx > -INFINITY, move = first || mx > Z::kTop;
+                            const bool first = (unset >> lane) & 1 && mx > -INFINITY, move = first || mx > Z::kTop - Z::kNear;
                             const uint32_t set = __ballot_sync(0xffffffffu, move);
                             const float d = move ? Z::kTop - Z::kGap - mx : 0.0f;
                             wred[lane] = d;
-                            if (move) nm[lane] += d;
                             wred[32 + lane] = first ? 1.0f : ex2(d);  // nothing to scale in a first one: its sums are zero
-                            if (lane == 0) reinterpret_cast<uint32_t *>(wred)[64] = unset & ~set;
+                            if (move) nm[lane] += d;
+                            if (lane == 0) reinterpret_cast<uint2 *>(wred)[32] = make_uint2(unset & ~set, set);
                         }
                         bar_n<128>(1 + wg);
-                        unset = reinterpret_cast<const uint32_t *>(wred)[64];
+                        const uint2 state = reinterpret_cast<const uint2 *>(wred)[32];
+                        unset = state.x;
 #pragma unroll
-                        for (int i = 0; i < CW / 2; ++i) {
-                            const uint64_t d = *reinterpret_cast<const uint64_t *>(wred + 2 * i);
-                            y[i] = add2(y[i], d);
-                            l[i] = mul2(l[i], *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * i));
+                        for (int i = 0; i < CW; i += 8) {
+                            if (!((state.y >> i) & 0xffu)) continue;
+#pragma unroll
+                            for (int k = i / 2; k < i / 2 + 4; ++k) {
+                                y[k] = add2(y[k], *reinterpret_cast<const uint64_t *>(wred + 2 * k));
+                                l[k] = mul2(l[k], *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * k));
+                            }
                         }
                         if (some) {
                             const int before = it - STEP;
                             ta_wait(&pv_done[before & 1], (unsigned)((before >> 1) & 1), c.status, kWaitRingFull, abort_flag);
                             tc_fence_after();
+                            constexpr int P = Z::MT * Z::PARTS;
 #pragma unroll 1
-                            for (int p = 0; p < Z::MT * Z::PARTS; ++p) {
-                                const uint32_t ad = tmem + lanes + 2 * N + (Z::PP ? wg * Z::MT * N : 0) + p * RT + col0;
-                                uint32_t o[CW];
-                                tmem_get(ad, o);
-                                tmem_got(o);
+                            for (int i = 0; i < CW; i += 8) {
+                                if (!((state.y >> i) & 0xffu)) continue;
+                                const uint32_t ad = tmem + lanes + 2 * N + (Z::PP ? wg * Z::MT * N : 0) + col0 + i;
+                                uint32_t o[P][8];
+                                float f[8];
 #pragma unroll
-                                for (int i = 0; i < CW / 2; ++i) {
-                                    const uint64_t v = mul2(u2(o[2 * i], o[2 * i + 1]), *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * i));
-                                    o[2 * i] = (uint32_t)v, o[2 * i + 1] = (uint32_t)(v >> 32);
+                                for (int p = 0; p < P; ++p) tmem_ld8_nw(ad + p * RT, o[p]);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) f[k] = wred[32 + i + k];
+#pragma unroll
+                                for (int p = 0; p < P; ++p) tmem_wait_ld8(o[p]);
+#pragma unroll
+                                for (int p = 0; p < P; ++p) {
+                                    float x[8];
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[p][k]) * f[k];
+                                    tmem_st8(ad + p * RT, x);
                                 }
-#pragma unroll
-                                for (int i = 0; i < CW; i += 16) tmem_st16(ad + i, o + i);
                             }
                             tmem_wait_st();
                         }
@@ -829,6 +905,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         } else {
                             *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + i)) ^ sw)) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
                             *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + i) + 16) ^ sw)) = make_uint4(bw[4], bw[5], bw[6], bw[7]);
+                        }
+                    }
+                    if (__builtin_expect(a.box && !__all_sync(0xffffffffu, seen), 0)) {
+                        // rows of V that are not there: weight 0 must meet a number
+                        const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * (r + 1 < n ? 2 * r + 2 : 2 * n - 1);
+                        for (int s = 0; s < Z::NS; ++s) {
+                            const int vs = (v0 + s) % SLOTS;
+                            ta_wait(&full[vs], (unsigned)(((v0 + s) / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
+                            if (!seen && (Z::PP || wg == 0))
+                                for (int h = 0; h < Z::SLOTROW / 16; ++h)
+                                    *reinterpret_cast<uint4 *>(ring + vs * Z::SLOT + (h / 8) * (kTaTile * 128) + tk * 128 + (h % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     some = true;
@@ -906,34 +993,39 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                             uint32_t o[16], ol[16];
                             tmem_get(ad, o);
                             if (kE4M3) tmem_get(ad + RT, ol);
+                            float f[16];
+                            load16(fac + g * 64 + i, f);
                             tmem_got(o);
                             if (kE4M3) tmem_got(ol);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
                                 float x = __uint_as_float(o[k]);
                                 if (kE4M3) x = fmaf(__uint_as_float(ol[k]), 0.03125f, x);
-                                v[k] = fmaf(x, fac[g * 64 + i + k], v[k]);
+                                v[k] = fmaf(x, f[k], v[k]);
                             }
                         }
                         if (d >= c.dim) continue;
+                        const int nr = min(16, rows - i);
                         float *pd = a.part + ((int64_t)slot * RT + i) * DP + d;
-                        int tok = ta_token(a, row0 + i), gi = row0 + i - tok * a.group;
-                        bf16 *po = a.out + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + gi) * c.dim + d;
+                        if (flushed) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            if (i + k >= rows) break;
-                            if (flushed) v[k] = fmaf(pd[k * DP], fac[128 + i + k], v[k]);
-                            if (last && whole) {
-                                *po = __float2bfloat16_rn(tok < w.cnt ? v[k] : 0.0f);
+                            for (int k = 0; k < 16; ++k)
+                                if (k < nr) v[k] = fmaf(pd[k * DP], fac[128 + i + k], v[k]);
+                        }
+                        if (last && whole) {
+                            int tok = ta_token(a, row0 + i), gi = row0 + i - tok * a.group;
+                            bf16 *po = a.out + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + gi) * c.dim + d;
+                            const int64_t jump = (int64_t)(a.q_heads - a.group) * c.dim;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                if (k < nr) *po = __float2bfloat16_rn(tok < w.cnt ? v[k] : 0.0f);
                                 po += c.dim;
-                                if (++gi == a.group) {
-                                    gi = 0;
-                                    ++tok;
-                                    po += (int64_t)(a.q_heads - a.group) * c.dim;
-                                }
-                            } else {
-                                pd[k * DP] = v[k];
+                                if (++gi == a.group) gi = 0, ++tok, po += jump;
                             }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if (k < nr) pd[k * DP] = v[k];
                         }
                     }
                     tc_fence_before();
@@ -948,6 +1040,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 const int64_t e = w.start + w.ntiles;
                 a.desc[blockIdx.x] = make_int4(w.b, w.u, (int)((e * w.ctas + w.total - 1) / w.total) - 1, 0);
             }
+            items += 2 * Z::NS * (t1 - t0);
             ta_next(w, c, units);
         }
     }
@@ -958,58 +1051,65 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 }
 
 // Joins the partial sums of the unit that CTA blockIdx.x began and others
-// finished; one block per row of it, contributors in CTA order.
-template <int DP, int RT>
+// finished, contributors in CTA order.  A block has G groups of lanes that
+// each cover a row: R rows of the unit, G / R groups sharing a row's
+// contributors (few rows come with many contributors and the other way round).
+template <int DP, int RT, int R>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TaArgs a)
 {
-    constexpr int L = DP / 4, G = 256 / L;  // 16-byte lanes of a row; groups that share the contributors
-    __shared__ float wgt[kTaMaxCtas + 1], redm[8], reds[8];
+    constexpr int L = DP / 4, G = 256 / L, S = G / R;  // 16-byte lanes of a row
+    __shared__ float wgt[R][kTaMaxCtas], inv[R];
     __shared__ float4 acc[G][L];
     pdl_wait();
     const int4 u = a.desc[blockIdx.x];
     if (u.x < 0) return;
     const CacheArgs &c = a.c;
-    const int r = blockIdx.y, hk = u.y / a.rtiles, g = (u.y - hk * a.rtiles) * RT + r;
-    if (g >= c.n * a.group) return;
-    const int n = u.z - (int)blockIdx.x + 1, t = threadIdx.x;  // contributors
-    auto slot = [&](int k) -> int64_t { return (int64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * RT + r; };
-    float2 ml = make_float2(kTaNone, 0.0f);
-    if (t < n) ml = a.ml[slot(t)];
-    float m = ml.x;
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (t % 32 == 0) redm[t / 32] = m;
+    const int hk = u.y / a.rtiles, row0 = (u.y - hk * a.rtiles) * RT, r0 = blockIdx.y * R, t = threadIdx.x, lane = t & 31;
+    const int rows = min(RT, c.n * a.group - row0) - r0;  // from r0 on
+    if (rows <= 0) return;
+    const int n = u.z - (int)blockIdx.x + 1;  // contributors
+    auto slot = [&](int k, int r) -> int64_t { return (int64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * RT + r0 + r; };
+    // a warp per row: the weights of its contributors
+    for (int r = t / 32; r < R && r < rows; r += 8) {
+        float m = kTaNone, s = 0.0f;
+        for (int k = lane; k < n; k += 32) m = fmaxf(m, a.ml[slot(k, r)].x);
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int k = lane; k < n; k += 32) {
+            const float2 ml = a.ml[slot(k, r)];
+            const float f = ex2(ml.x - m);
+            wgt[r][k] = f;
+            s = fmaf(ml.y, f, s);
+        }
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        const bool on = ta_token(a, row0 + r0 + r) < seq_count(c, u.x);
+        if (lane == 0) inv[r] = on ? (s == 0.0f ? 0.0f : 1.0f / s) : -1.0f;  // -1: a row past the count
+    }
     __syncthreads();
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, redm[i]);
-    const float f = t < n ? ex2(ml.x - m) : 0.0f;
-    if (t < n) wgt[t] = f;
-    float s = ml.y * f;
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (t % 32 == 0) reds[t / 32] = s;
-    __syncthreads();
-    s = 0.0f;
-    for (int i = 0; i < 8; ++i) s += reds[i];
-    const int lane = t % L, grp = t / L;
+    const int el = (t % L) * 4, grp = t / L, r = grp / S, part = grp % S;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (lane * 4 < c.dim) {
-#pragma unroll 8
-        for (int k = grp; k < n; k += G) {
-            const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(k) * DP + lane * 4);
-            const float h = wgt[k];
+    if (el < c.dim && r < rows) {
+#pragma unroll 4
+        for (int k = part; k < n; k += S) {
+            const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(k, r) * DP + el);
+            const float h = wgt[r][k];
             o.x = fmaf(v.x, h, o.x), o.y = fmaf(v.y, h, o.y), o.z = fmaf(v.z, h, o.z), o.w = fmaf(v.w, h, o.w);
         }
     }
-    acc[grp][lane] = o;
-    __syncthreads();
-    if (grp != 0 || lane * 4 >= c.dim) return;
-    for (int i = 1; i < G; ++i) {
-        const float4 v = acc[i][lane];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    if (S > 1) {
+        acc[grp][t % L] = o;
+        __syncthreads();
+        if (part == 0)
+            for (int i = 1; i < S; ++i) {
+                const float4 v = acc[grp + i][t % L];
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            }
     }
-    const int i = g / a.group;
-    const float inv = i < seq_count(c, u.x) && s != 0.0f ? 1.0f / s : 0.0f;
-    uint2 two = make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
-    if (i >= seq_count(c, u.x)) two = make_uint2(0u, 0u);
-    *reinterpret_cast<uint2 *>(a.out + (((int64_t)u.x * c.n + i) * a.q_heads + hk * a.group + g % a.group) * c.dim + lane * 4) = two;
+    if (part != 0 || el >= c.dim || r >= rows) return;
+    const int g = row0 + r0 + r, i = ta_token(a, g);
+    const float f = inv[r];
+    uint2 two = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
+    if (f == -1.0f) two = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2 *>(a.out + (((int64_t)u.x * c.n + i) * a.q_heads + hk * a.group + (g - i * a.group)) * c.dim + el) = two;
 }
 
 // -------------------------------------------------------------------- host --
@@ -1037,17 +1137,18 @@ static cudaError_t ta_launch(const TaArgs &a, int ctas, cudaStream_t st)
     e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
     // the join may become resident early; it waits for the whole first kernel
+    constexpr int G = 1024 / DP, R = RT == 16 ? 1 : G;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int rows = a.c.n * a.group;
-    cfg.gridDim = dim3(ctas - 1, rows < RT ? rows : RT);
+    const int rows = a.c.n * a.group < RT ? a.c.n * a.group : RT;
+    cfg.gridDim = dim3(ctas - 1, (rows + R - 1) / R);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<DP, RT>, a);
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<DP, RT, R>, a);
 }
 
 wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *mask, float scale, const wl_cache &cache,
@@ -1067,6 +1168,18 @@ wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *
     a.group_inv = group > 1 ? (uint32_t)(((1ull << 32) + group - 1) / group) : 0u;
     a.scale = scale;
     a.c = cache_args(cache, seqs, di->status);
+    // Runs of positions that never cross a page: the largest power of two that
+    // divides the page size, 128 at most.  Under 8 rows a box would start
+    // inside an 8-row swizzle group, so such pages go by 16-byte copies.
+    const int64_t rowb = cache.dim * (cache.format == WL_CACHE_E4M3 ? 1 : 2), nrows = cache.pages * cache.kv_heads * cache.page_size;
+    a.box = (int)(cache.page_size & -cache.page_size);
+    if (a.box > kTaTile) a.box = kTaTile;
+    if (a.box < 8 || nrows > 0x7fffffff) a.box = 0;
+    if (a.box > 0) {
+        wl_status s = tmap_rows_u8(cache.k, rowb, nrows, a.box, &a.kmap);
+        if (s == WL_OK) s = tmap_rows_u8(cache.v, rowb, nrows, a.box, &a.vmap);
+        if (s != WL_OK) return s;
+    }
     // at most one CTA per tile that the table can hold
     const int64_t tiles = seqs.batch * cache.kv_heads * a.rtiles * ((seqs.max_pages * cache.page_size + seqs.n + kTaTile - 1) / kTaTile);
     int ctas = di->sm_count < kTaMaxCtas ? di->sm_count : kTaMaxCtas;
