@@ -362,6 +362,13 @@ __device__ __forceinline__ uint32_t ta_row(const CacheArgs &c, int page, int hk,
     return page < 0 || page >= c.npages ? ~0u : ((uint32_t)page * c.kv_heads + hk) * c.page_size + off;
 }
 
+// Place of K or V of a segment's tile r (of n) among its ring items, which go
+// K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1).
+__device__ __forceinline__ int ta_item(int r, int n, bool isv)
+{
+    return isv ? (r + 1 < n ? 2 * r + 2 : 2 * n - 1) : (r > 0 ? 2 * r - 1 : 0);
+}
+
 // ------------------------------------------------------------------ kernel --
 template <bool kE4M3, int DP, int RT>
 __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __grid_constant__ TaArgs a)
@@ -480,57 +487,56 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 copy(c.v, tab + ((t1 - 1) & 1) * 32);
                 ta_next(w, c, units);
             }
-        } else if (warp == 12) {
-            // Boxes: lane r looks up run r of a.box positions; one lane copies
-            // them all.  A run at the end brings what its page holds beyond;
-            // what no box brings stays as it was: scores there are masked,
-            // and the softmax warps zero those rows of V.
+        } else if (warp < 14) {
+            // Boxes: warp 12 brings K, warp 13 V.  Lane r looks up run r of
+            // a.box positions; one lane copies them all.  A run at the end
+            // brings what its page holds beyond; what no box brings stays as
+            // it was: scores there are masked, and the softmax warps zero
+            // those rows of V.
+            const bool isv = warp == 13;
+            const CUtensorMap *map = isv ? &a.vmap : &a.kmap;
             const int runs = kTaTile / a.box;
             const uint32_t bytes = (uint32_t)(a.box * Z::SLOTROW);
-            auto copy = [&](const CUtensorMap *map, const uint32_t *tb, uint32_t have) {
-#pragma unroll
-                for (int s = 0; s < Z::NS; ++s, ++item) {
-                    const int slot = item % SLOTS;
-                    ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
-                    if (elect_one()) {
-                        mbar_expect_tx(&full[slot], (uint32_t)__popc(have) * bytes);
-                        char *dst = ring + slot * Z::SLOT;
-#pragma unroll 1
-                        for (int k = 0; k < runs; ++k, dst += a.box * 128) {
-                            const uint32_t row = tb[k];
-                            if (row == ~0u) continue;
-#pragma unroll
-                            for (int h = 0; h < Z::SLOTROW / 128; ++h)
-                                tma_load_2d(dst + h * (kTaTile * 128), map, s * Z::SLOTROW + h * 128, (int)row, &full[slot]);
-                        }
-                    }
-                    __syncwarp();
-                }
-            };
+            uint32_t *tab = rowtab + isv * 64;
+            int items = 0;
             while (w.left > 0) {
-                const int t1 = ta_end(w), hk = w.u / a.rtiles;
+                const int t1 = ta_end(w), n = t1 - w.tile, hk = w.u / a.rtiles;
                 const int end = lane < runs ? min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile) : 0;
                 int j = w.tile * kTaTile + lane * a.box;
-                auto place = [&](int t, int pg, int j) -> uint32_t {
+                int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
+                for (int r = 0; r < n; ++r, j += kTaTile) {
                     const uint32_t row = ta_row(c, pg, hk, j);
                     if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
-                    rowtab[(t & 1) * 32 + lane] = row;
-                    __syncwarp();
-                    return __ballot_sync(0xffffffffu, row != ~0u);
-                };
-                int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
-                uint32_t have = place(w.tile, pg, j), before = 0;
-                for (int t = w.tile; t < t1; ++t, j += kTaTile) {
+                    tab[(r & 1) * 32 + lane] = row;  // the other half may still be read
                     pg = pg1;
                     pg1 = ta_page(c, w.b, j + 2 * kTaTile, end);
-                    copy(&a.kmap, rowtab + (t & 1) * 32, have);
-                    if (t > w.tile) copy(&a.vmap, rowtab + ((t - 1) & 1) * 32, before);
-                    before = have;
-                    have = place(t + 1, pg, j + kTaTile);
+                    const uint32_t have = __ballot_sync(0xffffffffu, row != ~0u);
+                    item = items + Z::NS * ta_item(r, n, isv);
+                    __syncwarp();
+#pragma unroll
+                    for (int s = 0; s < Z::NS; ++s, ++item) {
+                        const int slot = item % SLOTS;
+                        ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
+                        if (elect_one()) {
+                            mbar_expect_tx(&full[slot], (uint32_t)__popc(have) * bytes);
+                            char *dst = ring + slot * Z::SLOT;
+                            const uint32_t *tb = tab + (r & 1) * 32;
+#pragma unroll 1
+                            for (int k = 0; k < runs; ++k, dst += a.box * 128) {
+                                const uint32_t at = tb[k];
+                                if (at == ~0u) continue;
+#pragma unroll
+                                for (int h = 0; h < Z::SLOTROW / 128; ++h)
+                                    tma_load_2d(dst + h * (kTaTile * 128), map, s * Z::SLOTROW + h * 128, (int)at, &full[slot]);
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
-                copy(&a.vmap, rowtab + ((t1 - 1) & 1) * 32, before);
+                items += 2 * Z::NS * n;
                 ta_next(w, c, units);
             }
+            item = items;
             // Boxes still in flight (only after a wait gave up) land before the CTA's shared memory goes.
             const long long t0 = wait_clock();
             for (int i = max(0, item - SLOTS); i < item; ++i)
@@ -909,7 +915,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     }
                     if (__builtin_expect(a.box && !__all_sync(0xffffffffu, seen), 0)) {
                         // rows of V that are not there: weight 0 must meet a number
-                        const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * (r + 1 < n ? 2 * r + 2 : 2 * n - 1);
+                        const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * ta_item(r, n, true);
                         for (int s = 0; s < Z::NS; ++s) {
                             const int vs = (v0 + s) % SLOTS;
                             ta_wait(&full[vs], (unsigned)(((v0 + s) / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
