@@ -50,7 +50,7 @@ struct TaArgs {
     bf16 *out;
     float *part;   // [2 * ctas][RT][DP] partial sums
     float2 *ml;    // [2 * ctas][RT] reference and sum of each row
-    int4 *desc;    // [ctas] unit that CTA c begins and others finish: sequence, unit, last CTA (sequence -1: none)
+    int4 *desc;    // [ctas] unit that CTA c begins and others finish: sequence (-1: none), unit, place of its last tile, cost of all
     int q_heads, group, rtiles;
     uint32_t group_inv;  // ceil(2^32 / group), 0 for 1
     float scale;
@@ -278,9 +278,16 @@ __device__ __forceinline__ int ta_token(const TaArgs &a, int g) { return a.group
 
 // ------------------------------------------------------------------ range --
 // Walks a CTA's range of the tiles of all units, unit by unit.
+// A unit change costs a CTA about as much as kTaSwitch tiles (its pipeline
+// drains, the sums leave, queries are set up), so a unit counts that many more
+// when the ranges are cut: without it the CTAs with more units finish last
+// (SM cycles of 16 trees over 4096 positions: 115 to 151 thousand).  With
+// fewer than that many tiles a CTA the ranges are cut by tiles alone.
+constexpr int kTaSwitch = 4;
+
 struct TaWalk {
-    int64_t total, start, left;  // all tiles; first tile of the next segment; tiles left
-    int b, u, tile, ntiles, len, cnt, ctas;  // ctas: CTAs with work (no more than tiles)
+    int total, start, left;  // cost of all units; place of the next segment in it; cost left
+    int b, u, tile, ntiles, len, cnt, change;  // change: cost of a unit beside its tiles
 };
 
 __device__ __forceinline__ int ta_tiles(const CacheArgs &c, int b, int &len, int &cnt)
@@ -290,37 +297,51 @@ __device__ __forceinline__ int ta_tiles(const CacheArgs &c, int b, int &len, int
     return cnt > 0 ? (len + cnt + kTaTile - 1) / kTaTile : 1;
 }
 
-// Called by whole warps.
+// Settles on a segment: a range that ends within a unit's change has none of
+// its tiles.
+__device__ __forceinline__ void ta_settle(TaWalk &w, int skip)
+{
+    // skip: how much of the change lies before the range
+    const int pay = w.change - skip;
+    if (pay > 0) {
+        w.start += pay;
+        w.left = max(w.left - pay, 0);
+    }
+}
+
+// Called by whole warps.  The first total % ctas ranges are one longer.
 __device__ __forceinline__ TaWalk ta_walk(const CacheArgs &c, int units)
 {
     const int lane = threadIdx.x & 31;
     TaWalk w;
     int len, cnt;
-    int64_t sum = 0;
-    for (int b = lane; b < c.batch; b += 32) sum += ta_tiles(c, b, len, cnt);
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    w.total = sum * units;
-    w.ctas = (int)min((int64_t)gridDim.x, w.total);
-    w.start = (int64_t)blockIdx.x * w.total / w.ctas;
-    w.left = (int)blockIdx.x < w.ctas ? ((int64_t)blockIdx.x + 1) * w.total / w.ctas - w.start : 0;
+    unsigned sum = 0;
+    for (int b = lane; b < c.batch; b += 32) sum += (unsigned)ta_tiles(c, b, len, cnt);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    w.change = sum * units >= kTaSwitch * gridDim.x ? kTaSwitch : 0;
+    w.total = ((int)sum + c.batch * w.change) * units;
+    const int ctas = min((int)gridDim.x, w.total), each = w.total / ctas, more = w.total - each * ctas, id = blockIdx.x;
+    w.start = id * each + min(id, more);
+    w.left = id < ctas ? each + (id < more) : 0;
     w.b = w.u = w.tile = w.ntiles = w.len = w.cnt = 0;
     if (w.left == 0) return w;
-    int64_t base = 0;
+    int base = 0;
     for (int b0 = 0; b0 < c.batch; b0 += 32) {
-        int64_t mine = b0 + lane < c.batch ? (int64_t)ta_tiles(c, b0 + lane, len, cnt) * units : 0;
-        int64_t incl = mine;
+        const int mine = b0 + lane < c.batch ? (ta_tiles(c, b0 + lane, len, cnt) + w.change) * units : 0;
+        int incl = mine;
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
         }
         const unsigned past = __ballot_sync(0xffffffffu, base + incl > w.start);
         if (past) {
-            const int l = __ffs(past) - 1;
-            const int64_t off = w.start - (base + __shfl_sync(0xffffffffu, incl - mine, l));
+            const int l = __ffs(past) - 1, off = w.start - (base + __shfl_sync(0xffffffffu, incl - mine, l));
             w.b = b0 + l;
             w.ntiles = ta_tiles(c, w.b, w.len, w.cnt);
-            w.u = (int)(off / w.ntiles);
-            w.tile = (int)(off - (int64_t)w.u * w.ntiles);
+            const int cost = w.ntiles + w.change, in = off % cost;
+            w.u = off / cost;
+            w.tile = max(in - w.change, 0);
+            ta_settle(w, in);
             return w;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -330,20 +351,23 @@ __device__ __forceinline__ TaWalk ta_walk(const CacheArgs &c, int units)
 }
 
 // The segment's end tile; then on to the next unit.
-__device__ __forceinline__ int ta_end(const TaWalk &w) { return (int)min((int64_t)w.ntiles, w.tile + w.left); }
+__device__ __forceinline__ int ta_end(const TaWalk &w) { return min(w.ntiles, w.tile + w.left); }
 __device__ __forceinline__ void ta_next(TaWalk &w, const CacheArgs &c, int units)
 {
     const int t1 = ta_end(w);
     w.left -= t1 - w.tile;
     w.start += t1 - w.tile;
     w.tile = t1;
-    if (t1 == w.ntiles && w.left > 0) {
+    if (t1 == w.ntiles && w.left > w.change) {
         w.tile = 0;
         if (++w.u == units) {
             w.u = 0;
             ++w.b;
             w.ntiles = ta_tiles(c, w.b, w.len, w.cnt);
         }
+        ta_settle(w, 0);
+    } else if (t1 == w.ntiles) {
+        w.left = 0;
     }
 }
 
@@ -1042,9 +1066,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 }
             }
             if (threadIdx.x == 0 && t0 == 0 && !whole) {
-                // unit ends at tile index e of all: CTA ceil(e * ctas / total) - 1 has its last tile
-                const int64_t e = w.start + w.ntiles;
-                a.desc[blockIdx.x] = make_int4(w.b, w.u, (int)((e * w.ctas + w.total - 1) / w.total) - 1, 0);
+                // (the place of the unit's last tile, and the cost of all)
+                a.desc[blockIdx.x] = make_int4(w.b, w.u, w.start + w.ntiles - 1, w.total);
             }
             items += 2 * Z::NS * (t1 - t0);
             ta_next(w, c, units);
@@ -1073,7 +1096,9 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int hk = u.y / a.rtiles, row0 = (u.y - hk * a.rtiles) * RT, r0 = blockIdx.y * R, t = threadIdx.x, lane = t & 31;
     const int rows = min(RT, c.n * a.group - row0) - r0;  // from r0 on
     if (rows <= 0) return;
-    const int n = u.z - (int)blockIdx.x + 1;  // contributors
+    // the CTA whose range has the unit's last tile (ranges as in ta_walk); contributors
+    const int ctas = min((int)gridDim.x + 1, u.w), each = u.w / ctas, more = u.w - each * ctas, cut = more * (each + 1);
+    const int n = (u.z < cut ? u.z / (each + 1) : more + (u.z - cut) / each) - (int)blockIdx.x + 1;
     auto slot = [&](int k, int r) -> int64_t { return (int64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * RT + r0 + r; };
     // a warp per row: the weights of its contributors
     for (int r = t / 32; r < R && r < rows; r += 8) {
@@ -1189,6 +1214,8 @@ wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *
     // at most one CTA per tile that the table can hold
     const int64_t tiles = seqs.batch * cache.kv_heads * a.rtiles * ((seqs.max_pages * cache.page_size + seqs.n + kTaTile - 1) / kTaTile);
     int ctas = di->sm_count < kTaMaxCtas ? di->sm_count : kTaMaxCtas;
+    if (tiles + seqs.batch * cache.kv_heads * a.rtiles * kTaSwitch > 0x7fffffff)
+        return fail(WL_ERR_UNSUPPORTED, "wl_tree_attention: batch * kv_heads * positions of the page table / 128 must be below 2^31");
     if (tiles < ctas) ctas = (int)tiles;
     cudaError_t e;
     if (cache.format == WL_CACHE_E4M3) {
