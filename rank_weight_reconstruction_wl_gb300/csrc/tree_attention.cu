@@ -206,6 +206,12 @@ __device__ __forceinline__ uint32_t half2_e4m3(__half2 h)
     return v;
 }
 
+__device__ __forceinline__ __half2 e4m3x2_half2(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return *reinterpret_cast<const __half2 *>(&h);
+}
+
 // Barrier `id` of `n` threads that also tells whether any of them brought true.
 template <int n>
 __device__ __forceinline__ bool bar_or(int id, bool in)
@@ -662,8 +668,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         const int wg = warp >> 2, tk = threadIdx.x & 127, col0 = Z::PP ? 0 : wg * CW;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         float *wred = red + wg * 128;
-        float *mine = reinterpret_cast<float *>(sp + wg * Z::PB);  // [4][CW] sums, [CW] references, when the buffer is idle
-        float *fac = reinterpret_cast<float *>(sp + 1024);         // [3][64] factors of both streams and of flushed sums
+        float *fac = reinterpret_cast<float *>(sp);  // [3][64] factors of both streams and of flushed sums, when the buffers are idle
         int it = 0, items = 0;  // tiles and ring items of earlier segments
         if (threadIdx.x == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
         while (w.left > 0) {
@@ -701,20 +706,28 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             // ---- the segment's queries: rows of the B operand
             float qscale = a.scale * kLog2e;
             {
-                constexpr int CH = DP / 8, PER = RT * CH / 256;  // 8-element chunks of a row, per thread
-                // all of a thread's chunks are in flight at once; they wait in the idle weight buffers
-                uint4 *raw = reinterpret_cast<uint4 *>(sp) + threadIdx.x;
-                uint4 v[PER];
+                // A lane has 8 elements of a row, a warp RPW rows at a time.
+                constexpr int CH = DP / 8, RPW = 32 / CH, PER = RT / (8 * RPW);
+                const int ck = lane % CH, d = ck * 8;
+                const bf16 *base = a.q + ((int64_t)w.b * c.n * a.q_heads + hk * a.group) * c.dim + d;
+                // where row `lane` (of 32, and of the next 32) lies; -1: zeros
+                auto where = [&](int r) -> int {
+                    const int tok = ta_token(a, row0 + r);
+                    return r < rows && tok < w.cnt ? (tok * a.q_heads + row0 + r - tok * a.group) * c.dim : -1;
+                };
+                const int off0 = where(lane), off1 = RT > 32 ? where(lane + 32) : -1;
+                uint4 raw[PER];  // all rows of a lane are in flight at once
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int e = threadIdx.x + i * 256, r = e / CH, d = (e % CH) * 8, g = row0 + r, tok = ta_token(a, g);
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows && d < c.dim && tok < w.cnt)
-                        v[i] = *reinterpret_cast<const uint4 *>(
-                            a.q + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + (g - tok * a.group)) * c.dim + d);
+                    const int r = (i * 8 + warp) * RPW + lane / CH;
+                    int off = __shfl_sync(0xffffffffu, off0, r & 31);
+                    if (RT > 32) {
+                        const int up = __shfl_sync(0xffffffffu, off1, r & 31);
+                        off = r < 32 ? off : up;
+                    }
+                    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (off >= 0 && d < c.dim) raw[i] = *reinterpret_cast<const uint4 *>(base + off);
                 }
-#pragma unroll
-                for (int i = 0; i < PER; ++i) raw[i * 256] = v[i];
                 if (threadIdx.x < RT) {
                     const int g = row0 + threadIdx.x, i = ta_token(a, g);
                     uint64_t m = 0;
@@ -725,21 +738,26 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     smask[threadIdx.x] = m;
                 }
                 float up = 1.0f;
+                bool odd = false;  // a NaN or an infinity among this lane's
                 if (kE4M3) {
                     // one power of two brings the largest |q| of the tile into [128, 256)
                     uint32_t two = 0;
 #pragma unroll
                     for (int i = 0; i < PER; ++i)
-                        two = __vmaxu2(__vmaxu2(two, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu)),
-                                       __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+                        two = __vmaxu2(two, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                                     __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
                     uint32_t amax = max(two & 0xffffu, two >> 16);
-                    if (__builtin_expect(amax >= 0x7f80u, 0)) {  // NaN or infinity: the largest of the others
+                    odd = amax >= 0x7f80u;
+                    if (__builtin_expect(odd, 0)) {  // the largest of the others
                         amax = 0;
-                        const uint16_t *e = reinterpret_cast<const uint16_t *>(raw);
-#pragma unroll 1
-                        for (int i = 0; i < PER * 8; ++i) {
-                            const uint32_t u = e[(i / 8) * 2048 + i % 8] & 0x7fffu;
-                            amax = max(amax, u < 0x7f80u ? u : 0u);
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t h = (u[k / 2] >> (16 * (k & 1))) & 0x7fffu;
+                                amax = max(amax, h < 0x7f80u ? h : 0u);
+                            }
                         }
                     }
                     amax = __reduce_max_sync(0xffffffffu, amax);
@@ -752,30 +770,34 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     up = __uint_as_float((uint32_t)(261 - be) << 23);  // 2^(134 - be)
                     qscale *= __uint_as_float((uint32_t)(be - 7) << 23);
                 }
-#pragma unroll 2
+                // K-major rows of 128-byte chunks, 16-byte units swizzled by the row
+                char *o0 = sq + (kE4M3 ? (ck / 16) * (N * 128) + (ck & 1) * 8 : (ck / 8) * (N * 128));
+                const int c16 = kE4M3 ? (ck / 2) & 7 : ck & 7;
+#pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int e = threadIdx.x + i * 256, r = e / CH, ck = e % CH;
-                    const uint4 v = raw[i * 256];
+                    const int r = (i * 8 + warp) * RPW + lane / CH;
+                    const uint4 v = raw[i];
+                    char *o = o0 + r * 128 + ((c16 ^ (r & 7)) << 4);
                     if (kE4M3) {
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t hi[2] = {}, lo[2] = {};
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = bf_lo(u[j]) * up, y = bf_hi(u[j]) * up;
-                            uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-                            const float2 b = e4m3x2_f32(h);
-                            const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2((x - b.x) * 32.0f, (y - b.y) * 32.0f), __NV_SATFINITE, __NV_E4M3);
-                            if ((u[j] & 0x7fffu) >= 0x7f80u) h |= 0x7fu;  // NaN, infinity: a NaN code
-                            if ((u[j] >> 16 & 0x7fffu) >= 0x7f80u) h |= 0x7f00u;
-                            hi[j / 2] |= h << (16 * (j & 1));
-                            lo[j / 2] |= l << (16 * (j & 1));
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 x = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);  // exact: 8 bits, below 256
+                            hi[k] = half2_e4m3(x);
+                            lo[k] = half2_e4m3(__hmul2(__hsub2(x, e4m3x2_half2(hi[k])), __float2half2_rn(32.0f)));
                         }
-                        const int cc = ck / 16, c16 = (ck / 2) & 7, half = (ck & 1) * 8;
-                        char *o = sq + cc * (N * 128) + half;
-                        *reinterpret_cast<uint2 *>(o + r * 128 + ((c16 ^ (r & 7)) << 4)) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2 *>(o + (RT + r) * 128 + ((c16 ^ (r & 7)) << 4)) = make_uint2(lo[0], lo[1]);
+                        if (__builtin_expect(odd, 0)) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((u[k] & 0x7fffu) >= 0x7f80u) hi[k] |= 0x7fu;  // NaN, infinity: a NaN code
+                                if ((u[k] >> 16 & 0x7fffu) >= 0x7f80u) hi[k] |= 0x7f00u;
+                            }
+                        }
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                        *reinterpret_cast<uint2 *>(o + RT * 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
                     } else {
-                        *reinterpret_cast<uint4 *>(sq + (ck / 8) * (N * 128) + r * 128 + (((ck & 7) ^ (r & 7)) << 4)) = v;
+                        *reinterpret_cast<uint4 *>(o) = v;
                     }
                 }
                 fence_async_smem();
@@ -915,8 +937,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                                 // 11 bits of the weight, cut into 4 + 4
                                 const __half2 h = __floats2half2_rn(p, q);
                                 const uint32_t c8 = half2_e4m3(h);
-                                const __half2_raw br = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c8, __NV_E4M3);
-                                const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2 *>(&br)), __float2half2_rn(32.0f));
+                                const __half2 rest = __hmul2(__hsub2(h, e4m3x2_half2(c8)), __float2half2_rn(32.0f));
                                 const uint32_t l8 = half2_e4m3(rest);
                                 if (k & 1) {
                                     hi[k / 2] |= c8 << 16;
@@ -958,23 +979,23 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 if (!last && (t + 1 - t0) % kTaFlush != 0) continue;
                 // ---- the sums leave tensor memory
                 {
-                    const int own = it - (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's last tile, if it had one
-                    if (some) ta_wait(&pv_done[own & 1], (unsigned)((own >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                    tc_fence_after();
                     float v[CW];
 #pragma unroll
                     for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(l[i]), v[2 * i + 1] = f2_hi(l[i]);
                     const float ls = warp_columns<CW>(v, [](float p, float q) { return p + q; });
-                    if (lane < CW) mine[(warp & 3) * CW + lane] = ls;
-                    if (tk < CW) mine[4 * CW + tk] = (unset >> tk) & 1 ? kTaNone : -nm[tk];
+                    if (lane < CW) wred[(warp & 3) * CW + lane] = ls;
+                    if (tk < CW && (unset >> tk) & 1) nm[tk] = -kTaNone;
+                    const int own = it - (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's last tile, if it had one
+                    if (some) ta_wait(&pv_done[own & 1], (unsigned)((own >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                    tc_fence_after();
                     bar_n<256>(3);
                     float top_r = kTaNone, sum = 0.0f;
                     if ((int)threadIdx.x < rows) {
                         const int r = threadIdx.x;
                         float f[3] = {1.0f, 0.0f, 0.0f};
                         auto side = [&](int g, int col, float &mr, float &sr) {
-                            const float *o = reinterpret_cast<const float *>(sp + g * Z::PB);
-                            mr = o[4 * CW + col];
+                            const float *o = red + g * 128;
+                            mr = -nms[g * 32 + col];
                             sr = (o[col] + o[CW + col]) + (o[2 * CW + col] + o[3 * CW + col]);
                         };
                         if (Z::PP) {
@@ -1081,12 +1102,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 
 // Joins the partial sums of the unit that CTA blockIdx.x began and others
 // finished, contributors in CTA order.  A block has G groups of lanes that
-// each cover a row: R rows of the unit, G / R groups sharing a row's
-// contributors (few rows come with many contributors and the other way round).
+// each cover a row.  R < G rows: G / R groups share a row's contributors (few
+// rows come with many contributors); R >= G: a group has R / G rows.
 template <int DP, int RT, int R>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TaArgs a)
 {
-    constexpr int L = DP / 4, G = 256 / L, S = G / R;  // 16-byte lanes of a row
+    constexpr int L = DP / 4, G = 256 / L, S = R < G ? G / R : 1, Q = R < G ? 1 : R / G;  // 16-byte lanes of a row
     __shared__ float wgt[R][kTaMaxCtas], inv[R];
     __shared__ float4 acc[G][L];
     pdl_wait();
@@ -1099,48 +1120,67 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     // the CTA whose range has the unit's last tile (ranges as in ta_walk); contributors
     const int ctas = min((int)gridDim.x + 1, u.w), each = u.w / ctas, more = u.w - each * ctas, cut = more * (each + 1);
     const int n = (u.z < cut ? u.z / (each + 1) : more + (u.z - cut) / each) - (int)blockIdx.x + 1;
+    const int cnt = seq_count(c, u.x);
     auto slot = [&](int k, int r) -> int64_t { return (int64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * RT + r0 + r; };
     // a warp per row: the weights of its contributors
+#pragma unroll 1
     for (int r = t / 32; r < R && r < rows; r += 8) {
+        float2 ml[(kTaMaxCtas + 31) / 32];
         float m = kTaNone, s = 0.0f;
-        for (int k = lane; k < n; k += 32) m = fmaxf(m, a.ml[slot(k, r)].x);
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int k = lane; k < n; k += 32) {
-            const float2 ml = a.ml[slot(k, r)];
-            const float f = ex2(ml.x - m);
-            wgt[r][k] = f;
-            s = fmaf(ml.y, f, s);
+#pragma unroll
+        for (int q = 0; q < (kTaMaxCtas + 31) / 32; ++q) {
+            ml[q] = q * 32 + lane < n ? a.ml[slot(q * 32 + lane, r)] : make_float2(kTaNone, 0.0f);
+            m = fmaxf(m, ml[q].x);
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+        for (int q = 0; q < (kTaMaxCtas + 31) / 32; ++q) {
+            const float f = ex2(ml[q].x - m);
+            if (q * 32 + lane < n) wgt[r][q * 32 + lane] = f;
+            s = fmaf(ml[q].y, f, s);
         }
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const bool on = ta_token(a, row0 + r0 + r) < seq_count(c, u.x);
-        if (lane == 0) inv[r] = on ? (s == 0.0f ? 0.0f : 1.0f / s) : -1.0f;  // -1: a row past the count
+        if (lane == 0) inv[r] = ta_token(a, row0 + r0 + r) < cnt ? (s == 0.0f ? 0.0f : 1.0f / s) : -1.0f;  // -1: a row past the count
     }
     __syncthreads();
-    const int el = (t % L) * 4, grp = t / L, r = grp / S, part = grp % S;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (el < c.dim && r < rows) {
+    const int el = (t % L) * 4, grp = t / L, part = grp % S;
+    float4 o[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (el < c.dim) {
 #pragma unroll 4
         for (int k = part; k < n; k += S) {
-            const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(k, r) * DP + el);
-            const float h = wgt[r][k];
-            o.x = fmaf(v.x, h, o.x), o.y = fmaf(v.y, h, o.y), o.z = fmaf(v.z, h, o.z), o.w = fmaf(v.w, h, o.w);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int r = R < G ? grp / S : q * G + grp;
+                if (r >= rows) continue;
+                const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(k, r) * DP + el);
+                const float h = wgt[r][k];
+                o[q].x = fmaf(v.x, h, o[q].x), o[q].y = fmaf(v.y, h, o[q].y), o[q].z = fmaf(v.z, h, o[q].z), o[q].w = fmaf(v.w, h, o[q].w);
+            }
         }
     }
     if (S > 1) {
-        acc[grp][t % L] = o;
+        acc[grp][t % L] = o[0];
         __syncthreads();
         if (part == 0)
             for (int i = 1; i < S; ++i) {
                 const float4 v = acc[grp + i][t % L];
-                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+                o[0].x += v.x, o[0].y += v.y, o[0].z += v.z, o[0].w += v.w;
             }
     }
-    if (part != 0 || el >= c.dim || r >= rows) return;
-    const int g = row0 + r0 + r, i = ta_token(a, g);
-    const float f = inv[r];
-    uint2 two = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
-    if (f == -1.0f) two = make_uint2(0u, 0u);
-    *reinterpret_cast<uint2 *>(a.out + (((int64_t)u.x * c.n + i) * a.q_heads + hk * a.group + (g - i * a.group)) * c.dim + el) = two;
+    if (part != 0 || el >= c.dim) return;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int r = R < G ? grp / S : q * G + grp;
+        if (r >= rows) continue;
+        const int g = row0 + r0 + r, i = ta_token(a, g);
+        const float f = inv[r];
+        uint2 two = make_uint2(bf16x2_bits(o[q].x * f, o[q].y * f), bf16x2_bits(o[q].z * f, o[q].w * f));
+        if (f == -1.0f) two = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2 *>(a.out + (((int64_t)u.x * c.n + i) * a.q_heads + hk * a.group + (g - i * a.group)) * c.dim + el) = two;
+    }
 }
 
 // -------------------------------------------------------------------- host --
@@ -1168,7 +1208,7 @@ static cudaError_t ta_launch(const TaArgs &a, int ctas, cudaStream_t st)
     e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
     // the join may become resident early; it waits for the whole first kernel
-    constexpr int G = 1024 / DP, R = RT == 16 ? 1 : G;
+    constexpr int R = RT == 16 ? 1 : 8;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
