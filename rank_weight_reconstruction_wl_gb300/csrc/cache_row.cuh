@@ -8,6 +8,24 @@
 
 namespace wl {
 
+// x / d for 0 <= x < 2^31 by a multiplication: with 2^L >= d the smallest,
+// umulhi(2 x, floor(2^(31 + L) / d) + 1) >> L is exact (Granlund and
+// Montgomery 1994).
+struct FastDiv {
+    uint32_t d, mul, shr;
+    __device__ __forceinline__ int div(int x) const { return (int)(__umulhi((uint32_t)x << 1, mul) >> shr); }
+};
+
+inline FastDiv fast_div(int64_t d)
+{
+    FastDiv f;
+    f.d = (uint32_t)d;
+    f.shr = 0;
+    while (((int64_t)1 << f.shr) < d) ++f.shr;
+    f.mul = (uint32_t)(((uint64_t)1 << (31 + f.shr)) / (uint64_t)d + 1);
+    return f;
+}
+
 // wl_cache and wl_seqs as the kernels take them.
 struct CacheArgs {
     char *k, *v;

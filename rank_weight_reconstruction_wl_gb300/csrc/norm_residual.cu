@@ -31,70 +31,87 @@ __device__ __forceinline__ float block_sum(float v, float *red)
     return s;
 }
 
-// V: chunks of 8 elements per thread.
+// 8 elements as loaded.
+template <typename T>
+struct Chunk8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);  // coherent: x_out may be x
+    }
+    __device__ __forceinline__ float operator[](int j) const
+    {
+        const uint4 &q = w[sizeof(T) == 4 ? j / 4 : 0];
+        const int k = sizeof(T) == 4 ? j % 4 : j / 2;
+        const uint32_t u = k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w;
+        return sizeof(T) == 4 ? __uint_as_float(u) : (j & 1) ? bf_hi(u) : bf_lo(u);
+    }
+};
+
+// V: chunks of 8 elements per thread, kept as loaded until they are used, so
+// that several rows fit an SM's registers and their loads overlap.
 template <typename Y, typename X, typename O, int V>
-__global__ void norm_residual_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(V == 1 ? 256 : V == 2 ? 384 : 256) norm_residual_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ float red[2][32];
     const int nchunk = a.H / 8;
     const int64_t row = (int64_t)blockIdx.x * a.H;
-    float u[V][8], x[V][8];
+    Chunk8<Y> y[V];
+    Chunk8<X> xr[V];
+    float x[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < nchunk) {
+            if (a.y) y[i].load(static_cast<const Y *>(a.y) + row + c * 8);
+            xr[i].load(static_cast<const X *>(a.x) + row + c * 8);
+        }
+    }
+    float f = a.beta;
+    if (a.y && a.w_post) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (threadIdx.x + i * blockDim.x < nchunk)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+        f *= rsqrtf(block_sum(ss, red[0]) / (float)a.H + a.eps);
+    }
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c < nchunk) {
-            load8(static_cast<const X *>(a.x) + row + c * 8, x[i]);
-            if (a.y) load8(static_cast<const Y *>(a.y) + row + c * 8, u[i]);
-        }
-    }
-    if (a.y) {
-        float f = a.beta;
-        if (a.w_post) {
+            if (a.y) {
+                float m[8];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (threadIdx.x + i * blockDim.x < nchunk)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ss += u[i][j] * u[i][j];
-            f *= rsqrtf(block_sum(ss, red[0]) / (float)a.H + a.eps);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c < nchunk) {
-                float w[8], g[8];
+                for (int j = 0; j < 8; ++j) m[j] = f * y[i][j];
                 if (a.w_post) {
+                    float w[8];
                     load8(a.w_post + c * 8, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) u[i][j] *= a.w_offset + w[j];
+                    for (int j = 0; j < 8; ++j) m[j] *= a.w_offset + w[j];
                 }
                 if (a.gate) {
+                    float g[8];
                     load8(static_cast<const Y *>(a.gate) + blockIdx.x * a.gate_stride + c * 8, g);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) u[i][j] *= g[j];
+                    for (int j = 0; j < 8; ++j) m[j] *= g[j];
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = a.alpha * x[i][j] + f * u[i][j];
+                for (int j = 0; j < 8; ++j) x[i][j] = fmaf(a.alpha, xr[i][j], m[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[i][j] = a.alpha * xr[i][j];
             }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] *= a.alpha;
-    }
-    ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c < nchunk) {
             if (a.x_out) store8(static_cast<X *>(a.x_out) + row + c * 8, x[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss += x[i][j] * x[i][j];
+            for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
         }
     }
     if (!a.h) return;
-    const float f = rsqrtf(block_sum(ss, red[1]) / (float)a.H + a.eps);
+    f = rsqrtf(block_sum(ss, red[1]) / (float)a.H + a.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
@@ -112,7 +129,7 @@ template <typename Y, typename X, typename O>
 static void norm_launch(const NormArgs &a, int64_t T, cudaStream_t st)
 {
     const int nchunk = a.H / 8;
-    const int V = nchunk <= 256 ? 1 : nchunk <= 512 ? 2 : nchunk <= 1024 ? 4 : 8;
+    const int V = nchunk <= 256 ? 1 : nchunk <= 768 ? 2 : nchunk <= 1024 ? 4 : 8;
     const int threads = ((nchunk + V - 1) / V + 31) / 32 * 32;
     const unsigned grid = (unsigned)T;
     switch (V) {

@@ -5,6 +5,7 @@
 namespace wl {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 4;  // rows of a lane group in flight
 
 struct RopeArgs {
     const void *q, *k, *v;
@@ -17,105 +18,177 @@ struct RopeArgs {
     CacheArgs c;
 };
 
+// 8 elements as they are loaded: 16 bytes of bf16 or 32 of fp32.
+template <typename X>
+struct Raw8 {
+    uint4 w[sizeof(X) / 2];
+    __device__ __forceinline__ void load(const X *p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ Raw8 from(int lane, int width) const
+    {
+        Raw8 o;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i)
+            o.w[i] = make_uint4(__shfl_sync(0xffffffffu, w[i].x, lane, width), __shfl_sync(0xffffffffu, w[i].y, lane, width),
+                                __shfl_sync(0xffffffffu, w[i].z, lane, width), __shfl_sync(0xffffffffu, w[i].w, lane, width));
+        return o;
+    }
+    __device__ __forceinline__ void values(float v[8]) const
+    {
+        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[sizeof(X) / 2 - 1].x, w[sizeof(X) / 2 - 1].y, w[sizeof(X) / 2 - 1].z, w[sizeof(X) / 2 - 1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = sizeof(X) == 4 ? __uint_as_float(u[j]) : (j & 1) ? bf_hi(u[j / 2]) : bf_lo(u[j / 2]);
+    }
+};
+
 // One CTA per token.  `width` lanes share a row (one head of q, k or v), 8
-// elements each.
+// elements each; a lane group has kRopeRows rows in flight.
 //   angle = frac(position * phase / 2^64) turns, from the wrapped 64-bit
 //   product, so no position loses accuracy in a range reduction;
 //   (a, b) -> A (a cos - b sin, a sin + b cos);
 //   k, v: e = row exponent of max|x|, code = e4m3(x 2^-e), scale = 2^e.
-template <typename X, bool kE4M3>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a)
+// All heads of the token share its angles (formed once, while the rows load)
+// and its place in the cache.  kHalves: pairs (i, i + rot/2) whose partners
+// are whole 8-element chunks away, so that they come by shuffle; otherwise
+// pairs are neighbours (interleaved, within the lane) or the row is staged in
+// shared memory.  Bound by DRAM bytes: a row is read once and written once.
+template <typename X, bool kE4M3, bool kHalves>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_append_kernel(const __grid_constant__ RopeArgs a)
 {
     __shared__ float2 trig[128];
-    __shared__ float row_buf[kRopeThreads * 8];
+    __shared__ float row_buf[kHalves ? 1 : kRopeThreads * 8];
     const CacheArgs &c = a.c;
     const int tok = blockIdx.x, b = tok / c.n, i = tok - b * c.n;
+    const int w = a.width, g = threadIdx.x / w, ngroups = kRopeThreads / w, sub = threadIdx.x % w;
+    const int e0 = sub * 8, half = a.rot / 2;
+    const bool mine = e0 < c.dim;
+    const int rows = a.q_heads + 2 * c.kv_heads, first_v = a.q_heads + c.kv_heads;
+    Raw8<X> raw[kRopeRows];
+    const X *qp = static_cast<const X *>(a.q) + tok * a.q_stride + e0;
+    const X *kp = static_cast<const X *>(a.k) + tok * a.k_stride - (int64_t)a.q_heads * c.dim + e0;
+    const X *vp = static_cast<const X *>(a.v) + tok * a.v_stride - (int64_t)first_v * c.dim + e0;
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int p = 0; p < kRopeRows; ++p) {
+            const int r = r0 + p * ngroups + g;
+            raw[p].zero();
+            if (r < rows && mine) raw[p].load((r < a.q_heads ? qp : r < first_v ? kp : vp) + r * c.dim);
+        }
+    };
+    load(0);
     const int len = seq_len(c, b);
     const bool live = i < seq_count(c, b);
-    if (live && threadIdx.x < a.rot / 2) {
+    const int64_t at0 = live ? cache_row(c, b, 0, len + i) : -1;  // row of head 0; head h is h * page_size on
+    if (live && threadIdx.x < half) {
         const int pos = a.positions ? a.positions[tok] : len + i;
         const uint64_t turn = (uint64_t)(int64_t)pos * a.phase[threadIdx.x];
         float s, co;
         sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &co);  // 2^-31: half turns
         trig[threadIdx.x] = make_float2(co * a.amplitude, s * a.amplitude);
     }
+    if (live && at0 < 0 && threadIdx.x == 0) atomicOr(c.status, kStatusPage);
     __syncthreads();
-    const int w = a.width, g = threadIdx.x / w, ngroups = kRopeThreads / w;
-    const int e0 = (threadIdx.x % w) * 8, half = a.rot / 2;
-    const bool mine = e0 < c.dim;
-    float *buf = row_buf + g * w * 8;
-    const int rows = a.q_heads + 2 * c.kv_heads;
-    for (int r0 = 0; r0 < rows; r0 += ngroups) {
-        const int r = r0 + g;
-        const bool isq = r < a.q_heads, isv = r >= a.q_heads + c.kv_heads, on = r < rows && mine;
-        const int h = isq ? r : (r - a.q_heads) % c.kv_heads;
-        float v[8] = {};
-        if (on && live) {
-            const X *src = isq ? static_cast<const X *>(a.q) + tok * a.q_stride
-                               : isv ? static_cast<const X *>(a.v) + tok * a.v_stride : static_cast<const X *>(a.k) + tok * a.k_stride;
-            load8(src + (int64_t)h * c.dim + e0, v);
-        }
-        if (on) store8(buf + e0, v);
-        __syncwarp();
-        if (on && live && !isv) {
+    float *buf = row_buf + (kHalves ? 0 : g * w * 8);
+    const bool upper = e0 >= half, turns = live && e0 < a.rot;
+    const int partner = !turns ? sub : upper ? sub - half / 8 : sub + half / 8;
+    float2 t[8];  // this lane's angles; the sine's sign is that of its side of the pair
+    if (kHalves) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = e0 + j;
-                if (e < a.rot) {
-                    const int pair = a.interleaved ? e >> 1 : (e < half ? e : e - half);
-                    const bool second = a.interleaved ? (e & 1) : e >= half;
-                    const int other = a.interleaved ? e ^ 1 : (second ? e - half : e + half);
-                    const float2 t = trig[pair];
-                    v[j] = second ? buf[other] * t.y + v[j] * t.x : v[j] * t.x - buf[other] * t.y;
+        for (int j = 0; j < 8; ++j) {
+            t[j] = turns ? trig[(upper ? e0 - half : e0) + j] : make_float2(0.0f, 0.0f);
+            if (!upper) t[j].y = -t[j].y;
+        }
+    }
+    const int last = (threadIdx.x | 31) / w;  // the warp's last lane group
+    bf16 *qo = a.q_out + (int64_t)tok * a.q_heads * c.dim + e0;
+    for (int r0 = 0; r0 < rows; r0 += kRopeRows * ngroups) {
+        if (r0 > 0) load(r0);
+#pragma unroll
+        for (int p = 0; p < kRopeRows; ++p) {
+            if (r0 + p * ngroups >= rows) break;  // (the same for all)
+            const int r = r0 + p * ngroups + g;
+            const bool isv = r >= first_v, on = r < rows && mine;
+            float v[8];
+            raw[p].values(v);
+            if (kHalves) {
+                float o[8];
+                raw[p].from(partner, w).values(o);
+                if (!isv && turns) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = fmaf(o[j], t[j].y, v[j] * t[j].x);
+                }
+            } else {
+                if (on) store8(buf + e0, v);
+                __syncwarp();
+                if (on && live && !isv) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = e0 + j;
+                        if (e < a.rot) {
+                            const int pair = a.interleaved ? e >> 1 : (e < half ? e : e - half);
+                            const bool second = a.interleaved ? (e & 1) : e >= half;
+                            const int other = a.interleaved ? e ^ 1 : (second ? e - half : e + half);
+                            const float2 t = trig[pair];
+                            v[j] = second ? buf[other] * t.y + v[j] * t.x : v[j] * t.x - buf[other] * t.y;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (r0 + p * ngroups + last >= a.q_heads) {  // some row of the warp goes to the cache
+                uint32_t amax = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+                for (int d = w / 2; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                if (on && r >= a.q_heads && at0 >= 0) {
+                    const int64_t at = at0 + (int64_t)(isv ? r - first_v : r - a.q_heads) * c.page_size;
+                    const bool bad = amax >= 0x7f800000u;  // a NaN or an infinity in the row
+                    float scale = 1.0f;
+                    if (kE4M3 && !bad) {
+                        const int e = row_exponent(amax);
+                        scale = exp2_int(e);
+                        const float inv = exp2_int(-e);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] *= inv;
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                        scale = __uint_as_float(0x7fc00000u);
+                    }
+                    char *codes = isv ? c.v : c.k;
+                    if (kE4M3)
+                        *reinterpret_cast<uint2 *>(codes + at * c.dim + e0) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+                    else
+                        store8(reinterpret_cast<bf16 *>(codes) + at * c.dim + e0, v);
+                    if (e0 == 0) (isv ? c.v_scale : c.k_scale)[at] = scale;
                 }
             }
-        }
-        __syncwarp();
-        uint32_t amax = 0;
+            if (on && r < a.q_heads) {
+                if (!live)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-        for (int d = w / 2; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        if (!on) continue;
-        if (isq) {
-            store8(a.q_out + ((int64_t)tok * a.q_heads + h) * c.dim + e0, v);
-            continue;
+                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                store8(qo + r * c.dim, v);
+            }
         }
-        if (!live) continue;
-        const int64_t at = cache_row(c, b, h, len + i);
-        if (at < 0) {
-            if (e0 == 0) atomicOr(c.status, kStatusPage);
-            continue;
-        }
-        const bool bad = amax >= 0x7f800000u;  // a NaN or an infinity in the row
-        float scale = 1.0f;
-        if (kE4M3 && !bad) {
-            const int e = row_exponent(amax);
-            scale = exp2_int(e);
-            const float inv = exp2_int(-e);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= inv;
-        }
-        if (bad) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-            scale = __uint_as_float(0x7fc00000u);
-        }
-        char *codes = isv ? c.v : c.k;
-        if (kE4M3)
-            *reinterpret_cast<uint2 *>(codes + at * c.dim + e0) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
-        else
-            store8(reinterpret_cast<bf16 *>(codes) + at * c.dim + e0, v);
-        if (e0 == 0) (isv ? c.v_scale : c.k_scale)[at] = scale;
     }
 }
 
-template <bool kE4M3>
+template <bool kE4M3, bool kHalves>
 static void rope_launch(const RopeArgs &a, int xdt, int64_t tokens, cudaStream_t st)
 {
     if (xdt == WL_OUT_F32)
-        rope_append_kernel<float, kE4M3><<<(unsigned)tokens, kRopeThreads, 0, st>>>(a);
+        rope_append_kernel<float, kE4M3, kHalves><<<(unsigned)tokens, kRopeThreads, 0, st>>>(a);
     else
-        rope_append_kernel<bf16, kE4M3><<<(unsigned)tokens, kRopeThreads, 0, st>>>(a);
+        rope_append_kernel<bf16, kE4M3, kHalves><<<(unsigned)tokens, kRopeThreads, 0, st>>>(a);
 }
 
 wl_status launch_rope_append(const void *q, const void *k, const void *v, bf16 *q_out, int64_t q_heads, int64_t q_stride,
@@ -130,72 +203,91 @@ wl_status launch_rope_append(const void *q, const void *k, const void *v, bf16 *
     a.c = cache_args(cache, seqs, di->status);
     a.width = 2;
     while (a.width * 8 < a.c.dim) a.width *= 2;
-    if (cache.format == WL_CACHE_E4M3)
-        rope_launch<true>(a, xdt, seqs.batch * seqs.n, st);
+    const bool e4 = cache.format == WL_CACHE_E4M3, halves = !rope.interleaved && rope.rot % 16 == 0;
+    const int64_t tokens = seqs.batch * seqs.n;
+    if (halves)
+        e4 ? rope_launch<true, true>(a, xdt, tokens, st) : rope_launch<false, true>(a, xdt, tokens, st);
     else
-        rope_launch<false>(a, xdt, seqs.batch * seqs.n, st);
+        e4 ? rope_launch<true, false>(a, xdt, tokens, st) : rope_launch<false, false>(a, xdt, tokens, st);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_rope_append launch");
 }
 
 // ------------------------------------------------------------------ read --
-// A thread decodes 16 consecutive codes of one row of k or v (blockIdx.y).
-template <typename Y, bool kE4M3>
-__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheArgs c, Y *k_out, Y *v_out)
-{
-    const int chunks = c.dim / 16;
-    const int64_t items = (int64_t)c.batch * c.n * c.kv_heads * chunks;
-    const int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (it >= items) return;
-    const int ch = (int)(it % chunks);
-    const int64_t row = it / chunks;
-    const int h = (int)(row % c.kv_heads);
-    const int64_t tok = row / c.kv_heads;
-    const int b = (int)(tok / c.n), i = (int)(tok % c.n);
-    Y *out = (blockIdx.y ? v_out : k_out) + row * c.dim + ch * 16;
-    float v[16] = {};
-    if (i < seq_count(c, b)) {
-        const int64_t at = cache_row(c, b, h, seq_len(c, b) + i);
-        if (at < 0) {
-            if (ch == 0) atomicOr(c.status, kStatusPage);
-        } else {
-            const float scale = (blockIdx.y ? c.v_scale : c.k_scale)[at];
-            const char *src = (blockIdx.y ? c.v : c.k) + (at * c.dim + ch * 16) * (kE4M3 ? 1 : 2);
-            if (kE4M3) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(src);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 16 codes as loaded, and their values.
+template <bool kE4M3>
+struct Codes16 {
+    uint4 w[kE4M3 ? 1 : 2];
+    __device__ __forceinline__ void load(const char *p)
+    {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 f = e4m3x2_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
-                    v[2 * j] = f.x;
-                    v[2 * j + 1] = f.y;
-                }
-            } else {
-                load8(reinterpret_cast<const bf16 *>(src), v);
-                load8(reinterpret_cast<const bf16 *>(src) + 8, v + 8);
-            }
+        for (int i = 0; i < (kE4M3 ? 1 : 2); ++i) w[i] = ld_stream16(p + 16 * i);
+    }
+    __device__ __forceinline__ void values(float v[16], float scale) const
+    {
+        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[kE4M3 ? 0 : 1].x, w[kE4M3 ? 0 : 1].y, w[kE4M3 ? 0 : 1].z, w[kE4M3 ? 0 : 1].w};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] *= scale;
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = kE4M3 ? e4m3x2_f32((u[j / 2] >> (16 * (j & 1))) & 0xffffu) : make_float2(bf_lo(u[j]), bf_hi(u[j]));
+            v[2 * j] = f.x * scale;
+            v[2 * j + 1] = f.y * scale;
         }
     }
-    store8(out, v);
-    store8(out + 8, v + 8);
+};
+
+// A thread decodes 16 consecutive codes of a row of k and of the same row of v
+// (one lookup, two independent loads).  `per` such items a token, `tokens`
+// tokens a CTA.  Bound by DRAM bytes; the divisions that find an item's place
+// are multiplications (64-bit ones took as long as the bytes: 39 us for 190 MB).
+constexpr int kReadThreads = 256;
+
+template <typename Y, bool kE4M3>
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ CacheArgs c, Y *k_out, Y *v_out,
+                                                                  FastDiv per, FastDiv chunks, FastDiv n, int tokens, int all)
+{
+    const int tok0 = blockIdx.x * tokens, end = min(tokens, all - tok0) * (int)per.d;
+    for (int e = threadIdx.x; e < end; e += kReadThreads) {
+        const int t = per.div(e), in = e - t * (int)per.d, h = chunks.div(in), ch = in - h * (int)chunks.d;
+        const int tok = tok0 + t, b = n.div(tok), i = tok - b * (int)n.d;
+        const int64_t o = ((int64_t)tok * c.kv_heads + h) * c.dim + ch * 16;
+        float v[16] = {}, u[16] = {};
+        if (i < seq_count(c, b)) {
+            const int64_t at = cache_row(c, b, h, seq_len(c, b) + i);
+            if (at < 0) {
+                if (ch == 0) atomicOr(c.status, kStatusPage);
+            } else {
+                const int64_t from = (at * c.dim + ch * 16) * (kE4M3 ? 1 : 2);
+                Codes16<kE4M3> ck, cv;
+                ck.load(c.k + from);
+                cv.load(c.v + from);
+                const float ks = __ldg(c.k_scale + at), vs = __ldg(c.v_scale + at);
+                ck.values(v, ks);
+                cv.values(u, vs);
+            }
+        }
+        store8(k_out + o, v);
+        store8(k_out + o + 8, v + 8);
+        store8(v_out + o, u);
+        store8(v_out + o + 8, u + 8);
+    }
 }
 
 wl_status launch_cache_read(const wl_cache &cache, const wl_seqs &seqs, void *k_out, void *v_out, int dt,
                             const DeviceInfo *di, cudaStream_t st)
 {
     const CacheArgs c = cache_args(cache, seqs, di->status);
-    const int64_t items = seqs.batch * seqs.n * cache.kv_heads * (cache.dim / 16);
-    if ((items + 255) / 256 > 0x7fffffff) return fail(WL_ERR_UNSUPPORTED, "wl_cache_read: too many elements for one call");
-    const dim3 grid((unsigned)((items + 255) / 256), 2);
+    const int64_t chunk = cache.dim / 16, per = cache.kv_heads * chunk, all = seqs.batch * seqs.n;
+    // one item per thread where a token has fewer than a CTA's worth
+    const int tokens = (int)(per >= kReadThreads ? 1 : kReadThreads / per);
+    const unsigned grid = (unsigned)((all + tokens - 1) / tokens);
+    const FastDiv dp = fast_div(per), dc = fast_div(chunk), dn = fast_div(seqs.n);
     const bool e4 = cache.format == WL_CACHE_E4M3;
     if (dt == WL_OUT_F32) {
         float *ko = static_cast<float *>(k_out), *vo = static_cast<float *>(v_out);
-        e4 ? cache_read_kernel<float, true><<<grid, 256, 0, st>>>(c, ko, vo) : cache_read_kernel<float, false><<<grid, 256, 0, st>>>(c, ko, vo);
+        e4 ? cache_read_kernel<float, true><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all) : cache_read_kernel<float, false><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all);
     } else {
         bf16 *ko = static_cast<bf16 *>(k_out), *vo = static_cast<bf16 *>(v_out);
-        e4 ? cache_read_kernel<bf16, true><<<grid, 256, 0, st>>>(c, ko, vo) : cache_read_kernel<bf16, false><<<grid, 256, 0, st>>>(c, ko, vo);
+        e4 ? cache_read_kernel<bf16, true><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all) : cache_read_kernel<bf16, false><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all);
     }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_cache_read launch");
