@@ -611,20 +611,37 @@ def _token_rows(t, name: str, dtype, tokens: int, width: int) -> int:
     return int(sd[lead - 1]) if sh[lead - 1] > 1 else int(sd[0]) if lead == 2 and sh[0] > 1 else width
 
 
-class _on:
-    """Makes `device` the current one for a call (nothing to do where it is)."""
+# The calls below are as short as their launches (a few microseconds), so the
+# binding keeps its own share small: one pass over the arguments, and the
+# current device and stream by torch's cheapest queries.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
-    def __init__(self, device):
-        self.device, self.back = device, None
 
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.device)
+def _checked(t, name: str, dtype, shape) -> int:
+    """The address of a contiguous CUDA tensor of this type and shape (None: any)."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape) and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    return t.data_ptr()
 
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+
+def _run(fn, device, stream, *args):
+    """fn(*args, stream) on `device`; raises what it reports."""
+    index = device.index
+    st = (_current_stream(index) if stream is None
+          else stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
+    if _current_device() == index:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, st)
+    if status:
+        _check(status)
+
+
+_NO_ROPE = _Rope(None, 0, 0, 1.0)
 
 
 def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, seqs: CacheSeqs, q_out=None, stream=None):
@@ -635,25 +652,26 @@ def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, s
     [batch, n], or None for len[b] + i.  rope None: no rotation."""
     dt = k.dtype
     code = _ydt(dt)
-    tokens, kvw = seqs.tokens, cache.kv_heads * cache.dim
+    tokens, dim = seqs.tokens, cache.dim
+    kvw = cache.kv_heads * dim
     ks, vs = _token_rows(k, "k", dt, tokens, kvw), _token_rows(v, "v", dt, tokens, kvw)
-    heads, qs = 0, 0
+    heads, qs, qp, op = 0, 0, None, None
     if q is not None:
-        heads = q.numel() // (tokens * cache.dim)
-        qs = _token_rows(q, "q", dt, tokens, heads * cache.dim)
+        heads = q.numel() // (tokens * dim)
+        qs = _token_rows(q, "q", dt, tokens, heads * dim)
+        qp = q.data_ptr()
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _need(q_out, "q_out", torch.bfloat16, q.shape)
+        op = _checked(q_out, "q_out", torch.bfloat16, q.shape)
     elif q_out is not None:
         raise ValueError("q_out needs q")
+    pp = None
     if positions is not None:
-        _need(positions, "positions", torch.int32)
+        pp = _checked(positions, "positions", torch.int32, None)
         if positions.numel() != tokens:
             raise ValueError(f"positions must hold batch * n = {tokens} numbers, got {tuple(positions.shape)}")
-    with _on(cache.device):
-        _check(lib().wl_rope_append(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), heads, qs, ks, vs, code, _ptr(positions),
-                                    rope._c if rope is not None else _Rope(None, 0, 0, 1.0), cache._c, seqs._c,
-                                    _stream(stream, cache.device)))
+    _run((_lib or lib()).wl_rope_append, cache.device, stream, qp, k.data_ptr(), v.data_ptr(), op, heads, qs, ks, vs, code, pp,
+         _NO_ROPE if rope is None else rope._c, cache._c, seqs._c)
     return q_out
 
 
@@ -661,13 +679,12 @@ def wl_cache_read(cache: KVCache, seqs: CacheSeqs, dt=torch.bfloat16, outs=None,
     """The cache's values at positions len[b] + i, i < count[b] (zeros beyond):
     (k, v) [batch, n, kv_heads, dim] as bf16 or fp32."""
     code = _ydt(dt)
+    td = _tdt(code)
     shape = (seqs.batch, seqs.n, cache.kv_heads, cache.dim)
     if outs is None:
-        outs = tuple(torch.empty(shape, dtype=_tdt(code), device=cache.device) for _ in range(2))
-    for o, name in zip(outs, ("k_out", "v_out")):
-        _need(o, name, _tdt(code), shape)
-    with _on(cache.device):
-        _check(lib().wl_cache_read(cache._c, seqs._c, outs[0].data_ptr(), outs[1].data_ptr(), code, _stream(stream, cache.device)))
+        outs = (torch.empty(shape, dtype=td, device=cache.device), torch.empty(shape, dtype=td, device=cache.device))
+    kp, vp = _checked(outs[0], "k_out", td, shape), _checked(outs[1], "v_out", td, shape)
+    _run((_lib or lib()).wl_cache_read, cache.device, stream, cache._c, seqs._c, kp, vp, code)
     return tuple(outs)
 
 
@@ -683,32 +700,31 @@ def wl_tree_attention(q, cache: KVCache, seqs: CacheSeqs, mask=None, scale: floa
     [batch * n, q_heads * dim]) -> out of the same shape.  scale defaults to
     dim ** -0.5.  workspace: at least wl_tree_attention_workspace_bytes() bytes,
     256-byte aligned; by default allocated for the call."""
-    tokens = seqs.tokens
-    heads = q.numel() // (tokens * cache.dim)
-    _need(q, "q", torch.bfloat16)
-    if heads * tokens * cache.dim != q.numel():
-        raise ValueError(f"q must hold batch * n = {tokens} rows of heads * {cache.dim} elements, got {tuple(q.shape)}")
+    tokens, dim = seqs.tokens, cache.dim
+    qp = _checked(q, "q", torch.bfloat16, None)
+    heads = q.numel() // (tokens * dim)
+    if heads * tokens * dim != q.numel():
+        raise ValueError(f"q must hold batch * n = {tokens} rows of heads * {dim} elements, got {tuple(q.shape)}")
+    mp = None
     if mask is not None:
-        _need(mask, "mask", torch.int64)
+        mp = _checked(mask, "mask", torch.int64, None)
         if mask.numel() != tokens:
             raise ValueError(f"mask must hold batch * n = {tokens} words, got {tuple(mask.shape)}")
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, q.shape)
-    with _on(cache.device):
-        st = _stream(stream, cache.device)
-        if workspace is None:
+    op = _checked(out, "out", torch.bfloat16, q.shape)
+    L = _lib or lib()
+    if workspace is None:
+        nb = max(256, L.wl_tree_attention_workspace_bytes(seqs.batch, seqs.n, heads, cache.kv_heads, dim))
+        if stream is None:
+            workspace = torch.empty(nb, dtype=torch.uint8, device=cache.device)
+        else:
             # of the call's own stream, so that the allocator hands it on only after the call
-            nb = lib().wl_tree_attention_workspace_bytes(seqs.batch, seqs.n, heads, cache.kv_heads, cache.dim)
-            if stream is None:
-                workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=cache.device)
-            else:
-                s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), cache.device)
-                with torch.cuda.stream(s):
-                    workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=cache.device)
-        _check(lib().wl_tree_attention(q.data_ptr(), heads, _ptr(mask), scale if scale is not None else cache.dim ** -0.5,
-                                       cache._c, seqs._c, out.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), st))
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), cache.device)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(nb, dtype=torch.uint8, device=cache.device)
+    _run(L.wl_tree_attention, cache.device, stream, qp, heads, mp, dim ** -0.5 if scale is None else scale, cache._c, seqs._c, op,
+         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -721,35 +737,40 @@ def wl_norm_residual(y, x, w_post=None, w_pre=None, gate=None, alpha: float = 1.
     norm after the block; no h).  Returns (x', h); x_out may be x (in place)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a tensor [T, H]")
-    T, H = x.shape
-    xc = _ydt(x.dtype)
-    _need(x, "x", x.dtype)
-    yc, gs = xc, 0
+    shape = x.shape
+    T, H = shape
+    dt = x.dtype
+    xc = yc = _ydt(dt)
+    xp = _checked(x, "x", dt, shape)
+    yp = gp = wp = wq = xo = hp = None
+    gs = 0
     if y is not None:
         yc = _ydt(y.dtype)
-        _need(y, "y", y.dtype, (T, H))
+        yp = _checked(y, "y", y.dtype, shape)
     if gate is not None:
         if y is None:
             raise ValueError("gate needs y")
-        _need(gate, "gate", y.dtype)
-        if gate.numel() != H and tuple(gate.shape) != (T, H):
-            raise ValueError(f"gate must be [{T}, {H}], [1, {H}] or [{H}], got {tuple(gate.shape)}")
-        gs = H if gate.numel() != H else 0
-    for w, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if w is not None:
-            _need(w, name, torch.float32, (H,))
+        gp = _checked(gate, "gate", y.dtype, None)
+        if gate.numel() != H:
+            if gate.shape != shape:
+                raise ValueError(f"gate must be [{T}, {H}], [1, {H}] or [{H}], got {tuple(gate.shape)}")
+            gs = H
+    if w_post is not None:
+        wp = _checked(w_post, "w_post", torch.float32, (H,))
+    if w_pre is not None:
+        wq = _checked(w_pre, "w_pre", torch.float32, (H,))
     if x_out is None and (y is not None or alpha != 1.0):
         x_out = torch.empty_like(x)
     if x_out is not None:
-        _need(x_out, "x_out", x.dtype, (T, H))
+        xo = _checked(x_out, "x_out", dt, shape)
     hc = _ydt(h_dt)
+    td = _tdt(hc)
     if w_pre is not None and h is None:
-        h = torch.empty(T, H, dtype=_tdt(hc), device=x.device)
+        h = torch.empty_like(x, dtype=td)
     if h is not None:
-        _need(h, "h", _tdt(hc), (T, H))
-    with _on(x.device):
-        _check(lib().wl_norm_residual(_ptr(y), _ptr(gate), gs, x.data_ptr(), _ptr(w_post), _ptr(w_pre), _ptr(x_out), _ptr(h), T,
-                                      H, alpha, beta, eps, w_offset, yc, xc, hc, _stream(stream, x.device)))
+        hp = _checked(h, "h", td, shape)
+    _run((_lib or lib()).wl_norm_residual, x.device, stream, yp, gp, gs, xp, wp, wq, xo, hp, T, H, alpha, beta, eps, w_offset, yc,
+         xc, hc)
     return (x if x_out is None else x_out), h
 
 

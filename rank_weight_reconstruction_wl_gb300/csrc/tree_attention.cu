@@ -25,6 +25,8 @@
 // laid end to end and cut into one equal range per CTA (one CTA per SM), so
 // ragged lengths balance; a unit cut by a range is joined from fp32 partials by
 // tree_join_kernel, in a fixed order.
+#include <atomic>
+
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
 #include "tc_ptx.cuh"
@@ -1199,11 +1201,17 @@ size_t tree_attention_workspace_bytes(int64_t, int64_t n, int64_t q_heads, int64
 }
 
 template <bool kE4M3, int DP, int RT>
-static cudaError_t ta_launch(const TaArgs &a, int ctas, cudaStream_t st)
+static cudaError_t ta_launch(const TaArgs &a, int ctas, int device, cudaStream_t st)
 {
     using Z = TaShape<kE4M3, DP, RT>;
-    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<kE4M3, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
-    if (e != cudaSuccess) return e;
+    // once per device (setting it twice is harmless)
+    static std::atomic<uint64_t> set{0};
+    cudaError_t e;
+    if (!((set.load(std::memory_order_relaxed) >> device) & 1)) {
+        e = cudaFuncSetAttribute(tree_attention_kernel<kE4M3, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::SMEM);
+        if (e != cudaSuccess) return e;
+        set.fetch_or((uint64_t)1 << device, std::memory_order_relaxed);
+    }
     tree_attention_kernel<kE4M3, DP, RT><<<ctas, kTaThreads, Z::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
@@ -1260,14 +1268,14 @@ wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *
     cudaError_t e;
     if (cache.format == WL_CACHE_E4M3) {
         if (DP == 128)
-            e = RT == 16 ? ta_launch<true, 128, 16>(a, ctas, st) : RT == 32 ? ta_launch<true, 128, 32>(a, ctas, st) : ta_launch<true, 128, 64>(a, ctas, st);
+            e = RT == 16 ? ta_launch<true, 128, 16>(a, ctas, di->device, st) : RT == 32 ? ta_launch<true, 128, 32>(a, ctas, di->device, st) : ta_launch<true, 128, 64>(a, ctas, di->device, st);
         else
-            e = RT == 16 ? ta_launch<true, 256, 16>(a, ctas, st) : RT == 32 ? ta_launch<true, 256, 32>(a, ctas, st) : ta_launch<true, 256, 64>(a, ctas, st);
+            e = RT == 16 ? ta_launch<true, 256, 16>(a, ctas, di->device, st) : RT == 32 ? ta_launch<true, 256, 32>(a, ctas, di->device, st) : ta_launch<true, 256, 64>(a, ctas, di->device, st);
     } else {
         if (DP == 128)
-            e = RT == 16 ? ta_launch<false, 128, 16>(a, ctas, st) : RT == 32 ? ta_launch<false, 128, 32>(a, ctas, st) : ta_launch<false, 128, 64>(a, ctas, st);
+            e = RT == 16 ? ta_launch<false, 128, 16>(a, ctas, di->device, st) : RT == 32 ? ta_launch<false, 128, 32>(a, ctas, di->device, st) : ta_launch<false, 128, 64>(a, ctas, di->device, st);
         else
-            e = RT == 16 ? ta_launch<false, 256, 16>(a, ctas, st) : RT == 32 ? ta_launch<false, 256, 32>(a, ctas, st) : ta_launch<false, 256, 64>(a, ctas, st);
+            e = RT == 16 ? ta_launch<false, 256, 16>(a, ctas, di->device, st) : RT == 32 ? ta_launch<false, 256, 32>(a, ctas, di->device, st) : ta_launch<false, 256, 64>(a, ctas, di->device, st);
     }
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_tree_attention launch");
 }
