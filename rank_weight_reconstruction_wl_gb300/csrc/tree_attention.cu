@@ -1103,86 +1103,82 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 }
 
 // Joins the partial sums of the unit that CTA blockIdx.x began and others
-// finished, contributors in CTA order.  A block has G groups of lanes that
-// each cover a row.  R < G rows: G / R groups share a row's contributors (few
-// rows come with many contributors); R >= G: a group has R / G rows.
-template <int DP, int RT, int R>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TaArgs a)
+// finished.  A block has G groups of lanes that each cover a row; S of them
+// share a row's contributors (few rows come with many contributors).  A lane
+// takes references, sums and its 4 dims of a few contributors at a time, so
+// that little lies between the first kernel's end and the stores but two
+// round trips to L2; contributors are taken in a fixed order.
+template <int DP, int RT, int S>
+__global__ void __launch_bounds__(256, 6) tree_join_kernel(const __grid_constant__ TaArgs a)
 {
-    constexpr int L = DP / 4, G = 256 / L, S = R < G ? G / R : 1, Q = R < G ? 1 : R / G;  // 16-byte lanes of a row
-    __shared__ float wgt[R][kTaMaxCtas], inv[R];
+    constexpr int L = DP / 4, G = 256 / L, R = G / S;  // 16-byte lanes of a row; rows of a block
     __shared__ float4 acc[G][L];
+    __shared__ float2 mls[G];
     pdl_wait();
     const int4 u = a.desc[blockIdx.x];
     if (u.x < 0) return;
     const CacheArgs &c = a.c;
-    const int hk = u.y / a.rtiles, row0 = (u.y - hk * a.rtiles) * RT, r0 = blockIdx.y * R, t = threadIdx.x, lane = t & 31;
-    const int rows = min(RT, c.n * a.group - row0) - r0;  // from r0 on
-    if (rows <= 0) return;
+    const int hk = u.y / a.rtiles, row0 = (u.y - hk * a.rtiles) * RT, t = threadIdx.x;
+    const int grp = t / L, el = (t % L) * 4, part = grp % S, r = blockIdx.y * R + grp / S;
+    const bool on = r < min(RT, c.n * a.group - row0);
+    const int cnt = seq_count(c, u.x);
     // the CTA whose range has the unit's last tile (ranges as in ta_walk); contributors
     const int ctas = min((int)gridDim.x + 1, u.w), each = u.w / ctas, more = u.w - each * ctas, cut = more * (each + 1);
     const int n = (u.z < cut ? u.z / (each + 1) : more + (u.z - cut) / each) - (int)blockIdx.x + 1;
-    const int cnt = seq_count(c, u.x);
-    auto slot = [&](int k, int r) -> int64_t { return (int64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * RT + r0 + r; };
-    // a warp per row: the weights of its contributors
-#pragma unroll 1
-    for (int r = t / 32; r < R && r < rows; r += 8) {
-        float2 ml[(kTaMaxCtas + 31) / 32];
-        float m = kTaNone, s = 0.0f;
+    float m = kTaNone, s = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int B = S > 1 ? 4 : 2;
+    for (int k0 = part; on && k0 < n; k0 += B * S) {
+        float2 ml[B];
+        float4 v[B];
 #pragma unroll
-        for (int q = 0; q < (kTaMaxCtas + 31) / 32; ++q) {
-            ml[q] = q * 32 + lane < n ? a.ml[slot(q * 32 + lane, r)] : make_float2(kTaNone, 0.0f);
-            m = fmaxf(m, ml[q].x);
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll
-        for (int q = 0; q < (kTaMaxCtas + 31) / 32; ++q) {
-            const float f = ex2(ml[q].x - m);
-            if (q * 32 + lane < n) wgt[r][q * 32 + lane] = f;
-            s = fmaf(ml[q].y, f, s);
-        }
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (lane == 0) inv[r] = ta_token(a, row0 + r0 + r) < cnt ? (s == 0.0f ? 0.0f : 1.0f / s) : -1.0f;  // -1: a row past the count
-    }
-    __syncthreads();
-    const int el = (t % L) * 4, grp = t / L, part = grp % S;
-    float4 o[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (el < c.dim) {
-#pragma unroll 4
-        for (int k = part; k < n; k += S) {
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int r = R < G ? grp / S : q * G + grp;
-                if (r >= rows) continue;
-                const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(k, r) * DP + el);
-                const float h = wgt[r][k];
-                o[q].x = fmaf(v.x, h, o[q].x), o[q].y = fmaf(v.y, h, o[q].y), o[q].z = fmaf(v.z, h, o[q].z), o[q].w = fmaf(v.w, h, o[q].w);
+        for (int q = 0; q < B; ++q) {
+            const int k = k0 + q * S;
+            const int64_t at = (int64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * RT + r;
+            ml[q] = make_float2(kTaNone, 0.0f);
+            v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k < n) {
+                ml[q] = a.ml[at];
+                if (el < c.dim) v[q] = *reinterpret_cast<const float4 *>(a.part + at * DP + el);
             }
+        }
+        float top = m;
+#pragma unroll
+        for (int q = 0; q < B; ++q) top = fmaxf(top, ml[q].x);
+        float f = ex2(m - top);
+        m = top;
+        s *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+            f = ex2(ml[q].x - top);
+            s = fmaf(ml[q].y, f, s);
+            o.x = fmaf(v[q].x, f, o.x), o.y = fmaf(v[q].y, f, o.y), o.z = fmaf(v[q].z, f, o.z), o.w = fmaf(v[q].w, f, o.w);
         }
     }
     if (S > 1) {
-        acc[grp][t % L] = o[0];
+        acc[grp][t % L] = o;
+        if (t % L == 0) mls[grp] = make_float2(m, s);
         __syncthreads();
-        if (part == 0)
-            for (int i = 1; i < S; ++i) {
-                const float4 v = acc[grp + i][t % L];
-                o[0].x += v.x, o[0].y += v.y, o[0].z += v.z, o[0].w += v.w;
-            }
-    }
-    if (part != 0 || el >= c.dim) return;
+        if (part != 0) return;
+        float top = m;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int r = R < G ? grp / S : q * G + grp;
-        if (r >= rows) continue;
-        const int g = row0 + r0 + r, i = ta_token(a, g);
-        const float f = inv[r];
-        uint2 two = make_uint2(bf16x2_bits(o[q].x * f, o[q].y * f), bf16x2_bits(o[q].z * f, o[q].w * f));
-        if (f == -1.0f) two = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2 *>(a.out + (((int64_t)u.x * c.n + i) * a.q_heads + hk * a.group + (g - i * a.group)) * c.dim + el) = two;
+        for (int i = 1; i < S; ++i) top = fmaxf(top, mls[grp + i].x);
+        float f = ex2(m - top);
+        s *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int i = 1; i < S; ++i) {
+            const float4 v = acc[grp + i][t % L];
+            f = ex2(mls[grp + i].x - top);
+            s = fmaf(mls[grp + i].y, f, s);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        }
     }
+    if (!on || el >= c.dim) return;
+    const int g = row0 + r, i = ta_token(a, g);
+    const float f = s == 0.0f ? 0.0f : 1.0f / s;
+    uint2 two = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
+    if (i >= cnt) two = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2 *>(a.out + (((int64_t)u.x * c.n + i) * a.q_heads + hk * a.group + (g - i * a.group)) * c.dim + el) = two;
 }
 
 // -------------------------------------------------------------------- host --
@@ -1216,7 +1212,7 @@ static cudaError_t ta_launch(const TaArgs &a, int ctas, int device, cudaStream_t
     e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
     // the join may become resident early; it waits for the whole first kernel
-    constexpr int R = RT == 16 ? 1 : 8;
+    constexpr int G = 1024 / DP, S = RT == 16 ? G : 1, R = G / S;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1227,7 +1223,7 @@ static cudaError_t ta_launch(const TaArgs &a, int ctas, int device, cudaStream_t
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<DP, RT, R>, a);
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<DP, RT, S>, a);
 }
 
 wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *mask, float scale, const wl_cache &cache,
