@@ -29,6 +29,8 @@
  *    written by the kernel launched immediately before the call on the same
  *    stream; weights written by a copy (cudaMemcpy*), on another stream
  *    joined by an event, or by any earlier kernel are fine.
+ *    The decoder-layer operators below launch the same way but touch no
+ *    caller memory before everything ahead of them on the stream is complete.
  *  Errors: return codes only; nothing is thrown or aborted across the ABI.
  *    Arguments are checked before anything is launched; on error nothing is
  *    launched and wl_last_error() describes the failure.  A failed launch

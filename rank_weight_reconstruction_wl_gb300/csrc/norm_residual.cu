@@ -8,6 +8,7 @@
 // One CTA per token.  The row stays in registers between the two sums of
 // squares, so y and x are read once and x' and h written once.
 #include "cache_row.cuh"
+#include "dec_ptx.cuh"
 
 namespace wl {
 
@@ -55,6 +56,8 @@ template <typename Y, typename X, typename O, int V>
 __global__ void __launch_bounds__(V == 1 ? 256 : V == 2 ? 384 : 256) norm_residual_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ float red[2][32];
+    pdl_wait();
+    pdl_trigger();  // only now: a kernel after this one may rely on all before it
     const int nchunk = a.H / 8;
     const int64_t row = (int64_t)blockIdx.x * a.H;
     Chunk8<Y> y[V];
@@ -126,17 +129,17 @@ __global__ void __launch_bounds__(V == 1 ? 256 : V == 2 ? 384 : 256) norm_residu
 }
 
 template <typename Y, typename X, typename O>
-static void norm_launch(const NormArgs &a, int64_t T, cudaStream_t st)
+static cudaError_t norm_launch(const NormArgs &a, int64_t T, cudaStream_t st)
 {
     const int nchunk = a.H / 8;
     const int V = nchunk <= 256 ? 1 : nchunk <= 768 ? 2 : nchunk <= 1024 ? 4 : 8;
     const int threads = ((nchunk + V - 1) / V + 31) / 32 * 32;
     const unsigned grid = (unsigned)T;
     switch (V) {
-    case 1: norm_residual_kernel<Y, X, O, 1><<<grid, threads, 0, st>>>(a); break;
-    case 2: norm_residual_kernel<Y, X, O, 2><<<grid, threads, 0, st>>>(a); break;
-    case 4: norm_residual_kernel<Y, X, O, 4><<<grid, threads, 0, st>>>(a); break;
-    default: norm_residual_kernel<Y, X, O, 8><<<grid, threads, 0, st>>>(a); break;
+    case 1: return launch_dependent(norm_residual_kernel<Y, X, O, 1>, dim3(grid), threads, 0, st, a);
+    case 2: return launch_dependent(norm_residual_kernel<Y, X, O, 2>, dim3(grid), threads, 0, st, a);
+    case 4: return launch_dependent(norm_residual_kernel<Y, X, O, 4>, dim3(grid), threads, 0, st, a);
+    default: return launch_dependent(norm_residual_kernel<Y, X, O, 8>, dim3(grid), threads, 0, st, a);
     }
 }
 
@@ -146,17 +149,17 @@ wl_status launch_norm_residual(const void *y, const void *gate, int64_t gate_str
 {
     const NormArgs a{y, gate, x, w_post, w_pre, x_out, h, gate_stride, (int)H, alpha, beta, eps, w_offset};
     const int kind = (ydt == WL_OUT_F32 ? 4 : 0) + (xdt == WL_OUT_F32 ? 2 : 0) + (hdt == WL_OUT_F32 ? 1 : 0);
+    cudaError_t e;
     switch (kind) {
-    case 0: norm_launch<bf16, bf16, bf16>(a, T, st); break;
-    case 1: norm_launch<bf16, bf16, float>(a, T, st); break;
-    case 2: norm_launch<bf16, float, bf16>(a, T, st); break;
-    case 3: norm_launch<bf16, float, float>(a, T, st); break;
-    case 4: norm_launch<float, bf16, bf16>(a, T, st); break;
-    case 5: norm_launch<float, bf16, float>(a, T, st); break;
-    case 6: norm_launch<float, float, bf16>(a, T, st); break;
-    default: norm_launch<float, float, float>(a, T, st); break;
+    case 0: e = norm_launch<bf16, bf16, bf16>(a, T, st); break;
+    case 1: e = norm_launch<bf16, bf16, float>(a, T, st); break;
+    case 2: e = norm_launch<bf16, float, bf16>(a, T, st); break;
+    case 3: e = norm_launch<bf16, float, float>(a, T, st); break;
+    case 4: e = norm_launch<float, bf16, bf16>(a, T, st); break;
+    case 5: e = norm_launch<float, bf16, float>(a, T, st); break;
+    case 6: e = norm_launch<float, float, bf16>(a, T, st); break;
+    default: e = norm_launch<float, float, float>(a, T, st); break;
     }
-    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_norm_residual launch");
 }
 

@@ -1,6 +1,7 @@
 // rope_cache.cu -- rotary positions with the quantising cache write, and the
 // cache read.
 #include "cache_row.cuh"
+#include "dec_ptx.cuh"
 
 namespace wl {
 
@@ -83,6 +84,8 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_app
             if (r < rows && mine) raw[p].load((r < a.q_heads ? qp : r < first_v ? kp : vp) + r * c.dim);
         }
     };
+    pdl_wait();
+    pdl_trigger();  // only now: a kernel after this one may rely on all before it
     load(0);
     const int len = seq_len(c, b);
     const bool live = i < seq_count(c, b);
@@ -183,12 +186,12 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_app
 }
 
 template <bool kE4M3, bool kHalves>
-static void rope_launch(const RopeArgs &a, int xdt, int64_t tokens, cudaStream_t st)
+static cudaError_t rope_launch(const RopeArgs &a, int xdt, int64_t tokens, cudaStream_t st)
 {
     if (xdt == WL_OUT_F32)
-        rope_append_kernel<float, kE4M3, kHalves><<<(unsigned)tokens, kRopeThreads, 0, st>>>(a);
+        return launch_dependent(rope_append_kernel<float, kE4M3, kHalves>, dim3((unsigned)tokens), kRopeThreads, 0, st, a);
     else
-        rope_append_kernel<bf16, kE4M3, kHalves><<<(unsigned)tokens, kRopeThreads, 0, st>>>(a);
+        return launch_dependent(rope_append_kernel<bf16, kE4M3, kHalves>, dim3((unsigned)tokens), kRopeThreads, 0, st, a);
 }
 
 wl_status launch_rope_append(const void *q, const void *k, const void *v, bf16 *q_out, int64_t q_heads, int64_t q_stride,
@@ -205,11 +208,8 @@ wl_status launch_rope_append(const void *q, const void *k, const void *v, bf16 *
     while (a.width * 8 < a.c.dim) a.width *= 2;
     const bool e4 = cache.format == WL_CACHE_E4M3, halves = !rope.interleaved && rope.rot % 16 == 0;
     const int64_t tokens = seqs.batch * seqs.n;
-    if (halves)
-        e4 ? rope_launch<true, true>(a, xdt, tokens, st) : rope_launch<false, true>(a, xdt, tokens, st);
-    else
-        e4 ? rope_launch<true, false>(a, xdt, tokens, st) : rope_launch<false, false>(a, xdt, tokens, st);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = halves ? (e4 ? rope_launch<true, true>(a, xdt, tokens, st) : rope_launch<false, true>(a, xdt, tokens, st))
+                                 : (e4 ? rope_launch<true, false>(a, xdt, tokens, st) : rope_launch<false, false>(a, xdt, tokens, st));
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_rope_append launch");
 }
 
@@ -245,6 +245,8 @@ template <typename Y, bool kE4M3>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ CacheArgs c, Y *k_out, Y *v_out,
                                                                   FastDiv per, FastDiv chunks, FastDiv n, int tokens, int all)
 {
+    pdl_wait();
+    pdl_trigger();  // only now: a kernel after this one may rely on all before it
     const int tok0 = blockIdx.x * tokens, end = min(tokens, all - tok0) * (int)per.d;
     for (int e = threadIdx.x; e < end; e += kReadThreads) {
         const int t = per.div(e), in = e - t * (int)per.d, h = chunks.div(in), ch = in - h * (int)chunks.d;
@@ -282,14 +284,13 @@ wl_status launch_cache_read(const wl_cache &cache, const wl_seqs &seqs, void *k_
     const unsigned grid = (unsigned)((all + tokens - 1) / tokens);
     const FastDiv dp = fast_div(per), dc = fast_div(chunk), dn = fast_div(seqs.n);
     const bool e4 = cache.format == WL_CACHE_E4M3;
-    if (dt == WL_OUT_F32) {
-        float *ko = static_cast<float *>(k_out), *vo = static_cast<float *>(v_out);
-        e4 ? cache_read_kernel<float, true><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all) : cache_read_kernel<float, false><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all);
-    } else {
-        bf16 *ko = static_cast<bf16 *>(k_out), *vo = static_cast<bf16 *>(v_out);
-        e4 ? cache_read_kernel<bf16, true><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all) : cache_read_kernel<bf16, false><<<grid, kReadThreads, 0, st>>>(c, ko, vo, dp, dc, dn, tokens, (int)all);
-    }
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (dt == WL_OUT_F32)
+        e = launch_dependent(e4 ? cache_read_kernel<float, true> : cache_read_kernel<float, false>, dim3(grid), kReadThreads, 0, st, c,
+                             static_cast<float *>(k_out), static_cast<float *>(v_out), dp, dc, dn, tokens, (int)all);
+    else
+        e = launch_dependent(e4 ? cache_read_kernel<bf16, true> : cache_read_kernel<bf16, false>, dim3(grid), kReadThreads, 0, st, c,
+                             static_cast<bf16 *>(k_out), static_cast<bf16 *>(v_out), dp, dc, dn, tokens, (int)all);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_cache_read launch");
 }
 

@@ -410,7 +410,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
     extern __shared__ __align__(1024) char smem_raw[];
     // The whole limit is used, so there is no room to align by hand.
     if (s32(smem_raw) & 1023u) {
-        if (threadIdx.x == 0) atomicOr(a.c.status, kStatusAlign);
+        pdl_wait();
+        if (threadIdx.x == 0) {
+            atomicOr(a.c.status, kStatusAlign);
+            a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        }
         return;
     }
     char *smem = smem_raw;
@@ -451,6 +455,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                      "n"(Z::COLS));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    pdl_wait();
     TaWalk w = ta_walk(c, units);
     tc_fence_before();
     __syncthreads();
@@ -1115,6 +1120,7 @@ __global__ void __launch_bounds__(256, 6) tree_join_kernel(const __grid_constant
     __shared__ float4 acc[G][L];
     __shared__ float2 mls[G];
     pdl_wait();
+    pdl_trigger();  // only now: a kernel after this one may rely on all before it
     const int4 u = a.desc[blockIdx.x];
     if (u.x < 0) return;
     const CacheArgs &c = a.c;
@@ -1208,22 +1214,12 @@ static cudaError_t ta_launch(const TaArgs &a, int ctas, int device, cudaStream_t
         if (e != cudaSuccess) return e;
         set.fetch_or((uint64_t)1 << device, std::memory_order_relaxed);
     }
-    tree_attention_kernel<kE4M3, DP, RT><<<ctas, kTaThreads, Z::SMEM, st>>>(a);
-    e = cudaGetLastError();
+    e = launch_dependent(tree_attention_kernel<kE4M3, DP, RT>, dim3(ctas), kTaThreads, Z::SMEM, st, a);
     if (e != cudaSuccess || ctas == 1) return e;
     // the join may become resident early; it waits for the whole first kernel
     constexpr int G = 1024 / DP, S = RT == 16 ? G : 1, R = G / S;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     const int rows = a.c.n * a.group < RT ? a.c.n * a.group : RT;
-    cfg.gridDim = dim3(ctas - 1, (rows + R - 1) / R);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<DP, RT, S>, a);
+    return launch_dependent(tree_join_kernel<DP, RT, S>, dim3(ctas - 1, (rows + R - 1) / R), 256, 0, st, a);
 }
 
 wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *mask, float scale, const wl_cache &cache,
