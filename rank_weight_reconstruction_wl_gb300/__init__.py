@@ -214,6 +214,10 @@ def _rank(th) -> int:
 
 
 def _ydt(dtype) -> int:
+    if dtype is torch.bfloat16:
+        return WL_OUT_BF16
+    if dtype is torch.float32:
+        return WL_OUT_F32
     if dtype in (torch.bfloat16, "bf16"):
         return WL_OUT_BF16
     if dtype in (torch.float32, "f32", "fp32"):
@@ -587,6 +591,8 @@ def _token_rows(t, name: str, dtype, tokens: int, width: int) -> int:
     """Row stride in elements of a tensor of `tokens` rows of `width` elements:
     [tokens, width], [tokens, heads, dim] or [batch, n, heads, dim], rows any
     one distance apart."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == tokens * width:
+        return width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -627,16 +633,23 @@ def _checked(t, name: str, dtype, shape) -> int:
     return t.data_ptr()
 
 
+def _on_device(fn, device, args):
+    """fn(*args) where another device than `device` is the current one."""
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _stream_of(index: int, stream) -> int:
+    if stream is None:
+        return _current_stream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _run(fn, device, stream, *args):
     """fn(*args, stream) on `device`; raises what it reports."""
     index = device.index
-    st = (_current_stream(index) if stream is None
-          else stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
-    if _current_device() == index:
-        status = fn(*args, st)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, st)
+    st = _current_stream(index) if stream is None else _stream_of(index, stream)
+    status = fn(*args, st) if _current_device() == index else _on_device(fn, device, (*args, st))
     if status:
         _check(status)
 
@@ -662,7 +675,9 @@ def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, s
         qp = q.data_ptr()
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        op = _checked(q_out, "q_out", torch.bfloat16, q.shape)
+            op = q_out.data_ptr()
+        else:
+            op = _checked(q_out, "q_out", torch.bfloat16, q.shape)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     pp = None
@@ -682,8 +697,11 @@ def wl_cache_read(cache: KVCache, seqs: CacheSeqs, dt=torch.bfloat16, outs=None,
     td = _tdt(code)
     shape = (seqs.batch, seqs.n, cache.kv_heads, cache.dim)
     if outs is None:
-        outs = (torch.empty(shape, dtype=td, device=cache.device), torch.empty(shape, dtype=td, device=cache.device))
-    kp, vp = _checked(outs[0], "k_out", td, shape), _checked(outs[1], "v_out", td, shape)
+        k = torch.empty(shape, dtype=td, device=cache.device)
+        outs = (k, torch.empty_like(k))
+        kp, vp = k.data_ptr(), outs[1].data_ptr()
+    else:
+        kp, vp = _checked(outs[0], "k_out", td, shape), _checked(outs[1], "v_out", td, shape)
     _run((_lib or lib()).wl_cache_read, cache.device, stream, cache._c, seqs._c, kp, vp, code)
     return tuple(outs)
 
@@ -712,7 +730,9 @@ def wl_tree_attention(q, cache: KVCache, seqs: CacheSeqs, mask=None, scale: floa
             raise ValueError(f"mask must hold batch * n = {tokens} words, got {tuple(mask.shape)}")
     if out is None:
         out = torch.empty_like(q)
-    op = _checked(out, "out", torch.bfloat16, q.shape)
+        op = out.data_ptr()
+    else:
+        op = _checked(out, "out", torch.bfloat16, q.shape)
     L = _lib or lib()
     if workspace is None:
         nb = max(256, L.wl_tree_attention_workspace_bytes(seqs.batch, seqs.n, heads, cache.kv_heads, dim))
@@ -759,16 +779,18 @@ def wl_norm_residual(y, x, w_post=None, w_pre=None, gate=None, alpha: float = 1.
         wp = _checked(w_post, "w_post", torch.float32, (H,))
     if w_pre is not None:
         wq = _checked(w_pre, "w_pre", torch.float32, (H,))
-    if x_out is None and (y is not None or alpha != 1.0):
-        x_out = torch.empty_like(x)
     if x_out is not None:
         xo = _checked(x_out, "x_out", dt, shape)
+    elif y is not None or alpha != 1.0:
+        x_out = torch.empty_like(x)
+        xo = x_out.data_ptr()
     hc = _ydt(h_dt)
     td = _tdt(hc)
-    if w_pre is not None and h is None:
-        h = torch.empty_like(x, dtype=td)
     if h is not None:
         hp = _checked(h, "h", td, shape)
+    elif w_pre is not None:
+        h = torch.empty_like(x) if td is dt else torch.empty_like(x, dtype=td)
+        hp = h.data_ptr()
     _run((_lib or lib()).wl_norm_residual, x.device, stream, yp, gp, gs, xp, wp, wq, xo, hp, T, H, alpha, beta, eps, w_offset, yc,
          xc, hc)
     return (x if x_out is None else x_out), h

@@ -154,6 +154,13 @@ __device__ __forceinline__ void load16(const float *p, float (&v)[16])
     }
 }
 
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -821,9 +828,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     const bool bad = vs != vs;
                     const float v1 = fmaxf(vs, 1.17549435e-38f);
                     // log2 of the scale: exponent exact, 0 for the mantissa of a power of two
-                    const float lv = bad ? vs : (float)((int)(__float_as_uint(v1) >> 23) - 127) +
-                                               __log2f(__uint_as_float((__float_as_uint(v1) & 0x7fffffu) | 0x3f800000u));
-                    const float iv = bad ? 1.0f : __frcp_rn(v1);
+                    const float lv = bad ? vs : __log2f(v1), iv = bad ? 1.0f : rcp_approx(v1);
                     const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv), iv2 = f2(iv, iv);
                     at = ta_row(c, pg1, hk, j + STEP * kTaTile);
                     ks = at != ~0u ? __ldg(c.k_scale + at) : 0.0f;
@@ -837,6 +842,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         uint32_t x[CW], xl[kE4M3 ? CW : 16];
                         tmem_get(sc, x);
                         if (kE4M3) tmem_get(sc + RT, xl);
+                        // the weights' buffer is free once tile it - 2 has been multiplied
+                        if (it >= 2)
+                            ta_wait(&pv_done[it & 1], (unsigned)(((it - 2) >> 1) & 1), c.status, kWaitRingEmpty, abort_flag);
                         tmem_got(x);
                         if (kE4M3) tmem_got(xl);
                         const uint64_t r32 = f2(0.03125f, 0.03125f);
@@ -901,9 +909,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                             }
                         }
                         if (some) {
-                            const int before = it - STEP;
-                            ta_wait(&pv_done[before & 1], (unsigned)((before >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                            tc_fence_after();
+                            if (!Z::PP) {  // (else the sums' last tile is it - 2: waited for above)
+                                ta_wait(&pv_done[(it - 1) & 1], (unsigned)(((it - 1) >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                                tc_fence_after();
+                            }
                             constexpr int P = Z::MT * Z::PARTS;
 #pragma unroll 1
                             for (int i = 0; i < CW; i += 8) {
@@ -929,8 +938,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         }
                     }
                     // weights: w = 2^(x - m) = p * v_scale
-                    if (it >= 2)
-                        ta_wait(&pv_done[it & 1], (unsigned)(((it - 2) >> 1) & 1), c.status, kWaitRingEmpty, abort_flag);
                     char *pr = sp + (it & 1) * Z::PB;
                     const uint32_t rowb = tk * Z::PW, sw = ((rowb >> 7) & (Z::PW / 16 - 1)) << 4;
 #pragma unroll
