@@ -19,7 +19,9 @@
 // (w = p * v_scale); a weight keeps 8 bits down to 2^-18 of the largest and is
 // dropped below 2^-22 of it.  Sums over more than kTaFlush tiles are therefore
 // flushed to fp32, which bounds what a CTA can drop by 8192 * 2^-22 = 0.2 %.
-// bf16 caches take one bf16 part.
+// bf16 caches take q as it is and a weight as two bf16 parts, 16 bits: with 8
+// the weights' rounding adds as much to the result as its own rounding to bf16
+// does (1.4 times the error; a lone heavy weight, 2.5 times).
 //
 // Work: (sequence, kv head, row tile) units of ceil(positions / 128) tiles are
 // laid end to end and cut into one equal range per CTA (one CTA per SM), so
@@ -70,7 +72,7 @@ struct TaShape {
     static constexpr int SLOT = kTaTile * SLOTROW;
     static constexpr int QB = N * ROWB;
     static constexpr int PW = 2 * RT;                // bytes of a position's weights
-    static constexpr int PB = kTaTile * PW;
+    static constexpr int PB1 = kTaTile * PW, PB = kE4M3 ? PB1 : 2 * PB1;  // bf16: the weights, then their remainders
     static constexpr int MISC = 3072;
     static constexpr int ROOM = (232448 - MISC - QB - 2 * PB) / SLOT;
     static constexpr int SLOTS = ROOM < 10 ? ROOM : 10;
@@ -648,10 +650,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 #pragma unroll
                     for (int m = 0; m < MS; ++m)
 #pragma unroll
-                        for (int k = 0; k < kTaTile / Z::KSTEP; ++k)
-                            mma(ocol + ((Z::PP ? (i & 1) * Z::MT : 0) + s * MS + m) * N,
-                                ta_desc(av + m * Z::ES * (kTaTile * 128) + k * Z::KSTEP * 128, kTaTile * 128, 1024, 2),
-                                ta_desc(pb + k * Z::KSTEP * Z::PW, 8 * Z::PW, 8 * Z::PW, Z::SWP), kIdPV, (first && k == 0) ? 0u : 1u);
+                        for (int h = 0; h < Z::PB / Z::PB1; ++h)
+#pragma unroll
+                            for (int k = 0; k < kTaTile / Z::KSTEP; ++k)
+                                mma(ocol + ((Z::PP ? (i & 1) * Z::MT : 0) + s * MS + m) * N,
+                                    ta_desc(av + m * Z::ES * (kTaTile * 128) + k * Z::KSTEP * 128, kTaTile * 128, 1024, 2),
+                                    ta_desc(pb + h * Z::PB1 + k * Z::KSTEP * Z::PW, 8 * Z::PW, 8 * Z::PW, Z::SWP), kIdPV,
+                                    (first && h + k == 0) ? 0u : 1u);
                     umma_commit(&empty[slot]);
                 }
                 umma_commit(&pv_done[i & 1]);
@@ -942,7 +947,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     const uint32_t rowb = tk * Z::PW, sw = ((rowb >> 7) & (Z::PW / 16 - 1)) << 4;
 #pragma unroll
                     for (int i = 0; i < CW; i += 16) {
-                        uint32_t hi[4], lo[4], bw[8];
+                        uint32_t hi[4], lo[4], bw[8], bl[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float p = ex2(f2_lo(y[i / 2 + k])), q = ex2(f2_hi(y[i / 2 + k]));
@@ -962,14 +967,18 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                                 }
                             } else {
                                 bw[k] = bf16x2_bits(p, q);
+                                bl[k] = bf16x2_bits(p - bf_lo(bw[k]), q - bf_hi(bw[k]));
                             }
                         }
                         if constexpr (kE4M3) {
                             *reinterpret_cast<uint4 *>(pr + ((rowb + col0 + i) ^ sw)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                             *reinterpret_cast<uint4 *>(pr + ((rowb + RT + col0 + i) ^ sw)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         } else {
-                            *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + i)) ^ sw)) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
-                            *reinterpret_cast<uint4 *>(pr + ((rowb + 2 * (col0 + i) + 16) ^ sw)) = make_uint4(bw[4], bw[5], bw[6], bw[7]);
+                            char *o0 = pr + ((rowb + 2 * (col0 + i)) ^ sw), *o1 = pr + ((rowb + 2 * (col0 + i) + 16) ^ sw);
+                            *reinterpret_cast<uint4 *>(o0) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+                            *reinterpret_cast<uint4 *>(o1) = make_uint4(bw[4], bw[5], bw[6], bw[7]);
+                            *reinterpret_cast<uint4 *>(o0 + Z::PB1) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
+                            *reinterpret_cast<uint4 *>(o1 + Z::PB1) = make_uint4(bl[4], bl[5], bl[6], bl[7]);
                         }
                     }
                     if (__builtin_expect(a.box && !__all_sync(0xffffffffu, seen), 0)) {
