@@ -88,7 +88,7 @@ struct TaShape {
     // gap is precision lost for fewer moves; bf16 has range to spare.
     static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f, kNear = kE4M3 ? 2.0f : 0.0f;
     static constexpr int SWP = PW == 128 ? 2 : PW == 64 ? 4 : 6;  // swizzle code of the weights' rows
-    static_assert(2 * PB >= RT * DP * 2 && SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
+    static_assert(SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
 };
 
 // ---------------------------------------------------------------- helpers --

@@ -396,6 +396,42 @@ def test_many_sequences_and_a_long_context(wl, gpu):
     _attend_case(wl, gpu, [30011], 1, 2, 1, 32, 128, BF, seed=42)
 
 
+@pytest.mark.parametrize("dtype", [E4, BF])
+@pytest.mark.parametrize("n,group", [(1, 2), (9, 2), (20, 2)])
+def test_many_long_contexts(wl, gpu, dtype, n, group):
+    """More tiles than a CTA sums in tensor memory at a time (64 tiles, 8192 positions), in units that one CTA
+    has whole and in units that several share."""
+    lens, kv, dim, page = [9000] * 10 + [60001] * 5, 8, 32, 64
+    B, G = len(lens), group
+    per = -(-(max(lens) + n) // page)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(n)
+    pages = torch.randperm(B * per, generator=g, device=gpu).to(torch.int32).view(B, per).contiguous()
+    mk = lambda std: (torch.randn(B * per, kv, page, dim, generator=g, device=gpu) * std).to(dtype)  # noqa: E731
+    one = torch.ones(B * per, kv, page, device=gpu)
+    vs = torch.exp2(torch.randint(-3, 4, one.shape, generator=g, device=gpu).float()) if dtype == E4 else one
+    cache = wl.KVCache(mk(1.0), mk(1.0), one, vs)
+    seqs = wl.CacheSeqs(pages, torch.tensor(lens, dtype=torch.int32, device=gpu), n)
+    q = (torch.randn(B, n, kv * G, dim, generator=g, device=gpu) * 2).to(BF)
+    out = wl.wl_tree_attention(q, cache, seqs)
+    assert wl.wl_device_status() == wl.WL_OK
+    for b in (0, 3, 9, 10, 14):
+        L = lens[b] + n
+        at = pages[b].long()
+        k, v = ((x[at].to(torch.float32).double() * s[at][..., None].double()).permute(1, 0, 2, 3).reshape(kv, -1, dim)[:, :L]
+                for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        see = torch.arange(L, device=gpu)[None] <= lens[b] + torch.arange(n, device=gpu)[:, None]
+        for h in (0, 3, kv * G - 1):
+            kk, vv, qq = k[h // G], v[h // G], q[b, :, h].double()
+            sc = torch.where(see, qq @ kk.T * dim ** -0.5, -math.inf)
+            p = torch.softmax(sc, -1)
+            want = p @ vv
+            ds = float((qq.abs() @ kk.abs().T).max()) * dim ** -0.5 * 2.0 ** -20
+            heavy = torch.stack([(p[i][:, None] * vv.abs()).amax(0) for i in range(n)])
+            bound = (2.0 ** -8 + 4 * ds) * (p @ vv.abs()) + 2.0 ** -22 * L * heavy + 2.0 ** -8 * want.abs()
+            assert bool(((out[b, :, h].double() - want).abs() <= bound).all()), (b, h)
+
+
 def test_offsets_past_32_bits(wl, gpu):
     """A cache of over 2^32 bytes, used at its far end by all three operators."""
     pages, page, dim = 140000, 128, 256  # 4.6e9 bytes of codes
