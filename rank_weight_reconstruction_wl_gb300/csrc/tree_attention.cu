@@ -16,9 +16,11 @@
 // 8 bits as two e4m3 parts side by side in N, x = hi + lo / 32: a bf16 number
 // is exactly two 4-bit parts, so q loses nothing but what lies 2^-22 below the
 // largest |q| of the tile.  The weights of v are folded with the row scales
-// (w = p * v_scale); a weight keeps 8 bits down to 2^-18 of the largest and is
-// dropped below 2^-22 of it.  Sums over more than kTaFlush tiles are therefore
-// flushed to fp32, which bounds what a CTA can drop by 8192 * 2^-22 = 0.2 %.
+// (w = p * v_scale).  The largest weight of a row is 2^5 or more, the finest
+// step 2^-14: a weight keeps 8 bits down to 2^-11 of the largest, and what lies
+// below 2^-20 of it is dropped.  Every kTaFlush tiles the sums go to fp32 and
+// the references start anew, so at most 8192 * 2^-20 = 0.8 % can be lost that
+// way, and only if every position but one lies just below that line.
 // bf16 caches take q as it is and a weight as two bf16 parts, 16 bits: with 8
 // the weights' rounding adds as much to the result as its own rounding to bf16
 // does (1.4 times the error; a lone heavy weight, 2.5 times).
@@ -27,6 +29,16 @@
 // laid end to end and cut into one equal range per CTA (one CTA per SM), so
 // ragged lengths balance; a unit cut by a range is joined from fp32 partials by
 // tree_join_kernel, in a fixed order.
+//
+// Measured on e4m3 caches (median of calls, L2 flushed).  Bound by HBM where a
+// kv head has few rows: one token on each of 32 contexts of 4224 to 8192
+// positions, 16 kv heads of 128 with 2 query heads each, 839 MB: 135 us, 6.2
+// TB/s (boxes of 8 KB at random pages read 6.4); 16 trees of 8 to 16 tokens on a
+// bf16 cache, 419 MB: 77 us, 5.5 TB/s.  Bound by the softmax warps'
+// instructions where it has many: 8 trees of 20 to 32 tokens, 4 query heads on
+// one kv head of 256, 18000 to 32000 positions: 52 us for 104 MB and 22 GFLOP;
+// 8 of 38 to 61 tokens, 16 heads on 4, 3375 to 6000 positions: 77 us, 32 GFLOP.
+// One token on 1001 positions: 11.5 us and 6.5 us for the join, latency.
 #include <atomic>
 
 #include "cache_row.cuh"
@@ -85,7 +97,10 @@ struct TaShape {
     static constexpr int CW = PP ? RT : RT / 2;      // columns per softmax thread
     // Exponents of weights: the limit, and how far below it a moved reference
     // puts the largest weight.  e4m3 ends at 448, so the limit is 2^8, and the
-    // gap is precision lost for fewer moves; bf16 has range to spare.
+    // gap is precision lost for fewer moves (the two wide-tree
+    // cases above: 55 and 79 us with a gap of 3, 51 and 73 with 5, which
+    // leaves two bits less).  bf16 has range to spare.  kNear: a column that another column's
+    // move finds so near the limit moves along.
     static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f, kNear = kE4M3 ? 2.0f : 0.0f;
     static constexpr int SWP = PW == 128 ? 2 : PW == 64 ? 4 : 6;  // swizzle code of the weights' rows
     static_assert(SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
@@ -298,7 +313,8 @@ __device__ __forceinline__ int ta_token(const TaArgs &a, int g) { return a.group
 // A unit change costs a CTA about as much as kTaSwitch tiles (its pipeline
 // drains, the sums leave, queries are set up), so a unit counts that many more
 // when the ranges are cut: without it the CTAs with more units finish last
-// (SM cycles of 16 trees over 4096 positions: 115 to 151 thousand).  With
+// (8 trees of up to 61 tokens: SMs busy for 130 thousand cycles, the last for
+// 165).  With
 // fewer than that many tiles a CTA the ranges are cut by tiles alone.
 constexpr int kTaSwitch = 4;
 
@@ -1204,9 +1220,10 @@ __global__ void __launch_bounds__(256, 6) tree_join_kernel(const __grid_constant
 }
 
 // -------------------------------------------------------------------- host --
-// Row tile: the smallest of 16, 32, 64 that holds the rows of a kv head.  The
-// loads of a tile cost the same for any of them, and a smaller one has fewer
-// columns to turn into weights.
+// Row tile: the smallest of 16, 32, 64 that holds the rows of a kv head, and
+// tiles of 64 above that.  The loads of a tile cost the same for any of them,
+// and a smaller one has fewer columns to turn into weights and less to join.
+// Above 64 rows the cache is read once per tile, from L2 after the first.
 static int ta_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 static size_t ta_part_bytes(int RT, int DP) { return (size_t)2 * kTaMaxCtas * RT * DP * sizeof(float); }
@@ -1257,7 +1274,10 @@ wl_status launch_tree_attention(const bf16 *q, int64_t q_heads, const uint64_t *
     a.c = cache_args(cache, seqs, di->status);
     // Runs of positions that never cross a page: the largest power of two that
     // divides the page size, 128 at most.  Under 8 rows a box would start
-    // inside an 8-row swizzle group, so such pages go by 16-byte copies.
+    // inside an 8-row swizzle group, so such pages go by 16-byte copies of four
+    // warps, as do caches of more rows than a box can address (the cases at the
+    // top: 143, 89, 75 and 112 us by copies when boxes took 144, 83, 64 and 88;
+    // the copies share the softmax warps' load and store unit).
     const int64_t rowb = cache.dim * (cache.format == WL_CACHE_E4M3 ? 1 : 2), nrows = cache.pages * cache.kv_heads * cache.page_size;
     a.box = (int)(cache.page_size & -cache.page_size);
     if (a.box > kTaTile) a.box = kTaTile;
