@@ -1022,6 +1022,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 #pragma unroll
                     for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(l[i]), v[2 * i + 1] = f2_hi(l[i]);
                     const float ls = warp_columns<CW>(v, [](float p, float q) { return p + q; });
+                    bar_n<128>(1 + wg);  // the last event's factors have been read
                     if (lane < CW) wred[(warp & 3) * CW + lane] = ls;
                     if (tk < CW && (unset >> tk) & 1) nm[tk] = -kTaNone;
                     const int own = it - (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's last tile, if it had one
