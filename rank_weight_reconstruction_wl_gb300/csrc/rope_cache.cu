@@ -67,7 +67,9 @@ struct Raw8 {
 template <typename X, bool kE4M3, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_append_kernel(const __grid_constant__ RopeArgs a)
 {
-    __shared__ float2 trig[128];
+    // cos, sin of pair p; kHalves: at (p % 8) * 17 + p / 8, so that the lanes of
+    // a row, 8 pairs apart, read neighbouring words
+    __shared__ float2 trig[kHalves ? 8 * 17 : 128];
     __shared__ float row_buf[kHalves ? 1 : kRopeThreads * 8];
     const CacheArgs &c = a.c;
     const int tok = blockIdx.x, b = tok / c.n, i = tok - b * c.n;
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_app
         const uint64_t turn = (uint64_t)(int64_t)pos * a.phase[threadIdx.x];
         float s, co;
         sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &co);  // 2^-31: half turns
-        trig[threadIdx.x] = make_float2(co * a.amplitude, s * a.amplitude);
+        trig[kHalves ? (threadIdx.x & 7) * 17 + (threadIdx.x >> 3) : threadIdx.x] = make_float2(co * a.amplitude, s * a.amplitude);
     }
     if (live && at0 < 0 && threadIdx.x == 0) atomicOr(c.status, kStatusPage);
     __syncthreads();
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_app
     if (kHalves) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            t[j] = turns ? trig[(upper ? e0 - half : e0) + j] : make_float2(0.0f, 0.0f);
+            t[j] = turns ? trig[j * 17 + (upper ? e0 - half : e0) / 8] : make_float2(0.0f, 0.0f);
             if (!upper) t[j].y = -t[j].y;
         }
     }
