@@ -62,7 +62,9 @@ struct Raw8 {
 // pairs are neighbours (interleaved, within the lane) or the row is staged in
 // shared memory.  A row is read once and written once, but what bounds a
 // prompt is the instructions between (4096 tokens of 32 + 16 + 16 bf16 heads of
-// 128 into an e4m3 cache: 34.6 us, 3.4 TB/s; the bytes alone would take 17.6).
+// 128 into an e4m3 cache: 31.9 us, 3.7 TB/s; the bytes alone would take 17.6).
+// Angles whose lanes read 64 bytes apart cost 2.7 us more, two rows in flight
+// 2 us, CTAs that walk several tokens and look ahead 5 us (spilled registers).
 // One token takes 5.5 us, launch and two chained loads.
 template <typename X, bool kE4M3, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_append_kernel(const __grid_constant__ RopeArgs a)
