@@ -44,6 +44,7 @@
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
 #include "tc_ptx.cuh"
+#include "tree_shape.h"
 
 namespace wl {
 
@@ -53,8 +54,6 @@ constexpr int kTaThreads = 512;  // warps 0-7 softmax, 8 MMA (9-11 idle), 12-15 
 // each and the others keep 88 (256 x 168 + 256 x 88 = 512 x 128).
 constexpr int kTaRegsSoftmax = 168, kTaRegsOther = 88;
 static_assert(kTaRegsSoftmax + kTaRegsOther == 2 * 128, "register split");
-constexpr int kTaTile = 128;     // positions per tile
-constexpr int kTaFlush = 64;     // tiles summed in tensor memory before the sums move to fp32 partials
 constexpr float kTaNone = -3.0e38f;  // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -71,39 +70,6 @@ struct TaArgs {
     uint32_t group_inv;  // ceil(2^32 / group), 0 for 1
     float scale;
     CacheArgs c;
-};
-
-template <bool kE4M3, int DP, int RT>
-struct TaShape {
-    static constexpr int ES = kE4M3 ? 1 : 2;
-    static constexpr int PARTS = kE4M3 ? 2 : 1;
-    static constexpr int N = PARTS * RT;             // columns of both products
-    static constexpr int ROWB = DP * ES;             // bytes of a cache row
-    static constexpr int SLOTROW = ROWB < 256 ? ROWB : 256;
-    static constexpr int NS = ROWB / SLOTROW;        // ring slots per K or V tile
-    static constexpr int SLOT = kTaTile * SLOTROW;
-    static constexpr int QB = N * ROWB;
-    static constexpr int PW = 2 * RT;                // bytes of a position's weights
-    static constexpr int PB1 = kTaTile * PW, PB = kE4M3 ? PB1 : 2 * PB1;  // bf16: the weights, then their remainders
-    static constexpr int MISC = 3072;
-    static constexpr int ROOM = (232448 - MISC - QB - 2 * PB) / SLOT;
-    static constexpr int SLOTS = ROOM < 10 ? ROOM : 10;
-    static constexpr int SMEM = MISC + QB + 2 * PB + SLOTS * SLOT;
-    static constexpr int MT = DP / 128;              // M tiles of the second product
-    static constexpr bool PP = RT <= 32;             // each softmax warpgroup has tiles and sums of its own
-    static constexpr int USED = (2 + (PP ? 2 : 1) * MT) * N;  // two score buffers, the sums
-    static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    static constexpr int KSTEP = 32 / ES;            // contraction elements per MMA: 32 bytes of a K-major row
-    static constexpr int CW = PP ? RT : RT / 2;      // columns per softmax thread
-    // Exponents of weights: the limit, and how far below it a moved reference
-    // puts the largest weight.  e4m3 ends at 448, so the limit is 2^8, and the
-    // gap is precision lost for fewer moves (the two wide-tree
-    // cases above: 55 and 79 us with a gap of 3, 51 and 73 with 5, which
-    // leaves two bits less).  bf16 has range to spare.  kNear: a column that another column's
-    // move finds so near the limit moves along.
-    static constexpr float kTop = kE4M3 ? 8.0f : 64.0f, kGap = kE4M3 ? 3.0f : 64.0f, kNear = kE4M3 ? 2.0f : 0.0f;
-    static constexpr int SWP = PW == 128 ? 2 : PW == 64 ? 4 : 6;  // swizzle code of the weights' rows
-    static_assert(SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
 };
 
 // ---------------------------------------------------------------- helpers --
@@ -254,6 +220,11 @@ template <int n>
 __device__ __forceinline__ void bar_n(int id)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(n) : "memory");
+}
+template <int n>
+__device__ __forceinline__ void bar_arrive_n(int id)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(n) : "memory");
 }
 
 // Reduction of v[CW] over the warp: the result of column lane % CW.
@@ -419,13 +390,6 @@ __device__ __forceinline__ uint32_t ta_row(const CacheArgs &c, int page, int hk,
     return page < 0 || page >= c.npages ? ~0u : ((uint32_t)page * c.kv_heads + hk) * c.page_size + off;
 }
 
-// Place of K or V of a segment's tile r (of n) among its ring items, which go
-// K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1).
-__device__ __forceinline__ int ta_item(int r, int n, bool isv)
-{
-    return isv ? (r + 1 < n ? 2 * r + 2 : 2 * n - 1) : (r > 0 ? 2 * r - 1 : 0);
-}
-
 // ------------------------------------------------------------------ kernel --
 template <bool kE4M3, int DP, int RT>
 __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __grid_constant__ TaArgs a)
@@ -555,6 +519,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             // brings what its page holds beyond; what no box brings stays as
             // it was: scores there are masked, and the softmax warps zero
             // those rows of V.
+            // Z::PACED: where a segment ends, K waits until V's last boxes have
+            // been issued, and V until K has issued the boxes that come before
+            // V's next ones, so that the parity of an empty slot is that of the
+            // round before (barriers 4 and 5; the ring's order is the same, and
+            // neither waits for what the other would issue later).
             const bool isv = warp == 13;
             const CUtensorMap *map = isv ? &a.vmap : &a.kmap;
             const int runs = kTaTile / a.box;
@@ -566,6 +535,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 const int end = lane < runs ? min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile) : 0;
                 int j = w.tile * kTaTile + lane * a.box;
                 int pg = ta_page(c, w.b, j, end), pg1 = ta_page(c, w.b, j + kTaTile, end);
+                if (Z::PACED && isv) bar_n<64>(5);
+                if (Z::PACED && !isv && items > 0) bar_n<64>(4);
                 for (int r = 0; r < n; ++r, j += kTaTile) {
                     const uint32_t row = ta_row(c, pg, hk, j);
                     if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
@@ -594,9 +565,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         }
                         __syncwarp();
                     }
+                    if (Z::PACED && !isv && r == min(n, 2) - 1) bar_arrive_n<64>(5);
                 }
                 items += 2 * Z::NS * n;
                 ta_next(w, c, units);
+                if (Z::PACED && isv && w.left > 0) bar_arrive_n<64>(4);
             }
             item = items;
             // Boxes still in flight (only after a wait gave up) land before the CTA's shared memory goes.
