@@ -517,8 +517,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             // Boxes: warp 12 brings K, warp 13 V.  Lane r looks up run r of
             // a.box positions; one lane copies them all.  A run at the end
             // brings what its page holds beyond; what no box brings stays as
-            // it was: scores there are masked, and the softmax warps zero
-            // those rows of V.
+            // it was: scores there are masked, and the softmax warps zero the
+            // rows of V that a segment's last tile lacks.  A run whose page
+            // is not valid, which any tile may have, gets a box past V's last
+            // row, which brings zeros.
             // Z::PACED: where a segment ends, K waits until V's last boxes have
             // been issued, and V until K has issued the boxes that come before
             // V's next ones, so that the parity of an empty slot is that of the
@@ -529,6 +531,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             const int runs = kTaTile / a.box;
             const uint32_t bytes = (uint32_t)(a.box * Z::SLOTROW);
             uint32_t *tab = rowtab + isv * 64;
+            const uint32_t beyond = (uint32_t)(c.npages * c.kv_heads * c.page_size);  // below 2^31 where there are boxes
             int items = 0;
             while (w.left > 0) {
                 const int t1 = ta_end(w), n = t1 - w.tile, hk = w.u / a.rtiles;
@@ -538,8 +541,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 if (Z::PACED && isv) bar_n<64>(5);
                 if (Z::PACED && !isv && items > 0) bar_n<64>(4);
                 for (int r = 0; r < n; ++r, j += kTaTile) {
-                    const uint32_t row = ta_row(c, pg, hk, j);
-                    if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
+                    uint32_t row = ta_row(c, pg, hk, j);
+                    if (row == ~0u && pg != -2) {
+                        atomicOr(c.status, kStatusPage);
+                        if (isv) row = beyond;
+                    }
                     tab[(r & 1) * 32 + lane] = row;  // the other half may still be read
                     pg = pg1;
                     pg1 = ta_page(c, w.b, j + 2 * kTaTile, end);
@@ -970,8 +976,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                             *reinterpret_cast<uint4 *>(o1 + Z::PB1) = make_uint4(bl[4], bl[5], bl[6], bl[7]);
                         }
                     }
-                    if (__builtin_expect(a.box && !__all_sync(0xffffffffu, seen), 0)) {
+                    if (__builtin_expect(a.box && t + 1 == t1 && !__all_sync(0xffffffffu, seen), 0)) {
                         // rows of V that are not there: weight 0 must meet a number
+                        // (only in a last tile: of an earlier one the wait below
+                        // could take the round of its slot before for its own)
                         const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * ta_item(r, n, true);
                         for (int s = 0; s < Z::NS; ++s) {
                             const int vs = (v0 + s) % SLOTS;

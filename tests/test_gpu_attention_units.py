@@ -107,3 +107,25 @@ def test_blocks_with_units_of_one_length(wl, gpu, dtype, dim, n):
         B = len(lens)
         check(wl, cache, seqs, lens, _q(gpu, B, n, 8, dim, 3), which=range(0, B, 7 if B < 121 else 11), what=f"{lens[0]} x {B}")
     assert wl.wl_device_status() == wl.WL_OK
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 256), (BF, 128), (E4, 256), (E4, 64)])
+@pytest.mark.parametrize("n", [4, 8, 16])
+@pytest.mark.parametrize("page", [16, 128, 4])
+def test_pages_that_are_not_there_in_long_contexts(wl, gpu, dtype, dim, n, page):
+    """Positions of an invalid page, in any tile, are seen by no query, reach nothing else, and are reported."""
+    B, kv, G = 60, 4, 4
+    lens = [700 + 13 * b for b in range(B)]
+    cache, seqs = filled(wl, gpu, lens, n, kv, dim, page, dtype, seed=5)
+    gone = [(3 * b + 1) % (600 // page) for b in range(B)]
+    for b in range(B):
+        seqs.pages[b, gone[b]] = (-1, cache.pages, 1 << 30)[b % 3]
+
+    def see(b):
+        m = chain(lens, b, n, gpu)
+        m[:, gone[b] * page:(gone[b] + 1) * page] = False
+        return m
+
+    check(wl, cache, seqs, lens, _q(gpu, B, n, kv * G, dim, 4), see, what=f"{dtype} dim {dim} n {n} page {page}")
+    assert wl.wl_device_status() == wl.WL_ERR_INVALID_ARG
+    assert wl.wl_device_status() == wl.WL_OK

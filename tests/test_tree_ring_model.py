@@ -75,15 +75,32 @@ class Ring:
             self.head[1][at + order[(n, 0)][1] * ns] = at + order[(n, min(n, 2) - 1)][0] * ns + ns - 1
             at += 2 * n * ns
         self.items = at
+        # [item of V, items consumed once the scores of its tile are there, last tile of its segment]
+        self.values = []
+        at = 0
+        for n in lengths:
+            self.values += [(at + order[(n, r)][1] * ns + s, at + (order[(n, r)][0] + 1) * ns, r == n - 1) for r in range(n) for s in range(ns)]
+            at += 2 * n * ns
         assert sorted(self.mine[0] + self.mine[1]) == list(range(at))
 
-    def faults(self, slots, paced):
-        """Walks every reachable (K's place, V's place, items consumed)."""
+    def faults(self, slots, paced, look="none"):
+        """Walks every reachable (K's place, V's place, items consumed).
+
+        look: the tiles whose V a softmax warp waits for on its own, by the full barrier's parity, between its
+        scores and its weights (the MMA warp cannot take that V before): "none", a segment's "last", "all"."""
         bad, seen, todo = set(), {(0, 0, 0)}, [(0, 0, 0)]
         while todo:
             state = todo.pop()
             k, v, c = state
             nxt = []
+            for y, scored, last in self.values:
+                if look == "none" or (look == "last" and not last) or not scored <= c <= y:
+                    continue
+                # rounds of the slot that have landed: all consumed ones, or also the one in flight
+                issued = sum(i % slots == y % slots for i in self.mine[0][:k] + self.mine[1][:v])
+                for landed in {len(range(y % slots, c, slots)), issued}:
+                    if passes(landed, y // slots) and landed != y // slots + 1:
+                        bad.add(("takes another round for V", y))
             for w, place in ((0, k), (1, v)):
                 if place == len(self.mine[w]):
                     continue
@@ -135,3 +152,14 @@ def test_four_slots_of_two_an_operand(compiled, lengths):
     ring = Ring(compiled[1], lengths, 2)
     assert any(f[0] == "fills a slot in use" for f in ring.faults(4, False))
     assert not ring.faults(4, True)
+
+
+def test_waits_of_the_softmax_warps_for_v(compiled):
+    """They look at a last tile's V in every shape; at any tile's only where the ring holds three operands' slots."""
+    shapes, order = compiled
+    some = LENGTHS[:155:3] + LENGTHS[-3:]
+    for ring in {(z["slots"], z["ns"], z["paced"]) for z in shapes.values()}:
+        for lengths in some:
+            assert not Ring(order, lengths, ring[1]).faults(*(ring[0], ring[2]), look="last"), (ring, lengths)
+        wrong = any(Ring(order, lengths, ring[1]).faults(*(ring[0], ring[2]), look="all") for lengths in some)
+        assert wrong == (ring[0] < 3 * ring[1]), ring
