@@ -14,8 +14,10 @@
 //
 // e4m3 caches are multiplied without decoding.  The other operand keeps bf16's
 // 8 bits as two e4m3 parts side by side in N, x = hi + lo / 32: a bf16 number
-// is exactly two 4-bit parts, so q loses nothing but what lies 2^-22 below the
-// largest |q| of the tile.  The weights of v are folded with the row scales
+// is exactly two 4-bit parts, so an element of q loses nothing down to 2^-14 of
+// the largest that shares its power of two: that of the row tile, or of the row
+// where rows lie kTaSpread powers of two apart; below that it loses what lies
+// under 2^-22 of it.  The weights of v are folded with the row scales
 // (w = p * v_scale).  The largest weight of a row is 2^5 or more, the finest
 // step 2^-14: a weight keeps 8 bits down to 2^-11 of the largest, and what lies
 // below 2^-20 of it is dropped.  Every kTaFlush tiles the sums go to fp32 and
@@ -40,6 +42,7 @@
 // 8 of 39 to 61 tokens, 16 heads on 4, 3375 to 6000 positions: 77 us, 32 GFLOP.
 // One token on 1001 positions: 11.5 us and 6.5 us for the join, latency.
 #include <atomic>
+#include <type_traits>
 
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
@@ -54,6 +57,7 @@ constexpr int kTaThreads = 512;  // warps 0-7 softmax, 8 MMA (9-11 idle), 12-15 
 // each and the others keep 88 (256 x 168 + 256 x 88 = 512 x 128).
 constexpr int kTaRegsSoftmax = 168, kTaRegsOther = 88;
 static_assert(kTaRegsSoftmax + kTaRegsOther == 2 * 128, "register split");
+constexpr int kTaSpread = 4;       // powers of two between query rows from which on each has a scale of its own
 constexpr float kTaNone = -3.0e38f;  // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
              *pv_done = s_full + 6, *q_ready = s_full + 8, *drain = s_full + 9;
     uint32_t *tmem_hold = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_hold + 1);
-    static_assert((2 * SLOTS + 11) * 8 <= 1792 - 1536, "barriers");
+    uint8_t *qexp = reinterpret_cast<uint8_t *>(misc + Z::QEXP);     // [RT]
 
     const CacheArgs &c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -719,6 +723,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             fresh();
             // ---- the segment's queries: rows of the B operand
             float qscale = a.scale * kLog2e;
+            int spread = 0;  // where rows have exponents of their own (qexp): the one that qscale stands for
             {
                 // A lane has 8 elements of a row, a warp RPW rows at a time.
                 constexpr int CH = DP / 8, RPW = 32 / CH, PER = RT / (8 * RPW);
@@ -751,38 +756,85 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     }
                     smask[threadIdx.x] = m;
                 }
-                float up = 1.0f;
+                // e4m3: a power of two brings the largest |q| of the tile into
+                // [128, 256), and the parts keep 8 bits of what lies up to 2^14
+                // below it.  Where a row's largest lies 2^kTaSpread or more
+                // below the tile's, each row has a power of two of its own, and
+                // the scores take the difference back.
+                int be = 0;        // biased exponent of the tile's largest
                 bool odd = false;  // a NaN or an infinity among this lane's
                 if (kE4M3) {
-                    // one power of two brings the largest |q| of the tile into [128, 256)
-                    uint32_t two = 0;
+                    // largest |q|, and the least (less 1) that is not zero of the
+                    // largest in each 16 elements of a row, as bits of bf16
+                    uint32_t mx = 0, mn = ~0u;
 #pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        two = __vmaxu2(two, __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                                                     __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
-                    uint32_t amax = max(two & 0xffffu, two >> 16);
-                    odd = amax >= 0x7f80u;
-                    if (__builtin_expect(odd, 0)) {  // the largest of the others
-                        amax = 0;
+                    for (int i = 0; i < PER; i += 2) {
+                        uint32_t two[2] = {0u, 0u};  // two rows of 8 elements
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t h = (u[k / 2] >> (16 * (k & 1))) & 0x7fffu;
-                                amax = max(amax, h < 0x7f80u ? h : 0u);
+                        for (int k = 0; k < 2; ++k)
+                            if (i + k < PER) {
+                                const uint4 &v = raw[i + k < PER ? i + k : i];
+                                two[k] = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
                             }
-                        }
+                        uint32_t top = __vmaxu2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[0], two[1], 0x7632));
+                        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        const uint32_t a = top & 0xffffu, b = top >> 16;
+                        mx = max(mx, max(a, b));
+                        mn = min(mn, min(a - 1, b - 1));
                     }
-                    amax = __reduce_max_sync(0xffffffffu, amax);
-                    if (lane == 0) red[warp] = __uint_as_float(amax << 16);
-                    bar_n<256>(3);
-                    float mx = 0.0f;
+                    odd = mx >= 0x7f80u;
+                    // largest |element| of 8, as bits of bf16, but for NaN and infinity
+                    auto top8 = [](const uint4 &v) {
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t top = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, red[i]);
-                    const int be = max((int)(__float_as_uint(mx) >> 23), 14);
-                    up = __uint_as_float((uint32_t)(261 - be) << 23);  // 2^(134 - be)
-                    qscale *= __uint_as_float((uint32_t)(be - 7) << 23);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t h = (u[k / 2] >> (16 * (k & 1))) & 0x7fffu;
+                            top = max(top, h < 0x7f80u ? h : 0u);
+                        }
+                        return top;
+                    };
+                    if (__builtin_expect(odd, 0)) {  // the largest of the others
+                        mx = 0;
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) mx = max(mx, top8(raw[i]));
+                    }
+                    mx = __reduce_max_sync(0xffffffffu, mx);
+                    mn = __reduce_min_sync(0xffffffffu, mn);
+                    if (lane == 0) reinterpret_cast<uint2 *>(red)[warp] = make_uint2(mx, mn);
+                    bar_n<256>(3);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint2 o = reinterpret_cast<const uint2 *>(red)[i];
+                        mx = max(mx, o.x);
+                        mn = min(mn, o.y);
+                    }
+                    be = max((int)(mx >> 7), 14);
+                    auto least = [&]() { return min(max((int)((min(mn, 0x7f7eu) + 1) >> 7), 14), be); };
+                    // (no 16 elements far below the tile's largest: no row either)
+                    if (__builtin_expect(be - least() >= kTaSpread, 0)) {
+                        mn = ~0u;
+                        // once more row by row, from memory: it is rare, and what is unrolled here slows the rest
+#pragma unroll 1
+                        for (int i = 0; i < PER; ++i) {
+                            const int r = (i * 8 + warp) * RPW + lane / CH, off = where(r);
+                            uint32_t top = off >= 0 && d < c.dim ? top8(*reinterpret_cast<const uint4 *>(base + off)) : 0u;
+#pragma unroll 1
+                            for (int x = CH / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+                            if (ck == 0) qexp[r] = (uint8_t)max(top >> 7, 14u);
+                            mn = min(mn, top - 1);
+                        }
+                        mn = __reduce_min_sync(0xffffffffu, mn);
+                        bar_n<256>(3);
+                        if (lane == 0) reinterpret_cast<uint32_t *>(red)[warp] = mn;
+                        bar_n<256>(3);
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) mn = min(mn, reinterpret_cast<const uint32_t *>(red)[i]);
+                        // the common exponent: 2^7 if rows lie on both sides of it, so that
+                        // neither it nor a row's distance from it leaves fp32's range
+                        if (be - least() >= kTaSpread) spread = be = min(max(134, least()), be);
+                    }
+                    qscale *= __uint_as_float((uint32_t)(be - 7) << 23);  // 2^(be - 134)
                 }
                 // K-major rows of 128-byte chunks, 16-byte units swizzled by the row
                 char *o0 = sq + (kE4M3 ? (ck / 16) * (N * 128) + (ck & 1) * 8 : (ck / 8) * (N * 128));
@@ -795,6 +847,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     if (kE4M3) {
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                         uint32_t hi[4], lo[4];
+                        const float up = __uint_as_float((uint32_t)(261 - (spread ? qexp[r] : be)) << 23);  // brings the largest into [128, 256)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const __half2 x = __floats2half2_rn(bf_lo(u[k]) * up, bf_hi(u[k]) * up);  // exact: 8 bits, below 256
@@ -821,291 +874,314 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             const int slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
             const bool whole = t0 == 0 && t1 == w.ntiles;
             bool flushed = false, some = false;  // some: this warpgroup has sums in tensor memory
-            for (int t = t0; t < t1; ++t, ++it) {
-                if (!Z::PP || (it & 1) == wg) {
-                    const int j = t * kTaTile + tk;
-                    const bool seen = at != ~0u;
-                    const bool bad = vs != vs;
-                    const float v1 = fmaxf(vs, 1.17549435e-38f);
-                    // log2 of the scale: exponent exact, 0 for the mantissa of a power of two
-                    const float lv = bad ? vs : __log2f(v1), iv = bad ? 1.0f : rcp_approx(v1);
-                    const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv), iv2 = f2(iv, iv);
-                    at = ta_row(c, pg1, hk, j + STEP * kTaTile);
-                    ks = at != ~0u ? __ldg(c.k_scale + at) : 0.0f;
-                    vs = at != ~0u ? __ldg(c.v_scale + at) : 1.0f;
-                    pg1 = ta_page(c, w.b, j + 2 * STEP * kTaTile, end);
-                    ta_wait(&s_full[it & 1], (unsigned)((it >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                    tc_fence_after();
-                    const uint32_t sc = tmem + lanes + (it & 1) * N + col0;
-                    uint64_t y[CW / 2];
-                    {
-                        uint32_t x[CW], xl[kE4M3 ? CW : 16];
-                        tmem_get(sc, x);
-                        if (kE4M3) tmem_get(sc + RT, xl);
-                        // the weights' buffer is free once tile it - 2 has been multiplied
-                        if (it >= 2)
-                            ta_wait(&pv_done[it & 1], (unsigned)(((it - 2) >> 1) & 1), c.status, kWaitRingEmpty, abort_flag);
-                        tmem_got(x);
-                        if (kE4M3) tmem_got(xl);
-                        const uint64_t r32 = f2(0.03125f, 0.03125f);
-#pragma unroll
-                        for (int i = 0; i < CW / 2; ++i) {
-                            y[i] = u2(x[2 * i], x[2 * i + 1]);
-                            if (kE4M3) y[i] = fma2(u2(xl[2 * i], xl[2 * i + 1]), r32, y[i]);
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_empty[it & 1]);
-                    // y = x - m
-#pragma unroll
-                    for (int i = 0; i < CW / 2; ++i) y[i] = add2(fma2(y[i], cs2, lv2), *reinterpret_cast<const uint64_t *>(nm + 2 * i));
-                    if (__builtin_expect(!__all_sync(0xffffffffu, seen && j < w.len), 0)) {
-                        const int bit = j - w.len;
-#pragma unroll
-                        for (int i = 0; i < CW / 2; ++i) {
-                            float p = f2_lo(y[i]), q = f2_hi(y[i]);
-                            if (!seen || (bit >= 0 && !((smask[col0 + 2 * i] >> bit) & 1))) p = -INFINITY;
-                            if (!seen || (bit >= 0 && !((smask[col0 + 2 * i + 1] >> bit) & 1))) q = -INFINITY;
-                            y[i] = f2(p, q);
-                        }
-                    }
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < CW / 2; ++i) top = max3(top, f2_lo(y[i]), f2_hi(y[i]));
-                    // Weights up to 2^kTop stay as they are; only a position
-                    // above that moves its column's reference, to kGap below.
-                    if (__builtin_expect(bar_or<128>(1 + wg, top > Z::kTop || unset), 0)) {
+            // Two copies of the tile loop, as rows with exponents of their own
+            // are rare: a branch around the factors in a single loop took the
+            // second wide-tree case above from 76 to 80 us.
+            auto tiles = [&](auto own) {
+                constexpr bool kOwn = decltype(own)::value;
+                for (int t = t0; t < t1; ++t, ++it) {
+                    if (!Z::PP || (it & 1) == wg) {
+                        const int j = t * kTaTile + tk;
+                        const bool seen = at != ~0u;
+                        const bool bad = vs != vs;
+                        const float v1 = fmaxf(vs, 1.17549435e-38f);
+                        // log2 of the scale: exponent exact, 0 for the mantissa of a power of two
+                        const float lv = bad ? vs : __log2f(v1), iv = bad ? 1.0f : rcp_approx(v1);
+                        const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv), iv2 = f2(iv, iv);
+                        at = ta_row(c, pg1, hk, j + STEP * kTaTile);
+                        ks = at != ~0u ? __ldg(c.k_scale + at) : 0.0f;
+                        vs = at != ~0u ? __ldg(c.v_scale + at) : 1.0f;
+                        pg1 = ta_page(c, w.b, j + 2 * STEP * kTaTile, end);
+                        ta_wait(&s_full[it & 1], (unsigned)((it >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                        tc_fence_after();
+                        const uint32_t sc = tmem + lanes + (it & 1) * N + col0;
+                        uint64_t y[CW / 2];
                         {
-                            float v[CW];
+                            uint32_t x[CW], xl[kE4M3 ? CW : 16];
+                            tmem_get(sc, x);
+                            if (kE4M3) tmem_get(sc + RT, xl);
+                            // the weights' buffer is free once tile it - 2 has been multiplied
+                            if (it >= 2)
+                                ta_wait(&pv_done[it & 1], (unsigned)(((it - 2) >> 1) & 1), c.status, kWaitRingEmpty, abort_flag);
+                            tmem_got(x);
+                            if (kE4M3) tmem_got(xl);
+                            const uint64_t r32 = f2(0.03125f, 0.03125f);
 #pragma unroll
-                            for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(y[i]), v[2 * i + 1] = f2_hi(y[i]);
-                            const float cm = warp_columns<CW>(v, [](float p, float q) { return fmaxf(p, q); });
-                            if (lane < CW) wred[(warp & 3) * 32 + lane] = cm;
-                        }
-                        bar_n<128>(1 + wg);
-                        // one warp decides: how far each column's exponents move
-                        // (also those about to reach the limit), the factor of its sums
-                        if (tk < 32) {
-                            const float mx = lane < CW ? fmaxf(fmaxf(wred[lane], wred[32 + lane]), fmaxf(wred[64 + lane], wred[96 + lane])) : -INFINITY;
-                            const bool first = (unset >> lane) & 1 && mx > -INFINITY, move = first || mx > Z::kTop - Z::kNear;
-                            const uint32_t set = __ballot_sync(0xffffffffu, move);
-                            const float d = move ? Z::kTop - Z::kGap - mx : 0.0f;
-                            wred[lane] = d;
-                            wred[32 + lane] = first ? 1.0f : ex2(d);  // nothing to scale in a first one: its sums are zero
-                            if (move) nm[lane] += d;
-                            if (lane == 0) reinterpret_cast<uint2 *>(wred)[32] = make_uint2(unset & ~set, set);
-                        }
-                        bar_n<128>(1 + wg);
-                        const uint2 state = reinterpret_cast<const uint2 *>(wred)[32];
-                        unset = state.x;
-#pragma unroll
-                        for (int i = 0; i < CW; i += 8) {
-                            if (!((state.y >> i) & 0xffu)) continue;
-#pragma unroll
-                            for (int k = i / 2; k < i / 2 + 4; ++k) {
-                                y[k] = add2(y[k], *reinterpret_cast<const uint64_t *>(wred + 2 * k));
-                                l[k] = mul2(l[k], *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * k));
+                            for (int i = 0; i < CW / 2; ++i) {
+                                y[i] = u2(x[2 * i], x[2 * i + 1]);
+                                if (kE4M3) y[i] = fma2(u2(xl[2 * i], xl[2 * i + 1]), r32, y[i]);
                             }
                         }
-                        if (some) {
-                            if (!Z::PP) {  // (else the sums' last tile is it - 2: waited for above)
-                                ta_wait(&pv_done[(it - 1) & 1], (unsigned)(((it - 1) >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                                tc_fence_after();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_empty[it & 1]);
+                        if constexpr (kOwn) {
+#pragma unroll
+                            for (int i = 0; i < CW / 2; i += 2) {
+                                const uint32_t e = *reinterpret_cast<const uint32_t *>(qexp + col0 + 2 * i);
+                                auto f = [&](uint32_t own) { return (own + 127 - spread) << 23; };
+                                y[i] = mul2(y[i], u2(f(e & 0xffu), f(e >> 8 & 0xffu)));
+                                y[i + 1] = mul2(y[i + 1], u2(f(e >> 16 & 0xffu), f(e >> 24)));
                             }
-                            constexpr int P = Z::MT * Z::PARTS;
-#pragma unroll 1
+                        }
+                        // y = x - m
+#pragma unroll
+                        for (int i = 0; i < CW / 2; ++i) y[i] = add2(fma2(y[i], cs2, lv2), *reinterpret_cast<const uint64_t *>(nm + 2 * i));
+                        if (__builtin_expect(!__all_sync(0xffffffffu, seen && j < w.len), 0)) {
+                            const int bit = j - w.len;
+#pragma unroll
+                            for (int i = 0; i < CW / 2; ++i) {
+                                float p = f2_lo(y[i]), q = f2_hi(y[i]);
+                                if (!seen || (bit >= 0 && !((smask[col0 + 2 * i] >> bit) & 1))) p = -INFINITY;
+                                if (!seen || (bit >= 0 && !((smask[col0 + 2 * i + 1] >> bit) & 1))) q = -INFINITY;
+                                y[i] = f2(p, q);
+                            }
+                        }
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < CW / 2; ++i) top = max3(top, f2_lo(y[i]), f2_hi(y[i]));
+                        // Weights up to 2^kTop stay as they are; only a position
+                        // above that moves its column's reference, to kGap below.
+                        if (__builtin_expect(bar_or<128>(1 + wg, top > Z::kTop || unset), 0)) {
+                            {
+                                float v[CW];
+#pragma unroll
+                                for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(y[i]), v[2 * i + 1] = f2_hi(y[i]);
+                                const float cm = warp_columns<CW>(v, [](float p, float q) { return fmaxf(p, q); });
+                                if (lane < CW) wred[(warp & 3) * 32 + lane] = cm;
+                            }
+                            bar_n<128>(1 + wg);
+                            // one warp decides: how far each column's exponents move
+                            // (also those about to reach the limit), the factor of its sums
+                            if (tk < 32) {
+                                const float mx = lane < CW ? fmaxf(fmaxf(wred[lane], wred[32 + lane]), fmaxf(wred[64 + lane], wred[96 + lane])) : -INFINITY;
+                                const bool first = (unset >> lane) & 1 && mx > -INFINITY, move = first || mx > Z::kTop - Z::kNear;
+                                const uint32_t set = __ballot_sync(0xffffffffu, move);
+                                const float d = move ? Z::kTop - Z::kGap - mx : 0.0f;
+                                wred[lane] = d;
+                                wred[32 + lane] = first ? 1.0f : ex2(d);  // nothing to scale in a first one: its sums are zero
+                                if (move) nm[lane] += d;
+                                if (lane == 0) reinterpret_cast<uint2 *>(wred)[32] = make_uint2(unset & ~set, set);
+                            }
+                            bar_n<128>(1 + wg);
+                            const uint2 state = reinterpret_cast<const uint2 *>(wred)[32];
+                            unset = state.x;
+#pragma unroll
                             for (int i = 0; i < CW; i += 8) {
                                 if (!((state.y >> i) & 0xffu)) continue;
-                                const uint32_t ad = tmem + lanes + 2 * N + (Z::PP ? wg * Z::MT * N : 0) + col0 + i;
-                                uint32_t o[P][8];
-                                float f[8];
 #pragma unroll
-                                for (int p = 0; p < P; ++p) tmem_ld8_nw(ad + p * RT, o[p]);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) f[k] = wred[32 + i + k];
-#pragma unroll
-                                for (int p = 0; p < P; ++p) tmem_wait_ld8(o[p]);
-#pragma unroll
-                                for (int p = 0; p < P; ++p) {
-                                    float x[8];
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[p][k]) * f[k];
-                                    tmem_st8(ad + p * RT, x);
+                                for (int k = i / 2; k < i / 2 + 4; ++k) {
+                                    y[k] = add2(y[k], *reinterpret_cast<const uint64_t *>(wred + 2 * k));
+                                    l[k] = mul2(l[k], *reinterpret_cast<const uint64_t *>(wred + 32 + 2 * k));
                                 }
                             }
-                            tmem_wait_st();
+                            if (some) {
+                                if (!Z::PP) {  // (else the sums' last tile is it - 2: waited for above)
+                                    ta_wait(&pv_done[(it - 1) & 1], (unsigned)(((it - 1) >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                                    tc_fence_after();
+                                }
+                                constexpr int P = Z::MT * Z::PARTS;
+#pragma unroll 1
+                                for (int i = 0; i < CW; i += 8) {
+                                    if (!((state.y >> i) & 0xffu)) continue;
+                                    const uint32_t ad = tmem + lanes + 2 * N + (Z::PP ? wg * Z::MT * N : 0) + col0 + i;
+                                    uint32_t o[P][8];
+                                    float f[8];
+#pragma unroll
+                                    for (int p = 0; p < P; ++p) tmem_ld8_nw(ad + p * RT, o[p]);
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) f[k] = wred[32 + i + k];
+#pragma unroll
+                                    for (int p = 0; p < P; ++p) tmem_wait_ld8(o[p]);
+#pragma unroll
+                                    for (int p = 0; p < P; ++p) {
+                                        float x[8];
+#pragma unroll
+                                        for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[p][k]) * f[k];
+                                        tmem_st8(ad + p * RT, x);
+                                    }
+                                }
+                                tmem_wait_st();
+                            }
                         }
-                    }
-                    // weights: w = 2^(x - m) = p * v_scale
-                    char *pr = sp + (it & 1) * Z::PB;
-                    const uint32_t rowb = tk * Z::PW, sw = ((rowb >> 7) & (Z::PW / 16 - 1)) << 4;
+                        // weights: w = 2^(x - m) = p * v_scale
+                        char *pr = sp + (it & 1) * Z::PB;
+                        const uint32_t rowb = tk * Z::PW, sw = ((rowb >> 7) & (Z::PW / 16 - 1)) << 4;
 #pragma unroll
-                    for (int i = 0; i < CW; i += 16) {
-                        uint32_t hi[4], lo[4], bw[8], bl[8];
+                        for (int i = 0; i < CW; i += 16) {
+                            uint32_t hi[4], lo[4], bw[8], bl[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float p = ex2(f2_lo(y[i / 2 + k])), q = ex2(f2_hi(y[i / 2 + k]));
-                            l[i / 2 + k] = fma2(f2(p, q), iv2, l[i / 2 + k]);
-                            if constexpr (kE4M3) {
-                                // 11 bits of the weight, cut into 4 + 4
-                                const __half2 h = __floats2half2_rn(p, q);
-                                const uint32_t c8 = half2_e4m3(h);
-                                const __half2 rest = __hmul2(__hsub2(h, e4m3x2_half2(c8)), __float2half2_rn(32.0f));
-                                const uint32_t l8 = half2_e4m3(rest);
-                                if (k & 1) {
-                                    hi[k / 2] |= c8 << 16;
-                                    lo[k / 2] |= l8 << 16;
+                            for (int k = 0; k < 8; ++k) {
+                                const float p = ex2(f2_lo(y[i / 2 + k])), q = ex2(f2_hi(y[i / 2 + k]));
+                                l[i / 2 + k] = fma2(f2(p, q), iv2, l[i / 2 + k]);
+                                if constexpr (kE4M3) {
+                                    // 11 bits of the weight, cut into 4 + 4
+                                    const __half2 h = __floats2half2_rn(p, q);
+                                    const uint32_t c8 = half2_e4m3(h);
+                                    const __half2 rest = __hmul2(__hsub2(h, e4m3x2_half2(c8)), __float2half2_rn(32.0f));
+                                    const uint32_t l8 = half2_e4m3(rest);
+                                    if (k & 1) {
+                                        hi[k / 2] |= c8 << 16;
+                                        lo[k / 2] |= l8 << 16;
+                                    } else {
+                                        hi[k / 2] = c8;
+                                        lo[k / 2] = l8;
+                                    }
                                 } else {
-                                    hi[k / 2] = c8;
-                                    lo[k / 2] = l8;
+                                    bw[k] = bf16x2_bits(p, q);
+                                    bl[k] = bf16x2_bits(p - bf_lo(bw[k]), q - bf_hi(bw[k]));
+                                }
+                            }
+                            if constexpr (kE4M3) {
+                                *reinterpret_cast<uint4 *>(pr + ((rowb + col0 + i) ^ sw)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                *reinterpret_cast<uint4 *>(pr + ((rowb + RT + col0 + i) ^ sw)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            } else {
+                                char *o0 = pr + ((rowb + 2 * (col0 + i)) ^ sw), *o1 = pr + ((rowb + 2 * (col0 + i) + 16) ^ sw);
+                                *reinterpret_cast<uint4 *>(o0) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
+                                *reinterpret_cast<uint4 *>(o1) = make_uint4(bw[4], bw[5], bw[6], bw[7]);
+                                *reinterpret_cast<uint4 *>(o0 + Z::PB1) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
+                                *reinterpret_cast<uint4 *>(o1 + Z::PB1) = make_uint4(bl[4], bl[5], bl[6], bl[7]);
+                            }
+                        }
+                        if (__builtin_expect(a.box && t + 1 == t1 && !__all_sync(0xffffffffu, seen), 0)) {
+                            // rows of V that are not there: weight 0 must meet a number
+                            // (only in a last tile: of an earlier one the wait below
+                            // could take the round of its slot before for its own)
+                            const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * ta_item(r, n, true);
+                            for (int s = 0; s < Z::NS; ++s) {
+                                const int vs = (v0 + s) % SLOTS;
+                                ta_wait(&full[vs], (unsigned)(((v0 + s) / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
+                                if (!seen && (Z::PP || wg == 0))
+                                    for (int h = 0; h < Z::SLOTROW / 16; ++h)
+                                        *reinterpret_cast<uint4 *>(ring + vs * Z::SLOT + (h / 8) * (kTaTile * 128) + tk * 128 + (h % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        some = true;
+                        fence_async_smem();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[it & 1]);
+                    }
+                    const bool last = t + 1 == t1;
+                    if (!last && (t + 1 - t0) % kTaFlush != 0) continue;
+                    // ---- the sums leave tensor memory
+                    {
+                        float v[CW];
+#pragma unroll
+                        for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(l[i]), v[2 * i + 1] = f2_hi(l[i]);
+                        const float ls = warp_columns<CW>(v, [](float p, float q) { return p + q; });
+                        bar_n<128>(1 + wg);  // the last event's factors have been read
+                        if (lane < CW) wred[(warp & 3) * CW + lane] = ls;
+                        if (tk < CW && (unset >> tk) & 1) nm[tk] = -kTaNone;
+                        const int own = it - (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's last tile, if it had one
+                        if (some) ta_wait(&pv_done[own & 1], (unsigned)((own >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                        tc_fence_after();
+                        bar_n<256>(3);
+                        float top_r = kTaNone, sum = 0.0f;
+                        if ((int)threadIdx.x < rows) {
+                            const int r = threadIdx.x;
+                            float f[3] = {1.0f, 0.0f, 0.0f};
+                            auto side = [&](int g, int col, float &mr, float &sr) {
+                                const float *o = red + g * 128;
+                                mr = -nms[g * 32 + col];
+                                sr = (o[col] + o[CW + col]) + (o[2 * CW + col] + o[3 * CW + col]);
+                            };
+                            if (Z::PP) {
+                                float m0, m1, s0, s1;
+                                side(0, r, m0, s0);
+                                side(1, r, m1, s1);
+                                top_r = fmaxf(m0, m1);
+                                f[0] = ex2(m0 - top_r);
+                                f[1] = ex2(m1 - top_r);
+                                sum = s0 * f[0] + s1 * f[1];
+                            } else {
+                                side(r / CW, r % CW, top_r, sum);
+                            }
+                            if (flushed) {
+                                const float2 o = a.ml[(int64_t)slot * RT + r];
+                                const float mm = fmaxf(o.x, top_r), g = ex2(top_r - mm);
+                                f[2] = ex2(o.x - mm);
+                                f[0] *= g, f[1] *= g;
+                                sum = sum * g + o.y * f[2];
+                                top_r = mm;
+                            }
+                            if (last && whole) {
+                                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                                for (int k = 0; k < 3; ++k) f[k] *= inv;
+                            } else {
+                                a.ml[(int64_t)slot * RT + r] = make_float2(top_r, sum);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) fac[k * 64 + r] = f[k];
+                        }
+                        bar_n<256>(3);
+                        // which streams have sums: in a segment of one tile only one has
+                        const int blk = (t - t0) % kTaFlush;  // tiles since the last flush, less one
+                        const bool both = blk > 0;
+                        const int lone = it & 1;
+#pragma unroll 1
+                        for (int q = wg; q < (RT / 16) * Z::MT; q += 2) {
+                            const int i = (q % (RT / 16)) * 16, mt = q / (RT / 16), d = mt * 128 + tk;
+                            if (i >= rows) continue;
+                            float v[16] = {};
+                            const int g0 = Z::PP && !both ? lone : 0, g1 = Z::PP && both ? 2 : g0 + 1;
+#pragma unroll 1
+                            for (int g = g0; g < g1; ++g) {
+                                const uint32_t ad = tmem + lanes + 2 * N + (g * Z::MT + mt) * N + i;
+                                uint32_t o[16], ol[16];
+                                tmem_get(ad, o);
+                                if (kE4M3) tmem_get(ad + RT, ol);
+                                float f[16];
+                                load16(fac + g * 64 + i, f);
+                                tmem_got(o);
+                                if (kE4M3) tmem_got(ol);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    float x = __uint_as_float(o[k]);
+                                    if (kE4M3) x = fmaf(__uint_as_float(ol[k]), 0.03125f, x);
+                                    v[k] = fmaf(x, f[k], v[k]);
+                                }
+                            }
+                            if (d >= c.dim) continue;
+                            const int nr = min(16, rows - i);
+                            float *pd = a.part + ((int64_t)slot * RT + i) * DP + d;
+                            if (flushed) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (k < nr) v[k] = fmaf(pd[k * DP], fac[128 + i + k], v[k]);
+                            }
+                            if (last && whole) {
+                                int tok = ta_token(a, row0 + i), gi = row0 + i - tok * a.group;
+                                bf16 *po = a.out + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + gi) * c.dim + d;
+                                const int64_t jump = (int64_t)(a.q_heads - a.group) * c.dim;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    if (k < nr) *po = __float2bfloat16_rn(tok < w.cnt ? v[k] : 0.0f);
+                                    po += c.dim;
+                                    if (++gi == a.group) gi = 0, ++tok, po += jump;
                                 }
                             } else {
-                                bw[k] = bf16x2_bits(p, q);
-                                bl[k] = bf16x2_bits(p - bf_lo(bw[k]), q - bf_hi(bw[k]));
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (k < nr) pd[k * DP] = v[k];
                             }
                         }
-                        if constexpr (kE4M3) {
-                            *reinterpret_cast<uint4 *>(pr + ((rowb + col0 + i) ^ sw)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4 *>(pr + ((rowb + RT + col0 + i) ^ sw)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        } else {
-                            char *o0 = pr + ((rowb + 2 * (col0 + i)) ^ sw), *o1 = pr + ((rowb + 2 * (col0 + i) + 16) ^ sw);
-                            *reinterpret_cast<uint4 *>(o0) = make_uint4(bw[0], bw[1], bw[2], bw[3]);
-                            *reinterpret_cast<uint4 *>(o1) = make_uint4(bw[4], bw[5], bw[6], bw[7]);
-                            *reinterpret_cast<uint4 *>(o0 + Z::PB1) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
-                            *reinterpret_cast<uint4 *>(o1 + Z::PB1) = make_uint4(bl[4], bl[5], bl[6], bl[7]);
-                        }
+                        tc_fence_before();
+                        flushed = true;
+                        some = false;
+                        fresh();
+                        bar_n<256>(3);  // factors, masks and sums may be overwritten
                     }
-                    if (__builtin_expect(a.box && t + 1 == t1 && !__all_sync(0xffffffffu, seen), 0)) {
-                        // rows of V that are not there: weight 0 must meet a number
-                        // (only in a last tile: of an earlier one the wait below
-                        // could take the round of its slot before for its own)
-                        const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * ta_item(r, n, true);
-                        for (int s = 0; s < Z::NS; ++s) {
-                            const int vs = (v0 + s) % SLOTS;
-                            ta_wait(&full[vs], (unsigned)(((v0 + s) / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
-                            if (!seen && (Z::PP || wg == 0))
-                                for (int h = 0; h < Z::SLOTROW / 16; ++h)
-                                    *reinterpret_cast<uint4 *>(ring + vs * Z::SLOT + (h / 8) * (kTaTile * 128) + tk * 128 + (h % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    some = true;
-                    fence_async_smem();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[it & 1]);
                 }
-                const bool last = t + 1 == t1;
-                if (!last && (t + 1 - t0) % kTaFlush != 0) continue;
-                // ---- the sums leave tensor memory
-                {
-                    float v[CW];
-#pragma unroll
-                    for (int i = 0; i < CW / 2; ++i) v[2 * i] = f2_lo(l[i]), v[2 * i + 1] = f2_hi(l[i]);
-                    const float ls = warp_columns<CW>(v, [](float p, float q) { return p + q; });
-                    bar_n<128>(1 + wg);  // the last event's factors have been read
-                    if (lane < CW) wred[(warp & 3) * CW + lane] = ls;
-                    if (tk < CW && (unset >> tk) & 1) nm[tk] = -kTaNone;
-                    const int own = it - (Z::PP ? (it ^ wg) & 1 : 0);  // this warpgroup's last tile, if it had one
-                    if (some) ta_wait(&pv_done[own & 1], (unsigned)((own >> 1) & 1), c.status, kWaitRingFull, abort_flag);
-                    tc_fence_after();
-                    bar_n<256>(3);
-                    float top_r = kTaNone, sum = 0.0f;
-                    if ((int)threadIdx.x < rows) {
-                        const int r = threadIdx.x;
-                        float f[3] = {1.0f, 0.0f, 0.0f};
-                        auto side = [&](int g, int col, float &mr, float &sr) {
-                            const float *o = red + g * 128;
-                            mr = -nms[g * 32 + col];
-                            sr = (o[col] + o[CW + col]) + (o[2 * CW + col] + o[3 * CW + col]);
-                        };
-                        if (Z::PP) {
-                            float m0, m1, s0, s1;
-                            side(0, r, m0, s0);
-                            side(1, r, m1, s1);
-                            top_r = fmaxf(m0, m1);
-                            f[0] = ex2(m0 - top_r);
-                            f[1] = ex2(m1 - top_r);
-                            sum = s0 * f[0] + s1 * f[1];
-                        } else {
-                            side(r / CW, r % CW, top_r, sum);
-                        }
-                        if (flushed) {
-                            const float2 o = a.ml[(int64_t)slot * RT + r];
-                            const float mm = fmaxf(o.x, top_r), g = ex2(top_r - mm);
-                            f[2] = ex2(o.x - mm);
-                            f[0] *= g, f[1] *= g;
-                            sum = sum * g + o.y * f[2];
-                            top_r = mm;
-                        }
-                        if (last && whole) {
-                            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) f[k] *= inv;
-                        } else {
-                            a.ml[(int64_t)slot * RT + r] = make_float2(top_r, sum);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) fac[k * 64 + r] = f[k];
-                    }
-                    bar_n<256>(3);
-                    // which streams have sums: in a segment of one tile only one has
-                    const int blk = (t - t0) % kTaFlush;  // tiles since the last flush, less one
-                    const bool both = blk > 0;
-                    const int lone = it & 1;
-#pragma unroll 1
-                    for (int q = wg; q < (RT / 16) * Z::MT; q += 2) {
-                        const int i = (q % (RT / 16)) * 16, mt = q / (RT / 16), d = mt * 128 + tk;
-                        if (i >= rows) continue;
-                        float v[16] = {};
-                        const int g0 = Z::PP && !both ? lone : 0, g1 = Z::PP && both ? 2 : g0 + 1;
-#pragma unroll 1
-                        for (int g = g0; g < g1; ++g) {
-                            const uint32_t ad = tmem + lanes + 2 * N + (g * Z::MT + mt) * N + i;
-                            uint32_t o[16], ol[16];
-                            tmem_get(ad, o);
-                            if (kE4M3) tmem_get(ad + RT, ol);
-                            float f[16];
-                            load16(fac + g * 64 + i, f);
-                            tmem_got(o);
-                            if (kE4M3) tmem_got(ol);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                float x = __uint_as_float(o[k]);
-                                if (kE4M3) x = fmaf(__uint_as_float(ol[k]), 0.03125f, x);
-                                v[k] = fmaf(x, f[k], v[k]);
-                            }
-                        }
-                        if (d >= c.dim) continue;
-                        const int nr = min(16, rows - i);
-                        float *pd = a.part + ((int64_t)slot * RT + i) * DP + d;
-                        if (flushed) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (k < nr) v[k] = fmaf(pd[k * DP], fac[128 + i + k], v[k]);
-                        }
-                        if (last && whole) {
-                            int tok = ta_token(a, row0 + i), gi = row0 + i - tok * a.group;
-                            bf16 *po = a.out + (((int64_t)w.b * c.n + tok) * a.q_heads + hk * a.group + gi) * c.dim + d;
-                            const int64_t jump = (int64_t)(a.q_heads - a.group) * c.dim;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                if (k < nr) *po = __float2bfloat16_rn(tok < w.cnt ? v[k] : 0.0f);
-                                po += c.dim;
-                                if (++gi == a.group) gi = 0, ++tok, po += jump;
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (k < nr) pd[k * DP] = v[k];
-                        }
-                    }
-                    tc_fence_before();
-                    flushed = true;
-                    some = false;
-                    fresh();
-                    bar_n<256>(3);  // factors, masks and sums may be overwritten
-                }
+            };
+            if constexpr (kE4M3) {
+                if (__builtin_expect(spread, 0))
+                    tiles(std::true_type{});
+                else
+                    tiles(std::false_type{});
+            } else {
+                tiles(std::false_type{});
             }
             if (threadIdx.x == 0 && t0 == 0 && !whole) {
                 // (the place of the unit's last tile, and the cost of all)

@@ -19,9 +19,12 @@ struct TaShape {
     static constexpr int QB = N * ROWB;
     static constexpr int PW = 2 * RT;                // bytes of a position's weights
     static constexpr int PB1 = kTaTile * PW, PB = kE4M3 ? PB1 : 2 * PB1;  // bf16: the weights, then their remainders
-    static constexpr int MISC = 3072;
-    static constexpr int ROOM = (232448 - MISC - QB - 2 * PB) / SLOT;
+    static constexpr int ROOM = (232448 - 3072 - QB - 2 * PB) / SLOT;
     static constexpr int SLOTS = ROOM < 10 ? ROOM : 10;
+    // e4m3: an exponent for each row, behind the barriers where a small ring
+    // leaves room there (and none elsewhere)
+    static constexpr int QEXP = SLOTS < 10 ? 1728 : 3072;
+    static constexpr int MISC = SLOTS < 10 ? 3072 : 3136;
     static constexpr int SMEM = MISC + QB + 2 * PB + SLOTS * SLOT;
     static constexpr int MT = DP / 128;              // M tiles of the second product
     static constexpr bool PP = RT <= 32;             // each softmax warpgroup has tiles and sums of its own
@@ -45,6 +48,7 @@ struct TaShape {
     // of a warp's items to its next is 2 NS + 1, at a change of segment, so a
     // ring of fewer slots has its warps keep in step there.
     static constexpr bool PACED = SLOTS < 2 * NS + 1;
+    static_assert((2 * SLOTS + 11) * 8 <= (SLOTS < 10 ? QEXP : 1792) - 1536, "barriers");
     static_assert(SLOTS >= 2 * NS && SLOTS >= 4 && SMEM <= 232448 && USED <= 512 && RT % 16 == 0, "tile shape");
 };
 

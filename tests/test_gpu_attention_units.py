@@ -71,6 +71,7 @@ def chain(lens, b, n, dev):
 
 
 def check(wl, cache, seqs, lens, q, see=None, which=None, what=""):
+    """The call against the formula, and against itself."""
     out = wl.wl_tree_attention(q, cache, seqs)
     again = wl.wl_tree_attention(q, cache, seqs)
     for b in which if which is not None else range(len(lens)):
