@@ -301,8 +301,9 @@ void wl_stack_destroy(wl_stack stack);
  *     max|row| <= 448 * 2^e (1 for a row of zeros).  A power of two loses
  *     nothing against max/448: the codes keep their 4 significant bits.
  *   WL_CACHE_BF16: codes are the values rounded to bf16, the scale is 1.
- *   A row with a NaN or an infinity is stored as codes 0 and scale NaN: all of
- *     it reads back as NaN, and only queries that see it become NaN.
+ *   A row with a NaN or an infinity (bf16: also one with a value that rounds to
+ *     an infinity) is stored as codes 0 and scale NaN: all of it reads back as
+ *     NaN, and only queries that see it become NaN.
  */
 typedef enum { WL_CACHE_E4M3 = 0, WL_CACHE_BF16 = 1 } wl_cache_format;
 

@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(X) == 2 ? 4 : 2) rope_app
                 for (int d = w / 2; d > 0; d >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
                 if (on && r >= a.q_heads && at0 >= 0) {
                     const int64_t at = at0 + (int64_t)(isv ? r - first_v : r - a.q_heads) * c.page_size;
-                    const bool bad = amax >= 0x7f800000u;  // a NaN or an infinity in the row
+                    // a NaN or an infinity in the row, or what rounds to an infinity of bf16
+                    const bool bad = amax >= (kE4M3 ? 0x7f800000u : 0x7f7f8000u);
                     float scale = 1.0f;
                     if (kE4M3 && !bad) {
                         const int e = row_exponent(amax);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import wl_synth
-from tests.test_gpu_attention_units import check, filled
+from tests.test_gpu_attention_units import check, filled, formula
 
 pytestmark = pytest.mark.gpu
 E4, BF = torch.float8_e4m3fn, torch.bfloat16
@@ -25,3 +25,38 @@ def test_query_rows_of_very_different_sizes(wl, gpu, dtype, dim, n, group):
         q[1, 0, -1] = 0.0
         check(wl, cache, seqs, lens, q.to(gpu), what=f"{dtype} dim {dim} n {n} sizes {sizes}")
     assert wl.wl_device_status() == wl.WL_OK
+
+
+@pytest.mark.parametrize("dtype", [E4, BF])
+def test_values_that_round_to_an_infinity(wl, gpu, dtype):
+    """A finite value beyond the cache's type marks its row as one with an infinity: only queries that see it know."""
+    edge = 3.3961776e38  # halfway from the largest bf16 number to the next power of two: rounds up
+    cache = wl.KVCache.empty(4, 1, 16, 64, dtype, gpu)
+    z = dict(dtype=torch.int32, device=gpu)
+    seqs = wl.CacheSeqs(torch.arange(4, **z)[None], torch.zeros(1, **z), 40)
+    k, v = (torch.randn(40, 64, generator=wl_synth.make_generator(i)) for i in (1, 2))
+    v[38, 5], k[39, 7] = edge, -edge
+    v[37, 9] = 3.3895e38  # below the middle: the largest bf16 number
+    wl.wl_rope_append(None, k.to(gpu), v.to(gpu), None, None, cache, seqs)
+    kk, vv = wl.wl_cache_read(cache, seqs, dt=torch.float32)
+    scales = torch.stack((cache.k_scale, cache.v_scale)).view(2, -1).cpu()
+    if dtype == BF:
+        assert not torch.isinf(kk).any() and not torch.isinf(vv).any()
+        assert torch.isnan(scales).nonzero().tolist() == [[0, 39], [1, 38]]
+        assert torch.isnan(kk[0, 39]).all() and torch.isnan(vv[0, 38]).all() and float(vv[0, 37, 0, 9]) == float(torch.finfo(BF).max)
+    else:  # codes hold such values; reading them back may pass the type's range
+        assert torch.isfinite(scales[:, :40]).all()
+    # tokens that see neither row: a result as without them
+    seqs = wl.CacheSeqs(seqs.pages, torch.full((1,), 30, **z), 10)
+    q = torch.randn(1, 10, 2, 64, generator=wl_synth.make_generator(3)).to(BF).to(gpu)
+    mask = torch.tensor([[1 << i for i in range(10)]], dtype=torch.int64, device=gpu)
+    out = wl.wl_tree_attention(q, cache, seqs, mask=mask)
+    cache.v_scale[2, 0, 5:8], cache.k_scale[2, 0, 5:8] = 1.0, 1.0
+    for x in (cache.k, cache.v):
+        x.view(torch.uint8)[2, 0, 5:8] = 0
+    see = torch.arange(40, device=gpu)[None] < 30
+    see = see | (torch.arange(40, device=gpu)[None] == 30 + torch.arange(10, device=gpu)[:, None])
+    want, bound = formula(cache, seqs, q, 0, see, 64 ** -0.5)
+    assert bool(((out[0, :7].double() - want[:7]).abs() <= bound[:7]).all())
+    if dtype == BF:
+        assert torch.isnan(out[0, 8:]).all()
