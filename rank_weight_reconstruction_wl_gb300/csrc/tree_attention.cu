@@ -58,6 +58,7 @@ constexpr int kTaThreads = 512;  // warps 0-7 softmax, 8 MMA (9-11 idle), 12-15 
 constexpr int kTaRegsSoftmax = 168, kTaRegsOther = 88;
 static_assert(kTaRegsSoftmax + kTaRegsOther == 2 * 128, "register split");
 constexpr int kTaSpread = 4;       // powers of two between query rows from which on each has a scale of its own
+constexpr float kTaZero = 64.0f;    // scale of a row of zeros in v, as far as weights go: 2^-kTaZero
 constexpr float kTaNone = -3.0e38f;  // reference of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -890,7 +891,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         // of 2^-20.  (The exponent apart, exactly: 76.8 us instead of 76.0 in the second
                         // wide-tree case.)
                         const float lv = bad ? vs : __log2f(v1), iv = bad ? 1.0f : rcp_approx(v1);
-                        const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv), iv2 = f2(iv, iv);
+                        const uint64_t cs2 = f2(ks * qscale, ks * qscale), lv2 = f2(lv, lv);
+                        uint64_t iv2 = f2(iv, iv);
                         at = ta_row(c, pg1, hk, j + STEP * kTaTile);
                         ks = at != ~0u ? __ldg(c.k_scale + at) : 0.0f;
                         vs = at != ~0u ? __ldg(c.v_scale + at) : 1.0f;
@@ -930,7 +932,28 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         // y = x - m
 #pragma unroll
                         for (int i = 0; i < CW / 2; ++i) y[i] = add2(fma2(y[i], cs2, lv2), *reinterpret_cast<const uint64_t *>(nm + 2 * i));
-                        if (__builtin_expect(!__all_sync(0xffffffffu, seen && j < w.len), 0)) {
+                        if (__builtin_expect(!__all_sync(0xffffffffu, seen && j < w.len && (!kE4M3 || iv != 1.0f)), 0)) {
+                            if (kE4M3 && __any_sync(0xffffffffu, seen && iv == 1.0f)) {
+                                // A row of zeros has scale 1, which may lie far above the others': its
+                                // weight, which V's product does not need, would take their bits.  It
+                                // counts as if its scale were 2^-kTaZero.  (The wait is sound in any tile:
+                                // an operand is one slot of at least three.)
+                                static_assert(!kE4M3 || (Z::NS == 1 && SLOTS >= 3), "a wait for V");
+                                const int v0 = items + ta_item(t - t0, t1 - t0, true), slot = v0 % SLOTS;
+                                ta_wait(&full[slot], (unsigned)((v0 / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
+                                const char *row = ring + slot * Z::SLOT + tk * 128;
+                                bool zero = seen && iv == 1.0f;
+#pragma unroll 1
+                                for (int h = 0; zero && h < Z::SLOTROW / 16; ++h) {
+                                    const uint4 u = *reinterpret_cast<const uint4 *>(row + (h / 8) * (kTaTile * 128) + (((h ^ tk) & 7) << 4));
+                                    zero = ((u.x | u.y | u.z | u.w) & 0x7f7f7f7fu) == 0;
+                                }
+                                __syncwarp();
+                                const uint64_t less = f2(zero ? -kTaZero : 0.0f, zero ? -kTaZero : 0.0f);
+#pragma unroll
+                                for (int i = 0; i < CW / 2; ++i) y[i] = add2(y[i], less);
+                                if (zero) iv2 = f2(exp2_int((int)kTaZero), exp2_int((int)kTaZero));
+                            }
                             const int bit = j - w.len;
 #pragma unroll
                             for (int i = 0; i < CW / 2; ++i) {

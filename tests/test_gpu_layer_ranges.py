@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import wl_synth
-from tests.test_gpu_attention_units import check, filled, formula
+from tests.test_gpu_attention_units import chain, check, filled, formula
 
 pytestmark = pytest.mark.gpu
 E4, BF = torch.float8_e4m3fn, torch.bfloat16
@@ -60,3 +60,45 @@ def test_values_that_round_to_an_infinity(wl, gpu, dtype):
     assert bool(((out[0, :7].double() - want[:7]).abs() <= bound[:7]).all())
     if dtype == BF:
         assert torch.isnan(out[0, 8:]).all()
+
+
+def test_rows_of_zeros_in_v_weigh_nothing(wl, gpu):
+    """A row of zeros has scale 1, far above a small row's: heavy scores on it must not take the others' bits."""
+    for dim, n, group in ((64, 1, 2), (128, 6, 4), (256, 1, 4), (256, 20, 4)):
+        lens = [900, 3000]
+        cache, seqs = filled(wl, gpu, lens, n, 1, dim, 16, E4, seed=dim)
+        rows = cache.v_scale
+        rows.mul_(2.0 ** -12)  # values of about 2^-12
+        q = torch.ones(2, n, group, dim, dtype=BF, device=gpu)
+        for b in range(2):
+            for j in (0, 5, 133, 260, 513):
+                p, t = int(seqs.pages[b, j // 16]), j % 16
+                cache.v.view(torch.uint8)[p, 0, t] = 0x80 if j == 5 else 0
+                rows[p, 0, t] = 1.0
+                cache.k.view(torch.uint8)[p, 0, t] = 0x38  # ones
+                cache.k_scale[p, 0, t] = 1.0
+        # a score of 16 on the rows of zeros, small ones elsewhere (k has both signs)
+        scale = 16.0 / dim
+        out = wl.wl_tree_attention(q, cache, seqs, scale=scale)
+        for b in range(2):
+            want, bound = formula(cache, seqs, q, b, chain(lens, b, n, gpu), scale)
+            worst = float(((out[b].double() - want).abs() / bound).max())
+            assert worst <= 1, f"dim {dim} n {n} sequence {b}: {worst:.3g} times the bound"
+            assert float((want.abs() / bound).median()) > 2  # the bound tells the result from none
+    assert wl.wl_device_status() == wl.WL_OK
+
+
+def test_all_of_v_zero_and_large_rows_of_scale_one(wl, gpu):
+    lens, n, dim = [300, 40], 3, 128
+    cache, seqs = filled(wl, gpu, lens, n, 2, dim, 16, E4, seed=1)
+    q = torch.randn(2, n, 4, dim, generator=wl_synth.make_generator(1)).to(BF).to(gpu)
+    live = ~torch.isnan(cache.v_scale)
+    cache.v_scale[live] = 1.0  # codes up to 448, as they are
+    check(wl, cache, seqs, lens, q, what="scale 1")
+    cache.v.view(torch.uint8)[live] = 0
+    out = wl.wl_tree_attention(q, cache, seqs)
+    assert bool((out == 0).all())
+    half = live.clone()
+    half[:, :, 8:] = False
+    cache.v.view(torch.uint8)[half] = 0x01  # the smallest code alone
+    check(wl, cache, seqs, lens, q, what="smallest codes")
