@@ -253,26 +253,31 @@ __device__ __forceinline__ float warp_columns(float (&v)[CW], Op op)
     return v[0];
 }
 
-// A bounded wait that gives up at once when the CTA is winding down.  A wait
-// that gives up sets the abort flag; every role then runs through its loops
-// without waiting, copying or issuing, so barriers stay matched.
-__device__ __forceinline__ void ta_wait(uint64_t *bar, unsigned parity, unsigned *status, unsigned site, volatile int *abort_flag)
+// A bounded wait that gives up at once when the CTA is winding down; true if
+// what it waits for has come.  A wait that gives up sets the abort flag.  Every
+// role then runs through its loops, so that barriers of threads stay matched,
+// but a role whose wait gave up copies, multiplies and signals no more: a ring
+// slot's barriers go on telling the truth, and what is still in flight can be
+// waited for at the end.  (Softmax warps go on; what they write is in bounds.)
+__device__ __forceinline__ bool ta_wait(uint64_t *bar, unsigned parity, unsigned *status, unsigned site, volatile int *abort_flag)
 {
-    if (mbar_test(bar, parity)) return;
+    if (mbar_test(bar, parity)) return true;
     const long long t0 = wait_clock();
-    while (!*abort_flag && !mbar_test(bar, parity)) {
+    while (!*abort_flag) {
+        if (mbar_test(bar, parity)) return true;
         if (wait_clock() - t0 > kWaitLimitCycles) {
             atomicOr(status, kStatusTimeout | site);
             *abort_flag = 1;
         }
     }
+    return false;
 }
 
-// The last wait, for MMAs in flight, also when the CTA is winding down.
-__device__ __forceinline__ void ta_drain(uint64_t *bar, unsigned *status)
+// A last wait, for MMAs or copies in flight, also when the CTA is winding down.
+__device__ __forceinline__ void ta_drain(uint64_t *bar, unsigned parity, unsigned *status)
 {
     const long long t0 = wait_clock();
-    while (!mbar_test(bar, 0)) {
+    while (!mbar_test(bar, parity)) {
         if (wait_clock() - t0 > kWaitLimitCycles) {
             atomicOr(status, kStatusTimeout | kWaitDrain);
             return;
@@ -464,6 +469,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
         // row: no copy waits for a lookup.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTaRegsOther));
         int item = 0;
+        bool live = true;  // no wait has given up
         if (a.box == 0) {
             // 16-byte copies: warp pw takes rows 32 pw .. of a tile; zeros
             // where there is no row
@@ -481,7 +487,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     const uint32_t dst = s32(ring + slot * Z::SLOT) + to, col = s * Z::SLOTROW + ch * 16;
                     const bool in = col < rowb;
                     const char *src = in ? base + col : base;
-                    ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
+                    live = __all_sync(0xffffffffu, ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag)) && live;
+                    if (!live) continue;
 #pragma unroll 4
                     for (int p = 0; p < 32 / RPP; ++p) {
                         const uint32_t r = tb[p * RPP + sub];
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             const uint32_t bytes = (uint32_t)(a.box * Z::SLOTROW);
             uint32_t *tab = rowtab + isv * 64;
             const uint32_t beyond = (uint32_t)(c.npages * c.kv_heads * c.page_size);  // below 2^31 where there are boxes
-            int items = 0;
+            int items = 0, last = -1;  // last: lane s's: the last item copied to slot s
             while (w.left > 0) {
                 const int t1 = ta_end(w), n = t1 - w.tile, hk = w.u / a.rtiles;
                 const int end = lane < runs ? min(w.cnt > 0 ? w.len + w.cnt : 0, t1 * kTaTile) : 0;
@@ -560,8 +567,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
 #pragma unroll
                     for (int s = 0; s < Z::NS; ++s, ++item) {
                         const int slot = item % SLOTS;
-                        ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
-                        if (elect_one()) {
+                        live = __all_sync(0xffffffffu, ta_wait(&empty[slot], (unsigned)(((item / SLOTS) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag)) && live;
+                        if (live && lane == slot) last = item;
+                        if (live && elect_one()) {
                             mbar_expect_tx(&full[slot], (uint32_t)__popc(have) * bytes);
                             char *dst = ring + slot * Z::SLOT;
                             const uint32_t *tb = tab + (r & 1) * 32;
@@ -582,17 +590,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 ta_next(w, c, units);
                 if (Z::PACED && isv && w.left > 0) bar_arrive_n<64>(4);
             }
-            item = items;
-            // Boxes still in flight (only after a wait gave up) land before the CTA's shared memory goes.
-            const long long t0 = wait_clock();
-            for (int i = max(0, item - SLOTS); i < item; ++i)
-                while (!mbar_test(&full[i % SLOTS], (unsigned)((i / SLOTS) & 1))) {
-                    if (wait_clock() - t0 > kWaitLimitCycles) {
-                        atomicOr(c.status, kStatusTimeout | kWaitDrain);
-                        i = item;
-                        break;
-                    }
-                }
+            tab[lane] = (uint32_t)last;
         }
     } else if (warp >= 8) {
         // ------------------------------------------------ MMA issuer
@@ -607,7 +605,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             const uint32_t bq = s32(sq), bp = s32(sp), br = s32(ring);
             const uint32_t ocol = tmem + 2 * N;
             int item = 0, it = 0, seg = 0;
+            bool live = true;  // no wait has given up
             auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t acc) {
+                if (!live) return;
                 if constexpr (kE4M3)
                     umma_f8(d, da, db, id, acc);
                 else
@@ -615,11 +615,11 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             };
             auto take = [&](int &slot) {
                 slot = item % SLOTS;
-                ta_wait(&full[slot], (unsigned)((item / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
+                live = ta_wait(&full[slot], (unsigned)((item / SLOTS) & 1), c.status, kWaitRingFull, abort_flag) && live;
                 ++item;
             };
             auto scores = [&](int i) {
-                ta_wait(&s_empty[i & 1], (unsigned)(((i >> 1) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag);
+                live = ta_wait(&s_empty[i & 1], (unsigned)(((i >> 1) & 1) ^ 1), c.status, kWaitRingEmpty, abort_flag) && live;
                 tc_fence_after();
                 const uint32_t d = tmem + (i & 1) * N;
 #pragma unroll
@@ -633,12 +633,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         mma(d, ta_desc(ak + (k / 4) * (kTaTile * 128) + (k % 4) * 32, 16, 1024, 2),
                             ta_desc(bq + (gk / 4) * (N * 128) + (gk % 4) * 32, 16, 1024, 2), kId, gk > 0 ? 1u : 0u);
                     }
-                    umma_commit(&empty[slot]);
+                    if (live) umma_commit(&empty[slot]);
                 }
-                umma_commit(&s_full[i & 1]);
+                if (live) umma_commit(&s_full[i & 1]);
             };
             auto values = [&](int i, bool first) {
-                ta_wait(&p_full[i & 1], (unsigned)((i >> 1) & 1), c.status, kWaitRingFull, abort_flag);
+                live = ta_wait(&p_full[i & 1], (unsigned)((i >> 1) & 1), c.status, kWaitRingFull, abort_flag) && live;
                 tc_fence_after();
                 const uint32_t pb = bp + (i & 1) * Z::PB;
 #pragma unroll
@@ -657,13 +657,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                                     ta_desc(av + m * Z::ES * (kTaTile * 128) + k * Z::KSTEP * 128, kTaTile * 128, 1024, 2),
                                     ta_desc(pb + h * Z::PB1 + k * Z::KSTEP * Z::PW, 8 * Z::PW, 8 * Z::PW, Z::SWP), kIdPV,
                                     (first && h + k == 0) ? 0u : 1u);
-                    umma_commit(&empty[slot]);
+                    if (live) umma_commit(&empty[slot]);
                 }
-                umma_commit(&pv_done[i & 1]);
+                if (live) umma_commit(&pv_done[i & 1]);
             };
             while (w.left > 0) {
                 const int t1 = ta_end(w);
-                ta_wait(q_ready, (unsigned)(seg & 1), c.status, kWaitRingFull, abort_flag);
+                live = ta_wait(q_ready, (unsigned)(seg & 1), c.status, kWaitRingFull, abort_flag) && live;
                 tc_fence_after();
                 for (int t = w.tile; t < t1; ++t, ++it) {
                     scores(it);
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 ta_next(w, c, units);
             }
             umma_commit(drain);
-            ta_drain(drain, c.status);
+            ta_drain(drain, 0, c.status);
         }
         __syncwarp();
     } else {
@@ -1076,8 +1076,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                             const int n = t1 - t0, r = t - t0, v0 = items + Z::NS * ta_item(r, n, true);
                             for (int s = 0; s < Z::NS; ++s) {
                                 const int vs = (v0 + s) % SLOTS;
-                                ta_wait(&full[vs], (unsigned)(((v0 + s) / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
-                                if (!seen && (Z::PP || wg == 0))
+                                const bool here = ta_wait(&full[vs], (unsigned)(((v0 + s) / SLOTS) & 1), c.status, kWaitRingFull, abort_flag);
+                                if (here && !seen && (Z::PP || wg == 0))
                                     for (int h = 0; h < Z::SLOTROW / 16; ++h)
                                         *reinterpret_cast<uint4 *>(ring + vs * Z::SLOT + (h / 8) * (kTaTile * 128) + tk * 128 + (h % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
                             }
@@ -1220,6 +1220,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (__builtin_expect(*abort_flag && a.box, 0) && warp == 8) {
+        // Boxes may be in flight: they land before the CTA's shared memory
+        // goes.  In a slot only the last item copied can be, K's or V's (the
+        // one before has been multiplied).
+        if (lane < SLOTS) {
+            const int last = max((int)rowtab[lane], (int)rowtab[64 + lane]);
+            if (last >= 0) ta_drain(&full[lane], (unsigned)((last / SLOTS) & 1), c.status);
+        }
+        __syncwarp();
+    }
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Z::COLS));
 }
 

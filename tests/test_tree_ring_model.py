@@ -83,7 +83,7 @@ class Ring:
             at += 2 * n * ns
         assert sorted(self.mine[0] + self.mine[1]) == list(range(at))
 
-    def faults(self, slots, paced, look="none"):
+    def faults(self, slots, paced, look="none", states=None):
         """Walks every reachable (K's place, V's place, items consumed).
 
         look: the tiles whose V a softmax warp waits for on its own, by the full barrier's parity, between its
@@ -117,6 +117,8 @@ class Ring:
                     nxt.append((k + 1, v, c) if w == 0 else (k, v + 1, c))
             if c in self.mine[0][:k] or c in self.mine[1][:v]:
                 nxt.append((k, v, c + 1))
+            if states is not None:
+                states.add(state)
             if not nxt and c < self.items:
                 bad.add(("stuck", state))
             for s in nxt:
@@ -163,3 +165,20 @@ def test_waits_of_the_softmax_warps_for_v(compiled):
             assert not Ring(order, lengths, ring[1]).faults(*(ring[0], ring[2]), look="last"), (ring, lengths)
         wrong = any(Ring(order, lengths, ring[1]).faults(*(ring[0], ring[2]), look="all") for lengths in some)
         assert wrong == (ring[0] < 3 * ring[1]), ring
+
+
+def test_what_is_in_flight_can_be_waited_for_at_any_point(compiled):
+    """Where every role stops, the last item copied to a slot is the one whose landing its full barrier's parity
+    tells, and only that one can be in flight."""
+    shapes, order = compiled
+    for slots, ns, paced in {(z["slots"], z["ns"], z["paced"]) for z in shapes.values()}:
+        for lengths in LENGTHS[:155:2] + LENGTHS[-3:]:
+            ring = Ring(order, lengths, ns)
+            states = set()
+            assert not ring.faults(slots, paced, states=states)
+            for k, v, c in states:
+                copied = ring.mine[0][:k] + ring.mine[1][:v]
+                for s in range(slots):
+                    mine = sorted(i for i in copied if i % slots == s)
+                    assert mine == list(range(s, s + slots * len(mine), slots))  # no round left out
+                    assert all(i < c for i in mine[:-1])                         # all but the last consumed
