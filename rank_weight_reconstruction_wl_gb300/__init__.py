@@ -645,6 +645,17 @@ def _stream_of(index: int, stream) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that the call runs on (None: the current one).
+    Of another stream's pool it could be a block that queued work of that stream
+    still uses, and the allocator would hand it on without waiting for the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _run(fn, device, stream, *args):
     """fn(*args, stream) on `device`; raises what it reports."""
     index = device.index
@@ -674,7 +685,7 @@ def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, s
         qs = _token_rows(q, "q", dt, tokens, heads * dim)
         qp = q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
             op = q_out.data_ptr()
         else:
             op = _checked(q_out, "q_out", torch.bfloat16, q.shape)
@@ -697,9 +708,8 @@ def wl_cache_read(cache: KVCache, seqs: CacheSeqs, dt=torch.bfloat16, outs=None,
     td = _tdt(code)
     shape = (seqs.batch, seqs.n, cache.kv_heads, cache.dim)
     if outs is None:
-        k = torch.empty(shape, dtype=td, device=cache.device)
-        outs = (k, torch.empty_like(k))
-        kp, vp = k.data_ptr(), outs[1].data_ptr()
+        outs = (_empty(shape, td, cache.device, stream), _empty(shape, td, cache.device, stream))
+        kp, vp = outs[0].data_ptr(), outs[1].data_ptr()
     else:
         kp, vp = _checked(outs[0], "k_out", td, shape), _checked(outs[1], "v_out", td, shape)
     _run((_lib or lib()).wl_cache_read, cache.device, stream, cache._c, seqs._c, kp, vp, code)
@@ -729,20 +739,14 @@ def wl_tree_attention(q, cache: KVCache, seqs: CacheSeqs, mask=None, scale: floa
         if mask.numel() != tokens:
             raise ValueError(f"mask must hold batch * n = {tokens} words, got {tuple(mask.shape)}")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
         op = out.data_ptr()
     else:
         op = _checked(out, "out", torch.bfloat16, q.shape)
     L = _lib or lib()
     if workspace is None:
         nb = max(256, L.wl_tree_attention_workspace_bytes(seqs.batch, seqs.n, heads, cache.kv_heads, dim))
-        if stream is None:
-            workspace = torch.empty(nb, dtype=torch.uint8, device=cache.device)
-        else:
-            # of the call's own stream, so that the allocator hands it on only after the call
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), cache.device)
-            with torch.cuda.stream(s):
-                workspace = torch.empty(nb, dtype=torch.uint8, device=cache.device)
+        workspace = _empty(nb, torch.uint8, cache.device, stream)
     _run(L.wl_tree_attention, cache.device, stream, qp, heads, mp, dim ** -0.5 if scale is None else scale, cache._c, seqs._c, op,
          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
@@ -782,14 +786,14 @@ def wl_norm_residual(y, x, w_post=None, w_pre=None, gate=None, alpha: float = 1.
     if x_out is not None:
         xo = _checked(x_out, "x_out", dt, shape)
     elif y is not None or alpha != 1.0:
-        x_out = torch.empty_like(x)
+        x_out = _empty(shape, dt, x.device, stream)
         xo = x_out.data_ptr()
     hc = _ydt(h_dt)
     td = _tdt(hc)
     if h is not None:
         hp = _checked(h, "h", td, shape)
     elif w_pre is not None:
-        h = torch.empty_like(x) if td is dt else torch.empty_like(x, dtype=td)
+        h = _empty(shape, td, x.device, stream)
         hp = h.data_ptr()
     _run((_lib or lib()).wl_norm_residual, x.device, stream, yp, gp, gs, xp, wp, wq, xo, hp, T, H, alpha, beta, eps, w_offset, yc,
          xc, hc)
