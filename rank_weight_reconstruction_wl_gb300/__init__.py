@@ -237,6 +237,23 @@ def _stream(stream, device):
     return C.c_void_p(int(stream))
 
 
+def _stream_object(stream, device):
+    """The torch stream of a call (None: the current one, which torch.cuda.stream() leaves as it is)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that the call runs on (None: the current one).
+    Of another stream's pool it could be a block that queued work of that stream
+    still uses, and the allocator would hand it on without waiting for the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(status: int):
     if status != WL_OK:
         raise WLError(status, lib().wl_last_error().decode())
@@ -255,7 +272,7 @@ def wl_linear(x, W0, s, U, V, y=None, ydt=torch.bfloat16, stream=None):
     if x.dtype == torch.float32:
         p = _proj_f32((W0, s, U, V), inp, r, "theta")
         if y is None:
-            y = torch.empty(T, out, dtype=_tdt(code), device=x.device)
+            y = _empty((T, out), _tdt(code), x.device, stream)
         _need(x, "x", torch.float32)
         _need(y, "y", _tdt(code), (T, out))
         with torch.cuda.device(x.device):
@@ -265,7 +282,7 @@ def wl_linear(x, W0, s, U, V, y=None, ydt=torch.bfloat16, stream=None):
     _need(x, "x", torch.bfloat16)
     p = _proj((W0, s, U, V), inp, r, "theta")
     if y is None:
-        y = torch.empty(T, out, dtype=_tdt(code), device=x.device)
+        y = _empty((T, out), _tdt(code), x.device, stream)
     _need(y, "y", _tdt(code), (T, out))
     with torch.cuda.device(x.device):
         _check(lib().wl_linear(_ptr(x), p.W0, p.s, p.U, p.V, _ptr(y), T, inp, out, r, code,
@@ -282,7 +299,7 @@ def wl_qkv_fused(x, q, k, v, outs=None, ydt=torch.bfloat16, stream=None):
         _need(x, "x", torch.float32)
         ps = [_proj_f32(th, inp, r, n) for th, n in ((q, "q"), (k, "k"), (v, "v"))]
         if outs is None:
-            outs = tuple(torch.empty(T, p.out, dtype=_tdt(code), device=x.device) for p in ps)
+            outs = tuple(_empty((T, p.out), _tdt(code), x.device, stream) for p in ps)
         for o, p, n in zip(outs, ps, ("yq", "yk", "yv")):
             _need(o, n, _tdt(code), (T, p.out))
         with torch.cuda.device(x.device):
@@ -292,7 +309,7 @@ def wl_qkv_fused(x, q, k, v, outs=None, ydt=torch.bfloat16, stream=None):
     _need(x, "x", torch.bfloat16)
     ps = [_proj(th, inp, r, n) for th, n in ((q, "q"), (k, "k"), (v, "v"))]
     if outs is None:
-        outs = tuple(torch.empty(T, p.out, dtype=_tdt(code), device=x.device) for p in ps)
+        outs = tuple(_empty((T, p.out), _tdt(code), x.device, stream) for p in ps)
     for o, p, n in zip(outs, ps, ("yq", "yk", "yv")):
         _need(o, n, _tdt(code), (T, p.out))
     with torch.cuda.device(x.device):
@@ -338,7 +355,7 @@ def wl_mlp_geglu_fused(x, gate, up, down, y=None, workspace=None, ydt=torch.bflo
     pu = _proj(up, hidden, r, "up")
     pd = _proj(down, inter, r, "down")
     if y is None:
-        y = torch.empty(T, hidden, dtype=_tdt(code), device=x.device)
+        y = _empty((T, hidden), _tdt(code), x.device, stream)
     _need(y, "y", _tdt(code), (T, hidden))
     if workspace is None:
         workspace = mlp_workspace(T, hidden, inter, r, ydt, x.device)
@@ -374,7 +391,7 @@ def wl_materialize(W0, s, U, V, dt=torch.bfloat16, out=None, stream=None):
     code = _ydt(dt)
     p = _proj((W0, s, U, V), inp, r, "theta")
     if out is None:
-        out = torch.empty(o, inp, dtype=_tdt(code), device=W0.device)
+        out = _empty((o, inp), _tdt(code), W0.device, stream)
     _need(out, "W_eff", _tdt(code), (o, inp))
     with torch.cuda.device(W0.device):
         _check(lib().wl_materialize(p.W0, p.s, p.U, p.V, _ptr(out), o, inp, r, code,
@@ -398,16 +415,17 @@ def wl_decompose_band(Ws, r, p=8, iters=4, omega=None, seed=0, stream=None):
     if omega is None:
         g = torch.Generator(device=dev)
         g.manual_seed(int(seed))
-        omega = torch.randn(inp, k, generator=g, device=dev, dtype=torch.float32)
+        with torch.cuda.stream(_stream_object(stream, dev)):
+            omega = torch.randn(inp, k, generator=g, device=dev, dtype=torch.float32)
     if r > 0:
         _need(omega, "omega", torch.float32, (inp, k))
-    W0 = torch.empty(out, inp, dtype=torch.bfloat16, device=dev)
-    s = torch.empty(n, out, dtype=torch.float32, device=dev)
-    U = torch.empty(n, out, r, dtype=torch.bfloat16, device=dev)
-    V = torch.empty(n, inp, r, dtype=torch.bfloat16, device=dev)
+    W0 = _empty((out, inp), torch.bfloat16, dev, stream)
+    s = _empty((n, out), torch.float32, dev, stream)
+    U = _empty((n, out, r), torch.bfloat16, dev, stream)
+    V = _empty((n, inp, r), torch.bfloat16, dev, stream)
     # 0 for sizes the library rejects: the call below then reports why
     nb = int(lib().wl_decompose_workspace_bytes(out, inp, r, p))
-    ws = torch.empty(nb + 256, dtype=torch.uint8, device=dev)
+    ws = _empty(nb + 256, torch.uint8, dev, stream)
     off = (-ws.data_ptr()) % 256
     ptrs = (C.c_void_p * n)(*[W.data_ptr() for W in Ws])
     with torch.cuda.device(dev):
@@ -643,17 +661,6 @@ def _stream_of(index: int, stream) -> int:
     if stream is None:
         return _current_stream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor of the stream that the call runs on (None: the current one).
-    Of another stream's pool it could be a block that queued work of that stream
-    still uses, and the allocator would hand it on without waiting for the call."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _run(fn, device, stream, *args):

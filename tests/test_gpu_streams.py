@@ -65,3 +65,25 @@ def test_norm_on_another_stream(wl, gpu):
     x = torch.randn(512, 1024, generator=wl_synth.make_generator(3)).to(gpu)
     w = torch.ones(1024, device=gpu)
     _check(gpu, lambda st: wl.wl_norm_residual(x, x, w, w, h_dt=torch.float32, stream=st), [((512, 1024), torch.float32)] * 2)
+
+
+def test_projections_on_another_stream(wl, gpu):
+    T, inp, out, r = 256, 1024, 1152, 8
+    g = wl_synth.make_generator(4)
+    x = wl_synth.draw_x(g, T, inp).to(gpu)
+    th = [t.to(gpu) for t in _bundle(g, inp, out, r)]
+    _check(gpu, lambda st: [wl.wl_linear(x, *th, stream=st)], [((T, out), BF)])
+    _check(gpu, lambda st: wl.wl_qkv_fused(x, th, th, th, stream=st), [((T, out), BF)] * 3)
+    _check(gpu, lambda st: [wl.wl_materialize(*th, stream=st)], [((out, inp), BF)])
+    f = [t.float() for t in th]
+    _check(gpu, lambda st: [wl.wl_linear(x.float(), *f, ydt=torch.float32, stream=st)], [((T, out), torch.float32)])
+    back = [t.to(gpu) for t in _bundle(g, out, inp, r)]
+    _check(gpu, lambda st: [wl.wl_mlp_geglu_fused(x, th, th, back, stream=st)], [((T, inp), BF)])
+    Ws = [th[0], th[0] + th[0]]
+    _check(gpu, lambda st: wl.wl_decompose_band(Ws, 4, stream=st),
+           [((out, inp), BF), ((2, out), torch.float32), ((2, out, 4), BF), ((2, inp, 4), BF), ((inp, 12), torch.float32)])
+
+
+def _bundle(g, inp, out, r):
+    th = wl_synth.draw_theta(g, inp, out, r)
+    return th.W0, th.s, th.U, th.V
