@@ -178,6 +178,12 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _one_device(t, name: str, index):
+    """Refuses a tensor of another device than `index` (None: any)."""
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
 def _theta(th):
     if isinstance(th, (tuple, list)):
         return tuple(th)
@@ -529,6 +535,7 @@ class RopeTable:
         _need(phases, "phases", torch.int64)
         self.phases, self.interleaved, self.amplitude = phases, bool(interleaved), float(amplitude)
         self.rot = 2 * phases.numel()
+        self.index = phases.get_device()
         self._c = _Rope(phases.data_ptr(), self.rot, int(self.interleaved), self.amplitude)
 
     @classmethod
@@ -569,7 +576,7 @@ class KVCache:
         if not (k.device == v.device == k_scale.device == v_scale.device):
             raise ValueError("the cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.pages, self.kv_heads, self.page_size, self.dim = (int(n) for n in k.shape)
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages, self.kv_heads,
                          self.page_size, self.dim, 0 if k.dtype == torch.float8_e4m3fn else 1)
@@ -599,17 +606,20 @@ class CacheSeqs:
         _need(len, "len", torch.int32, (B,))
         if count is not None:
             _need(count, "count", torch.int32, (B,))
+        if pages.device != len.device or (count is not None and pages.device != count.device):
+            raise ValueError("pages, len and count must be on one device")
+        self.index = pages.get_device()
         self.pages, self.len, self.n, self.count, self.batch = pages, len, int(n), count, B
         self.tokens = B * self.n
         self._c = _Seqs(pages.data_ptr(), len.data_ptr(), None if count is None else count.data_ptr(), B,
                         int(pages.shape[1]), self.n)
 
 
-def _token_rows(t, name: str, dtype, tokens: int, width: int) -> int:
+def _token_rows(t, name: str, dtype, tokens: int, width: int, index=None) -> int:
     """Row stride in elements of a tensor of `tokens` rows of `width` elements:
     [tokens, width], [tokens, heads, dim] or [batch, n, heads, dim], rows any
-    one distance apart."""
-    if t.__class__ is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == tokens * width:
+    one distance apart; on device `index` (None: any CUDA device)."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.numel() == tokens * width:
         return width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -617,6 +627,7 @@ def _token_rows(t, name: str, dtype, tokens: int, width: int) -> int:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _one_device(t, name, index)
     if t.numel() != tokens * width:
         raise ValueError(f"{name} must hold {tokens} rows of {width} elements, got {tuple(t.shape)}")
     if t.is_contiguous():
@@ -643,11 +654,12 @@ _current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                    or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
-def _checked(t, name: str, dtype, shape) -> int:
-    """The address of a contiguous CUDA tensor of this type and shape (None: any)."""
-    if t.__class__ is torch.Tensor and t.dtype is dtype and t.is_cuda and (shape is None or t.shape == shape) and t.is_contiguous():
+def _checked(t, name: str, dtype, shape, index) -> int:
+    """The address of a contiguous tensor of this type and shape (None: any) on device `index`."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.get_device() == index and (shape is None or t.shape == shape) and t.is_contiguous():
         return t.data_ptr()
     _need(t, name, dtype, shape)
+    _one_device(t, name, index)
     return t.data_ptr()
 
 
@@ -673,6 +685,7 @@ def _run(fn, device, stream, *args):
 
 
 _NO_ROPE = _Rope(None, 0, 0, 1.0)
+_OTHER_SEQS = "the sequences must be on the cache's device"
 
 
 def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, seqs: CacheSeqs, q_out=None, stream=None):
@@ -683,26 +696,30 @@ def wl_rope_append(q, k, v, positions, rope: RopeTable | None, cache: KVCache, s
     [batch, n], or None for len[b] + i.  rope None: no rotation."""
     dt = k.dtype
     code = _ydt(dt)
-    tokens, dim = seqs.tokens, cache.dim
+    tokens, dim, index = seqs.tokens, cache.dim, cache.index
+    if seqs.index != index:
+        raise ValueError(_OTHER_SEQS)
     kvw = cache.kv_heads * dim
-    ks, vs = _token_rows(k, "k", dt, tokens, kvw), _token_rows(v, "v", dt, tokens, kvw)
+    ks, vs = _token_rows(k, "k", dt, tokens, kvw, index), _token_rows(v, "v", dt, tokens, kvw, index)
     heads, qs, qp, op = 0, 0, None, None
     if q is not None:
-        heads = q.numel() // (tokens * dim)
-        qs = _token_rows(q, "q", dt, tokens, heads * dim)
+        heads = q.numel() // max(1, tokens * dim)
+        qs = _token_rows(q, "q", dt, tokens, heads * dim, index)
         qp = q.data_ptr()
         if q_out is None:
             q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
             op = q_out.data_ptr()
         else:
-            op = _checked(q_out, "q_out", torch.bfloat16, q.shape)
+            op = _checked(q_out, "q_out", torch.bfloat16, q.shape, index)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     pp = None
     if positions is not None:
-        pp = _checked(positions, "positions", torch.int32, None)
+        pp = _checked(positions, "positions", torch.int32, None, index)
         if positions.numel() != tokens:
             raise ValueError(f"positions must hold batch * n = {tokens} numbers, got {tuple(positions.shape)}")
+    if rope is not None and rope.index != index:
+        raise ValueError(f"the rotary table must be on the cache's device, cuda:{index}")
     _run((_lib or lib()).wl_rope_append, cache.device, stream, qp, k.data_ptr(), v.data_ptr(), op, heads, qs, ks, vs, code, pp,
          _NO_ROPE if rope is None else rope._c, cache._c, seqs._c)
     return q_out
@@ -712,13 +729,15 @@ def wl_cache_read(cache: KVCache, seqs: CacheSeqs, dt=torch.bfloat16, outs=None,
     """The cache's values at positions len[b] + i, i < count[b] (zeros beyond):
     (k, v) [batch, n, kv_heads, dim] as bf16 or fp32."""
     code = _ydt(dt)
-    td = _tdt(code)
+    td, index = _tdt(code), cache.index
+    if seqs.index != index:
+        raise ValueError(_OTHER_SEQS)
     shape = (seqs.batch, seqs.n, cache.kv_heads, cache.dim)
     if outs is None:
         outs = (_empty(shape, td, cache.device, stream), _empty(shape, td, cache.device, stream))
         kp, vp = outs[0].data_ptr(), outs[1].data_ptr()
     else:
-        kp, vp = _checked(outs[0], "k_out", td, shape), _checked(outs[1], "v_out", td, shape)
+        kp, vp = _checked(outs[0], "k_out", td, shape, index), _checked(outs[1], "v_out", td, shape, index)
     _run((_lib or lib()).wl_cache_read, cache.device, stream, cache._c, seqs._c, kp, vp, code)
     return tuple(outs)
 
@@ -735,27 +754,32 @@ def wl_tree_attention(q, cache: KVCache, seqs: CacheSeqs, mask=None, scale: floa
     [batch * n, q_heads * dim]) -> out of the same shape.  scale defaults to
     dim ** -0.5.  workspace: at least wl_tree_attention_workspace_bytes() bytes,
     256-byte aligned; by default allocated for the call."""
-    tokens, dim = seqs.tokens, cache.dim
-    qp = _checked(q, "q", torch.bfloat16, None)
-    heads = q.numel() // (tokens * dim)
+    tokens, dim, index = seqs.tokens, cache.dim, cache.index
+    if seqs.index != index:
+        raise ValueError(_OTHER_SEQS)
+    qp = _checked(q, "q", torch.bfloat16, None, index)
+    heads = q.numel() // max(1, tokens * dim)
     if heads * tokens * dim != q.numel():
         raise ValueError(f"q must hold batch * n = {tokens} rows of heads * {dim} elements, got {tuple(q.shape)}")
     mp = None
     if mask is not None:
-        mp = _checked(mask, "mask", torch.int64, None)
+        mp = _checked(mask, "mask", torch.int64, None, index)
         if mask.numel() != tokens:
             raise ValueError(f"mask must hold batch * n = {tokens} words, got {tuple(mask.shape)}")
     if out is None:
-        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _empty(q.shape, torch.bfloat16, q.device, stream)
         op = out.data_ptr()
     else:
-        op = _checked(out, "out", torch.bfloat16, q.shape)
+        op = _checked(out, "out", torch.bfloat16, q.shape, index)
     L = _lib or lib()
     if workspace is None:
         nb = max(256, L.wl_tree_attention_workspace_bytes(seqs.batch, seqs.n, heads, cache.kv_heads, dim))
         workspace = _empty(nb, torch.uint8, cache.device, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws = _checked(workspace, "workspace", getattr(workspace, "dtype", None), None, index)
     _run(L.wl_tree_attention, cache.device, stream, qp, heads, mp, dim ** -0.5 if scale is None else scale, cache._c, seqs._c, op,
-         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+         ws, workspace.numel() * workspace.element_size())
     return out
 
 
@@ -772,35 +796,39 @@ def wl_norm_residual(y, x, w_post=None, w_pre=None, gate=None, alpha: float = 1.
     T, H = shape
     dt = x.dtype
     xc = yc = _ydt(dt)
-    xp = _checked(x, "x", dt, shape)
+    index = x.get_device() if x.is_cuda else None
+    xp = _checked(x, "x", dt, shape, index)
     yp = gp = wp = wq = xo = hp = None
     gs = 0
     if y is not None:
         yc = _ydt(y.dtype)
-        yp = _checked(y, "y", y.dtype, shape)
+        yp = _checked(y, "y", y.dtype, shape, index)
     if gate is not None:
         if y is None:
             raise ValueError("gate needs y")
-        gp = _checked(gate, "gate", y.dtype, None)
+        gp = _checked(gate, "gate", y.dtype, None, index)
         if gate.numel() != H:
             if gate.shape != shape:
                 raise ValueError(f"gate must be [{T}, {H}], [1, {H}] or [{H}], got {tuple(gate.shape)}")
             gs = H
     if w_post is not None:
-        wp = _checked(w_post, "w_post", torch.float32, (H,))
+        wp = _checked(w_post, "w_post", torch.float32, (H,), index)
     if w_pre is not None:
-        wq = _checked(w_pre, "w_pre", torch.float32, (H,))
+        wq = _checked(w_pre, "w_pre", torch.float32, (H,), index)
     if x_out is not None:
-        xo = _checked(x_out, "x_out", dt, shape)
+        xo = _checked(x_out, "x_out", dt, shape, index)
     elif y is not None or alpha != 1.0:
-        x_out = _empty(shape, dt, x.device, stream)
+        x_out = torch.empty_like(x) if stream is None else _empty(shape, dt, x.device, stream)
         xo = x_out.data_ptr()
     hc = _ydt(h_dt)
     td = _tdt(hc)
     if h is not None:
-        hp = _checked(h, "h", td, shape)
+        hp = _checked(h, "h", td, shape, index)
     elif w_pre is not None:
-        h = _empty(shape, td, x.device, stream)
+        if stream is not None:
+            h = _empty(shape, td, x.device, stream)
+        else:
+            h = torch.empty_like(x) if td is dt else torch.empty_like(x, dtype=td)
         hp = h.data_ptr()
     _run((_lib or lib()).wl_norm_residual, x.device, stream, yp, gp, gs, xp, wp, wq, xo, hp, T, H, alpha, beta, eps, w_offset, yc,
          xc, hc)

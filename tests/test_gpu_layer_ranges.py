@@ -102,3 +102,16 @@ def test_all_of_v_zero_and_large_rows_of_scale_one(wl, gpu):
     half[:, :, 8:] = False
     cache.v.view(torch.uint8)[half] = 0x01  # the smallest code alone
     check(wl, cache, seqs, lens, q, what="smallest codes")
+
+
+def test_empty_calls_are_refused_by_name(wl, gpu):
+    """No tokens or no sequences: the library's own words, not a division by zero."""
+    z = dict(dtype=torch.int32, device=gpu)
+    cache = wl.KVCache.empty(4, 2, 16, 64, device=gpu)
+    x = torch.zeros(0, 128, dtype=BF, device=gpu)
+    for B, n, what in ((1, 0, "n must"), (0, 2, "batch must")):
+        s = wl.CacheSeqs(torch.zeros(B, 4, **z), torch.zeros(B, **z), n)
+        for call in (lambda: wl.wl_rope_append(x, x, x, None, None, cache, s), lambda: wl.wl_rope_append(None, x, x, None, None, cache, s),
+                     lambda: wl.wl_tree_attention(x, cache, s), lambda: wl.wl_cache_read(cache, s)):
+            with pytest.raises(wl.WLError, match=what):
+                call()
