@@ -13,7 +13,9 @@ Per layer and step (x: the fp32 residual stream, h: its normed bf16 form):
 A step takes the newest tokens of every sequence: one each (decoding), a
 drafted tree, or up to 64 of a prompt; ``prompt`` feeds longer ones in chunks.
 ``accept`` keeps a root-to-node path of the tree that a step put into the cache.
-All work runs on the current stream; nothing synchronises.
+All work runs on the current stream.  Nothing synchronises but a step that might
+not fit: the host knows a bound of the lengths, and reads them where the bound
+does not tell.
 """
 from __future__ import annotations
 
@@ -58,7 +60,16 @@ class Decoder:
         self.caches = [KVCache.empty(batch * per, kv_heads, page_size, self.dim, cache_dtype, dev) for _ in layers]
         self.pages = torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per).contiguous()
         self.len = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self._most = 0  # no sequence is longer
         self._drafted = None
+
+    def _fits(self, n: int, count: torch.Tensor | None):
+        if self._most + n <= self.max_len or torch.cuda.is_current_stream_capturing():
+            return
+        new = n if count is None else count.clamp(0, n)
+        self._most, most = torch.stack((self.len.max(), (self.len + new).max())).tolist()
+        if most > self.max_len:
+            raise ValueError(f"the step would fill a sequence to {most} of {self.max_len} positions")
 
     def step(self, x: torch.Tensor, n: int, mask: torch.Tensor | None = None, depth: torch.Tensor | None = None,
              count: torch.Tensor | None = None) -> torch.Tensor:
@@ -67,9 +78,12 @@ class Decoder:
         (int64 [batch, n], bit j of row i: node j is i or an ancestor of it) and
         depth (int32 [batch, n]).  The tokens are in the cache afterwards but
         not counted in len: accept() does that.  Returns the normed final
-        states, bf16 [batch * n, hidden]."""
+        states, bf16 [batch * n, hidden].  Raises ValueError where a sequence
+        would pass max_len (a captured step cannot tell: wl_device_status()
+        reports positions past the table)."""
         if not 1 <= n <= MAX_STEP:
             raise ValueError(f"a step takes 1 to {MAX_STEP} tokens of each sequence, got {n}")
+        self._fits(n, count)
         seqs = CacheSeqs(self.pages, self.len, n, count)
         positions = None if depth is None else (self.len[:, None] + depth).to(torch.int32).contiguous()
         norm = dict(eps=self.eps, w_offset=self.w_offset)
@@ -99,6 +113,7 @@ class Decoder:
         self._drafted = None
         if path is None:
             self.len += n if count is None else count
+            self._most += n
             return
         m = int(path.shape[1])
         rows = (torch.arange(self.batch, device=self.device)[:, None] * n + path).view(-1)
@@ -107,11 +122,13 @@ class Decoder:
         for cache, (k, v) in zip(self.caches, kept):
             wl_rope_append(None, k[rows], v[rows], pos, self.rope, cache, seqs)
         self.len += m if count is None else count
+        self._most += m
 
     def prompt(self, x: torch.Tensor) -> torch.Tensor:
         """x [batch, T, hidden] fp32, T tokens of each sequence; returns the last
         token's normed state, bf16 [batch, hidden]."""
         B, T, H = x.shape
+        self._fits(T, None)
         h = None
         for t in range(0, T, MAX_STEP):
             part = x[:, t:t + MAX_STEP]

@@ -141,3 +141,29 @@ def test_refusals(wl, gpu):
         dec.step(torch.zeros(130, SH["hidden"], device=gpu), 65)
     with pytest.raises(ValueError, match="needs a step"):
         dec.accept()
+
+
+def test_a_sequence_does_not_pass_its_room(wl, gpu):
+    """A step that would pass max_len is refused before anything runs; what fits goes on."""
+    dec = _decoder(wl, gpu, max_len=32)
+    x = _x(gpu, 2, 40)
+    for T in (40, 33):
+        with pytest.raises(ValueError, match=f"{T} of 32"):
+            dec.prompt(x[:, :T])
+    with pytest.raises(ValueError, match="100 of 32"):
+        dec.prompt(_x(gpu, 2, 100))
+    assert dec.len.tolist() == [0, 0]
+    dec.prompt(x[:, :30])
+    assert dec.len.tolist() == [30, 30]
+    with pytest.raises(ValueError, match="33 of 32"):
+        dec.step(x[:, :3].reshape(6, -1).contiguous(), 3)
+    # one sequence takes two more, the other none: the room of each counts, not n
+    some = torch.tensor([2, 0], dtype=torch.int32, device=gpu)
+    dec.step(x[:, :3].reshape(6, -1).contiguous(), 3, count=some)
+    dec.accept(count=some)
+    assert dec.len.tolist() == [32, 30]
+    with pytest.raises(ValueError, match="33 of 32"):
+        dec.step(x[:, :1].reshape(2, -1).contiguous(), 1)
+    dec.len.zero_()  # the sequences begin anew
+    dec.prompt(x[:, :32])
+    assert dec.len.tolist() == [32, 32] and wl.wl_device_status() == wl.WL_OK
