@@ -99,35 +99,39 @@ class Decoder:
             m = wl_mlp_geglu_fused(h, th.gate, th.up, th.down)
             pre = self.norms[l + 1].attn_pre if l + 1 < len(self.layers) else self.final
             x, h = wl_norm_residual(m, x, w_post=nm.mlp_post, w_pre=pre, **norm)
-        self._drafted = (n, positions, kept)
+        self._drafted = (n, count, positions, kept)
         return h
 
     def accept(self, path: torch.Tensor | None = None, count: torch.Tensor | None = None):
         """Counts tokens of the last step into the sequences.  path None: the
-        first count[b] (all n) as they lie.  Else path [batch, m] int: the nodes
-        of a root-to-node path, count[b] <= m of them; their k and v, kept from
-        the step, are written again at the positions that follow len."""
+        first count[b] (those of the step) as they lie.  Else path [batch, m]
+        int: the nodes of a root-to-node path, count[b] <= m of them (entries
+        beyond mean nothing); their k and v, kept from the step, are written
+        again at the positions that follow len."""
         if self._drafted is None:
             raise ValueError("accept() needs a step before it")
-        n, positions, kept = self._drafted
+        n, had, positions, kept = self._drafted
+        m = n if path is None else int(path.shape[-1])
+        if path is not None and (tuple(path.shape) != (self.batch, m) or not 1 <= m <= n):
+            raise ValueError(f"path must be [{self.batch}, 1..{n}], got {tuple(path.shape)}")
         self._drafted = None
-        if path is None:
-            self.len += n if count is None else count
-            self._most += n
-            return
-        m = int(path.shape[1])
-        rows = (torch.arange(self.batch, device=self.device)[:, None] * n + path).view(-1)
-        seqs = CacheSeqs(self.pages, self.len, m, count)
-        pos = None if positions is None else positions.view(-1)[rows].contiguous()
-        for cache, (k, v) in zip(self.caches, kept):
-            wl_rope_append(None, k[rows], v[rows], pos, self.rope, cache, seqs)
-        self.len += m if count is None else count
+        if path is not None:
+            rows = (torch.arange(self.batch, device=self.device)[:, None] * n + path.clamp(0, n - 1)).view(-1)
+            seqs = CacheSeqs(self.pages, self.len, m, count)
+            pos = None if positions is None else positions.view(-1)[rows].contiguous()
+            for cache, (k, v) in zip(self.caches, kept):
+                wl_rope_append(None, k[rows], v[rows], pos, self.rope, cache, seqs)
+        elif had is not None:
+            count = had if count is None else torch.minimum(count, had)
+        self.len += m if count is None else count.clamp(0, m)
         self._most += m
 
     def prompt(self, x: torch.Tensor) -> torch.Tensor:
         """x [batch, T, hidden] fp32, T tokens of each sequence; returns the last
         token's normed state, bf16 [batch, hidden]."""
         B, T, H = x.shape
+        if T < 1:
+            raise ValueError("a prompt has at least one token")
         self._fits(T, None)
         h = None
         for t in range(0, T, MAX_STEP):

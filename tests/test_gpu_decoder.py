@@ -160,10 +160,42 @@ def test_a_sequence_does_not_pass_its_room(wl, gpu):
     # one sequence takes two more, the other none: the room of each counts, not n
     some = torch.tensor([2, 0], dtype=torch.int32, device=gpu)
     dec.step(x[:, :3].reshape(6, -1).contiguous(), 3, count=some)
-    dec.accept(count=some)
+    dec.accept()
     assert dec.len.tolist() == [32, 30]
     with pytest.raises(ValueError, match="33 of 32"):
         dec.step(x[:, :1].reshape(2, -1).contiguous(), 1)
     dec.len.zero_()  # the sequences begin anew
     dec.prompt(x[:, :32])
     assert dec.len.tolist() == [32, 32] and wl.wl_device_status() == wl.WL_OK
+
+
+def test_accept_counts_what_the_step_had(wl, gpu):
+    """accept() after a ragged step counts the step's tokens, no more; paths may be padded with anything."""
+    x, draft, nxt = _x(gpu, 2, 10, 9), _x(gpu, 2, 4, 10), _x(gpu, 2, 1, 11)
+    had = torch.tensor([1, 3], dtype=torch.int32, device=gpu)
+    last = []
+    for how in ("plain", "more", "path"):
+        dec = _decoder(wl, gpu)
+        dec.prompt(x)
+        dec.step(draft.reshape(8, -1), 4, count=had)
+        if how == "plain":
+            dec.accept()
+        elif how == "more":
+            dec.accept(count=torch.tensor([4, 9], dtype=torch.int32, device=gpu))
+        else:
+            dec.accept(torch.tensor([[0, 1 << 40, -9, 4], [0, 1, 2, 1 << 40]], device=gpu), had)
+        assert dec.len.tolist() == [11, 13], how
+        last.append(dec.step(nxt.reshape(2, -1), 1))
+    assert torch.equal(last[0], last[1]) and torch.equal(last[0], last[2])
+    assert wl.wl_device_status() == wl.WL_OK
+
+
+def test_accept_refusals(wl, gpu):
+    dec = _decoder(wl, gpu)
+    dec.step(_x(gpu, 2, 3).reshape(6, -1), 3)
+    for bad in (torch.zeros(2, 4), torch.zeros(1, 2), torch.zeros(2, 0), torch.zeros(2)):
+        with pytest.raises(ValueError, match="path must be"):
+            dec.accept(bad.long().to(gpu))
+    dec.accept(torch.zeros(2, 1, dtype=torch.int64, device=gpu))  # the step is still there
+    with pytest.raises(ValueError, match="at least one token"):
+        dec.prompt(_x(gpu, 2, 1)[:, :0])
