@@ -885,7 +885,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         const int j = t * kTaTile + tk;
                         const bool seen = at != ~0u;
                         const bool bad = vs != vs;
-                        const float v1 = fmaxf(vs, 1.17549435e-38f);
+                        // w / v_scale of few rows below 2^-104 could pass fp32's range (w is up to 2^8): such
+                        // rows, nothing in them above 448 * 2^-104, count as if their scale were that
+                        const float v1 = fmaxf(vs, 4.93038066e-32f);
                         // log2 of the scale, to 2^-22 of itself, and the reciprocal, exact for a power
                         // of two: a weight and its share of the sum are off alike, by 3.3e-6 at a scale
                         // of 2^-20.  (The exponent apart, exactly: 76.8 us instead of 76.0 in the second

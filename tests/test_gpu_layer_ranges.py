@@ -104,6 +104,28 @@ def test_all_of_v_zero_and_large_rows_of_scale_one(wl, gpu):
     check(wl, cache, seqs, lens, q, what="smallest codes")
 
 
+@pytest.mark.parametrize("dim,n,group", [(128, 1, 2), (256, 1, 4), (128, 8, 8)])
+def test_runs_of_tiny_rows_in_v(wl, gpu, dim, n, group):
+    """Rows of v near fp32's smallest numbers, by the tile, beside ordinary ones: the softmax's sum stays finite.
+
+    A row counts as if its scale were 2^-104 at least, so what lies below 448 * 2^-104 may come out as large as that."""
+    lens = [2500, 700]
+    cache, seqs = filled(wl, gpu, lens, n, 1, dim, 16, E4, seed=dim + n)
+    q = torch.randn(2, n, group, dim, generator=wl_synth.make_generator(n)).to(BF).to(gpu)
+    plain = cache.v_scale.clone()
+    for first, last in ((0, 512), (128, 256), (0, 2000)):
+        cache.v_scale.copy_(plain)
+        for b in range(2):
+            at = seqs.pages[b, first // 16:min(last, lens[b]) // 16].long()
+            cache.v_scale[at] = 2.0 ** -126
+        out = wl.wl_tree_attention(q, cache, seqs)
+        for b in range(2):
+            want, bound = formula(cache, seqs, q, b, chain(lens, b, n, gpu), dim ** -0.5)
+            worst = float(((out[b].double() - want).abs() / (bound + 448 * 2.0 ** -104)).max())
+            assert worst <= 1, f"positions {first} to {last}, sequence {b}: {worst:.3g} times the bound"
+    assert wl.wl_device_status() == wl.WL_OK
+
+
 def test_empty_calls_are_refused_by_name(wl, gpu):
     """No tokens or no sequences: the library's own words, not a division by zero."""
     z = dict(dtype=torch.int32, device=gpu)
