@@ -47,6 +47,16 @@ struct TmapKeyHash {
 };
 static std::unordered_map<TmapKey, CUtensorMap, TmapKeyHash> g_tmaps;
 
+// Keeps a map for later calls; where the host has no memory for that, the call
+// goes on without (nothing is thrown across the ABI).
+static void remember(const TmapKey &key, const CUtensorMap &m)
+{
+    try {
+        g_tmaps.emplace(key, m);
+    } catch (...) {
+    }
+}
+
 static wl_status load_encoder()
 {
     if (g_encode) return WL_OK;
@@ -97,7 +107,7 @@ wl_status tmap_2d_bf16_swz(const void *base, int64_t inner, int64_t outer, int64
     if (r != CUDA_SUCCESS)
         return fail(WL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a [%lld, %lld] matrix", (int)r,
                     (long long)outer, (long long)inner);
-    g_tmaps.emplace(key, m);
+    remember(key, m);
     *out = m;
     return WL_OK;
 }
@@ -135,7 +145,7 @@ wl_status tmap_kblocks_bf16(const void *base, int64_t K, int64_t rows, int box_r
     if (r != CUDA_SUCCESS)
         return fail(WL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a k-block view of a [%lld, %lld] matrix", (int)r,
                     (long long)rows, (long long)K);
-    g_tmaps.emplace(key, m);
+    remember(key, m);
     *out = m;
     return WL_OK;
 }
@@ -165,7 +175,7 @@ wl_status tmap_rows_u8(const void *base, int64_t row_bytes, int64_t rows, int bo
     if (r != CUDA_SUCCESS)
         return fail(WL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld rows of %lld bytes", (int)r, (long long)rows,
                     (long long)row_bytes);
-    g_tmaps.emplace(key, m);
+    remember(key, m);
     *out = m;
     return WL_OK;
 }
