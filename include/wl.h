@@ -333,8 +333,9 @@ typedef struct {
 
 /*
  * Rotary positions.  Pair i of a head turns by position * phase[i] * 2^-64
- * turns (the product wraps at one turn, so the angle of any position is exact
- * to 2^-32 turn); cos and sin are multiplied by amplitude.  Pairs are
+ * turns; the product wraps at one turn, so no position loses accuracy in a range
+ * reduction.  The angle is then held in fp32, right to 2^-26 turn (9.4e-8
+ * radian); cos and sin are multiplied by amplitude.  Pairs are
  * (i, i + rot/2), or (2i, 2i + 1) if interleaved; dims >= rot are not changed.
  */
 typedef struct {
@@ -393,6 +394,19 @@ wl_status wl_cache_read(wl_cache cache, wl_seqs seqs, void *k_out, void *v_out, 
  * prompt goes through in chunks of 64.  Softmax of scale * q.k in fp32; query
  * head h reads kv head h / (q_heads / kv_heads).  A token that sees nothing,
  * and rows i >= count[b], give zeros.
+ *
+ * Number formats.  Scores, running references and sums are fp32.  bf16 caches
+ * are multiplied by q as it is and by weights of 16 bits.  e4m3 caches are
+ * multiplied by pairs of e4m3 parts, which hold 8 bits:
+ *   q: an element keeps all its bits down to 2^-14 of the largest of its row
+ *     (2^-10 where other rows of the call are up to 16 times larger), fewer
+ *     below, and is dropped below 2^-22 (2^-18).
+ *   weights p * v_scale: 8 bits down to 2^-11 of the row's largest, fewer below,
+ *     dropped below 2^-20.  What is dropped still counts in the softmax's sum,
+ *     so a result can lose 2^-20 of the largest weight for each position: 0.8 %
+ *     at most in 8192 positions, after which fp32 sums take over, and only if
+ *     nearly all of them lie just below that line.
+ *   rows of v of scale below 2^-104 count as if they had that scale.
  * q and out bf16 [batch, n, q_heads, dim], contiguous, 16-byte aligned.
  * workspace: wl_tree_attention_workspace_bytes(...) bytes (0 for invalid
  * sizes), 256-byte aligned, contents need no initialisation; calls that share
