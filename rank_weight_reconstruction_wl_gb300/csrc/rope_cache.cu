@@ -53,7 +53,7 @@ struct Raw8 {
 // One CTA per token.  `width` lanes share a row (one head of q, k or v), 8
 // elements each; a lane group has kRopeRows rows in flight.
 //   angle = frac(position * phase / 2^64) turns, from the wrapped 64-bit
-//   product, so no position loses accuracy in a range reduction;
+//   product, so no position loses accuracy in a range reduction (fp32: 2^-26 turn);
 //   (a, b) -> A (a cos - b sin, a sin + b cos);
 //   k, v: e = row exponent of max|x|, code = e4m3(x 2^-e), scale = 2^e.
 // All heads of the token share its angles (formed once, while the rows load)
@@ -61,7 +61,8 @@ struct Raw8 {
 // are whole 8-element chunks away, so that they come by shuffle; otherwise
 // pairs are neighbours (interleaved, within the lane) or the row is staged in
 // shared memory.  A row is read once and written once, but what bounds a
-// prompt is the instructions between (4096 tokens of 32 + 16 + 16 bf16 heads of
+// prompt is instruction issue, at three quarters of its rate, with the chain
+// of loads to a token's place between (4096 tokens of 32 + 16 + 16 bf16 heads of
 // 128 into an e4m3 cache: 31.9 us, 3.7 TB/s; the bytes alone would take 17.6).
 // Angles whose lanes read 64 bytes apart cost 2.7 us more, two rows in flight
 // 2 us, CTAs that walk several tokens and look ahead 5 us (spilled registers).

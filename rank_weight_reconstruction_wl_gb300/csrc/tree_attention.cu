@@ -38,7 +38,7 @@
 // TB/s (boxes of 8 KB at random pages read 6.4); 16 trees of 10 to 16 tokens on a
 // bf16 cache, 419 MB: 77 us, 5.5 TB/s.  Bound by the softmax warps'
 // instructions where it has many: 8 trees of 20 to 32 tokens, 4 query heads on
-// one kv head of 256, 18000 to 32000 positions: 52 us for 104 MB and 22 GFLOP;
+// one kv head of 256, 18000 to 32000 positions: 53 us for 104 MB and 22 GFLOP;
 // 8 of 39 to 61 tokens, 16 heads on 4, 3375 to 6000 positions: 77 us, 32 GFLOP.
 // One token on 1001 positions: 11.5 us and 6.5 us for the join, latency.
 #include <atomic>
