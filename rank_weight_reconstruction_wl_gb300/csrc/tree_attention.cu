@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             // brings what its page holds beyond; what no box brings stays as
             // it was: scores there are masked, and the softmax warps zero the
             // rows of V that a segment's last tile lacks.  A run whose page
-            // is not valid, which any tile may have, gets a box past V's last
+            // is not valid, which any tile may have, gets a box before V's first
             // row, which brings zeros.
             // Z::PACED: where a segment ends, K waits until V's last boxes have
             // been issued, and V until K has issued the boxes that come before
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
             const int runs = kTaTile / a.box;
             const uint32_t bytes = (uint32_t)(a.box * Z::SLOTROW);
             uint32_t *tab = rowtab + isv * 64;
-            const uint32_t beyond = (uint32_t)(c.npages * c.kv_heads * c.page_size);  // below 2^31 where there are boxes
+            const uint32_t ahead = (uint32_t)-a.box;
             int items = 0, last = -1;  // last: lane s's: the last item copied to slot s
             while (w.left > 0) {
                 const int t1 = ta_end(w), n = t1 - w.tile, hk = w.u / a.rtiles;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                     uint32_t row = ta_row(c, pg, hk, j);
                     if (row == ~0u && pg != -2) {
                         atomicOr(c.status, kStatusPage);
-                        if (isv) row = beyond;
+                        if (isv) row = ahead;
                     }
                     tab[(r & 1) * 32 + lane] = row;  // the other half may still be read
                     pg = pg1;
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                             uint32_t top = off >= 0 && d < c.dim ? top8(*reinterpret_cast<const uint4 *>(base + off)) : 0u;
 #pragma unroll 1
                             for (int x = CH / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-                            if (ck == 0) qexp[r] = (uint8_t)max(top >> 7, 14u);
+                            if (ck == 0) qexp[r] = (uint8_t)(top ? max(top >> 7, 14u) : 0u);
                             mn = min(mn, top - 1);
                         }
                         mn = __reduce_min_sync(0xffffffffu, mn);
@@ -834,6 +834,12 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                         // the common exponent: 2^7 if rows lie on both sides of it, so that
                         // neither it nor a row's distance from it leaves fp32's range
                         if (be - least() >= kTaSpread) spread = be = min(max(134, least()), be);
+                        // (a row of zeros takes the common one: its distance from a row's may be any)
+                        if (ck == 0)
+#pragma unroll 1
+                            for (int r = warp * RPW + lane / CH; r < RT; r += 8 * RPW)
+                                if (!qexp[r]) qexp[r] = (uint8_t)be;
+                        __syncwarp();
                     }
                     qscale *= __uint_as_float((uint32_t)(be - 7) << 23);  // 2^(be - 134)
                 }

@@ -27,6 +27,39 @@ def test_query_rows_of_very_different_sizes(wl, gpu, dtype, dim, n, group):
     assert wl.wl_device_status() == wl.WL_OK
 
 
+@pytest.mark.parametrize("n,group", [(1, 4), (5, 4), (16, 4)])
+def test_query_rows_of_zeros_beside_large_ones(wl, gpu, n, group):
+    """Rows of zeros, and rows beyond a sequence's count, beside rows that differ and are all large or all small."""
+    lens, kv, dim = [200, 37, 300], 2, 128
+    cache, seqs = filled(wl, gpu, lens, n, kv, dim, 16, E4, seed=n)
+    g = wl_synth.make_generator(n)
+    for sizes in ((16, 24), (40, 60, 70), (110, 120), (-60, -40), (-100, -120, -110)) + tuple((s, s + 6) for s in range(4, 20)):
+        e = torch.tensor(sizes)[torch.randint(0, len(sizes), (3, n, kv * group, 1), generator=g)]
+        e[:, :, ::group] = sizes[0]
+        if sizes[0] in range(4, 20):  # of one exponent
+            q = torch.randint(0, 2, (3, n, kv * group, dim), generator=g) * 2.0 - 1.0
+        else:
+            q = torch.randn(3, n, kv * group, dim, generator=g)
+        q = (q * torch.exp2(e.float())).to(BF)
+        q[:, :, 1::group] = q[:, :, ::group]
+        full = wl.wl_tree_attention(q.to(gpu), cache, seqs)
+        q[:, :, 1::group] = 0.0
+        q = q.to(gpu)
+        out = wl.wl_tree_attention(q, cache, seqs)
+        # a power of two more or less changes no row's bits, so neither does what its neighbours are
+        keep = torch.ones(kv * group, dtype=torch.bool)
+        keep[1::group] = False
+        assert torch.isfinite(full.float()).all() and torch.equal(out[:, :, keep], full[:, :, keep]), sizes
+        # a row of zeros: the mean of v
+        for b in range(3):
+            want, bound = formula(cache, seqs, q, b, chain(lens, b, n, gpu), dim ** -0.5)
+            assert bool(((out[b].double() - want).abs() <= bound)[:, ~keep].all()), sizes
+        some = wl.CacheSeqs(seqs.pages, seqs.len, n, torch.tensor([n, 0, n // 2], dtype=torch.int32, device=gpu))
+        part = wl.wl_tree_attention(q, cache, some)
+        assert torch.equal(part[0], out[0]) and bool((part[1] == 0).all()) and bool((part[2, n // 2:] == 0).all())
+    assert wl.wl_device_status() == wl.WL_OK
+
+
 @pytest.mark.parametrize("dtype", [E4, BF])
 def test_values_that_round_to_an_infinity(wl, gpu, dtype):
     """A finite value beyond the cache's type marks its row as one with an infinity: only queries that see it know."""
