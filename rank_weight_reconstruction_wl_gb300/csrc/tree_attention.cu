@@ -386,13 +386,13 @@ __device__ __forceinline__ void ta_next(TaWalk &w, const CacheArgs &c, int units
 }
 
 // A position's place in the cache, in two steps so that neither waits for the
-// other's load: the table's page (-2 past the end, -1 past the table), then
-// the row of the codes and scales, ~0 where there is none.
+// other's load: the table's page (-2 past the end, -1 past the table and for any
+// negative entry), then the row of the codes and scales, ~0 where there is none.
 __device__ __forceinline__ int ta_page(const CacheArgs &c, int b, int j, int end)
 {
     if (j >= end) return -2;
     const int p = c.page_shift >= 0 ? j >> c.page_shift : j / c.page_size;
-    return p < c.max_pages ? __ldg(c.pages + (int64_t)b * c.max_pages + p) : -1;
+    return p < c.max_pages ? max(__ldg(c.pages + (int64_t)b * c.max_pages + p), -1) : -1;
 }
 __device__ __forceinline__ uint32_t ta_row(const CacheArgs &c, int page, int hk, int j)
 {

@@ -120,7 +120,7 @@ def test_pages_that_are_not_there_in_long_contexts(wl, gpu, dtype, dim, n, page)
     cache, seqs = filled(wl, gpu, lens, n, kv, dim, page, dtype, seed=5)
     gone = [(3 * b + 1) % (600 // page) for b in range(B)]
     for b in range(B):
-        seqs.pages[b, gone[b]] = (-1, cache.pages, 1 << 30)[b % 3]
+        seqs.pages[b, gone[b]] = (-1, cache.pages, 1 << 30, -2, -(1 << 31))[b % 5]
 
     def see(b):
         m = chain(lens, b, n, gpu)
@@ -130,3 +130,13 @@ def test_pages_that_are_not_there_in_long_contexts(wl, gpu, dtype, dim, n, page)
     check(wl, cache, seqs, lens, _q(gpu, B, n, kv * G, dim, 4), see, what=f"{dtype} dim {dim} n {n} page {page}")
     assert wl.wl_device_status() == wl.WL_ERR_INVALID_ARG
     assert wl.wl_device_status() == wl.WL_OK
+
+
+@pytest.mark.parametrize("entry", [-2, -(1 << 31)])
+def test_any_negative_page_is_reported(wl, gpu, entry):
+    for dtype in (E4, BF):
+        cache, seqs = filled(wl, gpu, [700, 30], 4, 2, 128, 16, dtype)
+        seqs.pages[0, 3] = entry
+        wl.wl_tree_attention(_q(gpu, 2, 4, 4, 128, 1), cache, seqs)
+        assert wl.wl_device_status() == wl.WL_ERR_INVALID_ARG
+        assert wl.wl_device_status() == wl.WL_OK
