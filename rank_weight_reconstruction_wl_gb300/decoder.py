@@ -43,7 +43,8 @@ class BlockNorms:
 class Decoder:
     """layers: theta bundles (stack.LayerTheta); norms: one BlockNorms each;
     final: the last norm's weight.  batch sequences of up to max_len positions
-    in pages of page_size; head dim = k.out / kv_heads."""
+    in pages of page_size; head dim = k.out / kv_heads.  len (int32 [batch], on
+    the GPU) holds the lengths; beside accept(), write to it only to lower them."""
 
     def __init__(self, layers: list[LayerTheta], norms: list[BlockNorms], final: torch.Tensor, kv_heads: int, rope: RopeTable | None,
                  batch: int, max_len: int, page_size: int = 64, cache_dtype=torch.float8_e4m3fn, eps: float = 1e-6,
@@ -60,11 +61,15 @@ class Decoder:
         self.caches = [KVCache.empty(batch * per, kv_heads, page_size, self.dim, cache_dtype, dev) for _ in layers]
         self.pages = torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per).contiguous()
         self.len = torch.zeros(batch, dtype=torch.int32, device=dev)
-        self._most = 0  # no sequence is longer
+        self._most = 0  # no sequence is longer ...
+        self._known = True  # ... unless a captured step may have been replayed
         self._drafted = None
 
     def _fits(self, n: int, count: torch.Tensor | None):
-        if self._most + n <= self.max_len or torch.cuda.is_current_stream_capturing():
+        if torch.cuda.is_current_stream_capturing():
+            self._known = False
+            return
+        if self._known and self._most + n <= self.max_len:
             return
         new = n if count is None else count.clamp(0, n)
         self._most, most = torch.stack((self.len.max(), (self.len + new).max())).tolist()

@@ -199,3 +199,32 @@ def test_accept_refusals(wl, gpu):
     dec.accept(torch.zeros(2, 1, dtype=torch.int64, device=gpu))  # the step is still there
     with pytest.raises(ValueError, match="at least one token"):
         dec.prompt(_x(gpu, 2, 1)[:, :0])
+
+
+def test_a_captured_step_grows_the_sequences(wl, gpu):
+    """Replays of one captured step and accept() give what calls give; the room is checked on the lengths they left."""
+    x, buf = _x(gpu, 2, 60), torch.empty(2, SH["hidden"], device=gpu)
+    called, replayed = _decoder(wl, gpu, max_len=64), _decoder(wl, gpu, max_len=64)
+    for dec in (called, replayed):
+        dec.prompt(x[:, :20])
+    side = torch.cuda.Stream(gpu)
+    side.wait_stream(torch.cuda.current_stream(gpu))
+    with torch.cuda.stream(side):  # (what a first call sets up)
+        buf.copy_(x[:, 20])
+        replayed.step(buf, 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        h = replayed.step(buf, 1)
+        replayed.accept()
+    for t in range(20, 60):
+        buf.copy_(x[:, t])
+        graph.replay()
+        want = called.step(x[:, t].contiguous(), 1)
+        called.accept()
+        assert torch.equal(h, want), t
+    assert replayed.len.tolist() == called.len.tolist() == [60, 60]
+    with pytest.raises(ValueError, match="65 of 64"):
+        replayed.step(x[:, :5].reshape(10, -1).contiguous(), 5)
+    replayed.step(x[:, :4].reshape(8, -1).contiguous(), 4)
+    assert wl.wl_device_status() == wl.WL_OK
