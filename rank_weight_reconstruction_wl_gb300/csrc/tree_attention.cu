@@ -386,13 +386,14 @@ __device__ __forceinline__ void ta_next(TaWalk &w, const CacheArgs &c, int units
 }
 
 // A position's place in the cache, in two steps so that neither waits for the
-// other's load: the table's page (-2 past the end, -1 past the table and for any
-// negative entry), then the row of the codes and scales, ~0 where there is none.
+// other's load: the table's page (-1 past the end and past the table; nothing is
+// done with it yet, which would wait), then the row of the codes and scales, ~0
+// where there is none.
 __device__ __forceinline__ int ta_page(const CacheArgs &c, int b, int j, int end)
 {
-    if (j >= end) return -2;
+    if (j >= end) return -1;
     const int p = c.page_shift >= 0 ? j >> c.page_shift : j / c.page_size;
-    return p < c.max_pages ? max(__ldg(c.pages + (int64_t)b * c.max_pages + p), -1) : -1;
+    return p < c.max_pages ? __ldg(c.pages + (int64_t)b * c.max_pages + p) : -1;
 }
 __device__ __forceinline__ uint32_t ta_row(const CacheArgs &c, int page, int hk, int j)
 {
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 int j = w.tile * kTaTile + pw * 32 + lane;
                 auto place = [&](int t, int pg, int j) {
                     const uint32_t row = ta_row(c, pg, hk, j);
-                    if (row == ~0u && pg != -2) atomicOr(c.status, kStatusPage);
+                    if (row == ~0u && j < end) atomicOr(c.status, kStatusPage);
                     __syncwarp();  // the tile that had this table has been issued
                     tab[(t & 1) * 32 + lane] = row;
                     __syncwarp();
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tree_attention_kernel(const __g
                 if (Z::PACED && !isv && items > 0) bar_n<64>(4);
                 for (int r = 0; r < n; ++r, j += kTaTile) {
                     uint32_t row = ta_row(c, pg, hk, j);
-                    if (row == ~0u && pg != -2) {
+                    if (row == ~0u && j < end) {
                         atomicOr(c.status, kStatusPage);
                         if (isv) row = ahead;
                     }
