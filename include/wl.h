@@ -435,6 +435,106 @@ wl_status wl_norm_residual(const void *y, const void *gate, int64_t gate_stride,
                            void *stream);
 
 /*
+ * Operators between a step's last states and the next step
+ * --------------------------------------------------------
+ * The dense projection that no bundle covers (the vocabulary), the choice of
+ * the next tokens, and the cache pages of the sequences as they grow and
+ * shrink.  They launch like the decoder-layer operators (dependent launches
+ * that touch no caller memory before all ahead of them is complete).
+ *
+ * 8-bit floats with a scale for each block of 128: a matrix [rows, in] of e4m3
+ * codes (4 exponent, 3 mantissa bits, largest 448, no infinity), row-major and
+ * contiguous, and fp32 scales [ceil(in/128), ceil(rows/group)]: the value at
+ * (row, i) is code * scale[i/128][row/group].  group is 1 for activations (a
+ * scale for 128 elements of a row) and 128 for weights (128 x 128 blocks).
+ */
+
+/*
+ * wl_quant_f8 -- codes and scales of x [rows, in] (bf16 or fp32, rows x_stride
+ * elements apart).  A block's scale is the smallest power of two 2^e, e >=
+ * -126, with max|block| <= 448 * 2^e (1 for a block of zeros), so the division
+ * is exact and only the rounding to 4 significant bits is lost; codes are
+ * rounded to nearest, ties to even.  A block with a NaN or an infinity gets
+ * codes 0 and scale NaN: all of it reads as NaN.
+ * Limits: 1 <= rows <= 2^30; in a multiple of 16, 16 <= in <= 2^20; group 1 or
+ * 128; x_stride a multiple of 8, at least in; x and codes 16-byte aligned.
+ */
+wl_status wl_quant_f8(const void *x, int64_t x_stride, wl_out_dtype xdt, int64_t rows, int64_t in, int64_t group,
+                      void *codes, float *scales, void *stream);
+
+/*
+ * wl_linear_f8 -- y[t,o] = sum_b x_scale[b][t] w_scale[b][o/128] sum_{i in
+ * block b} W[o,i] x[t,i], x [T, in] and W [out, in] e4m3 codes, x_scale
+ * [ceil(in/128), T] and w_scale [ceil(in/128), ceil(out/128)] any fp32, y [T,
+ * out] of type ydt.  Products of a block are summed by the tensor cores (fp32),
+ * blocks are scaled and summed in fp32, and a result is rounded once.
+ * Limits: 1 <= T, out <= 2^30; in a multiple of 16, 16 <= in <= 2^20; x, W and
+ * y 16-byte aligned.
+ */
+wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const float *w_scale, void *y, int64_t T,
+                       int64_t in, int64_t out, wl_out_dtype ydt, void *stream);
+
+/*
+ * wl_verify -- which drafted tokens of each sequence hold, and the token after
+ * them, from given random numbers.  Node i < count[b] <= n of sequence b (count
+ * NULL: n) is a token of the last step; node 0 is known, the others are drafted:
+ * mask[b*n + i] has bit j set where node j is i or an ancestor of it (as for
+ * wl_tree_attention; NULL: a chain), and node i's parent is the highest node
+ * below i among them.  Row b*n + i of logits [batch*n, vocab] (rows
+ * logits_stride elements apart, bf16 or fp32) is the model's for the token after
+ * node i.  From u = node 0 on, with weights w_i = exp((logit_i - max) / t):
+ *     R = w;  for u's children c in order, token k = tokens[b*n + c], r =
+ *     uniforms[b*n + c], S = sum R:
+ *         accept c if  r * q_k * S < R_k:  u = c, and from the beginning;
+ *         else R = max(R - S q, 0)
+ * q: row b*n + u of draft [batch*n, vocab] (bf16 or fp32), the distribution
+ * that u's children were drawn from; draft NULL: each child is certain, q is 1
+ * at its own token.  Where no child is left, next[b] is the lowest i with R_i >
+ * 0 and R_0 + ... + R_i > uniforms[b*n] * S (the last with R_i > 0 where rounding
+ * leaves none); if R has no mass left, drawn from w.  So a sequence of accepted
+ * tokens is distributed as the model alone would draw it.  A temperature t below
+ * 1e-6 takes the most likely token, the lowest of equal ones, and accepts a
+ * child if it is that one; random numbers and draft are not used.
+ *     path[b*n ...]: the accepted nodes, node 0 first, then -1;  accepted[b]:
+ *     how many (0 where count[b] is 0, with next[b] = -1).
+ * t is temperatures[b] (device) or, where that is NULL, temperature.  Logits of
+ * -infinity are tokens of no weight.  A row with a NaN or +infinity or with no
+ * finite logit, or a t that is NaN, ends the path there with next[b] = -1.  Tokens outside
+ * [0, vocab) are rejected.  Weights, sums and decisions are held to 2^-33 of the
+ * row's sum.
+ * Limits: 1 <= batch <= 65536, 1 <= n <= 64, 1 <= vocab <= 2^24; strides at
+ * least vocab.
+ */
+wl_status wl_verify(const void *logits, int64_t logits_stride, wl_out_dtype ldt, const void *draft, int64_t draft_stride,
+                    wl_out_dtype ddt, const int32_t *tokens, const float *uniforms, const uint64_t *mask,
+                    const int32_t *count, const float *temperatures, float temperature, int64_t batch, int64_t n,
+                    int64_t vocab, int32_t *path, int32_t *accepted, int32_t *next, void *stream);
+
+/*
+ * wl_page_plan -- makes each sequence's row of the page table pages [batch,
+ * max_pages] fit len[b] + count[b] positions (count NULL: n each; n = 0: len[b]
+ * alone): need = ceil((len + count) / page_size), at most max_pages.  held[b]
+ * is how many entries of the row are in use.  Pages past need go back to the pool and
+ * their entries become -1; then missing pages are taken from it, sequences in order,
+ * all that a sequence is missing or none: once one goes without, those after it that
+ * miss pages do too.  The pool is a stack free_pages[0 .. top-1] of at most
+ * pool_pages page numbers (entries at and above top mean nothing): of the
+ * pages given back by a call the first of the first sequence ends on top, and pages
+ * are taken from the top, so a call that undoes the one before restores everything.
+ *     room[b]: how many of the count[b] new positions have pages;
+ *     slots[b*n + i] (NULL: not wanted): the cache row page * page_size + offset
+ *     of position len[b] + i, i < room[b], else -1.
+ * All of it is device memory, read and written when the kernels run; calls on one
+ * pool must not overlap.  Lengths and counts below 0 count as 0 and counts above n
+ * as n; held and top are taken as within [0, max_pages] and [0, pool_pages].
+ * Limits: 1 <= batch <= 65536, n >= 0, batch * n <= 2^30, batch * max_pages <=
+ * 2^30; max_pages and page_size as for wl_seqs; 1 <= pool_pages < 2^30.
+ */
+wl_status wl_page_plan(int32_t *free_pages, int32_t *top, int64_t pool_pages, int64_t page_size, int32_t *pages,
+                       int32_t *held, const int32_t *len, const int32_t *count, int64_t batch, int64_t max_pages,
+                       int64_t n, int32_t *room, int64_t *slots, void *stream);
+
+/*
  * wl_band_of_layer -- which of the G shared W0 blocks layer `layer` of an
  * L-layer stack uses: floor(layer * G / L) (contiguous bands).  G = L is the
  * passthrough point (one W0 per layer, "Set the fast path on NVIDIA"); G = 1

@@ -27,6 +27,7 @@ __all__ = [
     "wl_last_error", "wl_version", "wl_selftest_wait", "WLStack", "EXPORTED_SYMBOLS", "WL_OK", "WL_ERR_INVALID_ARG",
     "KVCache", "CacheSeqs", "RopeTable", "wl_rope_append", "wl_cache_read", "wl_tree_attention",
     "wl_tree_attention_workspace_bytes", "wl_norm_residual",
+    "F8Weight", "PagePool", "wl_quant_f8", "wl_linear_f8", "wl_verify", "wl_page_plan",
     "WL_ERR_UNSUPPORTED", "WL_ERR_CUDA", "WL_ERR_TIMEOUT", "WL_ERR_WORKSPACE", "WL_ERR_INTERNAL", "WL_MAX_RANK",
 ]
 
@@ -44,7 +45,8 @@ EXPORTED_SYMBOLS = ("wl_linear", "wl_qkv_fused", "wl_linear_f32", "wl_qkv_fused_
                     "wl_decompose_band", "wl_mlp_workspace_bytes", "wl_mlp_geglu_fused",
                     "wl_mlp_geglu_fused_noalloc", "wl_materialize", "wl_stack_create", "wl_stack_decode",
                     "wl_stack_destroy", "wl_rope_phases", "wl_rope_append", "wl_cache_read",
-                    "wl_tree_attention_workspace_bytes", "wl_tree_attention", "wl_norm_residual", "wl_band_of_layer", "wl_device_status", "wl_last_error", "wl_version", "wl_selftest_wait")
+                    "wl_tree_attention_workspace_bytes", "wl_tree_attention", "wl_norm_residual", "wl_quant_f8", "wl_linear_f8",
+                    "wl_verify", "wl_page_plan", "wl_band_of_layer", "wl_device_status", "wl_last_error", "wl_version", "wl_selftest_wait")
 
 
 class WLError(RuntimeError):
@@ -148,6 +150,14 @@ def lib():
         L.wl_norm_residual.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, f32, f32, f32, f32, C.c_int, C.c_int,
                                        C.c_int, vp]
         L.wl_norm_residual.restype = st
+        L.wl_quant_f8.argtypes = [vp, i64, C.c_int, i64, i64, i64, vp, vp, vp]
+        L.wl_quant_f8.restype = st
+        L.wl_linear_f8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, C.c_int, vp]
+        L.wl_linear_f8.restype = st
+        L.wl_verify.argtypes = [vp, i64, C.c_int, vp, i64, C.c_int, vp, vp, vp, vp, vp, f32, i64, i64, i64, vp, vp, vp, vp]
+        L.wl_verify.restype = st
+        L.wl_page_plan.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
+        L.wl_page_plan.restype = st
         L.wl_band_of_layer.argtypes = [i64, i64, i64]
         L.wl_band_of_layer.restype = i64
         L.wl_device_status.argtypes = [vp]
@@ -833,6 +843,205 @@ def wl_norm_residual(y, x, w_post=None, w_pre=None, gate=None, alpha: float = 1.
     _run((_lib or lib()).wl_norm_residual, x.device, stream, yp, gp, gs, xp, wp, wq, xo, hp, T, H, alpha, beta, eps, w_offset, yc,
          xc, hc)
     return (x if x_out is None else x_out), h
+
+
+# ------------------------- operators between a step's last states and the next --
+_F8 = torch.float8_e4m3fn
+
+
+def _rows_of(t, name: str, dtype, rows: int, width: int, index) -> int:
+    """Row stride in elements of a matrix [rows, width] on device `index` whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _one_device(t, name, index)
+    if t.dim() != 2 or tuple(t.shape) != (rows, width):
+        raise ValueError(f"{name} must have shape {(rows, width)}, got {tuple(t.shape)}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: each row must be contiguous")
+    return int(t.stride(0)) if rows > 1 else width
+
+
+def wl_quant_f8(x, group: int = 1, outs=None, stream=None):
+    """e4m3 codes [rows, in] and fp32 scales [ceil(in/128), ceil(rows/group)] of
+    x [rows, in] (bf16 or fp32, rows any multiple of 8 elements apart): a
+    power-of-two scale for each 128 elements of a row (group 1: activations) or
+    each 128 x 128 block (group 128: weights)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor [rows, in]")
+    rows, inp = x.shape
+    code = _ydt(x.dtype)
+    index = x.get_device() if x.is_cuda else None
+    if index is not None and x.is_contiguous():
+        xs = inp
+    else:
+        xs = _rows_of(x, "x", x.dtype, rows, inp, index)
+    shape = (-(-inp // 128), -(-rows // max(1, group)))
+    if outs is None:
+        codes, scales = _empty((rows, inp), _F8, x.device, stream), _empty(shape, torch.float32, x.device, stream)
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+    else:
+        codes, scales = outs
+        cp, sp = _checked(codes, "codes", _F8, (rows, inp), index), _checked(scales, "scales", torch.float32, shape, index)
+    _run((_lib or lib()).wl_quant_f8, x.device, stream, x.data_ptr(), xs, code, rows, inp, group, cp, sp)
+    return codes, scales
+
+
+class F8Weight:
+    """A dense weight of 8 bits: codes [out, in] float8_e4m3fn and fp32 scales
+    [ceil(in/128), ceil(out/128)]; a value is code * scale of its 128 x 128
+    block (checkpoints hold the scales transposed)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise ValueError("codes must be a tensor [out, in]")
+        _need(codes, "codes", _F8)
+        self.out, self.inp = (int(n) for n in codes.shape)
+        _need(scales, "scales", torch.float32, (-(-self.inp // 128), -(-self.out // 128)))
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales = codes, scales
+        self.device, self.index = codes.device, codes.get_device()
+        self._cp, self._sp = codes.data_ptr(), scales.data_ptr()
+
+    @classmethod
+    def quantise(cls, W: torch.Tensor, stream=None) -> "F8Weight":
+        """The nearest such weight to W [out, in] (bf16 or fp32), scales powers of two."""
+        return cls(*wl_quant_f8(W, group=128, stream=stream))
+
+
+def wl_linear_f8(codes, scales, weight: F8Weight, y=None, ydt=torch.bfloat16, stream=None):
+    """y = x W^T for x = (codes, scales) of wl_quant_f8 (any fp32 scales
+    [ceil(in/128), T]) and an F8Weight; y [T, out] bf16 or fp32."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("codes must be a tensor [T, in]")
+    index, inp = weight.index, weight.inp
+    T = codes.shape[0]
+    cp = _checked(codes, "codes", _F8, (T, inp), index)
+    sp = _checked(scales, "scales", torch.float32, (-(-inp // 128), T), index)
+    code = _ydt(ydt)
+    if y is None:
+        y = _empty((T, weight.out), _tdt(code), weight.device, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _checked(y, "y", _tdt(code), (T, weight.out), index)
+    _run((_lib or lib()).wl_linear_f8, weight.device, stream, cp, sp, weight._cp, weight._sp, yp, T, inp, weight.out, code)
+    return y
+
+
+def wl_verify(logits, tokens, uniforms, mask=None, count=None, draft=None, temperature=1.0, outs=None, stream=None):
+    """Which drafted tokens hold, and the token after them: (path [batch, n],
+    accepted [batch], next [batch]), int32, as Decoder.accept() takes them.
+
+    logits [batch * n, vocab] bf16 or fp32: row b * n + i is the model's for the
+    token after node i of sequence b; tokens int32 [batch, n] (node 0 is known,
+    the others are drafted), mask int64 [batch, n] as for wl_tree_attention
+    (None: a chain), count int32 [batch] nodes (None: n).  uniforms fp32
+    [batch, n] in [0, 1): entry i decides about node i, entry 0 draws the next
+    token.  draft [batch * n, vocab] bf16 or fp32: row b * n + u is the
+    distribution that node u's children were drawn from; None: they are certain
+    (a drafter's best tokens).  temperature: a number or fp32 [batch]; below 1e-6
+    the most likely token is taken.  n = 1 is plain sampling."""
+    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
+        raise ValueError("tokens must be a tensor [batch, n]")
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a tensor [batch * n, vocab]")
+    B, n = tokens.shape
+    V = logits.shape[1]
+    index = tokens.get_device() if tokens.is_cuda else None
+    tp = _checked(tokens, "tokens", torch.int32, None, index)
+    ldt = _ydt(logits.dtype)
+    ls = _rows_of(logits, "logits", logits.dtype, B * n, V, index)
+    up = _checked(uniforms, "uniforms", torch.float32, (B, n), index)
+    mp = cp = dp = tt = None
+    ddt, ds, temp = WL_OUT_F32, 0, 0.0
+    if mask is not None:
+        mp = _checked(mask, "mask", torch.int64, (B, n), index)
+    if count is not None:
+        cp = _checked(count, "count", torch.int32, (B,), index)
+    if draft is not None:
+        if not isinstance(draft, torch.Tensor):
+            raise TypeError("draft must be a torch.Tensor")
+        ddt = _ydt(draft.dtype)
+        ds = _rows_of(draft, "draft", draft.dtype, B * n, V, index)
+        dp = draft.data_ptr()
+    if isinstance(temperature, torch.Tensor):
+        tt = _checked(temperature, "temperature", torch.float32, (B,), index)
+    else:
+        temp = float(temperature)
+    if outs is None:
+        small = _empty((B * (n + 2),), torch.int32, tokens.device, stream)  # one allocation for the three
+        path, accepted, nxt = small[:B * n].view(B, n), small[B * n:B * n + B], small[B * n + B:]
+        pp = small.data_ptr()
+        ap, np_ = pp + 4 * B * n, pp + 4 * B * (n + 1)
+    else:
+        path, accepted, nxt = outs
+        pp = _checked(path, "path", torch.int32, (B, n), index)
+        ap, np_ = _checked(accepted, "accepted", torch.int32, (B,), index), _checked(nxt, "next", torch.int32, (B,), index)
+    _run((_lib or lib()).wl_verify, tokens.device, stream, logits.data_ptr(), ls, ldt, dp, ds, ddt, tp, up, mp, cp, tt, temp, B, n, V,
+         pp, ap, np_)
+    return path, accepted, nxt
+
+
+class PagePool:
+    """The free pages of a cache: a stack free[0 .. top - 1] (int32, on the GPU;
+    top int32 [1]) of page numbers, pages of page_size positions."""
+
+    def __init__(self, free: torch.Tensor, top: torch.Tensor, page_size: int):
+        _need(free, "free", torch.int32)
+        if free.dim() != 1:
+            raise ValueError("free must be [pages]")
+        _need(top, "top", torch.int32, (1,))
+        if free.device != top.device:
+            raise ValueError("free and top must be on one device")
+        self.free, self.top, self.page_size = free, top, int(page_size)
+        self.pages = int(free.shape[0])
+        self.device, self.index = free.device, free.get_device()
+
+    @classmethod
+    def full(cls, pages: int, page_size: int, device="cuda") -> "PagePool":
+        """All of `pages` pages free; page 0 is taken first."""
+        return cls(torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), pages, dtype=torch.int32, device=device), page_size)
+
+
+def wl_page_plan(pool: PagePool, pages, held, len, n: int = 0, count=None, slots=False, room=None, stream=None):
+    """Makes the page table pages [batch, max_pages] (int32) fit len[b] +
+    count[b] positions (n new ones each, or count[b] <= n of them): pages past
+    them go back to the pool, missing ones are taken, sequences in order, all
+    that a sequence misses or none.  held int32 [batch]: how many entries of
+    a row are in use.  pages, held and the pool are changed in place.  Returns
+    (room, slots): room int32 [batch], how many of the new positions have pages
+    (the count of CacheSeqs); slots (True, or an int64 tensor [batch, n]): cache
+    row page * page_size + offset of each new position, -1 beyond room."""
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages must be a tensor [batch, max_pages]")
+    index, dev = pool.index, pool.device
+    B, P = pages.shape
+    n = int(n)
+    pp = _checked(pages, "pages", torch.int32, None, index)
+    hp = _checked(held, "held", torch.int32, (B,), index)
+    lp = _checked(len, "len", torch.int32, (B,), index)
+    cp = None if count is None else _checked(count, "count", torch.int32, (B,), index)
+    if room is None:
+        room = _empty((B,), torch.int32, dev, stream)
+        rp = room.data_ptr()
+    else:
+        rp = _checked(room, "room", torch.int32, (B,), index)
+    sp = None
+    if slots is True:
+        slots = _empty((B, n), torch.int64, dev, stream)
+        sp = slots.data_ptr()
+    elif slots is None or slots is False:
+        slots = None
+    else:
+        sp = _checked(slots, "slots", torch.int64, (B, n), index)
+    _run((_lib or lib()).wl_page_plan, dev, stream, pool.free.data_ptr(), pool.top.data_ptr(), pool.pages, pool.page_size, pp, hp, lp, cp,
+         B, P, n, rp, sp)
+    return room, slots
 
 
 def wl_band_of_layer(layer: int, L: int, G: int) -> int:

@@ -161,6 +161,33 @@ wl_status launch_norm_residual(const void *y, const void *gate, int64_t gate_str
                                const float *w_pre, void *x_out, void *h, int64_t T, int64_t H, float alpha, float beta,
                                float eps, float w_offset, int ydt, int xdt, int hdt, cudaStream_t st);
 
+// Operators between a step's last states and the next step (quant_f8.cu, linear_f8.cu, verify.cu, page_plan.cu)
+wl_status launch_quant_f8(const void *x, int64_t x_stride, int xdt, int64_t rows, int64_t in, int64_t group, uint8_t *codes,
+                          float *scales, cudaStream_t st);
+wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale, void *y, int64_t T,
+                           int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st);
+struct VerifyArgs {
+    const void *logits, *draft;
+    int64_t logits_stride, draft_stride;
+    const int32_t *tokens;
+    const float *uniforms;
+    const uint64_t *mask;
+    const int32_t *count;
+    const float *temperatures;
+    float temperature;
+    int batch, n, vocab;
+    int32_t *path, *accepted, *next;
+};
+wl_status launch_verify(const VerifyArgs &a, int ldt, int ddt, const DeviceInfo *di, cudaStream_t st);
+struct PlanArgs {
+    int32_t *free_pages, *top, *pages, *held;
+    const int32_t *len, *count;
+    int32_t *room;
+    int64_t *slots;
+    int pool, page_size, batch, max_pages, n;
+};
+wl_status launch_page_plan(const PlanArgs &a, const DeviceInfo *di, cudaStream_t st);
+
 wl_status launch_materialize(const bf16 *W0, const float *s, const bf16 *U,
                              const bf16 *V, void *W_eff, int64_t out, int64_t in,
                              int64_t r, int dt, cudaStream_t st);
