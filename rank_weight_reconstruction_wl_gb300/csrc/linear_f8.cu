@@ -1,63 +1,362 @@
 // linear_f8.cu -- product of two e4m3 matrices with a scale for each block of
-// 128 along the sum.
+// 128 along the sum, on the fifth-generation tensor cores.
 //
 //     y[t,o] = sum_b x_scale[b][t] w_scale[b][o / 128] sum_{i in block b} W[o,i] x[t,i]
+//
+// A CTA takes a tile of 128 rows of W (M, one row of scales) by N tokens and
+// walks over the blocks of 128: TMA boxes of both operands into a ring of
+// stages, four MMAs (K = 32) into a tensor-memory accumulator of the block's
+// own, and from there, scaled, into registers: acc += d * (x_scale w_scale). So
+// the block sums are scaled in fp32 whatever the scales are, and the MMAs of the
+// next blocks run meanwhile in other accumulators.  W is M, so that one token
+// costs 16 columns, not 128 padded rows.  Where tiles are fewer than SMs the
+// sum is split over a cluster and joined through distributed shared memory.
+//
+// Warps 0-7 scale and store (4 warps per half of the tokens; a warp's lanes are
+// 32 rows of W), warp 8 loads, warp 9 multiplies.
+#include <cooperative_groups.h>
+
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
+#include "tc_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace wl {
 
 struct LinearF8Args {
-    const uint8_t *x, *W;
     const float *xs, *ws;
     void *y;
     int64_t T, out;
-    int in, ob, ydt;
+    int nkb, ob, nt;  // blocks of 128 along the sum, along out; token tiles
+    int64_t tiles;
+    unsigned *status;
 };
 
-// A 32 x 32 tile per CTA, two rows of outputs per thread.
-__global__ void __launch_bounds__(512) linear_f8_kernel(const __grid_constant__ LinearF8Args a)
+constexpr int kF8Threads = 320;
+
+template <int N>
+struct F8Shape {
+    static constexpr int STAGE = 16384 + N * 128;
+    static constexpr int NST = 200 * 1024 / STAGE;
+    static constexpr int NB = N == 256 ? 2 : 4;  // accumulators
+    static constexpr int COLS = N * NB;          // 64 .. 512: a power of two
+    static constexpr int HALF = N / 2;           // tokens of a warp
+    static constexpr int SCALES = 8 * 2 * HALF * 4;
+    static constexpr int SMEM = 1024 + NST * STAGE + SCALES;
+};
+
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t f8_idesc(int M, int N)
 {
-    __shared__ float xt[32][33], wt[32][33];
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+template <int C>
+__device__ __forceinline__ void f8_tmem_ld(uint32_t taddr, uint32_t *r)
+{
+    if constexpr (C == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+    }
+}
+// Waits for this thread's loads; the registers are operands so that nothing reads them before.
+template <int C>
+__device__ __forceinline__ void f8_tmem_wait(uint32_t *r)
+{
+    if constexpr (C == 8) {
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+    } else {
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                       "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+    }
+}
+
+// acc += d * s for two columns.
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t d0, uint32_t d1, uint64_t s)
+{
+    asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
+}
+
+// One column pair of a warp's rows: two fp32 rows of 32, or, bf16 and out even, 4 bytes a lane.
+template <int HALF>
+__device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t t0, int64_t o, const float v[HALF])
+{
+    const int lane = threadIdx.x % 32;
+    if (ydt == WL_OUT_F32) {
+        float *y = static_cast<float *>(a.y);
+        if (o < a.out)
+#pragma unroll
+            for (int c = 0; c < HALF; ++c)
+                if (t0 + c < a.T) y[(t0 + c) * a.out + o] = v[c];
+    } else if (a.out % 2 == 0) {
+        bf16 *y = static_cast<bf16 *>(a.y);
+        const int odd = lane & 1;
+#pragma unroll
+        for (int c = 0; c < HALF; c += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
+            const uint32_t two = odd ? bf16x2_bits(other, v[c + 1]) : bf16x2_bits(v[c], other);
+            const int64_t t = t0 + c + odd;
+            if (t < a.T && o - odd < a.out) *reinterpret_cast<uint32_t *>(y + t * a.out + o - odd) = two;
+        }
+    } else {
+        bf16 *y = static_cast<bf16 *>(a.y);
+        if (o < a.out)
+#pragma unroll
+            for (int c = 0; c < HALF; ++c)
+                if (t0 + c < a.T) y[(t0 + c) * a.out + o] = __float2bfloat16_rn(v[c]);
+    }
+}
+
+// SPLIT: the cluster's CTAs share a tile, each a run of blocks.
+template <int N, bool SPLIT>
+__global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_constant__ LinearF8Args a,
+                                                                  const __grid_constant__ CUtensorMap wmap,
+                                                                  const __grid_constant__ CUtensorMap xmap, int ydt)
+{
+    using S = F8Shape<N>;
+    extern __shared__ char f8_smem[];
+    __shared__ uint64_t full[S::NST], empty[S::NST], tfull[S::NB], tempty[S::NB], drain;
+    __shared__ uint32_t tmem_hold;
+    __shared__ int gave_up;
+    char *ring = f8_smem + (1024 - s32(f8_smem) % 1024) % 1024;
+    float *scales = reinterpret_cast<float *>(ring + S::NST * S::STAGE);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = SPLIT ? (int)cl.block_rank() : 0, ctas = SPLIT ? (int)cl.num_blocks() : 1;
+    const int kb0 = SPLIT ? (int)((int64_t)a.nkb * rank / ctas) : 0, kb1 = SPLIT ? (int)((int64_t)a.nkb * (rank + 1) / ctas) : a.nkb;
+    const int64_t first = SPLIT ? blockIdx.x / ctas : blockIdx.x, step = SPLIT ? gridDim.x / ctas : gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::NST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < S::NB; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 8);
+        mbar_init(&drain, 1);
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(S::COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_hold;
     pdl_wait();
     pdl_trigger();
-    const int64_t o0 = (int64_t)blockIdx.x * 32, t0 = (int64_t)blockIdx.y * 32;
-    const int i = threadIdx.x % 32, j = threadIdx.x / 32;
-    float acc[2] = {0.0f, 0.0f}, part[2] = {0.0f, 0.0f};
-    for (int k0 = 0; k0 < a.in; k0 += 32) {
-        for (int r = j; r < 32; r += 16) {
-            const bool in = k0 + i < a.in;
-            xt[r][i] = in && t0 + r < a.T ? e4m3x2_f32(a.x[(t0 + r) * a.in + k0 + i]).x : 0.0f;
-            wt[r][i] = in && o0 + r < a.out ? e4m3x2_f32(a.W[(o0 + r) * a.in + k0 + i]).x : 0.0f;
+
+    uint32_t issued = 0;  // ring items of the loading thread
+    if (warp == 8) {
+        if (lane == 0) {
+            bool good = true;
+            for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+                const int64_t mt = tile / a.nt;
+                const int o0 = (int)(mt * 128), t0 = (int)(tile - mt * a.nt) * N;
+                for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+                    const int st = issued % S::NST;
+                    if (issued >= S::NST && !ring_wait_empty(&empty[st], (issued / S::NST - 1) & 1, a.status)) {
+                        good = false;
+                        break;
+                    }
+                    char *p = ring + st * S::STAGE;
+                    mbar_expect_tx(&full[st], S::STAGE);
+                    tma_load_2d(p, &wmap, kb * 128, o0, &full[st]);
+                    tma_load_2d(p + 16384, &xmap, kb * 128, t0, &full[st]);
+                }
+            }
+            if (!good) gave_up = 1;
         }
-        __syncthreads();
+    } else if (warp == 9) {
+        if (lane == 0) {
+            uint32_t item = 0, blk = 0;
+            bool good = true;
+            for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++item, ++blk) {
+                    const int st = item % S::NST, buf = blk % S::NB;
+                    if ((blk >= S::NB && !mbar_wait(&tempty[buf], (blk / S::NB - 1) & 1, a.status, kWaitRingEmpty)) ||
+                        !ring_wait(&full[st], (item / S::NST) & 1, a.status)) {
+                        good = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = sdesc(s32(ring + st * S::STAGE)), db = sdesc(s32(ring + st * S::STAGE + 16384));
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-            for (int h = 0; h < 2; ++h) part[h] = fmaf(wt[i][k], xt[j + 16 * h][k], part[h]);
-        __syncthreads();
-        if ((k0 + 32) % 128 == 0 || k0 + 32 >= a.in) {
-            const int64_t b = k0 / 128;
-            for (int h = 0; h < 2; ++h) {
-                const int64_t t = t0 + j + 16 * h, o = o0 + i;
-                if (t < a.T && o < a.out) acc[h] = fmaf(part[h], a.xs[b * a.T + t] * a.ws[b * a.ob + o / 128], acc[h]);
-                part[h] = 0.0f;
+                    for (int j = 0; j < 4; ++j) f8_mma(tmem + buf * N, da + 2 * j, db + 2 * j, f8_idesc(128, N), j > 0);
+                    umma_commit(&empty[st]);
+                    umma_commit(&tfull[buf]);
+                }
+            }
+            if (!good) {
+                gave_up = 1;
+                umma_commit(&drain);
+                mbar_wait(&drain, 0, a.status, kWaitDrain);
             }
         }
+    } else {
+        const int half = warp / 4, quarter = warp % 4;
+        float *mine = scales + warp * 2 * S::HALF;
+        constexpr int C = S::HALF < 16 ? 8 : 16;         // columns of a tensor-memory load
+        constexpr int PER = (S::HALF + 31) / 32;         // scales of a lane
+        uint32_t blk = 0;
+        bool good = true;
+        for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+            const int64_t mt = tile / a.nt;
+            const int64_t t0 = (tile - mt * a.nt) * N + half * S::HALF;
+            uint64_t acc[S::HALF / 2];
+#pragma unroll
+            for (int i = 0; i < S::HALF / 2; ++i) acc[i] = 0;
+            float sc[PER];
+            auto fetch = [&](int kb) {
+                const float w = __ldg(a.ws + (int64_t)kb * a.ob + mt);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int c = lane + 32 * i;
+                    sc[i] = c < S::HALF && t0 + c < a.T ? w * __ldg(a.xs + (int64_t)kb * a.T + t0 + c) : 0.0f;
+                }
+            };
+            fetch(kb0);
+            for (int kb = kb0; kb < kb1; ++kb, ++blk) {
+                float *s = mine + (blk & 1) * S::HALF;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (lane + 32 * i < S::HALF) s[lane + 32 * i] = sc[i];
+                if (kb + 1 < kb1) fetch(kb + 1);
+                __syncwarp();
+                const int buf = blk % S::NB;
+                if (!mbar_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
+                    good = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * N + half * S::HALF;
+#pragma unroll
+                for (int c = 0; c < S::HALF; c += C) {
+                    uint32_t d[C];
+                    f8_tmem_ld<C>(at + c, d);
+                    f8_tmem_wait<C>(d);
+                    if (c + C == S::HALF) {
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive(&tempty[buf]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < C; i += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(s + c + i);
+                        fma2(acc[(c + i) / 2], d[i], d[i + 1], f.x);
+                        fma2(acc[(c + i) / 2 + 1], d[i + 2], d[i + 3], f.y);
+                    }
+                }
+            }
+            if (!good) break;
+            float v[S::HALF];
+#pragma unroll
+            for (int i = 0; i < S::HALF / 2; ++i)
+                v[2 * i] = __uint_as_float((uint32_t)acc[i]), v[2 * i + 1] = __uint_as_float((uint32_t)(acc[i] >> 32));
+            if (!SPLIT) {
+                f8_store<S::HALF>(a, ydt, t0, mt * 128 + quarter * 32 + lane, v);
+            } else {
+                // the ring is idle: all of this CTA's blocks have been multiplied
+                float *part = reinterpret_cast<float *>(ring);
+#pragma unroll
+                for (int c = 0; c < S::HALF; ++c) part[(half * S::HALF + c) * 128 + quarter * 32 + lane] = v[c];
+            }
+        }
+        if (!good && lane == 0) gave_up = 1;
     }
-    for (int h = 0; h < 2; ++h) {
-        const int64_t t = t0 + j + 16 * h, o = o0 + i;
-        if (t < a.T && o < a.out) store_out(a.y, a.ydt, t * a.out + o, acc[h]);
+    __syncwarp();
+    if (SPLIT) {
+        cl.sync();
+        // columns dealt out over the CTAs; contributions in CTA order
+        const int64_t mt = first / a.nt, t0 = (first - mt * a.nt) * N;
+        for (int i = threadIdx.x; i < (N + ctas - 1) / ctas * 128; i += kF8Threads) {
+            const int c = i / 128 * ctas + rank, row = i % 128;
+            const int64_t t = t0 + c, o = mt * 128 + row;
+            if (c < N && t < a.T && o < a.out) {
+                float v = 0.0f;
+                for (int r = 0; r < ctas; ++r) v += cl.map_shared_rank(reinterpret_cast<float *>(ring), r)[c * 128 + row];
+                store_out(a.y, ydt, t * a.out + o, v);
+            }
+        }
+        cl.sync();
     }
+    tc_fence_before();
+    __syncthreads();
+    if (gave_up && threadIdx.x == 256) {
+        // copies in flight land before this CTA ends
+        for (uint32_t i = issued > S::NST ? issued - S::NST : 0; i < issued; ++i)
+            mbar_wait(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::COLS));
+}
+
+template <int N, bool SPLIT>
+static cudaError_t f8_launch(const LinearF8Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, int ydt, int ctas, unsigned grid,
+                             cudaStream_t st)
+{
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_kernel<N, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, F8Shape<N>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kF8Threads);
+    cfg.dynamicSmemBytes = F8Shape<N>::SMEM;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = SPLIT ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_f8_kernel<N, SPLIT>, a, wmap, xmap, ydt);
+}
+
+template <int N>
+static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int64_t in, int ydt, const DeviceInfo *di, cudaStream_t st)
+{
+    CUtensorMap wmap, xmap;
+    wl_status s = tmap_rows_u8(W, in, a.out, 128, &wmap);
+    if (s != WL_OK) return s;
+    s = tmap_rows_u8(x, in, a.T, N, &xmap);
+    if (s != WL_OK) return s;
+    a.nt = (int)((a.T + N - 1) / N);
+    a.tiles = (int64_t)a.ob * a.nt;
+    int ctas = 1;
+    while (ctas < 8 && a.tiles * ctas * 2 <= di->sm_count && a.nkb >= 2 * ctas * 2) ctas *= 2;
+    const int64_t grid = ctas > 1 ? a.tiles * ctas : a.tiles < di->sm_count ? a.tiles : di->sm_count;
+    const cudaError_t e = ctas > 1 ? f8_launch<N, true>(a, wmap, xmap, ydt, ctas, (unsigned)grid, st)
+                                   : f8_launch<N, false>(a, wmap, xmap, ydt, 1, (unsigned)grid, st);
+    return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 
 wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale, void *y, int64_t T,
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
-    (void)di;
-    if (T > 32 * 65535) return fail(WL_ERR_UNSUPPORTED, "T = %lld", (long long)T);
-    const LinearF8Args a{x, W, x_scale, w_scale, y, T, out, (int)in, (int)((out + 127) / 128), ydt};
-    const cudaError_t e = launch_dependent(linear_f8_kernel, dim3((unsigned)((out + 31) / 32), (unsigned)((T + 31) / 32)), 512, 0, st, a);
-    return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
+    const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 0, di->status};
+    if (T <= 16) return f8_run<16>(a, x, W, in, ydt, di, st);
+    if (T <= 32) return f8_run<32>(a, x, W, in, ydt, di, st);
+    if (T <= 64) return f8_run<64>(a, x, W, in, ydt, di, st);
+    if (T <= 128) return f8_run<128>(a, x, W, in, ydt, di, st);
+    return f8_run<256>(a, x, W, in, ydt, di, st);
 }
 
 }  // namespace wl
