@@ -90,39 +90,64 @@ __device__ __forceinline__ void f8_tmem_wait(uint32_t *r)
     }
 }
 
+// The bounded wait without a call: code that holds the sums in registers would have to save them around one, and
+// register splits allow none.  CLUSTER: others of the cluster arrive.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool f8_wait(uint64_t *bar, unsigned parity, unsigned *status, unsigned site)
+{
+    if (CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+    const long long t0 = wait_clock();
+    while (!(CLUSTER ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity))) {
+        if (wait_clock() - t0 > kWaitLimitCycles) {
+            atomicOr(status, kStatusTimeout | site);
+            return false;
+        }
+    }
+    return true;
+}
+
 // acc += d * s for two columns.
 __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t d0, uint32_t d1, uint64_t s)
 {
     asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
 }
 
-// One column pair of a warp's rows: two fp32 rows of 32, or, bf16 and out even, 4 bytes a lane.
-template <int HALF>
-__device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t t0, int64_t o, const float v[HALF])
+__device__ __forceinline__ float f8_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f8_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// A warp's 32 rows of W (row o its lane's) by COLS tokens from t0 on; pairs of tokens in acc.
+template <int COLS>
+__device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t t0, int64_t o, const uint64_t acc[COLS / 2])
 {
-    const int lane = threadIdx.x % 32;
+    const int n = (int)min((int64_t)COLS, a.T - t0);
     if (ydt == WL_OUT_F32) {
-        float *y = static_cast<float *>(a.y);
+        float *y = static_cast<float *>(a.y) + t0 * a.out + o;
         if (o < a.out)
 #pragma unroll
-            for (int c = 0; c < HALF; ++c)
-                if (t0 + c < a.T) y[(t0 + c) * a.out + o] = v[c];
+            for (int c = 0; c < COLS; ++c) {
+                if (c < n) *y = c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]);
+                y += a.out;
+            }
     } else if (a.out % 2 == 0) {
-        bf16 *y = static_cast<bf16 *>(a.y);
-        const int odd = lane & 1;
+        // neighbouring lanes trade halves: 4 bytes of one token each
+        const int odd = threadIdx.x & 1;
+        bf16 *y = static_cast<bf16 *>(a.y) + (t0 + odd) * a.out + o - odd;
+        const bool in = o - odd < a.out;
 #pragma unroll
-        for (int c = 0; c < HALF; c += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-            const uint32_t two = odd ? bf16x2_bits(other, v[c + 1]) : bf16x2_bits(v[c], other);
-            const int64_t t = t0 + c + odd;
-            if (t < a.T && o - odd < a.out) *reinterpret_cast<uint32_t *>(y + t * a.out + o - odd) = two;
+        for (int c = 0; c < COLS; c += 2) {
+            const float lo = f8_lo(acc[c / 2]), hi = f8_hi(acc[c / 2]);
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            if (in && c + odd < n) *reinterpret_cast<uint32_t *>(y) = odd ? bf16x2_bits(other, hi) : bf16x2_bits(lo, other);
+            y += 2 * a.out;
         }
     } else {
-        bf16 *y = static_cast<bf16 *>(a.y);
+        bf16 *y = static_cast<bf16 *>(a.y) + t0 * a.out + o;
         if (o < a.out)
 #pragma unroll
-            for (int c = 0; c < HALF; ++c)
-                if (t0 + c < a.T) y[(t0 + c) * a.out + o] = __float2bfloat16_rn(v[c]);
+            for (int c = 0; c < COLS; ++c) {
+                if (c < n) *y = __float2bfloat16_rn(c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]));
+                y += a.out;
+            }
     }
 }
 
@@ -241,7 +266,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
                 if (kb + 1 < kb1) fetch(kb + 1);
                 __syncwarp();
                 const int buf = blk % S::NB;
-                if (!mbar_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
+                if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
                     good = false;
                     break;
                 }
@@ -265,17 +290,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
                 }
             }
             if (!good) break;
-            float v[S::HALF];
-#pragma unroll
-            for (int i = 0; i < S::HALF / 2; ++i)
-                v[2 * i] = __uint_as_float((uint32_t)acc[i]), v[2 * i + 1] = __uint_as_float((uint32_t)(acc[i] >> 32));
             if (!SPLIT) {
-                f8_store<S::HALF>(a, ydt, t0, mt * 128 + quarter * 32 + lane, v);
+                f8_store<S::HALF>(a, ydt, t0, mt * 128 + quarter * 32 + lane, acc);
             } else {
                 // the ring is idle: all of this CTA's blocks have been multiplied
                 float *part = reinterpret_cast<float *>(ring);
 #pragma unroll
-                for (int c = 0; c < S::HALF; ++c) part[(half * S::HALF + c) * 128 + quarter * 32 + lane] = v[c];
+                for (int c = 0; c < S::HALF; ++c) part[(half * S::HALF + c) * 128 + quarter * 32 + lane] = c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]);
             }
         }
         if (!good && lane == 0) gave_up = 1;
@@ -348,15 +369,324 @@ static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int6
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 
+// ------------------------------------------------------------- many tokens --
+// Tokens are M and 256 rows of W are N: a lane's sums belong to one token and a
+// warp's to one row of W's scales, so a block is scaled by one number a lane.
+// (With W as M the scales come by column, 512 bytes of shared-memory reads for
+// 32 columns: a tile of 256 tokens took 1.39 us a block, bound by that memory.)
+// PAIR: two SMs share a tile of 256 tokens by 256 rows: each loads its 128 tokens
+// and half of the rows, one MMA of M = 256 reads both, and each SM holds its
+// tokens' 128 x 256 sums; an SM so fetches 32 KB for a block where it would
+// need 48 KB alone.  Warps 0-7 scale and store (a warp: 32 tokens by 128 rows),
+// warp 8 loads, warp 9 (of the pair's first CTA) multiplies.
+template <bool PAIR>
+struct F8Many {
+    static constexpr int N = 256;
+    static constexpr int XBYTES = 128 * 128;
+    static constexpr int WBYTES = (PAIR ? 128 : 256) * 128;
+    static constexpr int STAGE = XBYTES + WBYTES;
+    static constexpr int NST = PAIR ? 6 : 4;
+    static constexpr int NB = 2;
+    static constexpr int HALF = 128;
+    static constexpr int THREADS = 384;
+    static constexpr int SMEM = 1024 + NST * STAGE;
+};
+
+__device__ __forceinline__ uint32_t in_cta(const void *p, unsigned rank)  // the same place in another CTA of the cluster
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(s32(p)), "r"(rank));
+    return r;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void f8_many_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+{
+    if constexpr (PAIR) {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void f8_many_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc)
+{
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(f8_idesc(256, 256)), "r"(acc));
+    } else {
+        f8_mma(d, a, b, f8_idesc(128, 256), acc);
+    }
+}
+
+// Arrives on the barrier (of both CTAs) once all MMAs so far are complete.
+template <bool PAIR>
+__device__ __forceinline__ void f8_many_commit(uint64_t *bar)
+{
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(s32(bar)),
+                     "h"((uint16_t)3)
+                     : "memory");
+    } else {
+        umma_commit(bar);
+    }
+}
+
+// acc += d * s for 16 columns.
+__device__ __forceinline__ void f8_scale16(uint64_t *acc, const uint32_t *d, uint64_t s)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) fma2(acc[i / 2], d[i], d[i + 1], s);
+}
+
+// A lane's row of 128 outputs from y on, the first n of them in the matrix.
+__device__ __forceinline__ void f8_store_row(void *y, int ydt, int64_t at, int n, bool vec, const uint64_t acc[64])
+{
+    if (ydt == WL_OUT_F32) {
+        float *p = static_cast<float *>(y) + at;
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+            if (vec && c + 4 <= n) {
+                *reinterpret_cast<float4 *>(p + c) = make_float4(f8_lo(acc[c / 2]), f8_hi(acc[c / 2]), f8_lo(acc[c / 2 + 1]), f8_hi(acc[c / 2 + 1]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < n) p[c + i] = i & 1 ? f8_hi(acc[(c + i) / 2]) : f8_lo(acc[(c + i) / 2]);
+            }
+        }
+    } else {
+        bf16 *p = static_cast<bf16 *>(y) + at;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+            if (vec && c + 8 <= n) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = bf16x2_bits(f8_lo(acc[c / 2 + i]), f8_hi(acc[c / 2 + i]));
+                *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < n) p[c + i] = __float2bfloat16_rn(i & 1 ? f8_hi(acc[(c + i) / 2]) : f8_lo(acc[(c + i) / 2]));
+            }
+        }
+    }
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kernel(const __grid_constant__ LinearF8Args a,
+                                                                                 const __grid_constant__ CUtensorMap wmap,
+                                                                                 const __grid_constant__ CUtensorMap xmap, int ydt)
+{
+    using S = F8Many<PAIR>;
+    extern __shared__ char f8_smem[];
+    __shared__ uint64_t full[S::NST], empty[S::NST], tfull[S::NB], tempty[S::NB], drain;
+    __shared__ uint32_t tmem_hold;
+    __shared__ int gave_up;
+    char *ring = f8_smem + (1024 - s32(f8_smem) % 1024) % 1024;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = PAIR ? (int)cl.block_rank() : 0;
+    constexpr int CTAS = PAIR ? 2 : 1;
+    const int64_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::NST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < S::NB; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 8 * CTAS);
+        mbar_init(&drain, 1);
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(512));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(512));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    tc_fence_before();
+    if (PAIR) cl.sync();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_hold;
+    pdl_wait();
+    pdl_trigger();
+
+    uint32_t issued = 0;  // ring items of the loading thread
+    if (warp >= 8) {
+        // the third warpgroup gives registers to the other two: 384 x 168 = 128 x 40 + 256 x 232
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 8 && lane == 0) {
+            bool good = true;
+            for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+                const int64_t mt = tile / a.nt;
+                const int o0 = (int)(mt * 256) + rank * 128, t0 = (int)(tile - mt * a.nt) * 128 * CTAS + rank * 128;
+                for (int kb = 0; kb < a.nkb; ++kb, ++issued) {
+                    const int st = issued % S::NST;
+                    if (issued >= S::NST && !f8_wait<PAIR>(&empty[st], (issued / S::NST - 1) & 1, a.status, kWaitRingEmpty)) {
+                        good = false;
+                        break;
+                    }
+                    const uint32_t p = s32(ring + st * S::STAGE), bar = PAIR ? in_cta(&full[st], 0) : s32(&full[st]);
+                    if (rank == 0) mbar_expect_tx(&full[st], CTAS * S::STAGE);  // both CTAs' bytes
+                    f8_many_load<PAIR>(p, &xmap, kb * 128, t0, bar);
+                    f8_many_load<PAIR>(p + S::XBYTES, &wmap, kb * 128, o0, bar);
+                }
+            }
+            if (!good) gave_up = 1;
+        } else if (warp == 9 && lane == 0 && rank == 0) {
+            uint32_t item = 0;
+            bool good = true;
+            for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+                for (int kb = 0; kb < a.nkb; ++kb, ++item) {
+                    const int st = item % S::NST, buf = item % S::NB;
+                    if ((item >= S::NB && !f8_wait<PAIR>(&tempty[buf], (item / S::NB - 1) & 1, a.status, kWaitRingEmpty)) ||
+                        !f8_wait<PAIR>(&full[st], (item / S::NST) & 1, a.status, kWaitRingFull)) {
+                        good = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = sdesc(s32(ring + st * S::STAGE)), db = sdesc(s32(ring + st * S::STAGE + S::XBYTES));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f8_many_mma<PAIR>(tmem + buf * S::N, da + 2 * j, db + 2 * j, j > 0);
+                    f8_many_commit<PAIR>(&empty[st]);
+                    f8_many_commit<PAIR>(&tfull[buf]);
+                }
+            }
+            if (!good) {
+                gave_up = 1;
+                f8_many_commit<PAIR>(&drain);
+                f8_wait<PAIR>(&drain, 0, a.status, kWaitDrain);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int half = warp / 4, quarter = warp % 4;
+        uint32_t blk = 0;
+        bool good = true;
+        for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+            const int64_t mt = tile / a.nt;
+            const int64_t o0 = mt * 256 + half * S::HALF, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
+            const float *wsp = a.ws + min(o0 / 128, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
+            uint64_t acc[S::HALF / 2];
+#pragma unroll
+            for (int i = 0; i < S::HALF / 2; ++i) acc[i] = 0;
+            float ws = __ldg(wsp), xs = __ldg(xsp);
+            for (int kb = 0; kb < a.nkb; ++kb, ++blk) {
+                const float f = ws * xs;
+                uint64_t s;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f)));
+                if (kb + 1 < a.nkb) {
+                    wsp += a.ob, xsp += a.T;
+                    ws = __ldg(wsp), xs = __ldg(xsp);
+                }
+                const int buf = blk % S::NB;
+                if (!f8_wait<PAIR>(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
+                    good = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * S::N + half * S::HALF;
+                uint32_t d0[16], d1[16];
+                f8_tmem_ld<16>(at, d0);
+#pragma unroll
+                for (int c = 0; c < S::HALF; c += 32) {  // a load in flight while the one before is scaled
+                    f8_tmem_wait<16>(d0);
+                    f8_tmem_ld<16>(at + c + 16, d1);
+                    f8_scale16(acc + c / 2, d0, s);
+                    f8_tmem_wait<16>(d1);
+                    if (c + 32 < S::HALF) {
+                        f8_tmem_ld<16>(at + c + 32, d0);
+                    } else {
+                        tc_fence_before();
+                        if (lane == 0) {
+                            if (PAIR) mbar_arrive_remote(&tempty[buf], 0);
+                            else mbar_arrive(&tempty[buf]);
+                        }
+                    }
+                    f8_scale16(acc + c / 2 + 8, d1, s);
+                }
+            }
+            if (!good) break;
+            if (t < a.T && o0 < a.out)
+                f8_store_row(a.y, ydt, t * a.out + o0, (int)min((int64_t)128, a.out - o0), a.out % (ydt == WL_OUT_F32 ? 4 : 8) == 0, acc);
+        }
+        if (!good && lane == 0) gave_up = 1;
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (gave_up && threadIdx.x == 256 && rank == 0) {
+        // copies in flight (both CTAs') land before a CTA ends
+        for (uint32_t i = issued > S::NST ? issued - S::NST : 0; i < issued; ++i)
+            f8_wait<PAIR>(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
+    }
+    if (PAIR) cl.sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 8) {
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+    }
+}
+
+template <bool PAIR>
+static wl_status f8_run_many(LinearF8Args a, const uint8_t *x, const uint8_t *W, int64_t in, int ydt, const DeviceInfo *di,
+                             cudaStream_t st)
+{
+    using S = F8Many<PAIR>;
+    constexpr int CTAS = PAIR ? 2 : 1;
+    CUtensorMap wmap, xmap;
+    wl_status s = tmap_rows_u8(W, in, a.out, PAIR ? 128 : 256, &wmap);
+    if (s != WL_OK) return s;
+    s = tmap_rows_u8(x, in, a.T, 128, &xmap);
+    if (s != WL_OK) return s;
+    a.nt = (int)((a.T + 128 * CTAS - 1) / (128 * CTAS));
+    a.tiles = (a.out + 255) / 256 * a.nt;
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_many_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return cuda_fail(e, "wl_linear_f8 attributes");
+    const int64_t most = di->sm_count / CTAS, groups = a.tiles < most ? a.tiles : most;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CTAS;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CTAS * groups));
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, linear_f8_many_kernel<PAIR>, a, wmap, xmap, ydt);
+    return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
+}
+
 wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale, void *y, int64_t T,
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
     const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 0, di->status};
     if (T <= 16) return f8_run<16>(a, x, W, in, ydt, di, st);
     if (T <= 32) return f8_run<32>(a, x, W, in, ydt, di, st);
-    if (T <= 64) return f8_run<64>(a, x, W, in, ydt, di, st);
-    if (T <= 128) return f8_run<128>(a, x, W, in, ydt, di, st);
-    return f8_run<256>(a, x, W, in, ydt, di, st);
+    // many tokens: tiles of 256 rows, where they fill half of the SMs
+    const int64_t wide = (out + 255) / 256;
+    if (T > 128 && wide * ((T + 255) / 256) * 4 >= di->sm_count) return f8_run_many<true>(a, x, W, in, ydt, di, st);
+    if (T > 64 && wide * ((T + 127) / 128) * 2 >= di->sm_count) return f8_run_many<false>(a, x, W, in, ydt, di, st);
+    return f8_run<64>(a, x, W, in, ydt, di, st);
 }
 
 }  // namespace wl
