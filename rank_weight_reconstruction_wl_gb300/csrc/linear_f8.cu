@@ -68,6 +68,15 @@ __device__ __forceinline__ void f8_tmem_ld(uint32_t taddr, uint32_t *r)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(taddr));
+    } else if constexpr (C == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+            "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+              "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+              "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(taddr));
     } else {
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -80,7 +89,10 @@ __device__ __forceinline__ void f8_tmem_ld(uint32_t taddr, uint32_t *r)
 template <int C>
 __device__ __forceinline__ void f8_tmem_wait(uint32_t *r)
 {
-    if constexpr (C == 8) {
+    if constexpr (C == 32) {
+        f8_tmem_wait<16>(r);
+        f8_tmem_wait<16>(r + 16);
+    } else if constexpr (C == 8) {
         asm volatile("tcgen05.wait::ld.sync.aligned;"
                      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
     } else {
@@ -399,6 +411,14 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, unsigned rank)  // the
     return r;
 }
 
+// Arrives on the barrier of the pair's first CTA.  Relaxed: what it tells is that this warp's tensor-memory loads are
+// done, which the fence before it orders; a release to the cluster waits for all of the warp's memory traffic (pairs
+// spent more than half of their time there: 216 -> 170 us for 2048 x 5376 -> 9728).
+__device__ __forceinline__ void f8_arrive_first(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
+}
+
 template <bool PAIR>
 __device__ __forceinline__ void f8_many_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
 {
@@ -444,11 +464,11 @@ __device__ __forceinline__ void f8_many_commit(uint64_t *bar)
     }
 }
 
-// acc += d * s for 16 columns.
-__device__ __forceinline__ void f8_scale16(uint64_t *acc, const uint32_t *d, uint64_t s)
+// acc += d * s for 32 columns.
+__device__ __forceinline__ void f8_scale32(uint64_t *acc, const uint32_t *d, uint64_t s)
 {
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) fma2(acc[i / 2], d[i], d[i + 1], s);
+    for (int i = 0; i < 32; i += 2) fma2(acc[i / 2], d[i], d[i + 1], s);
 }
 
 // A lane's row of 128 outputs from y on, the first n of them in the matrix.
@@ -594,31 +614,31 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
                     ws = __ldg(wsp), xs = __ldg(xsp);
                 }
                 const int buf = blk % S::NB;
-                if (!f8_wait<PAIR>(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
+                if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
                     good = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * S::N + half * S::HALF;
-                uint32_t d0[16], d1[16];
-                f8_tmem_ld<16>(at, d0);
-#pragma unroll
-                for (int c = 0; c < S::HALF; c += 32) {  // a load in flight while the one before is scaled
-                    f8_tmem_wait<16>(d0);
-                    f8_tmem_ld<16>(at + c + 16, d1);
-                    f8_scale16(acc + c / 2, d0, s);
-                    f8_tmem_wait<16>(d1);
-                    if (c + 32 < S::HALF) {
-                        f8_tmem_ld<16>(at + c + 32, d0);
-                    } else {
-                        tc_fence_before();
-                        if (lane == 0) {
-                            if (PAIR) mbar_arrive_remote(&tempty[buf], 0);
-                            else mbar_arrive(&tempty[buf]);
-                        }
-                    }
-                    f8_scale16(acc + c / 2 + 8, d1, s);
+                // two loads of 32 columns in flight; the accumulator is free once the last two have arrived
+                uint32_t d0[32], d1[32];
+                f8_tmem_ld<32>(at, d0);
+                f8_tmem_ld<32>(at + 32, d1);
+                f8_tmem_wait<32>(d0);
+                f8_tmem_wait<32>(d1);
+                f8_scale32(acc, d0, s);
+                f8_tmem_ld<32>(at + 64, d0);
+                f8_scale32(acc + 16, d1, s);
+                f8_tmem_ld<32>(at + 96, d1);
+                f8_tmem_wait<32>(d0);
+                f8_tmem_wait<32>(d1);
+                tc_fence_before();
+                if (lane == 0) {
+                    if (PAIR) f8_arrive_first(&tempty[buf]);
+                    else mbar_arrive(&tempty[buf]);
                 }
+                f8_scale32(acc + 32, d0, s);
+                f8_scale32(acc + 48, d1, s);
             }
             if (!good) break;
             if (t < a.T && o0 < a.out)
