@@ -401,7 +401,7 @@ struct F8Many {
     static constexpr int NB = 2;
     static constexpr int HALF = 128;
     static constexpr int THREADS = 384;
-    static constexpr int SMEM = 1024 + NST * STAGE;
+    static constexpr int SMEM = 1024 + NST * STAGE + 8 * 4096;
 };
 
 __device__ __forceinline__ uint32_t in_cta(const void *p, unsigned rank)  // the same place in another CTA of the cluster
@@ -471,35 +471,57 @@ __device__ __forceinline__ void f8_scale32(uint64_t *acc, const uint32_t *d, uin
     for (int i = 0; i < 32; i += 2) fma2(acc[i / 2], d[i], d[i + 1], s);
 }
 
-// A lane's row of 128 outputs from y on, the first n of them in the matrix.
-__device__ __forceinline__ void f8_store_row(void *y, int ydt, int64_t at, int n, bool vec, const uint64_t acc[64])
+// A lane's row of 128 outputs from place `at` of y on, the first n of them in the matrix.
+__device__ __forceinline__ void f8_store_row(void *y, int ydt, int64_t at, int n, const uint64_t acc[64])
 {
     if (ydt == WL_OUT_F32) {
         float *p = static_cast<float *>(y) + at;
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-            if (vec && c + 4 <= n) {
-                *reinterpret_cast<float4 *>(p + c) = make_float4(f8_lo(acc[c / 2]), f8_hi(acc[c / 2]), f8_lo(acc[c / 2 + 1]), f8_hi(acc[c / 2 + 1]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i < n) p[c + i] = i & 1 ? f8_hi(acc[(c + i) / 2]) : f8_lo(acc[(c + i) / 2]);
-            }
-        }
+        for (int c = 0; c < 128; ++c)
+            if (c < n) p[c] = c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]);
     } else {
         bf16 *p = static_cast<bf16 *>(y) + at;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-            if (vec && c + 8 <= n) {
-                uint32_t w[4];
+        for (int c = 0; c < 128; ++c)
+            if (c < n) p[c] = __float2bfloat16_rn(c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]));
+    }
+}
+
+// A warp's 32 tokens by 128 rows through its 4 KB of shared memory: boxes of 32 rows of 128 bytes, swizzled, stored by
+// TMA while the warp goes on to the next tile (16 bytes of 32 rows at a time straight from registers took 7 us a tile).
+// Boxes are clipped at the matrix's end; one that would begin there is left out.
+template <bool F32>
+__device__ __forceinline__ void f8_store_boxes(const CUtensorMap *map, char *stage, int64_t t0, int64_t o0, int64_t T, int64_t out,
+                                               const uint64_t acc[64])
+{
+    const int lane = threadIdx.x % 32;
+    constexpr int W = F32 ? 32 : 64;  // columns of a box
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = bf16x2_bits(f8_lo(acc[c / 2 + i]), f8_hi(acc[c / 2 + i]));
-                *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int b = 0; b < 128 / W; ++b) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint4 w;
+            if constexpr (F32) {
+                const uint64_t p = acc[(b * W + 4 * i) / 2], q = acc[(b * W + 4 * i) / 2 + 1];
+                w = make_uint4((uint32_t)p, (uint32_t)(p >> 32), (uint32_t)q, (uint32_t)(q >> 32));
             } else {
+                uint32_t v[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i < n) p[c + i] = __float2bfloat16_rn(i & 1 ? f8_hi(acc[(c + i) / 2]) : f8_lo(acc[(c + i) / 2]));
+                for (int k = 0; k < 4; ++k) v[k] = bf16x2_bits(f8_lo(acc[(b * W + 8 * i) / 2 + k]), f8_hi(acc[(b * W + 8 * i) / 2 + k]));
+                w = make_uint4(v[0], v[1], v[2], v[3]);
             }
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = w;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && t0 < T && o0 + b * W < out) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"((int)(o0 + b * W)), "r"((int)t0), "r"(s32(stage))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
     }
 }
@@ -507,7 +529,9 @@ __device__ __forceinline__ void f8_store_row(void *y, int ydt, int64_t at, int n
 template <bool PAIR>
 __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kernel(const __grid_constant__ LinearF8Args a,
                                                                                  const __grid_constant__ CUtensorMap wmap,
-                                                                                 const __grid_constant__ CUtensorMap xmap, int ydt)
+                                                                                 const __grid_constant__ CUtensorMap xmap,
+                                                                                 const __grid_constant__ CUtensorMap ymap, int ydt,
+                                                                                 int boxes)
 {
     using S = F8Many<PAIR>;
     extern __shared__ char f8_smem[];
@@ -595,6 +619,7 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int half = warp / 4, quarter = warp % 4;
+        char *stage = ring + S::NST * S::STAGE + warp * 4096;
         uint32_t blk = 0;
         bool good = true;
         for (int64_t tile = first; tile < a.tiles && good; tile += step) {
@@ -604,15 +629,26 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
             uint64_t acc[S::HALF / 2];
 #pragma unroll
             for (int i = 0; i < S::HALF / 2; ++i) acc[i] = 0;
-            float ws = __ldg(wsp), xs = __ldg(xsp);
-            for (int kb = 0; kb < a.nkb; ++kb, ++blk) {
-                const float f = ws * xs;
-                uint64_t s;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f)));
-                if (kb + 1 < a.nkb) {
-                    wsp += a.ob, xsp += a.T;
-                    ws = __ldg(wsp), xs = __ldg(xsp);
+            // scales come four blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time)
+            float wn[4], xn[4], f[4];
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = min(kb + i, a.nkb - 1);
+                    wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
                 }
+            };
+            fetch(0);
+#pragma unroll 1
+            for (int kb = 0; kb < a.nkb; ++kb, ++blk) {
+                if ((kb & 3) == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i];
+                    fetch(kb + 4);
+                }
+                uint64_t s;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f[0])));
+                f[0] = f[1], f[1] = f[2], f[2] = f[3];
                 const int buf = blk % S::NB;
                 if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
                     good = false;
@@ -641,9 +677,14 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
                 f8_scale32(acc + 48, d1, s);
             }
             if (!good) break;
-            if (t < a.T && o0 < a.out)
-                f8_store_row(a.y, ydt, t * a.out + o0, (int)min((int64_t)128, a.out - o0), a.out % (ydt == WL_OUT_F32 ? 4 : 8) == 0, acc);
+            if (boxes && ydt == WL_OUT_F32)
+                f8_store_boxes<true>(&ymap, stage, t - lane, o0, a.T, a.out, acc);
+            else if (boxes)
+                f8_store_boxes<false>(&ymap, stage, t - lane, o0, a.T, a.out, acc);
+            else if (t < a.T && o0 < a.out)
+                f8_store_row(a.y, ydt, t * a.out + o0, (int)min((int64_t)128, a.out - o0), acc);
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // before the memory they read goes
         if (!good && lane == 0) gave_up = 1;
     }
     __syncwarp();
@@ -669,11 +710,16 @@ static wl_status f8_run_many(LinearF8Args a, const uint8_t *x, const uint8_t *W,
 {
     using S = F8Many<PAIR>;
     constexpr int CTAS = PAIR ? 2 : 1;
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap, ymap = {};
     wl_status s = tmap_rows_u8(W, in, a.out, PAIR ? 128 : 256, &wmap);
     if (s != WL_OK) return s;
     s = tmap_rows_u8(x, in, a.T, 128, &xmap);
     if (s != WL_OK) return s;
+    const bool f32 = ydt == WL_OUT_F32, boxes = a.out % (f32 ? 4 : 8) == 0;  // a map's rows are 16 bytes apart
+    if (boxes) {
+        s = f32 ? tmap_2d_f32(a.y, a.out, a.T, 32, 32, &ymap) : tmap_2d_bf16(a.y, a.out, a.T, a.out, 64, 32, &ymap);
+        if (s != WL_OK) return s;
+    }
     a.nt = (int)((a.T + 128 * CTAS - 1) / (128 * CTAS));
     a.tiles = (a.out + 255) / 256 * a.nt;
     cudaError_t e = cudaFuncSetAttribute(linear_f8_many_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
@@ -692,7 +738,7 @@ static wl_status f8_run_many(LinearF8Args a, const uint8_t *x, const uint8_t *W,
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = PAIR ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, linear_f8_many_kernel<PAIR>, a, wmap, xmap, ydt);
+    e = cudaLaunchKernelEx(&cfg, linear_f8_many_kernel<PAIR>, a, wmap, xmap, ymap, ydt, (int)boxes);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 

@@ -89,6 +89,9 @@ wl_status tmap_kblocks_bf16(const void *base, int64_t K, int64_t rows, int box_r
 // Rows of row_bytes bytes as boxes of box_rows rows x 128 bytes (see tmap.cu).
 wl_status tmap_rows_u8(const void *base, int64_t row_bytes, int64_t rows, int box_rows, CUtensorMap *out);
 
+// Row-major fp32 matrix [outer, inner] (see tmap.cu).
+wl_status tmap_2d_f32(const void *base, int64_t inner, int64_t outer, int box_inner, int box_outer, CUtensorMap *out);
+
 // Record a message for wl_last_error() and return the status.
 wl_status fail(wl_status st, const char *fmt, ...);
 void clear_error();  // empties this thread's message (after a probe that may fail)
