@@ -61,6 +61,13 @@ __device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 
+__device__ __forceinline__ uint32_t f8_elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p;
+}
+
 template <int C>
 __device__ __forceinline__ void f8_tmem_ld(uint32_t taddr, uint32_t *r)
 {
@@ -573,46 +580,59 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
     if (warp >= 8) {
         // the third warpgroup gives registers to the other two: 384 x 168 = 128 x 40 + 256 x 232
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 8 && lane == 0) {
+        if (warp == 8) {
+            const uint32_t ring0 = s32(ring), issuer = f8_elect(), bar0 = PAIR ? in_cta(&full[0], 0) : s32(&full[0]);
+            uint32_t st = 0, phase = 1;
             bool good = true;
             for (int64_t tile = first; tile < a.tiles && good; tile += step) {
                 const int64_t mt = tile / a.nt;
                 const int o0 = (int)(mt * 256) + rank * 128, t0 = (int)(tile - mt * a.nt) * 128 * CTAS + rank * 128;
-                for (int kb = 0; kb < a.nkb; ++kb, ++issued) {
-                    const int st = issued % S::NST;
-                    if (issued >= S::NST && !f8_wait<PAIR>(&empty[st], (issued / S::NST - 1) & 1, a.status, kWaitRingEmpty)) {
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!f8_wait<PAIR>(&empty[st], phase, a.status, kWaitRingEmpty)) {
                         good = false;
                         break;
                     }
-                    const uint32_t p = s32(ring + st * S::STAGE), bar = PAIR ? in_cta(&full[st], 0) : s32(&full[st]);
-                    if (rank == 0) mbar_expect_tx(&full[st], CTAS * S::STAGE);  // both CTAs' bytes
-                    f8_many_load<PAIR>(p, &xmap, kb * 128, t0, bar);
-                    f8_many_load<PAIR>(p + S::XBYTES, &wmap, kb * 128, o0, bar);
+                    if (issuer) {
+                        const uint32_t p = ring0 + st * S::STAGE, bar = bar0 + st * 8;
+                        if (rank == 0) mbar_expect_tx(&full[st], CTAS * S::STAGE);  // both CTAs' bytes
+                        f8_many_load<PAIR>(p, &xmap, kb * 128, t0, bar);
+                        f8_many_load<PAIR>(p + S::XBYTES, &wmap, kb * 128, o0, bar);
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++st == S::NST) st = 0, phase ^= 1;
                 }
             }
             if (!good) gave_up = 1;
-        } else if (warp == 9 && lane == 0 && rank == 0) {
-            uint32_t item = 0;
+        } else if (warp == 9 && rank == 0) {
+            // The whole warp walks and waits, one lane issues: code that the compiler knows to be uniform keeps the
+            // descriptors in uniform registers (one lane alone took 630 cycles a block for MMAs of 512).
+            const uint32_t ring0 = s32(ring), issuer = f8_elect();
+            uint32_t st = 0, st_phase = 0, buf = 0, buf_phase = 1;
             bool good = true;
             for (int64_t tile = first; tile < a.tiles && good; tile += step) {
-                for (int kb = 0; kb < a.nkb; ++kb, ++item) {
-                    const int st = item % S::NST, buf = item % S::NB;
-                    if ((item >= S::NB && !f8_wait<PAIR>(&tempty[buf], (item / S::NB - 1) & 1, a.status, kWaitRingEmpty)) ||
-                        !f8_wait<PAIR>(&full[st], (item / S::NST) & 1, a.status, kWaitRingFull)) {
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!f8_wait<PAIR>(&tempty[buf], buf_phase, a.status, kWaitRingEmpty) ||
+                        !f8_wait<PAIR>(&full[st], st_phase, a.status, kWaitRingFull)) {
                         good = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t da = sdesc(s32(ring + st * S::STAGE)), db = sdesc(s32(ring + st * S::STAGE + S::XBYTES));
+                    const uint64_t da = sdesc(ring0 + st * S::STAGE), db = sdesc(ring0 + st * S::STAGE + S::XBYTES);
+                    if (issuer) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) f8_many_mma<PAIR>(tmem + buf * S::N, da + 2 * j, db + 2 * j, j > 0);
-                    f8_many_commit<PAIR>(&empty[st]);
-                    f8_many_commit<PAIR>(&tfull[buf]);
+                        for (int j = 0; j < 4; ++j) f8_many_mma<PAIR>(tmem + buf * S::N, da + 2 * j, db + 2 * j, j > 0);
+                        f8_many_commit<PAIR>(&tfull[buf]);
+                        f8_many_commit<PAIR>(&empty[st]);
+                    }
+                    __syncwarp();
+                    if (++st == S::NST) st = 0, st_phase ^= 1;
+                    if (++buf == S::NB) buf = 0, buf_phase ^= 1;
                 }
             }
             if (!good) {
                 gave_up = 1;
-                f8_many_commit<PAIR>(&drain);
+                if (issuer) f8_many_commit<PAIR>(&drain);
                 f8_wait<PAIR>(&drain, 0, a.status, kWaitDrain);
             }
         }
