@@ -400,13 +400,15 @@ static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int6
 // warp 8 loads, warp 9 (of the pair's first CTA) multiplies.
 template <bool PAIR>
 struct F8Many {
-    static constexpr int N = 256;
     static constexpr int XBYTES = 128 * 128;
     static constexpr int WBYTES = (PAIR ? 128 : 256) * 128;
     static constexpr int STAGE = XBYTES + WBYTES;
     static constexpr int NST = PAIR ? 6 : 4;
-    static constexpr int NB = 2;
-    static constexpr int HALF = 128;
+    // Accumulators: a pair's MMAs keep up only with 256 columns (a block in two halves of 128 reads the tokens twice as
+    // often: 475 us where one of 256 takes 359), so it has two; a single SM waits for W anyway and hands back halves.
+    static constexpr int COLS = PAIR ? 256 : 128;
+    static constexpr int NB = 512 / COLS;
+    static constexpr int PARTS = 256 / COLS;  // of a block
     static constexpr int THREADS = 384;
     static constexpr int SMEM = 1024 + NST * STAGE + 8 * 4096;
 };
@@ -454,7 +456,7 @@ __device__ __forceinline__ void f8_many_mma(uint32_t d, uint64_t a, uint64_t b, 
             "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(f8_idesc(256, 256)), "r"(acc));
     } else {
-        f8_mma(d, a, b, f8_idesc(128, 256), acc);
+        f8_mma(d, a, b, f8_idesc(128, 128), acc);
     }
 }
 
@@ -471,6 +473,13 @@ __device__ __forceinline__ void f8_many_commit(uint64_t *bar)
     }
 }
 
+__device__ __forceinline__ uint64_t f8_both(float f)
+{
+    uint64_t s;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f)));
+    return s;
+}
+
 // acc += d * s for 32 columns.
 __device__ __forceinline__ void f8_scale32(uint64_t *acc, const uint32_t *d, uint64_t s)
 {
@@ -478,33 +487,33 @@ __device__ __forceinline__ void f8_scale32(uint64_t *acc, const uint32_t *d, uin
     for (int i = 0; i < 32; i += 2) fma2(acc[i / 2], d[i], d[i + 1], s);
 }
 
-// A lane's row of 128 outputs from place `at` of y on, the first n of them in the matrix.
-__device__ __forceinline__ void f8_store_row(void *y, int ydt, int64_t at, int n, const uint64_t acc[64])
+// A lane's row of 64 outputs from place `at` of y on, the first n of them in the matrix.
+__device__ __forceinline__ void f8_store_row(void *y, int ydt, int64_t at, int n, const uint64_t acc[32])
 {
     if (ydt == WL_OUT_F32) {
         float *p = static_cast<float *>(y) + at;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
+        for (int c = 0; c < 64; ++c)
             if (c < n) p[c] = c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]);
     } else {
         bf16 *p = static_cast<bf16 *>(y) + at;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
+        for (int c = 0; c < 64; ++c)
             if (c < n) p[c] = __float2bfloat16_rn(c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]));
     }
 }
 
-// A warp's 32 tokens by 128 rows through its 4 KB of shared memory: boxes of 32 rows of 128 bytes, swizzled, stored by
+// A warp's 32 tokens by 64 rows through its 4 KB of shared memory: boxes of 32 rows of 128 bytes, swizzled, stored by
 // TMA while the warp goes on to the next tile (16 bytes of 32 rows at a time straight from registers took 7 us a tile).
 // Boxes are clipped at the matrix's end; one that would begin there is left out.
 template <bool F32>
 __device__ __forceinline__ void f8_store_boxes(const CUtensorMap *map, char *stage, int64_t t0, int64_t o0, int64_t T, int64_t out,
-                                               const uint64_t acc[64])
+                                               const uint64_t acc[32])
 {
     const int lane = threadIdx.x % 32;
     constexpr int W = F32 ? 32 : 64;  // columns of a box
 #pragma unroll
-    for (int b = 0; b < 128 / W; ++b) {
+    for (int b = 0; b < 64 / W; ++b) {
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
 #pragma unroll
@@ -531,6 +540,151 @@ __device__ __forceinline__ void f8_store_boxes(const CUtensorMap *map, char *sta
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
     }
+}
+
+// A warp's 32 tokens (t: the lane's) by 64 rows of W from o0 on.
+__device__ __forceinline__ void f8_store_part(const LinearF8Args &a, const CUtensorMap *map, char *stage, int ydt, int boxes, int64_t t,
+                                              int64_t o0, const uint64_t acc[32])
+{
+    const int lane = threadIdx.x % 32;
+    if (boxes && ydt == WL_OUT_F32) f8_store_boxes<true>(map, stage, t - lane, o0, a.T, a.out, acc);
+    else if (boxes) f8_store_boxes<false>(map, stage, t - lane, o0, a.T, a.out, acc);
+    else if (t < a.T && o0 < a.out) f8_store_row(a.y, ydt, t * a.out + o0, (int)min((int64_t)64, a.out - o0), acc);
+}
+
+// Scales and stores a pair's tiles, 32 tokens by the 128 rows of W of one of its SMs a warp.
+__device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUtensorMap &ymap, int ydt, int boxes, char *ring, uint32_t tmem,
+                                              uint64_t *tfull, uint64_t *tempty, int rank, int64_t first, int64_t step)
+{
+    using S = F8Many<true>;
+    constexpr int CTAS = 2;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int half = warp / 4, quarter = warp % 4;
+    char *stage = ring + S::NST * S::STAGE + warp * 4096;
+    uint32_t blk = 0;
+    bool good = true;
+    for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+        const int64_t mt = tile / a.nt;
+        const int64_t o0 = mt * 256 + half * 128, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
+        const float *wsp = a.ws + min(o0 / 128, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
+        uint64_t acc[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = 0;
+        // scales come four blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time)
+        float wn[4], xn[4], f[4];
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t k = min(kb + i, a.nkb - 1);
+                wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
+            }
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int kb = 0; kb < a.nkb; ++kb, ++blk) {
+            if ((kb & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i];
+                fetch(kb + 4);
+            }
+            const uint64_t s = f8_both(f[0]);
+            f[0] = f[1], f[1] = f[2], f[2] = f[3];
+            const int buf = blk % S::NB;
+            if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
+                good = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256 + half * 128;
+            // two loads of 32 columns in flight; the accumulator is free once the last two have arrived
+            uint32_t d0[32], d1[32];
+            f8_tmem_ld<32>(at, d0);
+            f8_tmem_ld<32>(at + 32, d1);
+            f8_tmem_wait<32>(d0);
+            f8_tmem_wait<32>(d1);
+            f8_scale32(acc, d0, s);
+            f8_tmem_ld<32>(at + 64, d0);
+            f8_scale32(acc + 16, d1, s);
+            f8_tmem_ld<32>(at + 96, d1);
+            f8_tmem_wait<32>(d0);
+            f8_tmem_wait<32>(d1);
+            tc_fence_before();
+            if (lane == 0) f8_arrive_first(&tempty[buf]);
+            f8_scale32(acc + 32, d0, s);
+            f8_scale32(acc + 48, d1, s);
+        }
+        if (!good) break;
+        f8_store_part(a, &ymap, stage, ydt, boxes, t, o0, acc);
+        f8_store_part(a, &ymap, stage, ydt, boxes, t, o0 + 64, acc + 32);
+    }
+    return good;
+}
+
+// Scales and stores a single SM's tiles, 32 tokens by 64 rows of W of each of the block's two parts a warp.
+__device__ __forceinline__ bool f8_single_tiles(const LinearF8Args &a, const CUtensorMap &ymap, int ydt, int boxes, char *ring, uint32_t tmem,
+                                                uint64_t *tfull, uint64_t *tempty, int64_t first, int64_t step)
+{
+    using S = F8Many<false>;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int side = warp / 4, quarter = warp % 4;
+    char *stage = ring + S::NST * S::STAGE + warp * 4096;
+    uint32_t buf = 0, phase = 0;
+    bool good = true;
+    for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+        const int64_t mt = tile / a.nt;
+        const int64_t t = (tile - mt * a.nt) * 128 + quarter * 32 + lane;
+        const int64_t o0 = mt * 256 + side * 64, o1 = o0 + 128;  // first row of W of each half
+        const float *wsp = a.ws + min(o0 / 128, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
+        const int64_t other = min(o1 / 128, (int64_t)a.ob - 1) - min(o0 / 128, (int64_t)a.ob - 1);
+        uint64_t acc[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = 0;
+        // scales come G blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time)
+        constexpr int G = 2;
+        float wn[G], vn[G], xn[G], f[G], g[G];
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int64_t k = min(kb + i, a.nkb - 1);
+                wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
+                vn[i] = __ldg(wsp + k * a.ob + other);
+            }
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int kb = 0; kb < a.nkb; ++kb) {
+            if (kb % G == 0) {
+#pragma unroll
+                for (int i = 0; i < G; ++i) f[i] = wn[i] * xn[i], g[i] = vn[i] * xn[i];
+                fetch(kb + G);
+            }
+            uint32_t d0[32], d1[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                good = good && f8_wait(&tfull[buf + h], phase, a.status, kWaitRingFull);
+                tc_fence_after();
+                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf + h) * 128 + side * 64;
+                const uint64_t s = f8_both(h ? g[0] : f[0]);
+                f8_tmem_ld<32>(at, d0);
+                f8_tmem_ld<32>(at + 32, d1);
+                f8_tmem_wait<32>(d0);
+                f8_tmem_wait<32>(d1);
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(&tempty[buf + h]);
+                f8_scale32(acc + 32 * h, d0, s);
+                f8_scale32(acc + 32 * h + 16, d1, s);
+            }
+            if (!good) break;
+#pragma unroll
+            for (int i = 0; i + 1 < G; ++i) f[i] = f[i + 1], g[i] = g[i + 1];
+            buf ^= 2;
+            if (buf == 0) phase ^= 1;
+        }
+        if (!good) break;
+        f8_store_part(a, &ymap, stage, ydt, boxes, t, o0, acc);
+        f8_store_part(a, &ymap, stage, ydt, boxes, t, o1, acc + 32);
+    }
+    return good;
 }
 
 template <bool PAIR>
@@ -621,13 +775,29 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
                     const uint64_t da = sdesc(ring0 + st * S::STAGE), db = sdesc(ring0 + st * S::STAGE + S::XBYTES);
                     if (issuer) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) f8_many_mma<PAIR>(tmem + buf * S::N, da + 2 * j, db + 2 * j, j > 0);
+                        for (int j = 0; j < 4; ++j) f8_many_mma<PAIR>(tmem + buf * S::COLS, da + 2 * j, db + 2 * j, j > 0);
                         f8_many_commit<PAIR>(&tfull[buf]);
-                        f8_many_commit<PAIR>(&empty[st]);
+                        if (S::PARTS == 1) f8_many_commit<PAIR>(&empty[st]);
                     }
                     __syncwarp();
+                    if constexpr (S::PARTS == 2) {
+                        if (!f8_wait<PAIR>(&tempty[buf + 1], buf_phase, a.status, kWaitRingEmpty)) {
+                            good = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (issuer) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                f8_many_mma<PAIR>(tmem + (buf + 1) * S::COLS, da + 2 * j, db + S::WBYTES / 32 + 2 * j, j > 0);
+                            f8_many_commit<PAIR>(&tfull[buf + 1]);
+                            f8_many_commit<PAIR>(&empty[st]);
+                        }
+                        __syncwarp();
+                    }
                     if (++st == S::NST) st = 0, st_phase ^= 1;
-                    if (++buf == S::NB) buf = 0, buf_phase ^= 1;
+                    buf ^= S::PARTS;
+                    if (buf == 0) buf_phase ^= 1;
                 }
             }
             if (!good) {
@@ -638,72 +808,9 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int half = warp / 4, quarter = warp % 4;
-        char *stage = ring + S::NST * S::STAGE + warp * 4096;
-        uint32_t blk = 0;
-        bool good = true;
-        for (int64_t tile = first; tile < a.tiles && good; tile += step) {
-            const int64_t mt = tile / a.nt;
-            const int64_t o0 = mt * 256 + half * S::HALF, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
-            const float *wsp = a.ws + min(o0 / 128, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
-            uint64_t acc[S::HALF / 2];
-#pragma unroll
-            for (int i = 0; i < S::HALF / 2; ++i) acc[i] = 0;
-            // scales come four blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time)
-            float wn[4], xn[4], f[4];
-            auto fetch = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t k = min(kb + i, a.nkb - 1);
-                    wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
-                }
-            };
-            fetch(0);
-#pragma unroll 1
-            for (int kb = 0; kb < a.nkb; ++kb, ++blk) {
-                if ((kb & 3) == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i];
-                    fetch(kb + 4);
-                }
-                uint64_t s;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f[0])));
-                f[0] = f[1], f[1] = f[2], f[2] = f[3];
-                const int buf = blk % S::NB;
-                if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
-                    good = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * S::N + half * S::HALF;
-                // two loads of 32 columns in flight; the accumulator is free once the last two have arrived
-                uint32_t d0[32], d1[32];
-                f8_tmem_ld<32>(at, d0);
-                f8_tmem_ld<32>(at + 32, d1);
-                f8_tmem_wait<32>(d0);
-                f8_tmem_wait<32>(d1);
-                f8_scale32(acc, d0, s);
-                f8_tmem_ld<32>(at + 64, d0);
-                f8_scale32(acc + 16, d1, s);
-                f8_tmem_ld<32>(at + 96, d1);
-                f8_tmem_wait<32>(d0);
-                f8_tmem_wait<32>(d1);
-                tc_fence_before();
-                if (lane == 0) {
-                    if (PAIR) f8_arrive_first(&tempty[buf]);
-                    else mbar_arrive(&tempty[buf]);
-                }
-                f8_scale32(acc + 32, d0, s);
-                f8_scale32(acc + 48, d1, s);
-            }
-            if (!good) break;
-            if (boxes && ydt == WL_OUT_F32)
-                f8_store_boxes<true>(&ymap, stage, t - lane, o0, a.T, a.out, acc);
-            else if (boxes)
-                f8_store_boxes<false>(&ymap, stage, t - lane, o0, a.T, a.out, acc);
-            else if (t < a.T && o0 < a.out)
-                f8_store_row(a.y, ydt, t * a.out + o0, (int)min((int64_t)128, a.out - o0), acc);
-        }
+        bool good;
+        if constexpr (PAIR) good = f8_pair_tiles(a, ymap, ydt, boxes, ring, tmem, tfull, tempty, rank, first, step);
+        else good = f8_single_tiles(a, ymap, ydt, boxes, ring, tmem, tfull, tempty, first, step);
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // before the memory they read goes
         if (!good && lane == 0) gave_up = 1;
     }
