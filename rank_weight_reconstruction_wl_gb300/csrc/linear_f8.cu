@@ -39,8 +39,8 @@ template <int N>
 struct F8Shape {
     static constexpr int STAGE = 16384 + N * 128;
     static constexpr int NST = 200 * 1024 / STAGE;
-    static constexpr int NB = N == 256 ? 2 : 4;  // accumulators
-    static constexpr int COLS = N * NB;          // 64 .. 512: a power of two
+    static constexpr int NB = 4;                 // accumulators
+    static constexpr int COLS = N * NB;          // 64 .. 256: a power of two
     static constexpr int HALF = N / 2;           // tokens of a warp
     static constexpr int SCALES = 8 * 2 * HALF * 4;
     static constexpr int SMEM = 1024 + NST * STAGE + SCALES;
@@ -207,52 +207,60 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
     pdl_wait();
     pdl_trigger();
 
-    uint32_t issued = 0;  // ring items of the loading thread
+    // The loading and the multiplying warp walk and wait whole and one lane issues: code that the compiler knows to be
+    // uniform keeps the descriptors in uniform registers.
+    uint32_t issued = 0;  // ring items of the loading warp
     if (warp == 8) {
-        if (lane == 0) {
-            bool good = true;
-            for (int64_t tile = first; tile < a.tiles && good; tile += step) {
-                const int64_t mt = tile / a.nt;
-                const int o0 = (int)(mt * 128), t0 = (int)(tile - mt * a.nt) * N;
-                for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-                    const int st = issued % S::NST;
-                    if (issued >= S::NST && !ring_wait_empty(&empty[st], (issued / S::NST - 1) & 1, a.status)) {
-                        good = false;
-                        break;
-                    }
-                    char *p = ring + st * S::STAGE;
-                    mbar_expect_tx(&full[st], S::STAGE);
-                    tma_load_2d(p, &wmap, kb * 128, o0, &full[st]);
-                    tma_load_2d(p + 16384, &xmap, kb * 128, t0, &full[st]);
+        const uint32_t ring0 = s32(ring), issuer = f8_elect();
+        uint32_t st = 0, phase = 1;
+        bool good = true;
+        for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+            const int64_t mt = tile / a.nt;
+            const int o0 = (int)(mt * 128), t0 = (int)(tile - mt * a.nt) * N;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!f8_wait(&empty[st], phase, a.status, kWaitRingEmpty)) {
+                    good = false;
+                    break;
                 }
+                if (issuer) {
+                    const uint32_t p = ring0 + st * S::STAGE;
+                    mbar_expect_tx(&full[st], S::STAGE);
+                    tma_load_2d_u32(p, &wmap, kb * 128, o0, &full[st]);
+                    tma_load_2d_u32(p + 16384, &xmap, kb * 128, t0, &full[st]);
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == S::NST) st = 0, phase ^= 1;
             }
-            if (!good) gave_up = 1;
         }
+        if (!good) gave_up = 1;
     } else if (warp == 9) {
-        if (lane == 0) {
-            uint32_t item = 0, blk = 0;
-            bool good = true;
-            for (int64_t tile = first; tile < a.tiles && good; tile += step) {
-                for (int kb = kb0; kb < kb1; ++kb, ++item, ++blk) {
-                    const int st = item % S::NST, buf = blk % S::NB;
-                    if ((blk >= S::NB && !mbar_wait(&tempty[buf], (blk / S::NB - 1) & 1, a.status, kWaitRingEmpty)) ||
-                        !ring_wait(&full[st], (item / S::NST) & 1, a.status)) {
-                        good = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t da = sdesc(s32(ring + st * S::STAGE)), db = sdesc(s32(ring + st * S::STAGE + 16384));
+        const uint32_t ring0 = s32(ring), issuer = f8_elect();
+        uint32_t st = 0, st_phase = 0, buf = 0, buf_phase = 1;
+        bool good = true;
+        for (int64_t tile = first; tile < a.tiles && good; tile += step) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!f8_wait(&tempty[buf], buf_phase, a.status, kWaitRingEmpty) || !f8_wait(&full[st], st_phase, a.status, kWaitRingFull)) {
+                    good = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = sdesc(ring0 + st * S::STAGE), db = sdesc(ring0 + st * S::STAGE + 16384);
+                if (issuer) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) f8_mma(tmem + buf * N, da + 2 * j, db + 2 * j, f8_idesc(128, N), j > 0);
-                    umma_commit(&empty[st]);
                     umma_commit(&tfull[buf]);
+                    umma_commit(&empty[st]);
                 }
+                __syncwarp();
+                if (++st == S::NST) st = 0, st_phase ^= 1;
+                if (++buf == S::NB) buf = 0, buf_phase ^= 1;
             }
-            if (!good) {
-                gave_up = 1;
-                umma_commit(&drain);
-                mbar_wait(&drain, 0, a.status, kWaitDrain);
-            }
+        }
+        if (!good) {
+            gave_up = 1;
+            if (issuer) umma_commit(&drain);
+            f8_wait(&drain, 0, a.status, kWaitDrain);
         }
     } else {
         const int half = warp / 4, quarter = warp % 4;
@@ -341,7 +349,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
     if (gave_up && threadIdx.x == 256) {
         // copies in flight land before this CTA ends
         for (uint32_t i = issued > S::NST ? issued - S::NST : 0; i < issued; ++i)
-            mbar_wait(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
+            f8_wait(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
     }
     __syncthreads();
     tc_fence_after();
@@ -393,22 +401,19 @@ static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int6
 // warp's to one row of W's scales, so a block is scaled by one number a lane.
 // (With W as M the scales come by column, 512 bytes of shared-memory reads for
 // 32 columns: a tile of 256 tokens took 1.39 us a block, bound by that memory.)
-// PAIR: two SMs share a tile of 256 tokens by 256 rows: each loads its 128 tokens
-// and half of the rows, one MMA of M = 256 reads both, and each SM holds its
-// tokens' 128 x 256 sums; an SM so fetches 32 KB for a block where it would
-// need 48 KB alone.  Warps 0-7 scale and store (a warp: 32 tokens by 128 rows),
-// warp 8 loads, warp 9 (of the pair's first CTA) multiplies.
-template <bool PAIR>
-struct F8Many {
+// Two SMs share a tile of 256 tokens by 256 rows: each loads its 128 tokens and
+// half of the rows, one MMA of M = 256 reads both, and each SM holds its tokens'
+// 128 x 256 sums; an SM so fetches 32 KB for a block where it would need 48 KB
+// alone.  Warps 0-7 scale and store (a warp: 32 tokens by 128 rows), warp 8
+// loads, warp 9 of the pair's first CTA multiplies.  What bounds it: a block's
+// MMAs take 512 cycles, its way through one of the two accumulators (done,
+// read, handed back) about 1000, so that a block takes 740 to 840.
+struct F8Pair {
     static constexpr int XBYTES = 128 * 128;
-    static constexpr int WBYTES = (PAIR ? 128 : 256) * 128;
-    static constexpr int STAGE = XBYTES + WBYTES;
-    static constexpr int NST = PAIR ? 6 : 4;
-    // Accumulators: a pair's MMAs keep up only with 256 columns (a block in two halves of 128 reads the tokens twice as
-    // often: 475 us where one of 256 takes 359), so it has two; a single SM waits for W anyway and hands back halves.
-    static constexpr int COLS = PAIR ? 256 : 128;
-    static constexpr int NB = 512 / COLS;
-    static constexpr int PARTS = 256 / COLS;  // of a block
+    static constexpr int STAGE = 2 * XBYTES;
+    static constexpr int NST = 6;
+    // Two accumulators of 256 columns.  (Four of 128 read the tokens twice as often and were slower, 475 against 359 us.)
+    static constexpr int NB = 2;
     static constexpr int THREADS = 384;
     static constexpr int SMEM = 1024 + NST * STAGE + 8 * 4096;
 };
@@ -422,55 +427,36 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, unsigned rank)  // the
 
 // Arrives on the barrier of the pair's first CTA.  Relaxed: what it tells is that this warp's tensor-memory loads are
 // done, which the fence before it orders; a release to the cluster waits for all of the warp's memory traffic (pairs
-// spent more than half of their time there: 216 -> 170 us for 2048 x 5376 -> 9728).
+// spent more than half of their time there: 826 -> 505 us for 4096 x 5376 -> 21504).
 __device__ __forceinline__ void f8_arrive_first(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void f8_many_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+__device__ __forceinline__ void f8_pair_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
 {
-    if constexpr (PAIR) {
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-            : "memory");
-    } else {
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-            : "memory");
-    }
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void f8_many_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc)
+__device__ __forceinline__ void f8_pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc)
 {
-    if constexpr (PAIR) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(f8_idesc(256, 256)), "r"(acc));
-    } else {
-        f8_mma(d, a, b, f8_idesc(128, 128), acc);
-    }
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(f8_idesc(256, 256)), "r"(acc));
 }
 
-// Arrives on the barrier (of both CTAs) once all MMAs so far are complete.
-template <bool PAIR>
-__device__ __forceinline__ void f8_many_commit(uint64_t *bar)
+// Arrives on the barrier of both CTAs once all MMAs so far are complete.
+__device__ __forceinline__ void f8_pair_commit(uint64_t *bar)
 {
-    if constexpr (PAIR) {
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(s32(bar)),
-                     "h"((uint16_t)3)
-                     : "memory");
-    } else {
-        umma_commit(bar);
-    }
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(s32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint64_t f8_both(float f)
@@ -556,7 +542,7 @@ __device__ __forceinline__ void f8_store_part(const LinearF8Args &a, const CUten
 __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUtensorMap &ymap, int ydt, int boxes, char *ring, uint32_t tmem,
                                               uint64_t *tfull, uint64_t *tempty, int rank, int64_t first, int64_t step)
 {
-    using S = F8Many<true>;
+    using S = F8Pair;
     constexpr int CTAS = 2;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int half = warp / 4, quarter = warp % 4;
@@ -629,81 +615,13 @@ __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUten
     return good;
 }
 
-// Scales and stores a single SM's tiles, 32 tokens by 64 rows of W of each of the block's two parts a warp.
-__device__ __forceinline__ bool f8_single_tiles(const LinearF8Args &a, const CUtensorMap &ymap, int ydt, int boxes, char *ring, uint32_t tmem,
-                                                uint64_t *tfull, uint64_t *tempty, int64_t first, int64_t step)
-{
-    using S = F8Many<false>;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int side = warp / 4, quarter = warp % 4;
-    char *stage = ring + S::NST * S::STAGE + warp * 4096;
-    uint32_t buf = 0, phase = 0;
-    bool good = true;
-    for (int64_t tile = first; tile < a.tiles && good; tile += step) {
-        const int64_t mt = tile / a.nt;
-        const int64_t t = (tile - mt * a.nt) * 128 + quarter * 32 + lane;
-        const int64_t o0 = mt * 256 + side * 64, o1 = o0 + 128;  // first row of W of each half
-        const float *wsp = a.ws + min(o0 / 128, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
-        const int64_t other = min(o1 / 128, (int64_t)a.ob - 1) - min(o0 / 128, (int64_t)a.ob - 1);
-        uint64_t acc[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0;
-        // scales come G blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time)
-        constexpr int G = 2;
-        float wn[G], vn[G], xn[G], f[G], g[G];
-        auto fetch = [&](int kb) {
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                const int64_t k = min(kb + i, a.nkb - 1);
-                wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
-                vn[i] = __ldg(wsp + k * a.ob + other);
-            }
-        };
-        fetch(0);
-#pragma unroll 1
-        for (int kb = 0; kb < a.nkb; ++kb) {
-            if (kb % G == 0) {
-#pragma unroll
-                for (int i = 0; i < G; ++i) f[i] = wn[i] * xn[i], g[i] = vn[i] * xn[i];
-                fetch(kb + G);
-            }
-            uint32_t d0[32], d1[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                good = good && f8_wait(&tfull[buf + h], phase, a.status, kWaitRingFull);
-                tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (buf + h) * 128 + side * 64;
-                const uint64_t s = f8_both(h ? g[0] : f[0]);
-                f8_tmem_ld<32>(at, d0);
-                f8_tmem_ld<32>(at + 32, d1);
-                f8_tmem_wait<32>(d0);
-                f8_tmem_wait<32>(d1);
-                tc_fence_before();
-                if (lane == 0) mbar_arrive(&tempty[buf + h]);
-                f8_scale32(acc + 32 * h, d0, s);
-                f8_scale32(acc + 32 * h + 16, d1, s);
-            }
-            if (!good) break;
-#pragma unroll
-            for (int i = 0; i + 1 < G; ++i) f[i] = f[i + 1], g[i] = g[i + 1];
-            buf ^= 2;
-            if (buf == 0) phase ^= 1;
-        }
-        if (!good) break;
-        f8_store_part(a, &ymap, stage, ydt, boxes, t, o0, acc);
-        f8_store_part(a, &ymap, stage, ydt, boxes, t, o1, acc + 32);
-    }
-    return good;
-}
-
-template <bool PAIR>
-__global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kernel(const __grid_constant__ LinearF8Args a,
+__global__ void __launch_bounds__(F8Pair::THREADS, 1) linear_f8_pair_kernel(const __grid_constant__ LinearF8Args a,
                                                                                  const __grid_constant__ CUtensorMap wmap,
                                                                                  const __grid_constant__ CUtensorMap xmap,
                                                                                  const __grid_constant__ CUtensorMap ymap, int ydt,
                                                                                  int boxes)
 {
-    using S = F8Many<PAIR>;
+    using S = F8Pair;
     extern __shared__ char f8_smem[];
     __shared__ uint64_t full[S::NST], empty[S::NST], tfull[S::NB], tempty[S::NB], drain;
     __shared__ uint32_t tmem_hold;
@@ -711,8 +629,8 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
     char *ring = f8_smem + (1024 - s32(f8_smem) % 1024) % 1024;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     cg::cluster_group cl = cg::this_cluster();
-    const int rank = PAIR ? (int)cl.block_rank() : 0;
-    constexpr int CTAS = PAIR ? 2 : 1;
+    const int rank = (int)cl.block_rank();
+    constexpr int CTAS = 2;
     const int64_t first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
@@ -723,17 +641,11 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
-        if constexpr (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(512));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(512));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc_fence_before();
-    if (PAIR) cl.sync();
-    else __syncthreads();
+    cl.sync();
     tc_fence_after();
     const uint32_t tmem = tmem_hold;
     pdl_wait();
@@ -744,22 +656,22 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
         // the third warpgroup gives registers to the other two: 384 x 168 = 128 x 40 + 256 x 232
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8) {
-            const uint32_t ring0 = s32(ring), issuer = f8_elect(), bar0 = PAIR ? in_cta(&full[0], 0) : s32(&full[0]);
+            const uint32_t ring0 = s32(ring), issuer = f8_elect(), bar0 = in_cta(&full[0], 0);
             uint32_t st = 0, phase = 1;
             bool good = true;
             for (int64_t tile = first; tile < a.tiles && good; tile += step) {
                 const int64_t mt = tile / a.nt;
                 const int o0 = (int)(mt * 256) + rank * 128, t0 = (int)(tile - mt * a.nt) * 128 * CTAS + rank * 128;
                 for (int kb = 0; kb < a.nkb; ++kb) {
-                    if (!f8_wait<PAIR>(&empty[st], phase, a.status, kWaitRingEmpty)) {
+                    if (!f8_wait<true>(&empty[st], phase, a.status, kWaitRingEmpty)) {
                         good = false;
                         break;
                     }
                     if (issuer) {
                         const uint32_t p = ring0 + st * S::STAGE, bar = bar0 + st * 8;
                         if (rank == 0) mbar_expect_tx(&full[st], CTAS * S::STAGE);  // both CTAs' bytes
-                        f8_many_load<PAIR>(p, &xmap, kb * 128, t0, bar);
-                        f8_many_load<PAIR>(p + S::XBYTES, &wmap, kb * 128, o0, bar);
+                        f8_pair_load(p, &xmap, kb * 128, t0, bar);
+                        f8_pair_load(p + S::XBYTES, &wmap, kb * 128, o0, bar);
                     }
                     __syncwarp();
                     ++issued;
@@ -775,8 +687,8 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
             bool good = true;
             for (int64_t tile = first; tile < a.tiles && good; tile += step) {
                 for (int kb = 0; kb < a.nkb; ++kb) {
-                    if (!f8_wait<PAIR>(&tempty[buf], buf_phase, a.status, kWaitRingEmpty) ||
-                        !f8_wait<PAIR>(&full[st], st_phase, a.status, kWaitRingFull)) {
+                    if (!f8_wait<true>(&tempty[buf], buf_phase, a.status, kWaitRingEmpty) ||
+                        !f8_wait<true>(&full[st], st_phase, a.status, kWaitRingFull)) {
                         good = false;
                         break;
                     }
@@ -784,42 +696,25 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
                     const uint64_t da = sdesc(ring0 + st * S::STAGE), db = sdesc(ring0 + st * S::STAGE + S::XBYTES);
                     if (issuer) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) f8_many_mma<PAIR>(tmem + buf * S::COLS, da + 2 * j, db + 2 * j, j > 0);
-                        f8_many_commit<PAIR>(&tfull[buf]);
-                        if (S::PARTS == 1) f8_many_commit<PAIR>(&empty[st]);
+                        for (int j = 0; j < 4; ++j) f8_pair_mma(tmem + buf * 256, da + 2 * j, db + 2 * j, j > 0);
+                        f8_pair_commit(&tfull[buf]);
+                        f8_pair_commit(&empty[st]);
                     }
                     __syncwarp();
-                    if constexpr (S::PARTS == 2) {
-                        if (!f8_wait<PAIR>(&tempty[buf + 1], buf_phase, a.status, kWaitRingEmpty)) {
-                            good = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (issuer) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                f8_many_mma<PAIR>(tmem + (buf + 1) * S::COLS, da + 2 * j, db + S::WBYTES / 32 + 2 * j, j > 0);
-                            f8_many_commit<PAIR>(&tfull[buf + 1]);
-                            f8_many_commit<PAIR>(&empty[st]);
-                        }
-                        __syncwarp();
-                    }
                     if (++st == S::NST) st = 0, st_phase ^= 1;
-                    buf ^= S::PARTS;
+                    buf ^= 1;
                     if (buf == 0) buf_phase ^= 1;
                 }
             }
             if (!good) {
                 gave_up = 1;
-                if (issuer) f8_many_commit<PAIR>(&drain);
-                f8_wait<PAIR>(&drain, 0, a.status, kWaitDrain);
+                if (issuer) f8_pair_commit(&drain);
+                f8_wait<true>(&drain, 0, a.status, kWaitDrain);
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        bool good;
-        if constexpr (PAIR) good = f8_pair_tiles(a, ymap, ydt, boxes, ring, tmem, tfull, tempty, rank, first, step);
-        else good = f8_single_tiles(a, ymap, ydt, boxes, ring, tmem, tfull, tempty, first, step);
+        const bool good = f8_pair_tiles(a, ymap, ydt, boxes, ring, tmem, tfull, tempty, rank, first, step);
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // before the memory they read goes
         if (!good && lane == 0) gave_up = 1;
     }
@@ -829,25 +724,20 @@ __global__ void __launch_bounds__(F8Many<PAIR>::THREADS, 1) linear_f8_many_kerne
     if (gave_up && threadIdx.x == 256 && rank == 0) {
         // copies in flight (both CTAs') land before a CTA ends
         for (uint32_t i = issued > S::NST ? issued - S::NST : 0; i < issued; ++i)
-            f8_wait<PAIR>(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
+            f8_wait<true>(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
     }
-    if (PAIR) cl.sync();
-    else __syncthreads();
+    cl.sync();
     tc_fence_after();
-    if (warp == 8) {
-        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
-        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
-    }
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-template <bool PAIR>
-static wl_status f8_run_many(LinearF8Args a, const uint8_t *x, const uint8_t *W, int64_t in, int ydt, const DeviceInfo *di,
+static wl_status f8_run_pair(LinearF8Args a, const uint8_t *x, const uint8_t *W, int64_t in, int ydt, const DeviceInfo *di,
                              cudaStream_t st)
 {
-    using S = F8Many<PAIR>;
-    constexpr int CTAS = PAIR ? 2 : 1;
+    using S = F8Pair;
+    constexpr int CTAS = 2;
     CUtensorMap wmap, xmap, ymap = {};
-    wl_status s = tmap_rows_u8(W, in, a.out, PAIR ? 128 : 256, &wmap);
+    wl_status s = tmap_rows_u8(W, in, a.out, 128, &wmap);
     if (s != WL_OK) return s;
     s = tmap_rows_u8(x, in, a.T, 128, &xmap);
     if (s != WL_OK) return s;
@@ -858,7 +748,7 @@ static wl_status f8_run_many(LinearF8Args a, const uint8_t *x, const uint8_t *W,
     }
     a.nt = (int)((a.T + 128 * CTAS - 1) / (128 * CTAS));
     a.tiles = (a.out + 255) / 256 * a.nt;
-    cudaError_t e = cudaFuncSetAttribute(linear_f8_many_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return cuda_fail(e, "wl_linear_f8 attributes");
     const int64_t most = di->sm_count / CTAS, groups = a.tiles < most ? a.tiles : most;
     cudaLaunchAttribute at[2];
@@ -873,8 +763,310 @@ static wl_status f8_run_many(LinearF8Args a, const uint8_t *x, const uint8_t *W,
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, linear_f8_many_kernel<PAIR>, a, wmap, xmap, ymap, ydt, (int)boxes);
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, linear_f8_pair_kernel, a, wmap, xmap, ymap, ydt, (int)boxes);
+    return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
+}
+
+// -------------------------------------------------------- few tokens, many rows --
+// Up to 128 tokens: W's bytes are the time.  Tokens are M (rows of the tile past
+// them hold whatever the ring holds: their sums are not stored), `rows` rows of W
+// are N, chosen so that the tiles fill whole waves of SMs: 84 tiles of 256 for
+// 21504 rows leave 68 SMs idle, 150 of 144 none.  A tile so begins at any
+// multiple of 16 and may cross from one row of scales to the next once in a warp's
+// columns.  Only the warps that hold tokens read the sums.
+struct F8Few {
+    int rows, xrows;   // rows of W of a tile; rows of the token box: T up to a multiple of 8
+    int stages, stage; // of the ring, bytes of one
+    int cols, bufs;    // accumulators: 64, 128 or 256 columns, 512 in all
+    int half;          // columns of side 0
+};
+
+constexpr int kFewStages = 16, kFewThreads = 384;
+
+// 32 tokens (t0: the first) by 32 rows of W through the warp's shared memory.
+template <bool F32>
+__device__ __forceinline__ void f8_store_box32(const CUtensorMap *map, char *stage, int t0, int64_t o, const uint64_t acc[16])
+{
+    const int lane = threadIdx.x % 32;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+        if constexpr (F32) {
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4((uint32_t)acc[2 * i], (uint32_t)(acc[2 * i] >> 32), (uint32_t)acc[2 * i + 1], (uint32_t)(acc[2 * i + 1] >> 32));
+        } else {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = bf16x2_bits(f8_lo(acc[4 * i + k]), f8_hi(acc[4 * i + k]));
+            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"((int)o), "r"(t0), "r"(s32(stage))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+// The lane's 16 outputs from place `at` of y on, the first n of them in the matrix; vec: 16-byte stores.
+__device__ __forceinline__ void f8_store16(void *y, int ydt, int64_t at, int n, bool vec, const uint64_t acc[8])
+{
+    if (ydt == WL_OUT_F32) {
+        float *p = static_cast<float *>(y) + at;
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+            if (vec && c + 4 <= n) {
+                *reinterpret_cast<float4 *>(p + c) = make_float4(f8_lo(acc[c / 2]), f8_hi(acc[c / 2]), f8_lo(acc[c / 2 + 1]), f8_hi(acc[c / 2 + 1]));
+            } else {
+#pragma unroll
+                for (int i = c; i < c + 4; ++i)
+                    if (i < n) p[i] = i & 1 ? f8_hi(acc[i / 2]) : f8_lo(acc[i / 2]);
+            }
+        }
+    } else {
+        bf16 *p = static_cast<bf16 *>(y) + at;
+#pragma unroll
+        for (int c = 0; c < 16; c += 8) {
+            if (vec && c + 8 <= n) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = bf16x2_bits(f8_lo(acc[c / 2 + i]), f8_hi(acc[c / 2 + i]));
+                *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int i = c; i < c + 8; ++i)
+                    if (i < n) p[i] = __float2bfloat16_rn(i & 1 ? f8_hi(acc[i / 2]) : f8_lo(acc[i / 2]));
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void f8_scale16(uint64_t *acc, const uint32_t *d, uint64_t s)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) fma2(acc[i / 2], d[i], d[i + 1], s);
+}
+
+__global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __grid_constant__ LinearF8Args a, const __grid_constant__ F8Few p,
+                                                                       const __grid_constant__ CUtensorMap wmap,
+                                                                       const __grid_constant__ CUtensorMap xmap,
+                                                                       const __grid_constant__ CUtensorMap ymap, int ydt, int boxes)
+{
+    extern __shared__ char f8_smem[];
+    __shared__ uint64_t full[kFewStages], empty[kFewStages], tfull[8], tempty[8], drain;
+    __shared__ uint32_t tmem_hold;
+    __shared__ int gave_up;
+    char *ring = f8_smem + (1024 - s32(f8_smem) % 1024) % 1024;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < p.bufs; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 8);
+        mbar_init(&drain, 1);
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(s32(&tmem_hold)), "n"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_hold;
+    pdl_wait();
+    pdl_trigger();
+
+    uint32_t issued = 0;  // ring items of the loading warp
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");  // as in the pairs' kernel
+        if (warp == 8) {
+            const uint32_t ring0 = s32(ring), issuer = f8_elect();
+            uint32_t st = 0, phase = 1;
+            bool good = true;
+            for (int64_t tile = blockIdx.x; tile < a.tiles && good; tile += gridDim.x) {
+                const int o0 = (int)(tile * p.rows);
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!f8_wait(&empty[st], phase, a.status, kWaitRingEmpty)) {
+                        good = false;
+                        break;
+                    }
+                    if (issuer) {
+                        const uint32_t at = ring0 + st * p.stage;
+                        mbar_expect_tx(&full[st], p.stage);
+                        tma_load_2d_u32(at, &wmap, kb * 128, o0, &full[st]);
+                        tma_load_2d_u32(at + p.rows * 128, &xmap, kb * 128, 0, &full[st]);
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++st == p.stages) st = 0, phase ^= 1;
+                }
+            }
+            if (!good) gave_up = 1;
+        } else if (warp == 9) {
+            const uint32_t ring0 = s32(ring), issuer = f8_elect(), idesc = f8_idesc(128, p.rows);
+            uint32_t st = 0, st_phase = 0, buf = 0, buf_phase = 1;
+            bool good = true;
+            for (int64_t tile = blockIdx.x; tile < a.tiles && good; tile += gridDim.x) {
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!f8_wait(&tempty[buf], buf_phase, a.status, kWaitRingEmpty) || !f8_wait(&full[st], st_phase, a.status, kWaitRingFull)) {
+                        good = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t db = sdesc(ring0 + st * p.stage), da = sdesc(ring0 + st * p.stage + p.rows * 128);
+                    if (issuer) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) f8_mma(tmem + buf * p.cols, da + 2 * j, db + 2 * j, idesc, j > 0);
+                        umma_commit(&tfull[buf]);
+                        umma_commit(&empty[st]);
+                    }
+                    __syncwarp();
+                    if (++st == p.stages) st = 0, st_phase ^= 1;
+                    if (++buf == p.bufs) buf = 0, buf_phase ^= 1;
+                }
+            }
+            if (!good) {
+                gave_up = 1;
+                if (issuer) umma_commit(&drain);
+                f8_wait(&drain, 0, a.status, kWaitDrain);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int side = warp / 4, quarter = warp % 4, t = quarter * 32 + lane;
+        const int c0 = side * p.half, chunks = (min(p.rows, c0 + p.half) - c0) / 16;  // columns of the warp, in 16s: 0 .. 8
+        const bool mine = quarter * 32 < a.T && chunks > 0;
+        char *stage = ring + p.stages * p.stage + warp * 4096;
+        uint32_t buf = 0, phase = 0;
+        bool good = true;
+        for (int64_t tile = blockIdx.x; tile < a.tiles && good; tile += gridDim.x) {
+            const int64_t o0 = tile * p.rows + c0, b0 = o0 / 128;
+            const int cut = (int)((b0 + 1) * 128 - o0) / 16;  // the chunk where the next row of scales begins
+            const float *wsp = a.ws + min(b0, (int64_t)a.ob - 1), *xsp = a.xs + min((int64_t)t, a.T - 1);
+            const int next = b0 + 1 < a.ob;
+            uint64_t acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            // scales come two blocks at a time, a group ahead
+            float wn[2], vn[2], xn[2], f[2], g[2];
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t k = min(kb + i, a.nkb - 1);
+                    wn[i] = __ldg(wsp + k * a.ob), vn[i] = __ldg(wsp + k * a.ob + next), xn[i] = __ldg(xsp + k * a.T);
+                }
+            };
+            if (mine) fetch(0);
+#pragma unroll 1
+            for (int kb = 0; kb < a.nkb; ++kb) {
+                if (mine && (kb & 1) == 0) {
+                    f[0] = wn[0] * xn[0], f[1] = wn[1] * xn[1], g[0] = vn[0] * xn[0], g[1] = vn[1] * xn[1];
+                    fetch(kb + 2);
+                }
+                if (!f8_wait(&tfull[buf], phase, a.status, kWaitRingFull)) {
+                    good = false;
+                    break;
+                }
+                if (mine) {
+                    tc_fence_after();
+                    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * p.cols + c0;
+                    const uint64_t s0 = f8_both(f[0]), s1 = f8_both(g[0]);
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        if (c < chunks) {
+                            uint32_t d0[16], d1[16];
+                            f8_tmem_ld<16>(at + 16 * c, d0);
+                            if (c + 1 < chunks) f8_tmem_ld<16>(at + 16 * c + 16, d1);
+                            f8_tmem_wait<16>(d0);
+                            f8_tmem_wait<16>(d1);
+                            f8_scale16(acc + 8 * c, d0, c < cut ? s0 : s1);
+                            f8_scale16(acc + 8 * c + 8, d1, c + 1 < cut ? s0 : s1);
+                        }
+                    }
+                    tc_fence_before();
+                    f[0] = f[1], g[0] = g[1];
+                }
+                if (lane == 0) mbar_arrive(&tempty[buf]);
+                if (++buf == p.bufs) buf = 0, phase ^= 1;
+            }
+            if (!good) break;
+            if (!mine) continue;
+            if (boxes) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (2 * b < chunks && o0 + 32 * b < a.out) {
+                        if (ydt == WL_OUT_F32) f8_store_box32<true>(&ymap, stage, quarter * 32, o0 + 32 * b, acc + 16 * b);
+                        else f8_store_box32<false>(&ymap, stage, quarter * 32, o0 + 32 * b, acc + 16 * b);
+                    }
+            } else if (t < a.T) {
+                const bool vec = a.out % 8 == 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < chunks && o0 + 16 * c < a.out)
+                        f8_store16(a.y, ydt, t * a.out + o0 + 16 * c, (int)min((int64_t)16, a.out - o0 - 16 * c), vec, acc + 8 * c);
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // before the memory they read goes
+        if (!good && lane == 0) gave_up = 1;
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (gave_up && threadIdx.x == 256) {
+        for (uint32_t i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+            f8_wait(&full[i % p.stages], (i / p.stages) & 1, a.status, kWaitDrain);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+}
+
+// The few tokens' tile height, and what it is thought to take: waves of tiles, a block's bytes at an SM's share of HBM
+// (44 bytes a ns) or the round of its copy, and 0.7 us a tile.
+static double f8_few_plan(int64_t T, int64_t out, int nkb, int sms, F8Few *p)
+{
+    const int step = T > 8 ? 64 : 16;  // more than a few tokens are stored in boxes of 32 rows of W a side
+    double best = 1e30;
+    p->xrows = (int)(T + 7) / 8 * 8;
+    for (int rows = step; rows <= 256; rows += step) {
+        const int64_t waves = ((out + rows - 1) / rows + sms - 1) / sms;
+        const double block = rows * 128.0 / 44 + p->xrows * 128.0 / 130, time = waves * (nkb * (block > 200 ? block : 200) + 700);
+        if (time < best) best = time, p->rows = rows;
+    }
+    p->half = step == 64 ? p->rows / 2 : (p->rows / 2 + 15) / 16 * 16;
+    p->stage = (p->rows + p->xrows) * 128;
+    p->stages = 192 * 1024 / p->stage < kFewStages ? 192 * 1024 / p->stage : kFewStages;
+    p->cols = p->rows <= 64 ? 64 : p->rows <= 128 ? 128 : 256;
+    p->bufs = 512 / p->cols;
+    return best;
+}
+
+static wl_status f8_run_few(LinearF8Args a, const F8Few &p, const uint8_t *x, const uint8_t *W, int64_t in, int ydt, const DeviceInfo *di,
+                            cudaStream_t st)
+{
+    CUtensorMap wmap, xmap, ymap = {};
+    wl_status s = tmap_rows_u8(W, in, a.out, p.rows, &wmap);
+    if (s != WL_OK) return s;
+    s = tmap_rows_u8(x, in, a.T, p.xrows, &xmap);
+    if (s != WL_OK) return s;
+    const bool f32 = ydt == WL_OUT_F32, boxes = a.T > 8 && a.out % (f32 ? 4 : 8) == 0;
+    if (boxes) {
+        s = f32 ? tmap_2d_f32(a.y, a.out, a.T, 32, 32, &ymap) : tmap_2d_bf16_swz(a.y, a.out, a.T, a.out, 32, 32, 64, &ymap);
+        if (s != WL_OK) return s;
+    }
+    a.tiles = (a.out + p.rows - 1) / p.rows;
+    const int smem = 1024 + p.stages * p.stage + 8 * 4096;
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + 192 * 1024 + 8 * 4096);
+    if (e != cudaSuccess) return cuda_fail(e, "wl_linear_f8 attributes");
+    const int64_t grid = a.tiles < di->sm_count ? a.tiles : di->sm_count;
+    e = launch_dependent(linear_f8_few_kernel, dim3((unsigned)grid), kFewThreads, (size_t)smem, st, a, p, wmap, xmap, ymap, ydt, (int)boxes);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 
@@ -882,12 +1074,20 @@ wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
     const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 0, di->status};
+    // Tiles of 256 rows by 256 tokens where they fill half of the pairs.
+    if (T > 128 && (out + 255) / 256 * ((T + 255) / 256) * 4 >= di->sm_count) return f8_run_pair(a, x, W, in, ydt, di, st);
+    if (T <= 128) {
+        F8Few p;
+        // against a tile of 128 rows, its sum split over up to 8 CTAs: about 0.4 us a block of a CTA and 4 us beside
+        const double time = f8_few_plan(T, out, a.nkb, di->sm_count, &p);
+        const int64_t tiles = a.ob * ((T + 63) / 64);
+        int ctas = 1;
+        while (ctas < 8 && tiles * ctas * 2 <= di->sm_count && a.nkb >= 2 * ctas * 2) ctas *= 2;
+        const double split = (double)((tiles * ctas + di->sm_count - 1) / di->sm_count) * (a.nkb / ctas) * 400.0 + 1500.0;
+        if (time <= split) return f8_run_few(a, p, x, W, in, ydt, di, st);
+    }
     if (T <= 16) return f8_run<16>(a, x, W, in, ydt, di, st);
     if (T <= 32) return f8_run<32>(a, x, W, in, ydt, di, st);
-    // many tokens: tiles of 256 rows, where they fill half of the SMs
-    const int64_t wide = (out + 255) / 256;
-    if (T > 128 && wide * ((T + 255) / 256) * 4 >= di->sm_count) return f8_run_many<true>(a, x, W, in, ydt, di, st);
-    if (T > 64 && wide * ((T + 127) / 128) * 2 >= di->sm_count) return f8_run_many<false>(a, x, W, in, ydt, di, st);
     return f8_run<64>(a, x, W, in, ydt, di, st);
 }
 

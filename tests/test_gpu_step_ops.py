@@ -84,7 +84,7 @@ def _check_product(y, x, xs, w, ws, dt):
 @pytest.mark.parametrize("T,inner,out", [
     (1, 16, 1), (1, 128, 128), (1, 1152, 300), (2, 144, 129), (3, 2304, 64), (5, 256, 1153), (8, 640, 127), (15, 384, 257), (16, 1152, 256), (17, 272, 100),
     (31, 512, 513), (33, 1296, 131), (37, 6912, 65), (64, 128, 384), (65, 1152, 255), (96, 1152, 640), (127, 144, 385), (129, 400, 200),
-    (200, 1152, 1000), (100, 272, 20001), (70, 1152, 19464), (300, 400, 9731), (1000, 144, 2500), (140, 2048, 19460), (257, 16, 9736), (256, 256, 256), (257, 640, 130), (300, 2048, 512), (513, 384, 700), (1, 21504, 40), (1025, 144, 72),
+    (200, 1152, 1000), (100, 272, 20001), (70, 1152, 19464), (300, 400, 9731), (1000, 144, 2500), (140, 2048, 19460), (1, 400, 9740), (3, 144, 21504), (8, 1296, 5376), (9, 128, 21501), (33, 272, 19336), (128, 144, 39000), (64, 1152, 30008), (1, 144, 262144), (257, 16, 9736), (256, 256, 256), (257, 640, 130), (300, 2048, 512), (513, 384, 700), (1, 21504, 40), (1025, 144, 72),
 ])
 def test_product(wl, gpu, T, inner, out, dt):
     x, xs, w, ws = _factors(T, inner, out, T + inner + out)
