@@ -29,21 +29,22 @@ struct LinearF8Args {
     void *y;
     int64_t T, out;
     int nkb, ob, nt;  // blocks of 128 along the sum, along out; token tiles
+    int rows;         // rows of W of a tile, a multiple of 8
+    int stages;       // of the ring
     int64_t tiles;
     unsigned *status;
 };
 
-constexpr int kF8Threads = 320;
+constexpr int kF8Threads = 320, kF8Stages = 24, kF8Ring = 192 * 1024;
 
 template <int N>
 struct F8Shape {
-    static constexpr int STAGE = 16384 + N * 128;
-    static constexpr int NST = 200 * 1024 / STAGE;
     static constexpr int NB = 4;                 // accumulators
     static constexpr int COLS = N * NB;          // 64 .. 256: a power of two
     static constexpr int HALF = N / 2;           // tokens of a warp
-    static constexpr int SCALES = 8 * 2 * HALF * 4;
-    static constexpr int SMEM = 1024 + NST * STAGE + SCALES;
+    static constexpr int SCALES = 8 * 2 * 2 * HALF * 4;
+    // the MMAs read 128 rows whatever the tile's height: past the last stage too
+    static constexpr int SMEM = 1024 + kF8Ring + 16384 + SCALES;
 };
 
 // Instruction descriptor of kind::f8f6f4: e4m3 A and B, both K-major, fp32 D.
@@ -134,14 +135,15 @@ __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t d0, uint32_t d1, ui
 __device__ __forceinline__ float f8_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float f8_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-// A warp's 32 rows of W (row o its lane's) by COLS tokens from t0 on; pairs of tokens in acc.
+// A warp's 32 rows of W (row o its lane's, in the tile where `in`) by COLS tokens from t0 on; pairs of tokens in acc.
+// Tiles are multiples of 8 rows high, so that of two neighbouring rows both or none are in it.
 template <int COLS>
-__device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t t0, int64_t o, const uint64_t acc[COLS / 2])
+__device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t t0, int64_t o, bool in, const uint64_t acc[COLS / 2])
 {
     const int n = (int)min((int64_t)COLS, a.T - t0);
     if (ydt == WL_OUT_F32) {
         float *y = static_cast<float *>(a.y) + t0 * a.out + o;
-        if (o < a.out)
+        if (in && o < a.out)
 #pragma unroll
             for (int c = 0; c < COLS; ++c) {
                 if (c < n) *y = c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]);
@@ -151,7 +153,7 @@ __device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t
         // neighbouring lanes trade halves: 4 bytes of one token each
         const int odd = threadIdx.x & 1;
         bf16 *y = static_cast<bf16 *>(a.y) + (t0 + odd) * a.out + o - odd;
-        const bool in = o - odd < a.out;
+        in = in && o - odd < a.out;
 #pragma unroll
         for (int c = 0; c < COLS; c += 2) {
             const float lo = f8_lo(acc[c / 2]), hi = f8_hi(acc[c / 2]);
@@ -161,7 +163,7 @@ __device__ __forceinline__ void f8_store(const LinearF8Args &a, int ydt, int64_t
         }
     } else {
         bf16 *y = static_cast<bf16 *>(a.y) + t0 * a.out + o;
-        if (o < a.out)
+        if (in && o < a.out)
 #pragma unroll
             for (int c = 0; c < COLS; ++c) {
                 if (c < n) *y = __float2bfloat16_rn(c & 1 ? f8_hi(acc[c / 2]) : f8_lo(acc[c / 2]));
@@ -178,11 +180,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
 {
     using S = F8Shape<N>;
     extern __shared__ char f8_smem[];
-    __shared__ uint64_t full[S::NST], empty[S::NST], tfull[S::NB], tempty[S::NB], drain;
+    __shared__ uint64_t full[kF8Stages], empty[kF8Stages], tfull[S::NB], tempty[S::NB], drain;
     __shared__ uint32_t tmem_hold;
     __shared__ int gave_up;
     char *ring = f8_smem + (1024 - s32(f8_smem) % 1024) % 1024;
-    float *scales = reinterpret_cast<float *>(ring + S::NST * S::STAGE);
+    float *scales = reinterpret_cast<float *>(ring + kF8Ring + 16384);
+    const int bytes = (a.rows + N) * 128;  // of a stage
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = SPLIT ? (int)cl.block_rank() : 0, ctas = SPLIT ? (int)cl.num_blocks() : 1;
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
     const int64_t first = SPLIT ? blockIdx.x / ctas : blockIdx.x, step = SPLIT ? gridDim.x / ctas : gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::NST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < S::NB; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 8);
         mbar_init(&drain, 1);
         gave_up = 0;
@@ -216,21 +219,21 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
         bool good = true;
         for (int64_t tile = first; tile < a.tiles && good; tile += step) {
             const int64_t mt = tile / a.nt;
-            const int o0 = (int)(mt * 128), t0 = (int)(tile - mt * a.nt) * N;
+            const int o0 = (int)(mt * a.rows), t0 = (int)(tile - mt * a.nt) * N;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!f8_wait(&empty[st], phase, a.status, kWaitRingEmpty)) {
                     good = false;
                     break;
                 }
                 if (issuer) {
-                    const uint32_t p = ring0 + st * S::STAGE;
-                    mbar_expect_tx(&full[st], S::STAGE);
+                    const uint32_t p = ring0 + st * bytes;
+                    mbar_expect_tx(&full[st], bytes);
                     tma_load_2d_u32(p, &wmap, kb * 128, o0, &full[st]);
-                    tma_load_2d_u32(p + 16384, &xmap, kb * 128, t0, &full[st]);
+                    tma_load_2d_u32(p + a.rows * 128, &xmap, kb * 128, t0, &full[st]);
                 }
                 __syncwarp();
                 ++issued;
-                if (++st == S::NST) st = 0, phase ^= 1;
+                if (++st == a.stages) st = 0, phase ^= 1;
             }
         }
         if (!good) gave_up = 1;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
                     break;
                 }
                 tc_fence_after();
-                const uint64_t da = sdesc(ring0 + st * S::STAGE), db = sdesc(ring0 + st * S::STAGE + 16384);
+                const uint64_t da = sdesc(ring0 + st * bytes), db = sdesc(ring0 + st * bytes + a.rows * 128);
                 if (issuer) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) f8_mma(tmem + buf * N, da + 2 * j, db + 2 * j, f8_idesc(128, N), j > 0);
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
                     umma_commit(&empty[st]);
                 }
                 __syncwarp();
-                if (++st == S::NST) st = 0, st_phase ^= 1;
+                if (++st == a.stages) st = 0, st_phase ^= 1;
                 if (++buf == S::NB) buf = 0, buf_phase ^= 1;
             }
         }
@@ -264,9 +267,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
         }
     } else {
         const int half = warp / 4, quarter = warp % 4;
-        float *mine = scales + warp * 2 * S::HALF;
+        float *mine = scales + warp * 4 * S::HALF;
         constexpr int C = S::HALF < 16 ? 8 : 16;         // columns of a tensor-memory load
-        constexpr int PER = (S::HALF + 31) / 32;         // scales of a lane
+        static_assert(S::HALF <= 32, "a lane has one token's scales");
         uint32_t blk = 0;
         bool good = true;
         for (int64_t tile = first; tile < a.tiles && good; tile += step) {
@@ -275,22 +278,30 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
             uint64_t acc[S::HALF / 2];
 #pragma unroll
             for (int i = 0; i < S::HALF / 2; ++i) acc[i] = 0;
-            float sc[PER];
+            // A tile lies in one or two rows of scales, o0 / 128 and the next: a warp keeps its tokens' scales times either,
+            // and a lane reads those of its row of W.  They come four blocks at a time, a group ahead.
+            float wn[4], vn[4], xn[4], f[4], g[4];
+            const int64_t t = min(t0 + lane, a.T - 1), o0 = mt * a.rows, b0 = o0 / 128;
+            const int next = b0 + 1 < a.ob, second = (int)((o0 + quarter * 32 + lane) / 128 - b0);
             auto fetch = [&](int kb) {
-                const float w = __ldg(a.ws + (int64_t)kb * a.ob + mt);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int c = lane + 32 * i;
-                    sc[i] = c < S::HALF && t0 + c < a.T ? w * __ldg(a.xs + (int64_t)kb * a.T + t0 + c) : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = min(kb + i, kb1 - 1);
+                    wn[i] = __ldg(a.ws + k * a.ob + b0), vn[i] = __ldg(a.ws + k * a.ob + b0 + next), xn[i] = __ldg(a.xs + k * a.T + t);
                 }
             };
             fetch(kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++blk) {
-                float *s = mine + (blk & 1) * S::HALF;
+                float *s = mine + (blk & 1) * 2 * S::HALF;
+                if (((kb - kb0) & 3) == 0) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (lane + 32 * i < S::HALF) s[lane + 32 * i] = sc[i];
-                if (kb + 1 < kb1) fetch(kb + 1);
+                    for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i], g[i] = vn[i] * xn[i];
+                    if (kb + 4 < kb1) fetch(kb + 4);
+                }
+                if (lane < S::HALF) s[lane] = f[0], s[S::HALF + lane] = g[0];
+                f[0] = f[1], f[1] = f[2], f[2] = f[3];
+                g[0] = g[1], g[1] = g[2], g[2] = g[3];
+                s += second ? S::HALF : 0;
                 __syncwarp();
                 const int buf = blk % S::NB;
                 if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
             }
             if (!good) break;
             if (!SPLIT) {
-                f8_store<S::HALF>(a, ydt, t0, mt * 128 + quarter * 32 + lane, acc);
+                f8_store<S::HALF>(a, ydt, t0, o0 + quarter * 32 + lane, quarter * 32 + lane < a.rows, acc);
             } else {
                 // the ring is idle: all of this CTA's blocks have been multiplied
                 float *part = reinterpret_cast<float *>(ring);
@@ -348,8 +359,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
     __syncthreads();
     if (gave_up && threadIdx.x == 256) {
         // copies in flight land before this CTA ends
-        for (uint32_t i = issued > S::NST ? issued - S::NST : 0; i < issued; ++i)
-            f8_wait(&full[i % S::NST], (i / S::NST) & 1, a.status, kWaitDrain);
+        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i)
+            f8_wait(&full[i % a.stages], (i / a.stages) & 1, a.status, kWaitDrain);
     }
     __syncthreads();
     tc_fence_after();
@@ -378,21 +389,46 @@ static cudaError_t f8_launch(const LinearF8Args &a, const CUtensorMap &wmap, con
     return cudaLaunchKernelEx(&cfg, linear_f8_kernel<N, SPLIT>, a, wmap, xmap, ydt);
 }
 
+// A tile's height and the CTAs that share its sum, for tiles of n tokens: the least of waves of CTAs times a CTA's blocks,
+// a block taken as its bytes at an SM's share of HBM (44 bytes a ns) or 200 ns.  128 rows of W for 21504 are 168 tiles, two
+// waves for the second of which most SMs have nothing; 72 rows fill both (1 token, 5376 -> 21504: 32.6 us against @@).
+struct F8Tiles {
+    int rows, ctas;
+    double time;
+};
+
+static F8Tiles f8_plan(const LinearF8Args &a, int n, int sms)
+{
+    F8Tiles best{128, 1, 1e30};
+    const int64_t nt = (a.T + n - 1) / n;
+    for (int rows = 128; rows >= 32; rows -= 8)
+        for (int ctas = 1; ctas <= (rows == 128 ? 8 : 1); ctas *= 2) {
+            if (ctas > 1 && a.nkb < 2 * ctas) break;
+            const int64_t waves = ((a.out + rows - 1) / rows * nt * ctas + sms - 1) / sms;
+            if (ctas > 1 && waves > 1) break;
+            const double block = rows * 128.0 / 44 + n * 128.0 / 130;
+            const double time = (double)waves * ((a.nkb + ctas - 1) / ctas) * (block > 200 ? block : 200) + (ctas > 1 ? 2500 : 1500);
+            if (time < best.time) best = F8Tiles{rows, ctas, time};
+        }
+    return best;
+}
+
 template <int N>
 static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int64_t in, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
+    const F8Tiles p = f8_plan(a, N, di->sm_count);
     CUtensorMap wmap, xmap;
-    wl_status s = tmap_rows_u8(W, in, a.out, 128, &wmap);
+    wl_status s = tmap_rows_u8(W, in, a.out, p.rows, &wmap);
     if (s != WL_OK) return s;
     s = tmap_rows_u8(x, in, a.T, N, &xmap);
     if (s != WL_OK) return s;
     a.nt = (int)((a.T + N - 1) / N);
-    a.tiles = (int64_t)a.ob * a.nt;
-    int ctas = 1;
-    while (ctas < 8 && a.tiles * ctas * 2 <= di->sm_count && a.nkb >= 2 * ctas * 2) ctas *= 2;
-    const int64_t grid = ctas > 1 ? a.tiles * ctas : a.tiles < di->sm_count ? a.tiles : di->sm_count;
-    const cudaError_t e = ctas > 1 ? f8_launch<N, true>(a, wmap, xmap, ydt, ctas, (unsigned)grid, st)
-                                   : f8_launch<N, false>(a, wmap, xmap, ydt, 1, (unsigned)grid, st);
+    a.rows = p.rows;
+    a.stages = kF8Ring / ((p.rows + N) * 128) < kF8Stages ? kF8Ring / ((p.rows + N) * 128) : kF8Stages;
+    a.tiles = (a.out + p.rows - 1) / p.rows * a.nt;
+    const int64_t grid = p.ctas > 1 ? a.tiles * p.ctas : a.tiles < di->sm_count ? a.tiles : di->sm_count;
+    const cudaError_t e = p.ctas > 1 ? f8_launch<N, true>(a, wmap, xmap, ydt, p.ctas, (unsigned)grid, st)
+                                     : f8_launch<N, false>(a, wmap, xmap, ydt, 1, (unsigned)grid, st);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 
@@ -549,29 +585,32 @@ __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUten
     char *stage = ring + S::NST * S::STAGE + warp * 4096;
     uint32_t blk = 0;
     bool good = true;
+    // Scales come four blocks at a time, a group ahead and over the end of a tile (one block ahead, waiting for them was
+    // most of a block's time).
+    float wn[4], xn[4], f[4];
+    auto fetch = [&](int64_t tile, int kb) {
+        const int64_t mt = tile / a.nt, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
+        const float *wsp = a.ws + min(mt * 2 + half, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = min(kb + i, a.nkb - 1);
+            wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
+        }
+    };
+    fetch(first, 0);
     for (int64_t tile = first; tile < a.tiles && good; tile += step) {
         const int64_t mt = tile / a.nt;
         const int64_t o0 = mt * 256 + half * 128, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
-        const float *wsp = a.ws + min(o0 / 128, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
         uint64_t acc[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0;
-        // scales come four blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time)
-        float wn[4], xn[4], f[4];
-        auto fetch = [&](int kb) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t k = min(kb + i, a.nkb - 1);
-                wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
-            }
-        };
-        fetch(0);
 #pragma unroll 1
         for (int kb = 0; kb < a.nkb; ++kb, ++blk) {
             if ((kb & 3) == 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i];
-                fetch(kb + 4);
+                const bool here = kb + 4 < a.nkb;
+                fetch(here ? tile : tile + step, here ? kb + 4 : 0);
             }
             const uint64_t s = f8_both(f[0]);
             f[0] = f[1], f[1] = f[2], f[2] = f[3];
@@ -1073,18 +1112,12 @@ static wl_status f8_run_few(LinearF8Args a, const F8Few &p, const uint8_t *x, co
 wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale, void *y, int64_t T,
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
-    const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 0, di->status};
+    const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 128, 0, 0, di->status};
     // Tiles of 256 rows by 256 tokens where they fill half of the pairs.
     if (T > 128 && (out + 255) / 256 * ((T + 255) / 256) * 4 >= di->sm_count) return f8_run_pair(a, x, W, in, ydt, di, st);
-    if (T <= 128) {
+    if (T > 64 && T <= 128) {
         F8Few p;
-        // against a tile of 128 rows, its sum split over up to 8 CTAs: about 0.4 us a block of a CTA and 4 us beside
-        const double time = f8_few_plan(T, out, a.nkb, di->sm_count, &p);
-        const int64_t tiles = a.ob * ((T + 63) / 64);
-        int ctas = 1;
-        while (ctas < 8 && tiles * ctas * 2 <= di->sm_count && a.nkb >= 2 * ctas * 2) ctas *= 2;
-        const double split = (double)((tiles * ctas + di->sm_count - 1) / di->sm_count) * (a.nkb / ctas) * 400.0 + 1500.0;
-        if (time <= split) return f8_run_few(a, p, x, W, in, ydt, di, st);
+        if (f8_few_plan(T, out, a.nkb, di->sm_count, &p) <= f8_plan(a, 64, di->sm_count).time) return f8_run_few(a, p, x, W, in, ydt, di, st);
     }
     if (T <= 16) return f8_run<16>(a, x, W, in, ydt, di, st);
     if (T <= 32) return f8_run<32>(a, x, W, in, ydt, di, st);
