@@ -39,10 +39,10 @@ constexpr int kF8Threads = 320, kF8Stages = 24, kF8Ring = 192 * 1024;
 
 template <int N>
 struct F8Shape {
-    static constexpr int NB = 4;                 // accumulators
-    static constexpr int COLS = N * NB;          // 64 .. 256: a power of two
+    static constexpr int NB = 4;                 // pairs of accumulators
+    static constexpr int COLS = 2 * N * NB;      // 128 .. 512: a power of two
     static constexpr int HALF = N / 2;           // tokens of a warp
-    static constexpr int SCALES = 8 * 2 * 2 * HALF * 4;
+    static constexpr int SCALES = 8 * 2 * 4 * HALF * 4;
     // the MMAs read 128 rows whatever the tile's height: past the last stage too
     static constexpr int SMEM = 1024 + kF8Ring + 16384 + SCALES;
 };
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
     __shared__ int gave_up;
     char *ring = f8_smem + (1024 - s32(f8_smem) % 1024) % 1024;
     float *scales = reinterpret_cast<float *>(ring + kF8Ring + 16384);
-    const int bytes = (a.rows + N) * 128;  // of a stage
+    const int wbytes = a.rows * 128, bytes = 2 * (wbytes + N * 128);  // of a stage: two blocks of W, two of x
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = SPLIT ? (int)cl.block_rank() : 0, ctas = SPLIT ? (int)cl.num_blocks() : 1;
@@ -220,16 +220,19 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
         for (int64_t tile = first; tile < a.tiles && good; tile += step) {
             const int64_t mt = tile / a.nt;
             const int o0 = (int)(mt * a.rows), t0 = (int)(tile - mt * a.nt) * N;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            for (int kb = kb0; kb < kb1; kb += 2) {
                 if (!f8_wait(&empty[st], phase, a.status, kWaitRingEmpty)) {
                     good = false;
                     break;
                 }
                 if (issuer) {
-                    const uint32_t p = ring0 + st * bytes;
-                    mbar_expect_tx(&full[st], bytes);
-                    tma_load_2d_u32(p, &wmap, kb * 128, o0, &full[st]);
-                    tma_load_2d_u32(p + a.rows * 128, &xmap, kb * 128, t0, &full[st]);
+                    const uint32_t w = ring0 + st * bytes, x = w + 2 * wbytes;
+                    const int n = min(2, kb1 - kb);
+                    mbar_expect_tx(&full[st], n * (bytes / 2));
+                    for (int i = 0; i < n; ++i) {
+                        tma_load_2d_u32(w + i * wbytes, &wmap, (kb + i) * 128, o0, &full[st]);
+                        tma_load_2d_u32(x + i * N * 128, &xmap, (kb + i) * 128, t0, &full[st]);
+                    }
                 }
                 __syncwarp();
                 ++issued;
@@ -242,16 +245,21 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
         uint32_t st = 0, st_phase = 0, buf = 0, buf_phase = 1;
         bool good = true;
         for (int64_t tile = first; tile < a.tiles && good; tile += step) {
-            for (int kb = kb0; kb < kb1; ++kb) {
+            for (int kb = kb0; kb < kb1; kb += 2) {
                 if (!f8_wait(&tempty[buf], buf_phase, a.status, kWaitRingEmpty) || !f8_wait(&full[st], st_phase, a.status, kWaitRingFull)) {
                     good = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t da = sdesc(ring0 + st * bytes), db = sdesc(ring0 + st * bytes + a.rows * 128);
+                const uint64_t da = sdesc(ring0 + st * bytes), db = sdesc(ring0 + st * bytes + 2 * wbytes);
                 if (issuer) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) f8_mma(tmem + buf * N, da + 2 * j, db + 2 * j, f8_idesc(128, N), j > 0);
+                    for (int j = 0; j < 4; ++j) f8_mma(tmem + buf * 2 * N, da + 2 * j, db + 2 * j, f8_idesc(128, N), j > 0);
+                    if (kb + 1 < kb1) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            f8_mma(tmem + buf * 2 * N + N, da + wbytes / 16 + 2 * j, db + N * 8 + 2 * j, f8_idesc(128, N), j > 0);
+                    }
                     umma_commit(&tfull[buf]);
                     umma_commit(&empty[st]);
                 }
@@ -267,7 +275,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
         }
     } else {
         const int half = warp / 4, quarter = warp % 4;
-        float *mine = scales + warp * 4 * S::HALF;
+        float *mine = scales + warp * 8 * S::HALF;
         constexpr int C = S::HALF < 16 ? 8 : 16;         // columns of a tensor-memory load
         static_assert(S::HALF <= 32, "a lane has one token's scales");
         uint32_t blk = 0;
@@ -291,39 +299,47 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
                 }
             };
             fetch(kb0);
-            for (int kb = kb0; kb < kb1; ++kb, ++blk) {
-                float *s = mine + (blk & 1) * 2 * S::HALF;
+            for (int kb = kb0; kb < kb1; kb += 2, ++blk) {
+                // two blocks' scales for either row of them: [block][row][token]
+                float *s = mine + (blk & 1) * 4 * S::HALF;
                 if (((kb - kb0) & 3) == 0) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i], g[i] = vn[i] * xn[i];
                     if (kb + 4 < kb1) fetch(kb + 4);
                 }
-                if (lane < S::HALF) s[lane] = f[0], s[S::HALF + lane] = g[0];
-                f[0] = f[1], f[1] = f[2], f[2] = f[3];
-                g[0] = g[1], g[1] = g[2], g[2] = g[3];
-                s += second ? S::HALF : 0;
+                if (lane < S::HALF) s[lane] = f[0], s[S::HALF + lane] = g[0], s[2 * S::HALF + lane] = f[1], s[3 * S::HALF + lane] = g[1];
+                f[0] = f[2], f[1] = f[3], g[0] = g[2], g[1] = g[3];
                 __syncwarp();
+                s += second ? S::HALF : 0;
                 const int buf = blk % S::NB;
                 if (!f8_wait(&tfull[buf], (blk / S::NB) & 1, a.status, kWaitRingFull)) {
                     good = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * N + half * S::HALF;
+                const bool two = kb + 1 < kb1;
+                const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 2 * N + half * S::HALF;
 #pragma unroll
                 for (int c = 0; c < S::HALF; c += C) {
-                    uint32_t d[C];
+                    uint32_t d[C], e[C];
                     f8_tmem_ld<C>(at + c, d);
+                    if (two) f8_tmem_ld<C>(at + N + c, e);
                     f8_tmem_wait<C>(d);
+                    f8_tmem_wait<C>(e);
                     if (c + C == S::HALF) {
                         tc_fence_before();
                         if (lane == 0) mbar_arrive(&tempty[buf]);
                     }
 #pragma unroll
                     for (int i = 0; i < C; i += 4) {
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(s + c + i);
-                        fma2(acc[(c + i) / 2], d[i], d[i + 1], f.x);
-                        fma2(acc[(c + i) / 2 + 1], d[i + 2], d[i + 3], f.y);
+                        const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(s + c + i);
+                        fma2(acc[(c + i) / 2], d[i], d[i + 1], p.x);
+                        fma2(acc[(c + i) / 2 + 1], d[i + 2], d[i + 3], p.y);
+                        if (two) {
+                            const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(s + 2 * S::HALF + c + i);
+                            fma2(acc[(c + i) / 2], e[i], e[i + 1], q.x);
+                            fma2(acc[(c + i) / 2 + 1], e[i + 2], e[i + 3], q.y);
+                        }
                     }
                 }
             }
@@ -389,9 +405,10 @@ static cudaError_t f8_launch(const LinearF8Args &a, const CUtensorMap &wmap, con
     return cudaLaunchKernelEx(&cfg, linear_f8_kernel<N, SPLIT>, a, wmap, xmap, ydt);
 }
 
-// A tile's height and the CTAs that share its sum, for tiles of n tokens: the least of waves of CTAs times a CTA's blocks,
-// a block taken as its bytes at an SM's share of HBM (44 bytes a ns) or 200 ns.  128 rows of W for 21504 are 168 tiles, two
-// waves for the second of which most SMs have nothing; 72 rows fill both (1 token, 5376 -> 21504: 32.6 us against @@).
+// A tile's height and the CTAs that share its sum, for tiles of n tokens: the least of waves of CTAs times what a CTA takes.
+// A block takes 0.22 us (n = 16; 0.33 for 64), from about 75 rows on more by its bytes, a tile 0.8 us beside (all measured).
+// 128 rows of W for 21504 are 168 tiles, two waves in the second of which most SMs have nothing: 1 token, 5376 -> 21504
+// takes 26.7 us with them and 22.1 with 72 rows, which fill both; 5376 -> 5376 11.6 with any height that fits one wave.
 struct F8Tiles {
     int rows, ctas;
     double time;
@@ -406,8 +423,8 @@ static F8Tiles f8_plan(const LinearF8Args &a, int n, int sms)
             if (ctas > 1 && a.nkb < 2 * ctas) break;
             const int64_t waves = ((a.out + rows - 1) / rows * nt * ctas + sms - 1) / sms;
             if (ctas > 1 && waves > 1) break;
-            const double block = rows * 128.0 / 44 + n * 128.0 / 130;
-            const double time = (double)waves * ((a.nkb + ctas - 1) / ctas) * (block > 200 ? block : 200) + (ctas > 1 ? 2500 : 1500);
+            const double least = 220 + 2.2 * (n - 16), bytes = 130 + 2.1 * (n - 16) + 1.2 * rows;
+            const double time = (double)waves * (((a.nkb + ctas - 1) / ctas) * (bytes > least ? bytes : least) + 800) + (ctas > 1 ? 3000 : 0);
             if (time < best.time) best = F8Tiles{rows, ctas, time};
         }
     return best;
@@ -424,7 +441,7 @@ static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int6
     if (s != WL_OK) return s;
     a.nt = (int)((a.T + N - 1) / N);
     a.rows = p.rows;
-    a.stages = kF8Ring / ((p.rows + N) * 128) < kF8Stages ? kF8Ring / ((p.rows + N) * 128) : kF8Stages;
+    a.stages = kF8Ring / ((p.rows + N) * 256) < kF8Stages ? kF8Ring / ((p.rows + N) * 256) : kF8Stages;
     a.tiles = (a.out + p.rows - 1) / p.rows * a.nt;
     const int64_t grid = p.ctas > 1 ? a.tiles * p.ctas : a.tiles < di->sm_count ? a.tiles : di->sm_count;
     const cudaError_t e = p.ctas > 1 ? f8_launch<N, true>(a, wmap, xmap, ydt, p.ctas, (unsigned)grid, st)
@@ -807,18 +824,17 @@ static wl_status f8_run_pair(LinearF8Args a, const uint8_t *x, const uint8_t *W,
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 
-// -------------------------------------------------------- few tokens, many rows --
-// Up to 128 tokens: W's bytes are the time.  Tokens are M (rows of the tile past
-// them hold whatever the ring holds: their sums are not stored), `rows` rows of W
-// are N, chosen so that the tiles fill whole waves of SMs: 84 tiles of 256 for
-// 21504 rows leave 68 SMs idle, 150 of 144 none.  A tile so begins at any
-// multiple of 16 and may cross from one row of scales to the next once in a warp's
-// columns.  Only the warps that hold tokens read the sums.
+// ------------------------------------------------------------- 65 to 128 tokens --
+// W's bytes are the time, and each is read once: tokens are M (rows of the tile
+// past them hold whatever the ring holds: their sums are not stored), `rows` rows
+// of W are N, chosen so that the tiles fill whole waves of SMs.  A tile so begins
+// at any multiple of 64 and crosses from one row of scales to the next at most
+// once in a warp's columns.
 struct F8Few {
     int rows, xrows;   // rows of W of a tile; rows of the token box: T up to a multiple of 8
     int stages, stage; // of the ring, bytes of one
     int cols, bufs;    // accumulators: 64, 128 or 256 columns, 512 in all
-    int half;          // columns of side 0
+    int half;          // columns of a side
 };
 
 constexpr int kFewStages = 16, kFewThreads = 384;
@@ -1067,19 +1083,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __g
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-// The few tokens' tile height, and what it is thought to take: waves of tiles, a block's bytes at an SM's share of HBM
-// (44 bytes a ns) or the round of its copy, and 0.7 us a tile.
+// The tile height for 65 to 128 tokens and what it is thought to take: waves of tiles, a block's and a tile's time as
+// measured (96 tokens, 1152 -> 262144: 58.7 us with 256 rows, 65 with 192; 128 tokens, 5376 -> 21504: 26.5 with 192, 42 with 128).
 static double f8_few_plan(int64_t T, int64_t out, int nkb, int sms, F8Few *p)
 {
-    const int step = T > 8 ? 64 : 16;  // more than a few tokens are stored in boxes of 32 rows of W a side
     double best = 1e30;
     p->xrows = (int)(T + 7) / 8 * 8;
-    for (int rows = step; rows <= 256; rows += step) {
+    for (int rows = 64; rows <= 256; rows += 64) {
         const int64_t waves = ((out + rows - 1) / rows + sms - 1) / sms;
-        const double block = rows * 128.0 / 44 + p->xrows * 128.0 / 130, time = waves * (nkb * (block > 200 ? block : 200) + 700);
+        const double time = (double)waves * (nkb * (300 + 1.35 * rows) + 10.5 * rows);
         if (time < best) best = time, p->rows = rows;
     }
-    p->half = step == 64 ? p->rows / 2 : (p->rows / 2 + 15) / 16 * 16;
+    p->half = p->rows / 2;  // a multiple of 32: boxes of 32 rows of W
     p->stage = (p->rows + p->xrows) * 128;
     p->stages = 192 * 1024 / p->stage < kFewStages ? 192 * 1024 / p->stage : kFewStages;
     p->cols = p->rows <= 64 ? 64 : p->rows <= 128 ? 128 : 256;
@@ -1095,7 +1110,7 @@ static wl_status f8_run_few(LinearF8Args a, const F8Few &p, const uint8_t *x, co
     if (s != WL_OK) return s;
     s = tmap_rows_u8(x, in, a.T, p.xrows, &xmap);
     if (s != WL_OK) return s;
-    const bool f32 = ydt == WL_OUT_F32, boxes = a.T > 8 && a.out % (f32 ? 4 : 8) == 0;
+    const bool f32 = ydt == WL_OUT_F32, boxes = a.out % (f32 ? 4 : 8) == 0;
     if (boxes) {
         s = f32 ? tmap_2d_f32(a.y, a.out, a.T, 32, 32, &ymap) : tmap_2d_bf16_swz(a.y, a.out, a.T, a.out, 32, 32, 64, &ymap);
         if (s != WL_OK) return s;
