@@ -13,7 +13,7 @@
 // Decisions.  A random number closer to a border between two tokens than the
 // sums' rounding would give another token than exact arithmetic does, and a
 // vocabulary has 10^5 borders.  So the sums that decide are made of weights held
-// as two floats (about 2^-36 of each weight), and the sums of the fast pass
+// as two floats (about 2^-31 of each weight), and the sums of the fast pass
 // decide only where their error (kTol of the row's sum) cannot matter.
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -25,29 +25,56 @@ namespace cg = cooperative_groups;
 
 namespace wl {
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 1024;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kVerCtas = 8;   // CTAs of a cluster at most
+constexpr int kVerCtas = 16;  // CTAs of a cluster at most
 constexpr double kTol = 5e-6; // fast sums are right to this part of the row's sum
 
-// 2^(j/32) as two floats.
-__constant__ float2 kExp2Table[32] = {
-    {0x1.0p+0f, 0x0.0p+0f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f},
-    {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.11301ep+0f, -0x1.fdb496p-25f},
-    {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
-    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f},
-    {0x1.306fep+0f, 0x1.4636e2p-25f}, {0x1.371a74p+0f, -0x1.18aac6p-25f},
-    {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
-    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5342b6p+0f, -0x1.2c561p-25f},
-    {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.6247ecp+0f, -0x1.f8b55p-25f},
-    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f},
-    {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f},
-    {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.93737cp+0f, -0x1.e64744p-25f},
-    {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
-    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b7f77p+0f, -0x1.a09438p-25f},
-    {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.cb720ep+0f, -0x1.8837ccp-27f},
-    {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
-    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.f50766p+0f, -0x1.246ebp-26f}};
+// 2^(j/128) as two floats.
+__constant__ float2 kExp2Table[128] = {
+    {0x1.0p+0f, 0x0.0p+0f}, {0x1.0163dap+0f, 0x1.3f6666p-25f}, {0x1.02c9a4p+0f, -0x1.887fap-28f},
+    {0x1.04315ep+0f, 0x1.0dcffp-25f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0706b2p+0f, 0x1.3bbedcp-25f},
+    {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.09e3ecp+0f, 0x1.58de7p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f},
+    {0x1.0cc922p+0f, 0x1.6e48fep-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f}, {0x1.0fb66ap+0f, 0x1.ffda64p-25f},
+    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.12abdcp+0f, 0x1.b0c73p-30f}, {0x1.1429aap+0f, 0x1.d525bcp-25f},
+    {0x1.15a98cp+0f, 0x1.14b1cap-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.18af94p+0f, -0x1.dcdc86p-26f},
+    {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1bbe08p+0f, 0x1.011734p-26f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
+    {0x1.1ed502p+0f, 0x1.7e6c8ep-27f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f}, {0x1.21f49ap+0f, -0x1.d0446ep-25f},
+    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.251ce4p+0f, 0x1.f654c8p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f},
+    {0x1.284dfep+0f, 0x1.f5638p-28f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f}, {0x1.2b87fep+0f, -0x1.e4a4cep-25f},
+    {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.2ecafap+0f, 0x1.27c5eap-25f}, {0x1.306fep+0f, 0x1.4636e2p-25f},
+    {0x1.32171p+0f, -0x1.d993e8p-27f}, {0x1.33c08cp+0f, -0x1.b37d2p-25f}, {0x1.356c56p+0f, -0x1.b5803cp-30f},
+    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.38cae6p+0f, 0x1.a0bb0cp-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f},
+    {0x1.3c32dcp+0f, 0x1.89d472p-27f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.3fa45p+0f, 0x1.2b2006p-26f},
+    {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.431f5ep+0f, -0x1.abd5dap-26f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.46a41ep+0f, 0x1.a3a00ap-25f}, {0x1.486a2cp+0f, -0x1.47d866p-25f}, {0x1.4a32bp+0f, -0x1.e50584p-25f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4dcb2ap+0f, -0x1.8088bcp-26f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f},
+    {0x1.516daap+0f, 0x1.67b32p-27f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.551a4cp+0f, 0x1.4bb242p-25f},
+    {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.58d12ep+0f, -0x1.6d07p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
+    {0x1.5c9268p+0f, 0x1.4b28d6p-25f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f}, {0x1.605e1cp+0f, -0x1.a248fep-26f},
+    {0x1.6247ecp+0f, -0x1.f8b55p-25f}, {0x1.643464p+0f, -0x1.66679cp-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f},
+    {0x1.68155ep+0f, -0x1.766ad2p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.6c0128p+0f, -0x1.5e84a8p-25f},
+    {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.6ff7ep+0f, -0x1.ab9aep-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f},
+    {0x1.73f9a4p+0f, 0x1.14b02ep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f}, {0x1.780694p+0f, 0x1.fbcba8p-25f},
+    {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.7c1edp+0f, 0x1.30c132p-28f}, {0x1.7e2f34p+0f, -0x1.261634p-25f},
+    {0x1.804276p+0f, -0x1.783cbep-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8471a4p+0f, 0x1.88f1ecp-26f},
+    {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.88ac7ep+0f, -0x1.9d665ap-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f},
+    {0x1.8cf322p+0f, -0x1.29576ep-25f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f}, {0x1.9145bp+0f, 0x1.723ff8p-25f},
+    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.95a44cp+0f, 0x1.790a42p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f},
+    {0x1.9a0f18p+0f, -0x1.e6bf08p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.9e8632p+0f, -0x1.873738p-26f},
+    {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a309bep+0f, 0x1.8945a6p-25f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.a799e2p+0f, -0x1.99e994p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f}, {0x1.ac36bcp+0f, -0x1.606432p-31f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b0e072p+0f, 0x1.31b6ccp-25f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f},
+    {0x1.b59728p+0f, 0x1.bcab28p-25f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.ba5b04p+0f, -0x1.ebdf36p-25f},
+    {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.bf2c26p+0f, -0x1.0a387ep-26f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f},
+    {0x1.c40ab6p+0f, -0x1.7c2c98p-39f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f}, {0x1.c8f6dap+0f, -0x1.7f230ap-25f},
+    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.cdf0b6p+0f, -0x1.54478p-25f}, {0x1.d072d4p+0f, 0x1.40f13p-25f},
+    {0x1.d2f87p+0f, 0x1.01b13ep-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.d80e32p+0f, -0x1.26cf8ep-25f},
+    {0x1.da9e6p+0f, 0x1.ed9942p-27f}, {0x1.dd322p+0f, -0x1.9fc974p-25f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
+    {0x1.e26462p+0f, -0x1.614bdap-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f}, {0x1.e7a52p+0f, -0x1.0e2cep-26f},
+    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.ecf482p+0f, 0x1.b1ccfep-25f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f},
+    {0x1.f252b4p+0f, -0x1.1288aep-25f}, {0x1.f50766p+0f, -0x1.246ebp-26f}, {0x1.f7bfdap+0f, 0x1.b397c2p-25f},
+    {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}, {0x1.fd3c22p+0f, 0x1.71ee3ep-25f}};
 
 // ------------------------------------------------------------ two floats --
 struct FF {
@@ -68,32 +95,24 @@ __device__ __forceinline__ FF ff_of(double d)
     return FF{h, (float)(d - (double)h)};
 }
 
-// 2^((l - m) c), l <= m, right to about 2^-36 of itself; 0 below 2^-100.
+// 2^((l - m) c), l <= m, right to about 2^-31 of itself; 0 below 2^-100 and where l is -infinity (rows with a NaN do not
+// come here).  h has the table's bits, l is up to 2^-8 of h.
 __device__ __forceinline__ FF weight(float l, float m, FF c, const float2 *table)
 {
     const float d = l - m, t = d - l;
-    const float dl = (l - (d - t)) - (m + t);
-    const float y = d * c.h;
-    if (!(y >= -100.0f)) return FF{0.0f, 0.0f};
+    const float dl = (l - (d - t)) - (m + t);  // what d has lost
+    const float y = fmaxf(d * c.h, -128.0f);
     const float yl = fmaf(dl, c.h, fmaf(d, c.l, fmaf(d, c.h, -y)));
-    // y + yl = k/32 + f, |f| <= 1/64
+    // y + yl = k/128 + f, |f| <= 1/256
     const float magic = 12582912.0f;  // 1.5 * 2^23
-    const float z = fmaf(y, 32.0f, magic);
-    const int j = __float_as_int(z) - 0x4b400000;
-    const float fh = fmaf(z - magic, -0.03125f, y);
-    const float f = fh + yl, fl = yl - (f - fh);
-    // 2^f - 1 = f ln2 + f^2 (ln2^2/2 + f ln2^3/6 + ...), the first term as two floats
-    const float ln2 = 0x1.62e43p-1f, ln2l = -0x1.05c61p-29f;
-    const float e2 = f * f * fmaf(f, fmaf(f, fmaf(f, 0x1.5d87fep-10f, 0x1.3b2ab6p-7f), 0x1.c6b08ep-5f), 0x1.ebfbep-3f);
-    const float gh = f * ln2;
-    const float gl = fmaf(f, ln2, -gh) + fmaf(f, ln2l, fmaf(fl, ln2, e2));
-    const float2 T = table[j & 31];
-    const float p = T.x * gh;
-    const float pl = fmaf(T.x, gh, -p) + fmaf(T.x, gl, fmaf(T.y, gh, T.y));
-    const float wh = T.x + p;
-    const float wl = (p - (wh - T.x)) + pl;
-    const float s = exp2_int(j >> 5);
-    return FF{wh * s, wl * s};
+    const float z = fmaf(y, 128.0f, magic);
+    const float f = fmaf(z - magic, -0.0078125f, y) + yl;
+    // 2^f - 1 = f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6, the next term below 2^-38
+    const float g = f * fmaf(f, fmaf(f, 0x1.c6b08ep-5f, 0x1.ebfbep-3f), 0x1.62e43p-1f);
+    const float2 T = table[__float_as_int(z) & 127];
+    // 2^k by its bits: z's integer part from bit 7 on
+    const float s = __int_as_float(((__float_as_int(z) & ~127) << 16) + 0x3f800000);
+    return y > -100.0f ? FF{T.x * s, fmaf(T.x, g, T.y) * s} : FF{0.0f, 0.0f};
 }
 
 // max(R - S q, 0)
@@ -196,7 +215,7 @@ struct VerShared {
     FF warp_total[kVerWarps];
     FF S[kMaxTree];  // sum of R before rejection j
     int excluded[kMaxTree], nex, rejected;
-    float2 table[32];
+    float2 table[128];
     int path[kMaxTree];
     float m;          // the row's maximum ...
     int best;         // ... and its place, -1 for a row without a distribution
@@ -217,6 +236,16 @@ struct VerRow {
         v1 = min(v0 + per, vecs.nv);
     }
 };
+
+// This warp's share of another row, which begins at `next`, into L2.
+template <typename T, typename L>
+__device__ __forceinline__ void prefetch_row(const T *next, const VerRow<L> &r)
+{
+    constexpr int LINE = 128 / (int)sizeof(T);
+    const int e1 = min(r.vecs.first(r.v1), r.vecs.n);
+    for (int e = max(r.vecs.first(r.v0), 0) + (int)threadIdx.x % 32 * LINE; e < e1; e += 32 * LINE)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + e));
+}
 
 __device__ __forceinline__ VerPart join(VerPart a, float c)  // over the warp
 {
@@ -304,6 +333,19 @@ __device__ __forceinline__ void residuals(const VerShared &sh, const VerRow<L> &
     }
 }
 
+// The sum of a vector's numbers: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
+template <int E>
+__device__ __forceinline__ FF vec_sum(const FF R[E])
+{
+    FF s{0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float h = (R[i].h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
+        s.h += h, s.l += (R[i].h - h) + R[i].l;
+    }
+    return s;
+}
+
 __device__ __forceinline__ FF ff_warp_sum(FF a)
 {
 #pragma unroll
@@ -325,8 +367,7 @@ __device__ __forceinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, c
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
         FF R[E];
         residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, rejected, nex, R);
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc = ff_add(acc, R[i]);
+        acc = ff_add(acc, vec_sum<E>(R));
     }
     acc = ff_warp_sum(acc);
     if (lane == 0) sh.warp_total[warp] = acc;
@@ -394,14 +435,12 @@ __device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const 
 #pragma unroll
             for (int i = 0; i < E; ++i) R[i] = FF{0.0f, 0.0f};
         }
-        FF acc{0.0f, 0.0f};
+        const FF acc = vec_sum<E>(R);
         const int e0 = r.vecs.first(v0 + lane);
         int top = -1;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            acc = ff_add(acc, R[i]);
+        for (int i = 0; i < E; ++i)
             if (R[i].h > 0.0f) top = e0 + i;
-        }
         top = __reduce_max_sync(0xffffffffu, top);
         if (top >= 0) last = top;
         const double tile = ff_double(ff_warp_sum(acc));
@@ -440,7 +479,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
     const int b = (int)blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t row0 = (int64_t)b * a.n;
-    if (tid < 32) sh.table[tid] = kExp2Table[tid];
+    if (tid < 128) sh.table[tid] = kExp2Table[tid];
     cl.sync();  // from here on peers write into this CTA's memory
     pdl_wait();
     pdl_trigger();
@@ -491,6 +530,13 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                     p->child_l[side][i] = l, p->child_q[side][i] = q;
                 }
             }
+        }
+        if (a.n > 1) {
+            // the first child's row is the likeliest next one: towards L2 while this one is read
+            const unsigned lo = __ballot_sync(0xffffffffu, lane < sh.count && lane > node && sh.parent[lane] == node);
+            const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 < sh.count && lane + 32 > node && sh.parent[lane + 32] == node);
+            const int kid = lo ? __ffs((int)lo) - 1 : hi ? 31 + __ffs((int)hi) : 0;
+            if (kid) prefetch_row(static_cast<const L *>(a.logits) + (row0 + kid) * a.logits_stride, row);
         }
         const VerPart mine = join(row_part(row, greedy, sh.c.h), sh.c.h);
         if (lane == 0) sh.warp_part[warp] = mine;
@@ -574,6 +620,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
             }
             __syncthreads();
             if (sh.code != kPass) break;
+            if (DRAFT && sh.rejected == 0) prefetch_row(qrow, row);  // wanted if the child is rejected, as it nearly is
             sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
             turn ^= 1;
             if (warp == 0) S = sh.sum, exact = true;
@@ -623,6 +670,10 @@ static cudaError_t verify_launch(const VerifyArgs &a, int ctas, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
+    if (ctas > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(verify_kernel<L, Q, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     return cudaLaunchKernelEx(&cfg, verify_kernel<L, Q, DRAFT>, a);
 }
 
@@ -637,7 +688,7 @@ wl_status launch_verify(const VerifyArgs &a, int ldt, int ddt, const DeviceInfo 
 {
     // A sequence's CTAs: as many as fill the GPU, at most one for 8192 tokens of the vocabulary.
     int ctas = kVerCtas;
-    while (ctas > 1 && (a.batch * ctas > di->sm_count || (int64_t)a.vocab < 8192 * (ctas / 2))) ctas /= 2;
+    while (ctas > 1 && ((int64_t)a.batch * ctas > di->sm_count || (int64_t)a.vocab < 8192 * (ctas / 2))) ctas /= 2;
     const cudaError_t e = ldt == WL_OUT_F32 ? verify_draft<float>(a, ddt, ctas, st) : verify_draft<bf16>(a, ddt, ctas, st);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_verify launch");
 }
