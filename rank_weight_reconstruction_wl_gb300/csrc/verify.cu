@@ -13,8 +13,8 @@
 // Decisions.  A random number closer to a border between two tokens than the
 // sums' rounding would give another token than exact arithmetic does, and a
 // vocabulary has 10^5 borders.  So the sums that decide are made of weights held
-// as two floats (about 2^-31 of each weight), and the sums of the fast pass
-// decide only where their error (kTol of the row's sum) cannot matter.
+// as two floats (about 2^-30 of each weight), and the sums of the fast pass
+// decide only where their error (a few 10^-6 of the row's sum) cannot matter.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -28,53 +28,27 @@ namespace wl {
 constexpr int kVerThreads = 1024;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerCtas = 16;  // CTAs of a cluster at most
-constexpr double kTol = 5e-6; // fast sums are right to this part of the row's sum
+constexpr float kTolSum = 6e-7f, kTolBit = 1.3e-7f;
+// A fast sum is right to kTolSum + kTolBit log2(vocab) of the row's sum: 2^-22 for ex2, three roundings of 2^-24 in a
+// vector's sum, and three of y = (l - max) c, each |y| 2^-24 ln2 of the weight, whose sum over the row is at most
+// log2(vocab) 2^-24 ln2 of its sum (the entropy of the weights is at most log2(vocab)).
 
-// 2^(j/128) as two floats.
-__constant__ float2 kExp2Table[128] = {
-    {0x1.0p+0f, 0x0.0p+0f}, {0x1.0163dap+0f, 0x1.3f6666p-25f}, {0x1.02c9a4p+0f, -0x1.887fap-28f},
-    {0x1.04315ep+0f, 0x1.0dcffp-25f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0706b2p+0f, 0x1.3bbedcp-25f},
-    {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.09e3ecp+0f, 0x1.58de7p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f},
-    {0x1.0cc922p+0f, 0x1.6e48fep-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f}, {0x1.0fb66ap+0f, 0x1.ffda64p-25f},
-    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.12abdcp+0f, 0x1.b0c73p-30f}, {0x1.1429aap+0f, 0x1.d525bcp-25f},
-    {0x1.15a98cp+0f, 0x1.14b1cap-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.18af94p+0f, -0x1.dcdc86p-26f},
-    {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1bbe08p+0f, 0x1.011734p-26f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
-    {0x1.1ed502p+0f, 0x1.7e6c8ep-27f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f}, {0x1.21f49ap+0f, -0x1.d0446ep-25f},
-    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.251ce4p+0f, 0x1.f654c8p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f},
-    {0x1.284dfep+0f, 0x1.f5638p-28f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f}, {0x1.2b87fep+0f, -0x1.e4a4cep-25f},
-    {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.2ecafap+0f, 0x1.27c5eap-25f}, {0x1.306fep+0f, 0x1.4636e2p-25f},
-    {0x1.32171p+0f, -0x1.d993e8p-27f}, {0x1.33c08cp+0f, -0x1.b37d2p-25f}, {0x1.356c56p+0f, -0x1.b5803cp-30f},
-    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.38cae6p+0f, 0x1.a0bb0cp-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f},
-    {0x1.3c32dcp+0f, 0x1.89d472p-27f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.3fa45p+0f, 0x1.2b2006p-26f},
-    {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.431f5ep+0f, -0x1.abd5dap-26f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
-    {0x1.46a41ep+0f, 0x1.a3a00ap-25f}, {0x1.486a2cp+0f, -0x1.47d866p-25f}, {0x1.4a32bp+0f, -0x1.e50584p-25f},
-    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4dcb2ap+0f, -0x1.8088bcp-26f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f},
-    {0x1.516daap+0f, 0x1.67b32p-27f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.551a4cp+0f, 0x1.4bb242p-25f},
-    {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.58d12ep+0f, -0x1.6d07p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
-    {0x1.5c9268p+0f, 0x1.4b28d6p-25f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f}, {0x1.605e1cp+0f, -0x1.a248fep-26f},
-    {0x1.6247ecp+0f, -0x1.f8b55p-25f}, {0x1.643464p+0f, -0x1.66679cp-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f},
-    {0x1.68155ep+0f, -0x1.766ad2p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.6c0128p+0f, -0x1.5e84a8p-25f},
-    {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.6ff7ep+0f, -0x1.ab9aep-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f},
-    {0x1.73f9a4p+0f, 0x1.14b02ep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f}, {0x1.780694p+0f, 0x1.fbcba8p-25f},
-    {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.7c1edp+0f, 0x1.30c132p-28f}, {0x1.7e2f34p+0f, -0x1.261634p-25f},
-    {0x1.804276p+0f, -0x1.783cbep-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8471a4p+0f, 0x1.88f1ecp-26f},
-    {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.88ac7ep+0f, -0x1.9d665ap-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f},
-    {0x1.8cf322p+0f, -0x1.29576ep-25f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f}, {0x1.9145bp+0f, 0x1.723ff8p-25f},
-    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.95a44cp+0f, 0x1.790a42p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f},
-    {0x1.9a0f18p+0f, -0x1.e6bf08p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.9e8632p+0f, -0x1.873738p-26f},
-    {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a309bep+0f, 0x1.8945a6p-25f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
-    {0x1.a799e2p+0f, -0x1.99e994p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f}, {0x1.ac36bcp+0f, -0x1.606432p-31f},
-    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b0e072p+0f, 0x1.31b6ccp-25f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f},
-    {0x1.b59728p+0f, 0x1.bcab28p-25f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.ba5b04p+0f, -0x1.ebdf36p-25f},
-    {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.bf2c26p+0f, -0x1.0a387ep-26f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f},
-    {0x1.c40ab6p+0f, -0x1.7c2c98p-39f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f}, {0x1.c8f6dap+0f, -0x1.7f230ap-25f},
-    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.cdf0b6p+0f, -0x1.54478p-25f}, {0x1.d072d4p+0f, 0x1.40f13p-25f},
-    {0x1.d2f87p+0f, 0x1.01b13ep-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.d80e32p+0f, -0x1.26cf8ep-25f},
-    {0x1.da9e6p+0f, 0x1.ed9942p-27f}, {0x1.dd322p+0f, -0x1.9fc974p-25f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
-    {0x1.e26462p+0f, -0x1.614bdap-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f}, {0x1.e7a52p+0f, -0x1.0e2cep-26f},
-    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.ecf482p+0f, 0x1.b1ccfep-25f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f},
-    {0x1.f252b4p+0f, -0x1.1288aep-25f}, {0x1.f50766p+0f, -0x1.246ebp-26f}, {0x1.f7bfdap+0f, 0x1.b397c2p-25f},
-    {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}, {0x1.fd3c22p+0f, 0x1.71ee3ep-25f}};
+// 2^(j/32) as two floats, in two tables: 32 entries of 4 bytes are 32 banks, so that lanes never collide (128 pairs of
+// floats took six accesses a warp).
+__constant__ float kExp2High[32] = {
+    0x1.0p+0f, 0x1.059b0ep+0f, 0x1.0b5586p+0f, 0x1.11301ep+0f, 0x1.172b84p+0f, 0x1.1d4874p+0f,
+    0x1.2387a6p+0f, 0x1.29e9ep+0f, 0x1.306fep+0f, 0x1.371a74p+0f, 0x1.3dea64p+0f, 0x1.44e086p+0f,
+    0x1.4bfdaep+0f, 0x1.5342b6p+0f, 0x1.5ab07ep+0f, 0x1.6247ecp+0f, 0x1.6a09e6p+0f, 0x1.71f75ep+0f,
+    0x1.7a1148p+0f, 0x1.82589ap+0f, 0x1.8ace54p+0f, 0x1.93737cp+0f, 0x1.9c4918p+0f, 0x1.a5503cp+0f,
+    0x1.ae89fap+0f, 0x1.b7f77p+0f, 0x1.c199bep+0f, 0x1.cb720ep+0f, 0x1.d5818ep+0f, 0x1.dfc974p+0f,
+    0x1.ea4afap+0f, 0x1.f50766p+0f};
+__constant__ float kExp2Low[32] = {
+    0x0.0p+0f, -0x1.9d4f52p-25f, 0x1.9f3122p-25f, -0x1.fdb496p-25f, -0x1.c15742p-27f, -0x1.d2e8cap-25f,
+    0x1.ceac48p-25f, -0x1.5c0424p-25f, 0x1.4636e2p-25f, -0x1.18aac6p-25f, 0x1.824684p-25f, 0x1.8624b4p-30f,
+    -0x1.593abcp-25f, -0x1.2c561p-25f, -0x1.5bd5ecp-27f, -0x1.f8b55p-25f, 0x1.9fcef4p-26f, 0x1.1d8beep-25f,
+    -0x1.829fdp-25f, -0x1.accc7cp-26f, 0x1.15506ep-27f, -0x1.e64744p-25f, 0x1.51f848p-27f, -0x1.b83b54p-25f,
+    -0x1.a94b14p-26f, -0x1.a09438p-25f, -0x1.3d56b2p-27f, -0x1.8837ccp-27f, -0x1.822dbcp-27f, -0x1.908c94p-25f,
+    0x1.52486cp-27f, -0x1.246ebp-26f};
 
 // ------------------------------------------------------------ two floats --
 struct FF {
@@ -88,6 +62,26 @@ __device__ __forceinline__ FF ff_add(FF a, FF b)
     return FF{s, e + (a.l + b.l)};
 }
 
+// The same with l below half a step of h, so that two of them compare by h, then l.
+__device__ __forceinline__ FF ff_norm(FF a)
+{
+    const float s = a.h + a.l;
+    return FF{s, a.l - (s - a.h)};
+}
+__device__ __forceinline__ FF ff_mul(FF a, float f)
+{
+    const float p = a.h * f;
+    return ff_norm(FF{p, fmaf(a.h, f, -p) + a.l * f});
+}
+__device__ __forceinline__ bool ff_less(FF a, FF b)  // false where one is NaN
+{
+    return a.h < b.h || (a.h == b.h && a.l < b.l);
+}
+__device__ __forceinline__ FF ff_mul(FF a, FF b)
+{
+    const float p = a.h * b.h;
+    return FF{p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h)};
+}
 __device__ __forceinline__ double ff_double(FF a) { return (double)a.h + (double)a.l; }
 __device__ __forceinline__ FF ff_of(double d)
 {
@@ -95,24 +89,25 @@ __device__ __forceinline__ FF ff_of(double d)
     return FF{h, (float)(d - (double)h)};
 }
 
-// 2^((l - m) c), l <= m, right to about 2^-31 of itself; 0 below 2^-100 and where l is -infinity (rows with a NaN do not
-// come here).  h has the table's bits, l is up to 2^-8 of h.
-__device__ __forceinline__ FF weight(float l, float m, FF c, const float2 *table)
+// 2^((l - m) c), l <= m, right to about 2^-30 of itself; 0 below 2^-100 and where l is -infinity (rows with a NaN do not
+// come here).  h has the table's bits, l is up to 2^-6 of h.
+__device__ __forceinline__ FF weight(float l, float m, FF c, const float *table)
 {
     const float d = l - m, t = d - l;
     const float dl = (l - (d - t)) - (m + t);  // what d has lost
     const float y = fmaxf(d * c.h, -128.0f);
     const float yl = fmaf(dl, c.h, fmaf(d, c.l, fmaf(d, c.h, -y)));
-    // y + yl = k/128 + f, |f| <= 1/256
+    // y + yl = k/32 + f, |f| <= 1/64
     const float magic = 12582912.0f;  // 1.5 * 2^23
-    const float z = fmaf(y, 128.0f, magic);
-    const float f = fmaf(z - magic, -0.0078125f, y) + yl;
-    // 2^f - 1 = f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6, the next term below 2^-38
-    const float g = f * fmaf(f, fmaf(f, 0x1.c6b08ep-5f, 0x1.ebfbep-3f), 0x1.62e43p-1f);
-    const float2 T = table[__float_as_int(z) & 127];
-    // 2^k by its bits: z's integer part from bit 7 on
-    const float s = __int_as_float(((__float_as_int(z) & ~127) << 16) + 0x3f800000);
-    return y > -100.0f ? FF{T.x * s, fmaf(T.x, g, T.y) * s} : FF{0.0f, 0.0f};
+    const float z = fmaf(y, 32.0f, magic);
+    const float f = fmaf(z - magic, -0.03125f, y) + yl;
+    // 2^f - 1 = f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6 + (f ln2)^4 / 24, the next term below 2^-39
+    const float g = f * fmaf(f, fmaf(f, fmaf(f, 0x1.3b2ab6p-7f, 0x1.c6b08ep-5f), 0x1.ebfbep-3f), 0x1.62e43p-1f);
+    const int j = __float_as_int(z) & 31;
+    const float Th = table[j], Tl = table[32 + j];
+    // 2^k by its bits: z's integer part from bit 5 on
+    const float s = __int_as_float(((__float_as_int(z) & ~31) << 18) + 0x3f800000);
+    return y > -100.0f ? FF{Th * s, fmaf(Th, g, Tl) * s} : FF{0.0f, 0.0f};
 }
 
 // max(R - S q, 0)
@@ -131,6 +126,13 @@ __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The largest of the warp; NaN if one is.
+__device__ __forceinline__ float warp_max_nan(float a)
+{
+    float y;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(a));
     return y;
 }
 // The larger; NaN if one is.
@@ -192,8 +194,29 @@ __device__ __forceinline__ void load_at(const T *row, int at, int n, float x[E])
     }
 }
 
-struct VerPart {  // a CTA's share of a row's statistics
-    float m, s;
+// The sum of a vector's numbers: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
+template <int E>
+__device__ __forceinline__ FF vec_sum(const FF R[E])
+{
+    FF s{0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float h = (R[i].h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
+        s.h += h, s.l += (R[i].h - h) + R[i].l;
+    }
+    return s;
+}
+
+__device__ __forceinline__ FF ff_warp_sum(FF a)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) a = ff_add(a, FF{__shfl_xor_sync(0xffffffffu, a.h, d), __shfl_xor_sync(0xffffffffu, a.l, d)});
+    return a;
+}
+
+struct VerPart {  // a share of a row: its largest logit, the first place of it, the sum of the weights relative to it
+    float m;
+    FF s;
     int idx;
 };
 
@@ -209,19 +232,22 @@ struct VerShared {
     float child_l[2][kMaxTree], child_q[2][kMaxTree];
     // the CTAs' shares of a row's maximum and sum, and of a pass's sum
     VerPart part[2][kVerCtas];
-    double total[2][kVerCtas];
+    FF total[2][kVerCtas];
     // within the CTA
     VerPart warp_part[kVerWarps];
     FF warp_total[kVerWarps];
     FF S[kMaxTree];  // sum of R before rejection j
     int excluded[kMaxTree], nex, rejected;
-    float2 table[128];
+    float out_w[kMaxTree];  // weights of the excluded
+    float table[64];
     int path[kMaxTree];
+    float part_sum;   // the row's sum by the fast pass
     float m;          // the row's maximum ...
     int best;         // ... and its place, -1 for a row without a distribution
     int code, node, current;
-    double sum, base;
-    int sel;
+    FF sum, base, target;
+    FF tile_sum[kVerWarps], tile_base;
+    int sel, sure, again, tile, over;
 };
 
 // One row of logits and its share of this warp.
@@ -247,16 +273,18 @@ __device__ __forceinline__ void prefetch_row(const T *next, const VerRow<L> &r)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(next + e));
 }
 
-__device__ __forceinline__ VerPart join(VerPart a, float c)  // over the warp
+// A share's sum relative to a larger maximum.
+__device__ __forceinline__ FF rescaled(const VerPart &a, float top, const VerShared &sh)
 {
-    float top = a.m;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (!(a.m > -CUDART_INF_F)) return FF{a.m == a.m ? 0.0f : a.m, 0.0f};
+    return ff_norm(ff_mul(a.s, weight(a.m, top, sh.c, sh.table)));
+}
+
+__device__ __forceinline__ VerPart join(const VerPart &a, const VerShared &sh)  // over the warp
+{
+    const float top = warp_max_nan(a.m);
     const int first = (int)__reduce_min_sync(0xffffffffu, (unsigned)(a.m == top ? a.idx : 0x7fffffff));
-    float s = a.m > -CUDART_INF_F ? a.s * ex2((a.m - top) * c) : a.m == a.m ? 0.0f : a.m;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    return VerPart{top, s, first};
+    return VerPart{top, ff_norm(ff_warp_sum(rescaled(a, top, sh))), first};
 }
 
 // The lane's share of a row's maximum and its place (greedy) or sum.
@@ -308,7 +336,7 @@ __device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, flo
             s = t;
         }
     }
-    return VerPart{m, s + sl, best};
+    return VerPart{m, ff_norm(FF{s, sl}), best};
 }
 
 // R of the E elements from vector v on: after `rejected` rejections (draft), or without the excluded tokens (no draft).
@@ -333,26 +361,6 @@ __device__ __forceinline__ void residuals(const VerShared &sh, const VerRow<L> &
     }
 }
 
-// The sum of a vector's numbers: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
-template <int E>
-__device__ __forceinline__ FF vec_sum(const FF R[E])
-{
-    FF s{0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float h = (R[i].h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
-        s.h += h, s.l += (R[i].h - h) + R[i].l;
-    }
-    return s;
-}
-
-__device__ __forceinline__ FF ff_warp_sum(FF a)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) a = ff_add(a, FF{__shfl_xor_sync(0xffffffffu, a.h, d), __shfl_xor_sync(0xffffffffu, a.l, d)});
-    return a;
-}
-
 // Sum of R over the row, by all threads of the cluster: sh.sum, the CTAs' shares in sh.total[turn], the warps' in sh.warp_total.
 template <typename L, typename Q, bool DRAFT>
 __device__ __forceinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, const VerRow<L> &r, const Q *qrow, int vocab, int turn)
@@ -369,105 +377,149 @@ __device__ __forceinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, c
         residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, rejected, nex, R);
         acc = ff_add(acc, vec_sum<E>(R));
     }
-    acc = ff_warp_sum(acc);
+    acc = ff_norm(ff_warp_sum(acc));
     if (lane == 0) sh.warp_total[warp] = acc;
     __syncthreads();
     if (warp == 0) {
-        double t = lane < kVerWarps ? ff_double(sh.warp_total[lane]) : 0.0;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+        const FF t = ff_norm(ff_warp_sum(sh.warp_total[lane]));
         if (lane < ctas) cl.map_shared_rank(&sh, lane)->total[turn][rank] = t;
     }
     cl.sync();
-    if (threadIdx.x == 0) {
-        double t = 0.0;
-        for (int i = 0; i < ctas; ++i) t += sh.total[turn][i];
-        sh.sum = t;
+    if (warp == 0) {
+        const FF t = ff_norm(ff_warp_sum(lane < ctas ? sh.total[turn][lane] : FF{0.0f, 0.0f}));
+        if (lane == 0) sh.sum = t;
     }
     __syncthreads();
 }
 
-// The token that the draw falls on: the CTA, then its warp, then the element, by running sums.
-template <typename L, typename Q, bool DRAFT>
-__device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const VerRow<L> &r, const Q *qrow, int vocab, int turn,
+// Inclusive running sums over the warp.
+__device__ __forceinline__ FF ff_warp_scan(FF a)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const FF o{__shfl_up_sync(0xffffffffu, a.h, d), __shfl_up_sync(0xffffffffu, a.l, d)};
+        if ((int)threadIdx.x % 32 >= d) a = ff_norm(ff_add(a, o));
+    }
+    return a;
+}
+
+// The first lane whose running sum of `mine` from `base` on passes target, or the last with any; *before: the sum up to
+// it; *end: the sum of all; false where none passes.
+__device__ __forceinline__ bool pick(FF mine, FF base, FF target, int *at, FF *before, FF *end)
+{
+    const int lane = threadIdx.x % 32;
+    const FF upto = ff_norm(ff_add(base, ff_warp_scan(mine)));
+    const unsigned some = __ballot_sync(0xffffffffu, mine.h > 0.0f), over = __ballot_sync(0xffffffffu, mine.h > 0.0f && ff_less(target, upto));
+    const int i = over ? __ffs((int)over) - 1 : some ? 31 - __clz((int)some) : -1;
+    FF b{__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+    if (lane == 0) b = base;
+    *before = FF{__shfl_sync(0xffffffffu, b.h, i & 31), __shfl_sync(0xffffffffu, b.l, i & 31)};
+    *end = FF{__shfl_sync(0xffffffffu, upto.h, 31), __shfl_sync(0xffffffffu, upto.l, 31)};
+    *at = i;
+    return over != 0;
+}
+
+// What the fast pass has of a share of the row, without the excluded tokens in its vectors [v0, v1).
+template <typename L>
+__device__ __forceinline__ FF fast_share(const VerShared &sh, const VerPart &p, const VerRow<L> &r, int v0, int v1)
+{
+    FF s = rescaled(p, sh.m, sh);
+    for (int j = 0; j < sh.nex; ++j)
+        if (sh.excluded[j] >= r.vecs.first(v0) && sh.excluded[j] < r.vecs.first(v1)) s = ff_norm(ff_add(s, FF{-sh.out_w[j], 0.0f}));
+    return s.h > 0.0f ? s : FF{0.0f, 0.0f};
+}
+
+// The token that the draw falls on: the CTA, its warp, of that warp's elements the tile (all warps of the CTA sum one
+// each), then the element, by running sums.  FAST: CTA and warp by the sums of the fast pass, which are `tol` off at most;
+// sh.sure tells (in the CTA that has the token) whether that decides it.  Else by those of sum_pass.
+template <typename L, typename Q, bool DRAFT, bool FAST>
+__device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const VerRow<L> &r, const Q *qrow, int vocab, int turn, float tol,
                                        int32_t *next)
 {
     constexpr int E = RowVecs<L>::E;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const double target = (double)sh.draw[0] * sh.sum;
+    const int per = (r.vecs.nv + ctas * kVerWarps - 1) / (ctas * kVerWarps);
     if (warp == 0) {
-        double before = 0.0, base = 0.0;
-        int sel = -1, last = 0;
-        for (int i = 0; i < ctas; ++i) {
-            const double t = sh.total[turn][i];
-            if (t > 0.0) {
-                last = i;
-                if (sel < 0) base = before;
-                if (sel < 0 && before + t > target) sel = i;
-            }
-            before += t;
+        FF mine{0.0f, 0.0f}, base, end, sum = sh.sum;
+        if (lane < ctas) mine = FAST ? fast_share(sh, sh.part[turn][lane], r, lane * kVerWarps * per, (lane + 1) * kVerWarps * per) : sh.total[turn][lane];
+        if (FAST) sum = ff_norm(ff_warp_sum(mine));
+        const FF target = ff_mul(sum, sh.draw[0]);
+        int cta, w = -1;
+        pick(mine, FF{0.0f, 0.0f}, target, &cta, &base, &end);
+        if (max(cta, 0) == rank) {
+            const int g = rank * kVerWarps + lane;
+            pick(FAST ? fast_share(sh, sh.warp_part[lane], r, g * per, (g + 1) * per) : sh.warp_total[lane], base, target, &w, &base, &end);
+            w = max(w, 0);
         }
-        int w = -1;
-        if ((sel < 0 ? last : sel) == rank) {
-            const double mine = lane < kVerWarps ? ff_double(sh.warp_total[lane]) : 0.0;
-            double upto = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double o = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += o;
-            }
-            const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0);
-            const unsigned over = __ballot_sync(0xffffffffu, mine > 0.0 && base + upto > target);
-            w = over ? __ffs((int)over) - 1 : 31 - __clz((int)some);
-            if (lane == w) sh.base = base + (upto - mine);
-        }
-        if (lane == 0) sh.sel = w;
+        if (lane == 0) sh.sel = w, sh.base = base, sh.target = target, sh.sure = 0;
     }
     __syncthreads();
-    if (warp != sh.sel) return;
-    double base = sh.base;
-    int last = 0;
-    for (int v0 = r.v0; v0 < r.v1; v0 += 32) {
-        FF R[E];
-        if (v0 + lane < r.v1) {
-            residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v0 + lane, sh.rejected, sh.nex, R);
+    if (sh.sel < 0) return;
+    const FF target = sh.target;
+    const int v0 = min((rank * kVerWarps + sh.sel) * per, r.vecs.nv), v1 = min(v0 + per, r.vecs.nv);
+    FF R[E];
+    int tile = -1;
+    for (int t0 = 0; v0 + 32 * t0 < v1; t0 += kVerWarps) {
+        const int v = v0 + 32 * (t0 + warp) + lane;
+        if (v < v1) {
+            residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, sh.rejected, sh.nex, R);
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) R[i] = FF{0.0f, 0.0f};
         }
-        const FF acc = vec_sum<E>(R);
-        const int e0 = r.vecs.first(v0 + lane);
-        int top = -1;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (R[i].h > 0.0f) top = e0 + i;
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (top >= 0) last = top;
-        const double tile = ff_double(ff_warp_sum(acc));
-        if (base + tile > target) {
-            double upto = ff_double(acc);
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double o = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += o;
-            }
-            double run = base + __shfl_up_sync(0xffffffffu, upto, 1);
-            if (lane == 0) run = base;
-            unsigned hit = 0x7fffffffu;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                run += ff_double(R[i]);
-                if (R[i].h > 0.0f && run > target) hit = min(hit, (unsigned)(e0 + i));
-            }
-            hit = __reduce_min_sync(0xffffffffu, hit);
-            if (hit != 0x7fffffffu) {
-                last = (int)hit;
-                break;
+        const FF s = ff_norm(ff_warp_sum(vec_sum<E>(R)));
+        if (lane == 0) sh.tile_sum[warp] = s;
+        __syncthreads();
+        if (warp == 0) {
+            FF before, end;
+            int at;
+            const bool over = pick(sh.tile_sum[lane], sh.base, target, &at, &before, &end);
+            __syncwarp();
+            if (lane == 0) {
+                sh.over = over;
+                if (at >= 0) sh.tile = t0 + at, sh.tile_base = before;
+                else if (t0 == 0) sh.tile = 0, sh.tile_base = before;
+                sh.base = end;
             }
         }
-        base += tile;
+        __syncthreads();
+        tile = sh.tile;
+        if (sh.over) break;
     }
-    if (lane == 0) *next = last;
+    if (warp != tile % kVerWarps) return;
+    const int v = v0 + 32 * tile + lane;
+    if (v < v1) {
+        residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, sh.rejected, sh.nex, R);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) R[i] = FF{0.0f, 0.0f};
+    }
+    const int e0 = r.vecs.first(v);
+    const FF mine = ff_norm(vec_sum<E>(R));
+    FF run;
+    int top = -1;
+    const FF upto = ff_norm(ff_add(sh.tile_base, ff_warp_scan(mine)));
+    run = FF{__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+    if (lane == 0) run = sh.tile_base;
+    unsigned hit = 0x7fffffffu;
+    bool clear = false;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const FF was = run;
+        run = ff_norm(ff_add(run, R[i]));
+        if (R[i].h > 0.0f) top = e0 + i;
+        if (hit == 0x7fffffffu && R[i].h > 0.0f && ff_less(target, run)) {
+            hit = (unsigned)(e0 + i);
+            clear = target.h - was.h > tol && run.h - target.h > tol;
+        }
+    }
+    const unsigned first = __reduce_min_sync(0xffffffffu, hit);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool sure = __any_sync(0xffffffffu, first != 0x7fffffffu && hit == first && clear);
+    if (lane == 0) {
+        sh.sure = sure;
+        if (!FAST || sure) *next = first != 0x7fffffffu ? (int)first : max(top, 0);
+    }
 }
 
 template <typename L, typename Q, bool DRAFT>
@@ -479,7 +531,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
     const int b = (int)blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t row0 = (int64_t)b * a.n;
-    if (tid < 128) sh.table[tid] = kExp2Table[tid];
+    if (tid < 64) sh.table[tid] = tid < 32 ? kExp2High[tid] : kExp2Low[tid - 32];
     cl.sync();  // from here on peers write into this CTA's memory
     pdl_wait();
     pdl_trigger();
@@ -513,6 +565,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
     }
 
     const bool greedy = sh.greedy;
+    const float tol = kTolSum + kTolBit * (float)(32 - __clz(a.vocab));
     int node = 0, level = 0, turn = 0;
     for (;;) {
         const VerRow<L> row(static_cast<const L *>(a.logits) + (row0 + node) * a.logits_stride, a.vocab, rank, ctas);
@@ -538,11 +591,11 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
             const int kid = lo ? __ffs((int)lo) - 1 : hi ? 31 + __ffs((int)hi) : 0;
             if (kid) prefetch_row(static_cast<const L *>(a.logits) + (row0 + kid) * a.logits_stride, row);
         }
-        const VerPart mine = join(row_part(row, greedy, sh.c.h), sh.c.h);
+        const VerPart mine = join(row_part(row, greedy, sh.c.h), sh);
         if (lane == 0) sh.warp_part[warp] = mine;
         __syncthreads();
         if (warp == 0) {
-            const VerPart p = join(lane < kVerWarps ? sh.warp_part[lane] : VerPart{-CUDART_INF_F, 0.0f, 0x7fffffff}, sh.c.h);
+            const VerPart p = join(lane < kVerWarps ? sh.warp_part[lane] : VerPart{-CUDART_INF_F, {0.0f, 0.0f}, 0x7fffffff}, sh);
             if (lane < ctas) cl.map_shared_rank(&sh, lane)->part[turn][rank] = p;
         }
         cl.sync();
@@ -555,9 +608,9 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
         int k = 0, nex = 0;
         FF R[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // of nodes lane and lane + 32
         if (warp == 0) {
-            const VerPart p = join(lane < ctas ? sh.part[turn][lane] : VerPart{-CUDART_INF_F, 0.0f, 0x7fffffff}, sh.c.h);
+            const VerPart p = join(lane < ctas ? sh.part[turn][lane] : VerPart{-CUDART_INF_F, {0.0f, 0.0f}, 0x7fffffff}, sh);
             const bool valid = sh.valid && p.m > -CUDART_INF_F && p.m < CUDART_INF_F;
-            S = S0 = p.s;
+            S = S0 = ff_double(p.s);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int i = lane + 32 * h;
@@ -565,10 +618,12 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                 kids |= (uint64_t)__ballot_sync(0xffffffffu, kid) << (32 * h);
                 if (kid && !greedy) R[h] = weight(sh.child_l[side][i], p.m, sh.c, sh.table);
             }
+            if (lane == 0) sh.part_sum = p.s.h;
             if (lane == 0) sh.m = p.m, sh.best = valid ? p.idx : -1, sh.nex = 0, sh.rejected = 0;
             if (lane == 0 && valid && !greedy) sh.best = 0;
             __syncwarp();
         }
+        const int fast_turn = turn;
         turn ^= 1;
         for (;;) {
             if (warp == 0) {
@@ -586,7 +641,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                     const FF Ri{__shfl_sync(0xffffffffu, i < 32 ? R[0].h : R[1].h, i % 32), __shfl_sync(0xffffffffu, i < 32 ? R[0].l : R[1].l, i % 32)};
                     const double have = ff_double(Ri), want = (double)sh.draw[i] * (double)sh.child_q[side][i] * S;
                     const bool yes = want < have;
-                    if (!exact && ((have > 0.0 && fabs(want - have) <= kTol * S0) || (DRAFT && !yes))) {
+                    if (!exact && ((have > 0.0 && fabs(want - have) <= tol * S0) || (DRAFT && !yes))) {
                         code = kPass;
                         break;
                     }
@@ -608,7 +663,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                     const int token = sh.token[i];
                     if (have > 0.0) {
                         S -= have;
-                        if (lane == 0) sh.excluded[nex] = token;
+                        if (lane == 0) sh.excluded[nex] = token, sh.out_w[nex] = (float)have;
                         ++nex;
                         exact = false;  // the last pass's shares no longer hold
                     }
@@ -623,7 +678,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
             if (DRAFT && sh.rejected == 0) prefetch_row(qrow, row);  // wanted if the child is rejected, as it nearly is
             sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
             turn ^= 1;
-            if (warp == 0) S = sh.sum, exact = true;
+            if (warp == 0) S = ff_double(sh.sum), exact = true;
         }
         if (sh.code == kAccept) {
             node = sh.node;
@@ -634,18 +689,31 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
         if (greedy || sh.best < 0) {
             if (rank == 0 && tid == 0) a.next[b] = sh.best;
         } else {
-            if (!sh.current) {
-                sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
-                turn ^= 1;
-            }
-            if (!(sh.sum > 0.0)) {  // nothing is left: from the row itself
+            bool done = false;
+            if (!sh.current && sh.rejected == 0) {
+                // by the fast sums, where no border is near; the CTA that has the token tells the others
+                if (tid == 0) sh.again = 0;
+                cl.sync();
+                choose<L, Q, DRAFT, true>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, 2.0f * tol * sh.part_sum, a.next + b);
                 __syncthreads();
-                if (tid == 0) sh.rejected = 0, sh.nex = 0;
-                __syncthreads();
-                sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
-                turn ^= 1;
+                if (sh.sel >= 0 && !sh.sure && tid < ctas) cl.map_shared_rank(&sh, tid)->again = 1;
+                cl.sync();
+                done = !sh.again;
             }
-            choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, turn ^ 1, a.next + b);
+            if (!done) {
+                if (!sh.current) {
+                    sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
+                    turn ^= 1;
+                }
+                if (!(sh.sum.h > 0.0f)) {  // nothing is left: from the row itself
+                    __syncthreads();
+                    if (tid == 0) sh.rejected = 0, sh.nex = 0;
+                    __syncthreads();
+                    sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
+                    turn ^= 1;
+                }
+                choose<L, Q, DRAFT, false>(sh, rank, ctas, row, qrow, a.vocab, turn ^ 1, 0.0f, a.next + b);
+            }
         }
         break;
     }
@@ -687,7 +755,9 @@ static cudaError_t verify_draft(const VerifyArgs &a, int ddt, int ctas, cudaStre
 wl_status launch_verify(const VerifyArgs &a, int ldt, int ddt, const DeviceInfo *di, cudaStream_t st)
 {
     // A sequence's CTAs: as many as fill the GPU, at most one for 8192 tokens of the vocabulary.
-    int ctas = kVerCtas;
+    // (16 only for up to 4 sequences: clusters of 16 that fit the GPU at once are fewer than its SMs hold, and 8 of them
+    // took two waves.)
+    int ctas = a.batch <= 4 ? kVerCtas : 8;
     while (ctas > 1 && ((int64_t)a.batch * ctas > di->sm_count || (int64_t)a.vocab < 8192 * (ctas / 2))) ctas /= 2;
     const cudaError_t e = ldt == WL_OUT_F32 ? verify_draft<float>(a, ddt, ctas, st) : verify_draft<bf16>(a, ddt, ctas, st);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_verify launch");
