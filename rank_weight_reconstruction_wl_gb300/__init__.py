@@ -851,6 +851,8 @@ _F8 = torch.float8_e4m3fn
 
 def _rows_of(t, name: str, dtype, rows: int, width: int, index) -> int:
     """Row stride in elements of a matrix [rows, width] on device `index` whose rows are contiguous."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.shape == (rows, width) and t.is_contiguous():
+        return width
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -973,10 +975,10 @@ def wl_verify(logits, tokens, uniforms, mask=None, count=None, draft=None, tempe
     else:
         temp = float(temperature)
     if outs is None:
-        small = _empty((B * (n + 2),), torch.int32, tokens.device, stream)  # one allocation for the three
-        path, accepted, nxt = small[:B * n].view(B, n), small[B * n:B * n + B], small[B * n + B:]
-        pp = small.data_ptr()
-        ap, np_ = pp + 4 * B * n, pp + 4 * B * (n + 1)
+        dev = tokens.device
+        path, accepted, nxt = (_empty((B, n), torch.int32, dev, stream), _empty((B,), torch.int32, dev, stream),
+                               _empty((B,), torch.int32, dev, stream))
+        pp, ap, np_ = path.data_ptr(), accepted.data_ptr(), nxt.data_ptr()
     else:
         path, accepted, nxt = outs
         pp = _checked(path, "path", torch.int32, (B, n), index)

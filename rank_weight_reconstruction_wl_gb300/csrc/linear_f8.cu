@@ -1128,11 +1128,14 @@ wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
     const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 128, 0, 0, di->status};
-    // Tiles of 256 rows by 256 tokens where they fill half of the pairs.
-    if (T > 128 && (out + 255) / 256 * ((T + 255) / 256) * 4 >= di->sm_count) return f8_run_pair(a, x, W, in, ydt, di, st);
-    if (T > 64 && T <= 128) {
+    if (T > 64) {
+        // The least of what the kernels are thought to take: pairs 0.46 us a block and 2.5 us a tile (measured), the others above.
         F8Few p;
-        if (f8_few_plan(T, out, a.nkb, di->sm_count, &p) <= f8_plan(a, 64, di->sm_count).time) return f8_run_few(a, p, x, W, in, ydt, di, st);
+        const int64_t pairs = (out + 255) / 256 * ((T + 255) / 256), at_once = di->sm_count / 2;
+        const double pair = (double)((pairs + at_once - 1) / at_once) * (a.nkb * 460.0 + 2500.0) + 1000.0;
+        const double few = T <= 128 ? f8_few_plan(T, out, a.nkb, di->sm_count, &p) : 1e30, split = f8_plan(a, 64, di->sm_count).time;
+        if (pair <= few && pair <= split) return f8_run_pair(a, x, W, in, ydt, di, st);
+        if (few <= split) return f8_run_few(a, p, x, W, in, ydt, di, st);
     }
     if (T <= 16) return f8_run<16>(a, x, W, in, ydt, di, st);
     if (T <= 32) return f8_run<32>(a, x, W, in, ydt, di, st);

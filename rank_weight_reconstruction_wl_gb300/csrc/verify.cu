@@ -25,7 +25,7 @@ namespace cg = cooperative_groups;
 
 namespace wl {
 
-constexpr int kVerThreads = 1024;
+constexpr int kVerThreads = 512;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerCtas = 16;  // CTAs of a cluster at most
 constexpr float kTolSum = 6e-7f, kTolBit = 1.3e-7f;
@@ -158,20 +158,34 @@ struct RowVecs {
         nv = (mis + n + E - 1) / E;
     }
     __device__ __forceinline__ int first(int v) const { return v * E - mis; }
-    // Elements of vector v; `fill` outside the row.
-    __device__ __forceinline__ void load(int v, float fill, float x[E]) const
+    // Vector v as loaded; -infinity outside the row (v < v1, the end of a share).
+    __device__ __forceinline__ uint4 raw(int v, int v1) const
     {
         const int e0 = first(v);
-        if (v < nv && e0 >= 0 && e0 + E <= n) {
-            const uint4 u = ld_stream16(row + e0);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if (v < v1 && e0 >= 0 && e0 + E <= n) return ld_stream16(row + e0);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+        if (v < v1) {
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                x[i] = sizeof(T) == 4 ? __uint_as_float(w[i % 4]) : (i & 1) ? bf_hi(w[i / 2 % 4]) : bf_lo(w[i / 2 % 4]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = e0 + i >= 0 && e0 + i < n ? to_f(row[e0 + i]) : fill;
+                if (e0 + i >= 0 && e0 + i < n) {
+                    if constexpr (sizeof(T) == 4) {
+                        w[i % 4] = __float_as_uint(row[e0 + i]);
+                    } else {
+                        const uint32_t u = __float_as_uint(to_f(row[e0 + i])) >> 16;
+                        w[i / 2 % 4] = i & 1 ? (w[i / 2 % 4] & 0xffffu) | u << 16 : (w[i / 2 % 4] & 0xffff0000u) | u;
+                    }
+                }
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void unpack(const uint4 &u, float x[E])
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            x[i] = sizeof(T) == 4 ? __uint_as_float(w[i % 4]) : (i & 1) ? bf_hi(w[i / 2 % 4]) : bf_lo(w[i / 2 % 4]);
     }
 };
 
@@ -234,8 +248,8 @@ struct VerShared {
     VerPart part[2][kVerCtas];
     FF total[2][kVerCtas];
     // within the CTA
-    VerPart warp_part[kVerWarps];
-    FF warp_total[kVerWarps];
+    VerPart warp_part[32];  // empty past kVerWarps, as the two below
+    FF warp_total[32];
     FF S[kMaxTree];  // sum of R before rejection j
     int excluded[kMaxTree], nex, rejected;
     float out_w[kMaxTree];  // weights of the excluded
@@ -246,7 +260,7 @@ struct VerShared {
     int best;         // ... and its place, -1 for a row without a distribution
     int code, node, current;
     FF sum, base, target;
-    FF tile_sum[kVerWarps], tile_base;
+    FF tile_sum[32], tile_base;
     int sel, sure, again, tile, over;
 };
 
@@ -291,46 +305,50 @@ __device__ __forceinline__ VerPart join(const VerPart &a, const VerShared &sh)  
 template <typename L>
 __device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, float c)
 {
-    constexpr int E = RowVecs<L>::E, U = 4;
+    constexpr int E = RowVecs<L>::E, U = 8;
     float m = -CUDART_INF_F, s = 0.0f, sl = 0.0f;
     int best = 0x7fffffff;
-    for (int v = r.v0 + (int)threadIdx.x % 32; v < r.v1; v += 32 * U) {
-        float x[U][E];
+    uint4 ahead[U];  // the next vectors, under way while these are summed
+    const int lane = threadIdx.x % 32;
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (v + 32 * j < r.v1) {
-                r.vecs.load(v + 32 * j, -CUDART_INF_F, x[j]);
-            } else {
+    for (int j = 0; j < U; ++j) ahead[j] = r.vecs.raw(r.v0 + lane + 32 * j, r.v1);
+    for (int v = r.v0 + lane; v < r.v1; v += 32 * U) {
+        uint4 now[U];
+        float x[E], top = -CUDART_INF_F;
 #pragma unroll
-                for (int i = 0; i < E; ++i) x[j][i] = -CUDART_INF_F;
-            }
-        }
+        for (int j = 0; j < U; ++j) now[j] = ahead[j];
+#pragma unroll
+        for (int j = 0; j < U; ++j) ahead[j] = r.vecs.raw(v + 32 * (U + j), r.v1);
         if (greedy) {
 #pragma unroll
-            for (int j = 0; j < U; ++j)
+            for (int j = 0; j < U; ++j) {
+                RowVecs<L>::unpack(now[j], x);
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    if (x[j][i] > m) best = r.vecs.first(v + 32 * j) + i;
-                    m = max_nan(m, x[j][i]);
+                    if (x[i] > m) best = r.vecs.first(v + 32 * j) + i;
+                    m = max_nan(m, x[i]);
                 }
+            }
             continue;
         }
-        float top = x[0][0];
 #pragma unroll
-        for (int j = 0; j < U; ++j)
+        for (int j = 0; j < U; ++j) {
+            RowVecs<L>::unpack(now[j], x);
 #pragma unroll
-            for (int i = 0; i < E; ++i) top = max_nan(top, x[j][i]);
+            for (int i = 0; i < E; ++i) top = max_nan(top, x[i]);
+        }
         if (!(top <= m)) {
-            const float now = max_nan(m, top);
-            const float f = m > -CUDART_INF_F ? ex2((m - now) * c) : 0.0f;
-            s *= f, sl *= f, m = now;
+            const float next = max_nan(m, top);
+            const float f = m > -CUDART_INF_F ? ex2((m - next) * c) : 0.0f;
+            s *= f, sl *= f, m = next;
         }
         if (m == -CUDART_INF_F) continue;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
+            RowVecs<L>::unpack(now[j], x);
             float w = 0.0f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) w += ex2((x[j][i] - m) * c);
+            for (int i = 0; i < E; ++i) w += ex2((x[i] - m) * c);
             const float t = s + w, z = t - s;
             sl += (s - (t - z)) + (w - z);
             s = t;
@@ -341,13 +359,13 @@ __device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, flo
 
 // R of the E elements from vector v on: after `rejected` rejections (draft), or without the excluded tokens (no draft).
 template <typename L, typename Q, bool DRAFT>
-__device__ __forceinline__ void residuals(const VerShared &sh, const VerRow<L> &r, const Q *qrow, int vocab, int v, int rejected, int nex,
-                                          FF R[RowVecs<L>::E])
+__device__ __forceinline__ void residuals(const VerShared &sh, const VerRow<L> &r, const uint4 &raw, const Q *qrow, int vocab, int v,
+                                          int rejected, int nex, FF R[RowVecs<L>::E])
 {
     constexpr int E = RowVecs<L>::E;
     float x[E], q[E];
     const int e0 = r.vecs.first(v);
-    r.vecs.load(v, -CUDART_INF_F, x);
+    RowVecs<L>::unpack(raw, x);
     if (DRAFT && rejected > 0) load_at<Q, E>(qrow, e0, vocab, q);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -372,9 +390,12 @@ __device__ __forceinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, c
     for (int j = 0; j < sh.nex; ++j)
         if (sh.excluded[j] >= r.vecs.first(r.v0) && sh.excluded[j] < r.vecs.first(r.v1)) nex = sh.nex;
     FF acc{0.0f, 0.0f};
+    uint4 ahead[2] = {r.vecs.raw(r.v0 + lane, r.v1), r.vecs.raw(r.v0 + lane + 32, r.v1)};
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
         FF R[E];
-        residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, rejected, nex, R);
+        const uint4 raw = ahead[0];
+        ahead[0] = ahead[1], ahead[1] = r.vecs.raw(v + 64, r.v1);
+        residuals<L, Q, DRAFT>(sh, r, raw, qrow, vocab, v, rejected, nex, R);
         acc = ff_add(acc, vec_sum<E>(R));
     }
     acc = ff_norm(ff_warp_sum(acc));
@@ -461,12 +482,7 @@ __device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const 
     int tile = -1;
     for (int t0 = 0; v0 + 32 * t0 < v1; t0 += kVerWarps) {
         const int v = v0 + 32 * (t0 + warp) + lane;
-        if (v < v1) {
-            residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, sh.rejected, sh.nex, R);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) R[i] = FF{0.0f, 0.0f};
-        }
+        residuals<L, Q, DRAFT>(sh, r, r.vecs.raw(v, v1), qrow, vocab, v, sh.rejected, sh.nex, R);  // past v1: nothing
         const FF s = ff_norm(ff_warp_sum(vec_sum<E>(R)));
         if (lane == 0) sh.tile_sum[warp] = s;
         __syncthreads();
@@ -488,12 +504,7 @@ __device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const 
     }
     if (warp != tile % kVerWarps) return;
     const int v = v0 + 32 * tile + lane;
-    if (v < v1) {
-        residuals<L, Q, DRAFT>(sh, r, qrow, vocab, v, sh.rejected, sh.nex, R);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) R[i] = FF{0.0f, 0.0f};
-    }
+    residuals<L, Q, DRAFT>(sh, r, r.vecs.raw(v, v1), qrow, vocab, v, sh.rejected, sh.nex, R);
     const int e0 = r.vecs.first(v);
     const FF mine = ff_norm(vec_sum<E>(R));
     FF run;
@@ -531,6 +542,10 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
     const int b = (int)blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t row0 = (int64_t)b * a.n;
+    if (tid < 32) {
+        sh.warp_part[tid] = VerPart{-CUDART_INF_F, {0.0f, 0.0f}, 0x7fffffff};
+        sh.warp_total[tid] = sh.tile_sum[tid] = FF{0.0f, 0.0f};
+    }
     if (tid < 64) sh.table[tid] = tid < 32 ? kExp2High[tid] : kExp2Low[tid - 32];
     cl.sync();  // from here on peers write into this CTA's memory
     pdl_wait();
