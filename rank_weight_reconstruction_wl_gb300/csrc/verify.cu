@@ -208,19 +208,6 @@ __device__ __forceinline__ void load_at(const T *row, int at, int n, float x[E])
     }
 }
 
-// The sum of a vector's numbers: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
-template <int E>
-__device__ __forceinline__ FF vec_sum(const FF R[E])
-{
-    FF s{0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float h = (R[i].h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
-        s.h += h, s.l += (R[i].h - h) + R[i].l;
-    }
-    return s;
-}
-
 __device__ __forceinline__ FF ff_warp_sum(FF a)
 {
 #pragma unroll
@@ -357,33 +344,55 @@ __device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, flo
     return VerPart{m, ff_norm(FF{s, sl}), best};
 }
 
-// R of the E elements from vector v on: after `rejected` rejections (draft), or without the excluded tokens (no draft).
-template <typename L, typename Q, bool DRAFT>
-__device__ __forceinline__ void residuals(const VerShared &sh, const VerRow<L> &r, const uint4 &raw, const Q *qrow, int vocab, int v,
-                                          int rejected, int nex, FF R[RowVecs<L>::E])
+// f(i, R_i) for the elements of a vector as loaded, from element e0 on: R after `rejected` rejections (draft), or without
+// the excluded tokens (no draft).  A word at a time, not unrolled: this code runs a few times in a launch, and unrolled
+// it took longer to be fetched than to run (5 us of 14 for a vocabulary of 1000).
+template <typename L, typename Q, bool DRAFT, typename F>
+__device__ __forceinline__ void each_R(const VerShared &sh, uint4 w, const Q *qrow, int vocab, int e0, int rejected, int nex, F f)
 {
-    constexpr int E = RowVecs<L>::E;
-    float x[E], q[E];
-    const int e0 = r.vecs.first(v);
-    RowVecs<L>::unpack(raw, x);
+    constexpr int E = RowVecs<L>::E, P = E / 4;  // elements of a word
+    float q[E];
     if (DRAFT && rejected > 0) load_at<Q, E>(qrow, e0, vocab, q);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        R[i] = weight(x[i], sh.m, sh.c, sh.table);
+        for (int h = 0; h < P; ++h) {
+            const int i = e0 + k * P + h;
+            FF R = weight(P == 1 ? __uint_as_float(w.x) : h ? bf_hi(w.x) : bf_lo(w.x), sh.m, sh.c, sh.table);
+            if (DRAFT) {
+#pragma unroll 1
+                for (int j = 0; j < rejected; ++j) R = residual(R, q[h], sh.S[j]);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < nex; ++j)
+                    if (sh.excluded[j] == i) R = FF{0.0f, 0.0f};
+            }
+            f(i, R);
+        }
+        w.x = w.y, w.y = w.z, w.z = w.w;
         if (DRAFT) {
-            for (int j = 0; j < rejected; ++j) R[i] = residual(R[i], q[i], sh.S[j]);
-        } else {
-            for (int j = 0; j < nex; ++j)
-                if (sh.excluded[j] == e0 + i) R[i] = FF{0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i + P < E; ++i) q[i] = q[i + P];
         }
     }
 }
 
+// The sum of a vector's R: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
+template <typename L, typename Q, bool DRAFT>
+__device__ __forceinline__ FF vec_sum(const VerShared &sh, const uint4 &w, const Q *qrow, int vocab, int e0, int rejected, int nex)
+{
+    FF s{0.0f, 0.0f};
+    each_R<L, Q, DRAFT>(sh, w, qrow, vocab, e0, rejected, nex, [&](int, FF R) {
+        const float h = (R.h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
+        s.h += h, s.l += (R.h - h) + R.l;
+    });
+    return s;
+}
+
 // Sum of R over the row, by all threads of the cluster: sh.sum, the CTAs' shares in sh.total[turn], the warps' in sh.warp_total.
 template <typename L, typename Q, bool DRAFT>
-__device__ __forceinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, const VerRow<L> &r, const Q *qrow, int vocab, int turn)
+__device__ __noinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, const VerRow<L> &r, const Q *qrow, int vocab, int turn)
 {
-    constexpr int E = RowVecs<L>::E;
     const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks(), lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int rejected = sh.rejected;
     int nex = 0;  // excluded tokens, where any is among this warp's elements
@@ -392,11 +401,9 @@ __device__ __forceinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, c
     FF acc{0.0f, 0.0f};
     uint4 ahead[2] = {r.vecs.raw(r.v0 + lane, r.v1), r.vecs.raw(r.v0 + lane + 32, r.v1)};
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
-        FF R[E];
         const uint4 raw = ahead[0];
         ahead[0] = ahead[1], ahead[1] = r.vecs.raw(v + 64, r.v1);
-        residuals<L, Q, DRAFT>(sh, r, raw, qrow, vocab, v, rejected, nex, R);
-        acc = ff_add(acc, vec_sum<E>(R));
+        acc = ff_add(acc, vec_sum<L, Q, DRAFT>(sh, raw, qrow, vocab, r.vecs.first(v), rejected, nex));
     }
     acc = ff_norm(ff_warp_sum(acc));
     if (lane == 0) sh.warp_total[warp] = acc;
@@ -451,25 +458,24 @@ __device__ __forceinline__ FF fast_share(const VerShared &sh, const VerPart &p, 
 }
 
 // The token that the draw falls on: the CTA, its warp, of that warp's elements the tile (all warps of the CTA sum one
-// each), then the element, by running sums.  FAST: CTA and warp by the sums of the fast pass, which are `tol` off at most;
+// each), then the element, by running sums.  fast: CTA and warp by the sums of the fast pass, which are `tol` off at most;
 // sh.sure tells (in the CTA that has the token) whether that decides it.  Else by those of sum_pass.
-template <typename L, typename Q, bool DRAFT, bool FAST>
-__device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const VerRow<L> &r, const Q *qrow, int vocab, int turn, float tol,
-                                       int32_t *next)
+template <typename L, typename Q, bool DRAFT>
+__device__ __noinline__ void choose(VerShared &sh, int rank, int ctas, const VerRow<L> &r, const Q *qrow, int vocab, int turn, bool fast,
+                                    float tol, int32_t *next)
 {
-    constexpr int E = RowVecs<L>::E;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int per = (r.vecs.nv + ctas * kVerWarps - 1) / (ctas * kVerWarps);
     if (warp == 0) {
         FF mine{0.0f, 0.0f}, base, end, sum = sh.sum;
-        if (lane < ctas) mine = FAST ? fast_share(sh, sh.part[turn][lane], r, lane * kVerWarps * per, (lane + 1) * kVerWarps * per) : sh.total[turn][lane];
-        if (FAST) sum = ff_norm(ff_warp_sum(mine));
+        if (lane < ctas) mine = fast ? fast_share(sh, sh.part[turn][lane], r, lane * kVerWarps * per, (lane + 1) * kVerWarps * per) : sh.total[turn][lane];
+        if (fast) sum = ff_norm(ff_warp_sum(mine));
         const FF target = ff_mul(sum, sh.draw[0]);
         int cta, w = -1;
         pick(mine, FF{0.0f, 0.0f}, target, &cta, &base, &end);
         if (max(cta, 0) == rank) {
             const int g = rank * kVerWarps + lane;
-            pick(FAST ? fast_share(sh, sh.warp_part[lane], r, g * per, (g + 1) * per) : sh.warp_total[lane], base, target, &w, &base, &end);
+            pick(fast ? fast_share(sh, sh.warp_part[lane], r, g * per, (g + 1) * per) : sh.warp_total[lane], base, target, &w, &base, &end);
             w = max(w, 0);
         }
         if (lane == 0) sh.sel = w, sh.base = base, sh.target = target, sh.sure = 0;
@@ -478,12 +484,15 @@ __device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const 
     if (sh.sel < 0) return;
     const FF target = sh.target;
     const int v0 = min((rank * kVerWarps + sh.sel) * per, r.vecs.nv), v1 = min(v0 + per, r.vecs.nv);
-    FF R[E];
     int tile = -1;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    FF mine{0.0f, 0.0f};
+#pragma unroll 1
     for (int t0 = 0; v0 + 32 * t0 < v1; t0 += kVerWarps) {
         const int v = v0 + 32 * (t0 + warp) + lane;
-        residuals<L, Q, DRAFT>(sh, r, r.vecs.raw(v, v1), qrow, vocab, v, sh.rejected, sh.nex, R);  // past v1: nothing
-        const FF s = ff_norm(ff_warp_sum(vec_sum<E>(R)));
+        raw = r.vecs.raw(v, v1);
+        mine = vec_sum<L, Q, DRAFT>(sh, raw, qrow, vocab, r.vecs.first(v), sh.rejected, sh.nex);
+        const FF s = ff_norm(ff_warp_sum(mine));
         if (lane == 0) sh.tile_sum[warp] = s;
         __syncthreads();
         if (warp == 0) {
@@ -503,33 +512,32 @@ __device__ __forceinline__ void choose(VerShared &sh, int rank, int ctas, const 
         if (sh.over) break;
     }
     if (warp != tile % kVerWarps) return;
-    const int v = v0 + 32 * tile + lane;
-    residuals<L, Q, DRAFT>(sh, r, r.vecs.raw(v, v1), qrow, vocab, v, sh.rejected, sh.nex, R);
-    const int e0 = r.vecs.first(v);
-    const FF mine = ff_norm(vec_sum<E>(R));
-    FF run;
-    int top = -1;
-    const FF upto = ff_norm(ff_add(sh.tile_base, ff_warp_scan(mine)));
-    run = FF{__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+    const int v = v0 + 32 * tile + lane, e0 = r.vecs.first(v);
+    if (!sh.over) {  // the last tile with any, perhaps not of the last round
+        raw = r.vecs.raw(v, v1);
+        mine = vec_sum<L, Q, DRAFT>(sh, raw, qrow, vocab, e0, sh.rejected, sh.nex);
+    }
+    const FF upto = ff_norm(ff_add(sh.tile_base, ff_warp_scan(ff_norm(mine))));
+    FF run{__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
     if (lane == 0) run = sh.tile_base;
+    int top = -1;
     unsigned hit = 0x7fffffffu;
     bool clear = false;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
+    each_R<L, Q, DRAFT>(sh, raw, qrow, vocab, e0, sh.rejected, sh.nex, [&](int i, FF R) {
         const FF was = run;
-        run = ff_norm(ff_add(run, R[i]));
-        if (R[i].h > 0.0f) top = e0 + i;
-        if (hit == 0x7fffffffu && R[i].h > 0.0f && ff_less(target, run)) {
-            hit = (unsigned)(e0 + i);
+        run = ff_norm(ff_add(run, R));
+        if (R.h > 0.0f) top = i;
+        if (hit == 0x7fffffffu && R.h > 0.0f && ff_less(target, run)) {
+            hit = (unsigned)i;
             clear = target.h - was.h > tol && run.h - target.h > tol;
         }
-    }
+    });
     const unsigned first = __reduce_min_sync(0xffffffffu, hit);
     top = __reduce_max_sync(0xffffffffu, top);
     const bool sure = __any_sync(0xffffffffu, first != 0x7fffffffu && hit == first && clear);
     if (lane == 0) {
         sh.sure = sure;
-        if (!FAST || sure) *next = first != 0x7fffffffu ? (int)first : max(top, 0);
+        if (!fast || sure) *next = first != 0x7fffffffu ? (int)first : max(top, 0);
     }
 }
 
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                 // by the fast sums, where no border is near; the CTA that has the token tells the others
                 if (tid == 0) sh.again = 0;
                 cl.sync();
-                choose<L, Q, DRAFT, true>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, 2.0f * tol * sh.part_sum, a.next + b);
+                choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, true, 2.0f * tol * sh.part_sum, a.next + b);
                 __syncthreads();
                 if (sh.sel >= 0 && !sh.sure && tid < ctas) cl.map_shared_rank(&sh, tid)->again = 1;
                 cl.sync();
@@ -727,7 +735,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                     sum_pass<L, Q, DRAFT>(sh, cl, row, qrow, a.vocab, turn);
                     turn ^= 1;
                 }
-                choose<L, Q, DRAFT, false>(sh, rank, ctas, row, qrow, a.vocab, turn ^ 1, 0.0f, a.next + b);
+                choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, turn ^ 1, false, 0.0f, a.next + b);
             }
         }
         break;

@@ -13,9 +13,18 @@ Per layer and step (x: the fp32 residual stream, h: its normed bf16 form):
 A step takes the newest tokens of every sequence: one each (decoding), a
 drafted tree, or up to 64 of a prompt; ``prompt`` feeds longer ones in chunks.
 ``accept`` keeps a root-to-node path of the tree that a step put into the cache.
+With a head, ``logits`` are the step's and ``verify`` decides which drafted tokens
+hold, keeps them and draws the next:
+
+    h = dec.step(x, n, mask, depth)            x: embeddings of the drafted tree
+    path, accepted, token = dec.verify(dec.logits(h), tokens, uniforms, mask)
+
+With pool_pages the sequences share that many cache pages instead of owning
+max_len positions each: a step takes the pages that it needs, gives back what the
+last one's rejected drafts had, and ``release`` gives back ended sequences'.
 All work runs on the current stream.  Nothing synchronises but a step that might
-not fit: the host knows a bound of the lengths, and reads them where the bound
-does not tell.
+not fit, and a prompt with shared pages: the host knows a bound of the lengths,
+and reads them where the bound does not tell.
 """
 from __future__ import annotations
 
@@ -23,8 +32,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (CacheSeqs, KVCache, RopeTable, wl_linear, wl_mlp_geglu_fused, wl_norm_residual, wl_qkv_fused, wl_rope_append,
-               wl_tree_attention)
+from . import (CacheSeqs, F8Weight, KVCache, PagePool, RopeTable, wl_linear, wl_linear_f8, wl_mlp_geglu_fused, wl_norm_residual,
+               wl_page_plan, wl_qkv_fused, wl_quant_f8, wl_rope_append, wl_tree_attention, wl_verify)
 from .stack import LayerTheta
 
 MAX_STEP = 64  # tokens of one sequence in a step (wl_tree_attention)
@@ -44,13 +53,21 @@ class Decoder:
     """layers: theta bundles (stack.LayerTheta); norms: one BlockNorms each;
     final: the last norm's weight.  batch sequences of up to max_len positions
     in pages of page_size; head dim = k.out / kv_heads.  len (int32 [batch], on
-    the GPU) holds the lengths; beside accept(), write to it only to lower them."""
+    the GPU) holds the lengths; beside accept(), write to it only to lower them.
+    head: the vocabulary's projection (F8Weight [vocab, hidden]).  pool_pages: how
+    many pages the sequences share (None: enough for max_len each); where they
+    run out, sequences in order get all that a step needs or take no token in
+    it, and room (int32 [batch], on the GPU) tells how many each took."""
 
     def __init__(self, layers: list[LayerTheta], norms: list[BlockNorms], final: torch.Tensor, kv_heads: int, rope: RopeTable | None,
                  batch: int, max_len: int, page_size: int = 64, cache_dtype=torch.float8_e4m3fn, eps: float = 1e-6,
-                 w_offset: float = 1.0, scale: float | None = None):
+                 w_offset: float = 1.0, scale: float | None = None, head: F8Weight | None = None, pool_pages: int | None = None):
         if len(layers) != len(norms):
             raise ValueError("one BlockNorms per layer")
+        if head is not None and head.inp != layers[0].q.W0.shape[1]:
+            raise ValueError(f"the head must take {layers[0].q.W0.shape[1]} inputs, got {head.inp}")
+        if pool_pages is not None and pool_pages < 1:
+            raise ValueError(f"pool_pages must be at least 1, got {pool_pages}")
         self.layers, self.norms, self.final = layers, norms, final
         self.hidden = int(layers[0].q.W0.shape[1])
         self.kv_heads, self.dim = kv_heads, int(layers[0].k.W0.shape[0]) // kv_heads
@@ -58,9 +75,16 @@ class Decoder:
         dev = self.device = layers[0].q.W0.device
         per = -(-max_len // page_size)
         self.max_len = per * page_size
-        self.caches = [KVCache.empty(batch * per, kv_heads, page_size, self.dim, cache_dtype, dev) for _ in layers]
-        self.pages = torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per).contiguous()
+        held = batch * per if pool_pages is None else pool_pages
+        self.caches = [KVCache.empty(held, kv_heads, page_size, self.dim, cache_dtype, dev) for _ in layers]
         self.len = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.head, self.pool, self.held, self.room = head, None, None, None
+        if pool_pages is None:
+            self.pages = torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per).contiguous()
+        else:
+            self.pool = PagePool.full(pool_pages, page_size, dev)
+            self.pages = torch.full((batch, per), -1, dtype=torch.int32, device=dev)
+            self.held = torch.zeros(batch, dtype=torch.int32, device=dev)
         self._most = 0  # no sequence is longer ...
         self._known = True  # ... unless a captured step may have been replayed
         self._drafted = None
@@ -89,6 +113,9 @@ class Decoder:
         if not 1 <= n <= MAX_STEP:
             raise ValueError(f"a step takes 1 to {MAX_STEP} tokens of each sequence, got {n}")
         self._fits(n, count)
+        if self.pool is not None:
+            count, _ = wl_page_plan(self.pool, self.pages, self.held, self.len, n, count)
+            self.room = count
         seqs = CacheSeqs(self.pages, self.len, n, count)
         positions = None if depth is None else (self.len[:, None] + depth).to(torch.int32).contiguous()
         norm = dict(eps=self.eps, w_offset=self.w_offset)
@@ -120,6 +147,8 @@ class Decoder:
         if path is not None and (tuple(path.shape) != (self.batch, m) or not 1 <= m <= n):
             raise ValueError(f"path must be [{self.batch}, 1..{n}], got {tuple(path.shape)}")
         self._drafted = None
+        if path is not None and self.pool is not None:  # no more than there were pages for
+            count = had if count is None else torch.minimum(count, had)
         if path is not None:
             rows = (torch.arange(self.batch, device=self.device)[:, None] * n + path.clamp(0, n - 1)).view(-1)
             seqs = CacheSeqs(self.pages, self.len, m, count)
@@ -131,6 +160,37 @@ class Decoder:
         self.len += m if count is None else count.clamp(0, m)
         self._most += m
 
+    def logits(self, h: torch.Tensor, ydt=torch.bfloat16) -> torch.Tensor:
+        """The head's logits [rows, vocab] of h [rows, hidden], a step's normed states."""
+        if self.head is None:
+            raise ValueError("logits() needs a head")
+        return wl_linear_f8(*wl_quant_f8(h), self.head, ydt=ydt)
+
+    def verify(self, logits: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor, mask: torch.Tensor | None = None,
+               draft: torch.Tensor | None = None, temperature=1.0):
+        """Which of the last step's drafted tokens hold (wl_verify: logits
+        [batch * n, vocab], tokens and uniforms [batch, n], mask as given to the
+        step), counted into the sequences as accept() does; returns (path,
+        accepted, next): next [batch] is node 0 of the next step."""
+        if self._drafted is None:
+            raise ValueError("verify() needs a step before it")
+        n, had = self._drafted[:2]
+        if tuple(tokens.shape) != (self.batch, n):
+            raise ValueError(f"tokens must be [{self.batch}, {n}] as the step's, got {tuple(tokens.shape)}")
+        path, accepted, token = wl_verify(logits, tokens, uniforms, mask, had, draft, temperature)
+        self.accept(None if mask is None else path, accepted)  # a chain's path lies as it is
+        return path, accepted, token
+
+    def release(self, done: torch.Tensor):
+        """Ends the sequences with done[b] (bool [batch]): their lengths become 0
+        and their shared pages go back.  An open step is dropped."""
+        if tuple(done.shape) != (self.batch,) or done.dtype != torch.bool:
+            raise ValueError(f"done must be bool [{self.batch}], got {done.dtype} {tuple(done.shape)}")
+        self._drafted = None
+        self.len.masked_fill_(done, 0)
+        if self.pool is not None:
+            wl_page_plan(self.pool, self.pages, self.held, self.len)
+
     def prompt(self, x: torch.Tensor) -> torch.Tensor:
         """x [batch, T, hidden] fp32, T tokens of each sequence; returns the last
         token's normed state, bf16 [batch, hidden]."""
@@ -138,6 +198,11 @@ class Decoder:
         if T < 1:
             raise ValueError("a prompt has at least one token")
         self._fits(T, None)
+        if self.pool is not None and not torch.cuda.is_current_stream_capturing():
+            page = self.pool.page_size
+            want = ((self.len + T + page - 1) // page - self.held).clamp(min=0).sum()
+            if int(want - self.pool.top[0]) > 0:
+                raise ValueError(f"the prompt needs {int(want)} pages of {int(self.pool.top)} free ones")
         h = None
         for t in range(0, T, MAX_STEP):
             part = x[:, t:t + MAX_STEP]
