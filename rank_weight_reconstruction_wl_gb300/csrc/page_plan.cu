@@ -21,7 +21,7 @@ namespace cg = cooperative_groups;
 namespace wl {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCtas = 8;
+constexpr int kPlanCtas = 16;
 
 struct PlanDevice {
     PlanArgs a;
@@ -123,18 +123,41 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         all_back += sums[0][r];
     }
     const int up = min(top + all_back, a.pool);
-    for (int x = threadIdx.x; x < backs; x += kPlanThreads) {
-        const int i = plan_find(back0, nb, x);
-        int32_t *entry = a.pages + (int64_t)(b0 + i) * a.max_pages + need[i] + (x - back0[i]);
-        const int place = up - 1 - (back_base + x);
-        if (place >= 0) a.free_pages[place] = *entry;
-        *entry = -1;
+    // Four moves of a thread at a time, so that their loads overlap (one at a time: 512 prompts' pages and back 43 us).
+    constexpr int U = 4;
+    for (int x0 = threadIdx.x; x0 < backs; x0 += U * kPlanThreads) {
+        int32_t *entry[U];
+        int32_t page[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * kPlanThreads, i = plan_find(back0, nb, min(x, backs - 1));
+            entry[u] = x < backs ? a.pages + (int64_t)(b0 + i) * a.max_pages + need[i] + (x - back0[i]) : nullptr;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) page[u] = entry[u] ? *entry[u] : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (entry[u]) {
+                const int place = up - 1 - (back_base + x0 + u * kPlanThreads);
+                if (place >= 0) a.free_pages[place] = page[u];
+                *entry[u] = -1;
+            }
     }
     cl.sync();
-    for (int x = threadIdx.x; x < wants; x += kPlanThreads) {
-        const int i = plan_find(want0, nb, x);
-        if (want_base + want0[i] + need[i] - have[i] <= up)
-            a.pages[(int64_t)(b0 + i) * a.max_pages + have[i] + (x - want0[i])] = __ldcg(a.free_pages + up - 1 - (want_base + x));
+    const int fitting = min(wants, up - want_base);  // moves of sequences past the pool's end are not looked at
+    for (int x0 = threadIdx.x; x0 < fitting; x0 += U * kPlanThreads) {
+        int32_t *entry[U];
+        int32_t page[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * kPlanThreads, i = plan_find(want0, nb, min(x, fitting - 1));
+            const bool fits = x < fitting && want_base + want0[i] + need[i] - have[i] <= up;
+            entry[u] = fits ? a.pages + (int64_t)(b0 + i) * a.max_pages + have[i] + (x - want0[i]) : nullptr;
+            page[u] = fits ? __ldcg(a.free_pages + up - 1 - (want_base + x)) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (entry[u]) *entry[u] = page[u];
     }
     __syncthreads();  // below, have[] becomes the room
     int taken = 0;  // of the whole call, up to this thread's last sequence that fits
@@ -176,20 +199,23 @@ __global__ void __launch_bounds__(256) page_slots_kernel(const __grid_constant__
 {
     pdl_wait();
     pdl_trigger();
-    const int64_t total = (int64_t)p.a.batch * p.a.n;
-    for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += (int64_t)gridDim.x * 256) {
-        const int b = p.by_n.div((int)x);
-        p.a.slots[x] = plan_slot(p, b, plan_len(p.a, b), __ldg(p.a.room + b), (int)(x - (int64_t)b * p.a.n));
-    }
+    // a sequence's slots by a run of blocks: the length, the room and a page are looked up once for the slots that share them
+    const int b = (int)blockIdx.x;
+    const int64_t len = plan_len(p.a, b);
+    const int room = __ldg(p.a.room + b);
+    int64_t *out = p.a.slots + (int64_t)b * p.a.n;
+    for (int i = (int)blockIdx.y * 256 + threadIdx.x; i < p.a.n; i += (int)gridDim.y * 256) out[i] = plan_slot(p, b, len, room, i);
 }
 
 wl_status launch_page_plan(const PlanArgs &args, const DeviceInfo *di, cudaStream_t st)
 {
     PlanDevice p{args, fast_div(args.page_size), fast_div(args.n > 0 ? args.n : 1), 0};
-    const int ctas = args.batch > 64 ? kPlanCtas : 1;
+    // One CTA has no cluster barriers to wait for; many sequences move many pages (512 prompts and back: 30.7 us with 16, 41.6 with 8).
+    const int ctas = args.batch > 256 ? kPlanCtas : args.batch > 64 ? 8 : 1;
     p.per = (args.batch + ctas - 1) / ctas;
     const size_t smem = (size_t)p.per * 4 * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 131072);
+    if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "wl_page_plan attributes");
     const bool slots = args.slots && args.n > 0;
     const bool inl = slots && (int64_t)args.batch * args.n <= 8192 * ctas;
@@ -209,8 +235,9 @@ wl_status launch_page_plan(const PlanArgs &args, const DeviceInfo *di, cudaStrea
     e = cudaLaunchKernelEx(&cfg, page_plan_kernel, p, (int)inl);
     if (e != cudaSuccess) return cuda_fail(e, "wl_page_plan launch");
     if (slots && !inl) {
-        const int64_t blocks = ((int64_t)args.batch * args.n + 1023) / 1024;
-        e = launch_dependent(page_slots_kernel, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, st, p);
+        int64_t blocks = (args.n + 255) / 256;
+        while (blocks > 1 && (blocks > 65535 || blocks * args.batch > 16 * di->sm_count)) blocks = (blocks + 1) / 2;
+        e = launch_dependent(page_slots_kernel, dim3((unsigned)args.batch, (unsigned)blocks), 256, 0, st, p);
         if (e != cudaSuccess) return cuda_fail(e, "wl_page_plan slots launch");
     }
     return WL_OK;

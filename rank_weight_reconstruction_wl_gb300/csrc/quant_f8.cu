@@ -19,16 +19,12 @@ struct QuantArgs {
     FastDiv by_nb;
 };
 
-// The largest of two magnitudes; a NaN wins.
-__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) { return max(a, b); }
-
-template <typename T>
 __device__ __forceinline__ uint32_t amax8(const float v[8])
 {
     // magnitudes as integers order like the numbers, with infinities and NaN above all
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_bits(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
     return m;
 }
 
@@ -79,9 +75,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            uint32_t m = amax8<T>(v[j]);
+            uint32_t m = amax8(v[j]);
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) m = max_bits(m, __shfl_xor_sync(0xffffffffu, m, d));
+            for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
             const int i = kb[j] * 128 + lane * 8;
             if (u0 + 16 * j < units && i < a.in)
                 put_codes(a.codes + row[j] * a.in + i, a.scales + (int64_t)kb[j] * a.rows + row[j], lane == 0, v[j], m);
@@ -112,14 +108,14 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
         }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max_bits(m, amax8<T>(v[j]));
+    for (int j = 0; j < 8; ++j) m = max(m, amax8(v[j]));
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = max_bits(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = 16; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = m;
     __syncthreads();
     m = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = max_bits(m, red[w]);
+    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int64_t row = g * 128 + r + 16 * j;
@@ -134,8 +130,8 @@ wl_status launch_quant_f8(const void *x, int64_t x_stride, int xdt, int64_t rows
     QuantArgs a{x, x_stride, rows, codes, scales, (int)in, (int)((in + 127) / 128), 1, fast_div((in + 127) / 128)};
     cudaError_t e;
     if (group == 1) {
-        // rows of a CTA: up to 8, so that their scales, neighbours in memory, are written together
-        a.rows_per_cta = (int)(rows >= 8 * 608 ? 8 : rows >= 1216 ? rows / 608 : rows >= 304 ? 2 : 1);
+        // rows of a CTA: up to 8, so that their scales, neighbours in memory, are written together, while 8 CTAs an SM are left
+        a.rows_per_cta = (int)(rows >= 8 * 1216 ? 8 : rows >= 2432 ? rows / 1216 : 1);
         const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta));
         e = xdt == WL_OUT_F32 ? launch_dependent(quant_rows_kernel<float>, grid, 256, 0, st, a)
                               : launch_dependent(quant_rows_kernel<bf16>, grid, 256, 0, st, a);
