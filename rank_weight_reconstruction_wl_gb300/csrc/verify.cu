@@ -347,12 +347,15 @@ __device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, flo
 // f(i, R_i) for the elements of a vector as loaded, from element e0 on: R after `rejected` rejections (draft), or without
 // the excluded tokens (no draft).  A word at a time, not unrolled: this code runs a few times in a launch, and unrolled
 // it took longer to be fetched than to run (5 us of 14 for a vocabulary of 1000).
-template <typename L, typename Q, bool DRAFT, typename F>
-__device__ __forceinline__ void each_R(const VerShared &sh, uint4 w, const Q *qrow, int vocab, int e0, int rejected, int nex, F f)
+template <typename L, bool DRAFT, typename F>
+__device__ __forceinline__ void each_R(const VerShared &sh, uint4 w, const float *qs, int e0, int rejected, int nex, F f)
 {
     constexpr int E = RowVecs<L>::E, P = E / 4;  // elements of a word
     float q[E];
-    if (DRAFT && rejected > 0) load_at<Q, E>(qrow, e0, vocab, q);
+    if (DRAFT) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) q[i] = qs[i];
+    }
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -378,11 +381,11 @@ __device__ __forceinline__ void each_R(const VerShared &sh, uint4 w, const Q *qr
 }
 
 // The sum of a vector's R: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
-template <typename L, typename Q, bool DRAFT>
-__device__ __forceinline__ FF vec_sum(const VerShared &sh, const uint4 &w, const Q *qrow, int vocab, int e0, int rejected, int nex)
+template <typename L, bool DRAFT>
+__device__ __forceinline__ FF vec_sum(const VerShared &sh, const uint4 &w, const float *q, int e0, int rejected, int nex)
 {
     FF s{0.0f, 0.0f};
-    each_R<L, Q, DRAFT>(sh, w, qrow, vocab, e0, rejected, nex, [&](int, FF R) {
+    each_R<L, DRAFT>(sh, w, q, e0, rejected, nex, [&](int, FF R) {
         const float h = (R.h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
         s.h += h, s.l += (R.h - h) + R.l;
     });
@@ -399,11 +402,20 @@ __device__ __noinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, cons
     for (int j = 0; j < sh.nex; ++j)
         if (sh.excluded[j] >= r.vecs.first(r.v0) && sh.excluded[j] < r.vecs.first(r.v1)) nex = sh.nex;
     FF acc{0.0f, 0.0f};
+    // the next vectors, of the draft row too, are under way while these are summed
+    constexpr int E = RowVecs<L>::E;
     uint4 ahead[2] = {r.vecs.raw(r.v0 + lane, r.v1), r.vecs.raw(r.v0 + lane + 32, r.v1)};
+    float q[E], qa[E];
+    if (DRAFT && rejected > 0) load_at<Q, E>(qrow, r.vecs.first(r.v0 + lane), vocab, qa);
     for (int v = r.v0 + lane; v < r.v1; v += 32) {
         const uint4 raw = ahead[0];
         ahead[0] = ahead[1], ahead[1] = r.vecs.raw(v + 64, r.v1);
-        acc = ff_add(acc, vec_sum<L, Q, DRAFT>(sh, raw, qrow, vocab, r.vecs.first(v), rejected, nex));
+        if (DRAFT && rejected > 0) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) q[i] = qa[i];
+            load_at<Q, E>(qrow, r.vecs.first(v + 32), vocab, qa);
+        }
+        acc = ff_add(acc, vec_sum<L, DRAFT>(sh, raw, q, r.vecs.first(v), rejected, nex));
     }
     acc = ff_norm(ff_warp_sum(acc));
     if (lane == 0) sh.warp_total[warp] = acc;
@@ -485,13 +497,16 @@ __device__ __noinline__ void choose(VerShared &sh, int rank, int ctas, const Ver
     const FF target = sh.target;
     const int v0 = min((rank * kVerWarps + sh.sel) * per, r.vecs.nv), v1 = min(v0 + per, r.vecs.nv);
     int tile = -1;
+    constexpr int E = RowVecs<L>::E;
     uint4 raw = make_uint4(0, 0, 0, 0);
+    float q[E];
     FF mine{0.0f, 0.0f};
 #pragma unroll 1
     for (int t0 = 0; v0 + 32 * t0 < v1; t0 += kVerWarps) {
         const int v = v0 + 32 * (t0 + warp) + lane;
         raw = r.vecs.raw(v, v1);
-        mine = vec_sum<L, Q, DRAFT>(sh, raw, qrow, vocab, r.vecs.first(v), sh.rejected, sh.nex);
+        if (DRAFT && sh.rejected > 0) load_at<Q, E>(qrow, r.vecs.first(v), vocab, q);
+        mine = vec_sum<L, DRAFT>(sh, raw, q, r.vecs.first(v), sh.rejected, sh.nex);
         const FF s = ff_norm(ff_warp_sum(mine));
         if (lane == 0) sh.tile_sum[warp] = s;
         __syncthreads();
@@ -515,7 +530,8 @@ __device__ __noinline__ void choose(VerShared &sh, int rank, int ctas, const Ver
     const int v = v0 + 32 * tile + lane, e0 = r.vecs.first(v);
     if (!sh.over) {  // the last tile with any, perhaps not of the last round
         raw = r.vecs.raw(v, v1);
-        mine = vec_sum<L, Q, DRAFT>(sh, raw, qrow, vocab, e0, sh.rejected, sh.nex);
+        if (DRAFT && sh.rejected > 0) load_at<Q, E>(qrow, e0, vocab, q);
+        mine = vec_sum<L, DRAFT>(sh, raw, q, e0, sh.rejected, sh.nex);
     }
     const FF upto = ff_norm(ff_add(sh.tile_base, ff_warp_scan(ff_norm(mine))));
     FF run{__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
@@ -523,7 +539,7 @@ __device__ __noinline__ void choose(VerShared &sh, int rank, int ctas, const Ver
     int top = -1;
     unsigned hit = 0x7fffffffu;
     bool clear = false;
-    each_R<L, Q, DRAFT>(sh, raw, qrow, vocab, e0, sh.rejected, sh.nex, [&](int i, FF R) {
+    each_R<L, DRAFT>(sh, raw, q, e0, sh.rejected, sh.nex, [&](int i, FF R) {
         const FF was = run;
         run = ff_norm(ff_add(run, R));
         if (R.h > 0.0f) top = i;
@@ -662,9 +678,9 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                         continue;
                     }
                     const FF Ri{__shfl_sync(0xffffffffu, i < 32 ? R[0].h : R[1].h, i % 32), __shfl_sync(0xffffffffu, i < 32 ? R[0].l : R[1].l, i % 32)};
-                    const double have = ff_double(Ri), want = (double)sh.draw[i] * (double)sh.child_q[side][i] * S;
+                    const double have = ff_double(Ri), rq = (double)sh.draw[i] * (double)sh.child_q[side][i], want = rq * S;
                     const bool yes = want < have;
-                    if (!exact && ((have > 0.0 && fabs(want - have) <= tol * S0) || (DRAFT && !yes))) {
+                    if (!exact && ((have > 0.0 && fabs(want - have) <= fabs(rq) * tol * S0) || (DRAFT && !yes))) {
                         code = kPass;
                         break;
                     }
@@ -717,7 +733,9 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                 // by the fast sums, where no border is near; the CTA that has the token tells the others
                 if (tid == 0) sh.again = 0;
                 cl.sync();
-                choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, true, 2.0f * tol * sh.part_sum, a.next + b);
+                // the draw's target and the sum before its token are each off by at most tol of the sum that they are of
+                const float share = sh.nex > 0 ? 1.0f : fminf(fmaxf(sh.draw[0], 0.0f), 1.0f);
+                choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, true, 2.0f * tol * share * sh.part_sum, a.next + b);
                 __syncthreads();
                 if (sh.sel >= 0 && !sh.sure && tid < ctas) cl.map_shared_rank(&sh, tid)->again = 1;
                 cl.sync();
