@@ -18,6 +18,8 @@
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
 
@@ -765,42 +767,59 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
 }
 
 template <typename L, typename Q, bool DRAFT>
-static cudaError_t verify_launch(const VerifyArgs &a, int ctas, cudaStream_t st)
+static cudaError_t verify_launch(const VerifyArgs &a, const DeviceInfo *di, cudaStream_t st)
 {
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)ctas;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    at[1].val.clusterDim.x = at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.batch * ctas));
     cfg.blockDim = dim3(kVerThreads);
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
-    if (ctas > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(verify_kernel<L, Q, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
+    // A sequence's CTAs: as many as let the clusters of all sequences run at once (a second wave doubles the time: 16
+    // sequences on clusters of 8, of which fewer fit the GPU's partitions than its SMs would hold, took 118 us where
+    // clusters of 7 take 96), one for 4096 tokens of the vocabulary at most.  How many clusters run at once is asked once a device.
+    static std::atomic<int> at_once[64][kVerCtas + 1];
+    static const int sizes[] = {16, 12, 8, 7, 6, 5, 4, 3, 2, 1};
+    for (const int *size = sizes;; ++size) {
+        const int ctas = *size;
+        at[1].val.clusterDim.x = (unsigned)ctas;
+        cfg.gridDim = dim3((unsigned)(a.batch * ctas));
+        if (ctas == 1) break;
+        if ((int64_t)a.vocab < 4096 * ctas || (int64_t)a.batch * ctas > di->sm_count) continue;
+        std::atomic<int> *known = di->device < 64 ? &at_once[di->device][ctas] : nullptr;
+        int n = known ? known->load(std::memory_order_relaxed) : 0;
+        if (n == 0) {
+            cfg.numAttrs = 2;
+            cudaError_t e = ctas > 8 ? cudaFuncSetAttribute(verify_kernel<L, Q, DRAFT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
+            if (e == cudaSuccess) {
+                cudaLaunchConfig_t ask = cfg;
+                ask.attrs = at + 1;
+                ask.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&n, verify_kernel<L, Q, DRAFT>, &ask);
+            }
+            if (e != cudaSuccess) return e;
+            n = n > 0 ? n : -1;
+            if (known) known->store(n, std::memory_order_relaxed);
+        }
+        if (a.batch <= n) break;
     }
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, verify_kernel<L, Q, DRAFT>, a);
 }
 
 template <typename L>
-static cudaError_t verify_draft(const VerifyArgs &a, int ddt, int ctas, cudaStream_t st)
+static cudaError_t verify_draft(const VerifyArgs &a, int ddt, const DeviceInfo *di, cudaStream_t st)
 {
-    if (!a.draft) return verify_launch<L, float, false>(a, ctas, st);
-    return ddt == WL_OUT_F32 ? verify_launch<L, float, true>(a, ctas, st) : verify_launch<L, bf16, true>(a, ctas, st);
+    if (!a.draft) return verify_launch<L, float, false>(a, di, st);
+    return ddt == WL_OUT_F32 ? verify_launch<L, float, true>(a, di, st) : verify_launch<L, bf16, true>(a, di, st);
 }
 
 wl_status launch_verify(const VerifyArgs &a, int ldt, int ddt, const DeviceInfo *di, cudaStream_t st)
 {
-    // A sequence's CTAs: as many as fill the GPU, at most one for 8192 tokens of the vocabulary.
-    // (16 only for up to 4 sequences: clusters of 16 that fit the GPU at once are fewer than its SMs hold, and 8 of them
-    // took two waves.)
-    int ctas = a.batch <= 4 ? kVerCtas : 8;
-    while (ctas > 1 && ((int64_t)a.batch * ctas > di->sm_count || (int64_t)a.vocab < 8192 * (ctas / 2))) ctas /= 2;
-    const cudaError_t e = ldt == WL_OUT_F32 ? verify_draft<float>(a, ddt, ctas, st) : verify_draft<bf16>(a, ddt, ctas, st);
+    const cudaError_t e = ldt == WL_OUT_F32 ? verify_draft<float>(a, ddt, di, st) : verify_draft<bf16>(a, ddt, di, st);
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_verify launch");
 }
 
