@@ -500,8 +500,8 @@ wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const
  * t is temperatures[b] (device) or, where that is NULL, temperature.  Logits of
  * -infinity are tokens of no weight.  A row with a NaN or +infinity or with no
  * finite logit, or a t that is NaN, ends the path there with next[b] = -1.  Tokens outside
- * [0, vocab) are rejected.  Weights, sums and decisions are held to 2^-33 of the
- * row's sum.
+ * [0, vocab) are rejected.  Decisions are those of exact arithmetic where no
+ * border lies within 2^-29 of the row's sum.
  * Limits: 1 <= batch <= 65536, 1 <= n <= 64, 1 <= vocab <= 2^24; strides at
  * least vocab.
  */

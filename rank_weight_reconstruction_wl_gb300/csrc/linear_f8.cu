@@ -3,17 +3,28 @@
 //
 //     y[t,o] = sum_b x_scale[b][t] w_scale[b][o / 128] sum_{i in block b} W[o,i] x[t,i]
 //
-// A CTA takes a tile of 128 rows of W (M, one row of scales) by N tokens and
-// walks over the blocks of 128: TMA boxes of both operands into a ring of
-// stages, four MMAs (K = 32) into a tensor-memory accumulator of the block's
-// own, and from there, scaled, into registers: acc += d * (x_scale w_scale). So
-// the block sums are scaled in fp32 whatever the scales are, and the MMAs of the
-// next blocks run meanwhile in other accumulators.  W is M, so that one token
-// costs 16 columns, not 128 padded rows.  Where tiles are fewer than SMs the
-// sum is split over a cluster and joined through distributed shared memory.
+// All three kernels walk over the blocks of 128: TMA boxes of both operands into
+// a ring of stages, four MMAs (K = 32) into a tensor-memory accumulator of the
+// block's own, and from there, scaled, into registers: acc += d * (x_scale
+// w_scale).  So the block sums are scaled in fp32 whatever the scales are, and the
+// MMAs of the next blocks run meanwhile in other accumulators.  They differ in
+// what is M and what an SM holds:
+//   up to 64 tokens (linear_f8_kernel): W is M, so that one token costs 16
+//     columns, not 128 padded rows; tiles of a height that fills whole waves of
+//     SMs, or the sum split over a cluster.  Bound by HBM: 1 x 1152 -> 262144
+//     51 us, 0.88 of the copy rate; 1 x 5376 -> 21504 22 us.
+//   65 to 128 tokens (linear_f8_few_kernel): tokens are M; each byte of W is read
+//     once.  96 x 1152 -> 262144 59 us, 0.87 of the copy rate.
+//   more (linear_f8_pair_kernel): two SMs share 256 x 256 tiles.  Bound by the
+//     way of a block through its accumulator: 4096 x 5376 -> 21504 340 us, 2.8
+//     PFLOP/s.
+// From 65 tokens on the one that is thought to be the fastest is taken.
 //
-// Warps 0-7 scale and store (4 warps per half of the tokens; a warp's lanes are
-// 32 rows of W), warp 8 loads, warp 9 multiplies.
+// linear_f8_kernel: a CTA takes a tile of up to 128 rows of W by N tokens.  Stages
+// and hand-overs are of two blocks: a block alone took 0.36 us however small its
+// tile, most of it barriers' round trips.  Warps 0-7 scale and store (4 warps per
+// half of the tokens; a warp's lanes are 32 rows of W), warp 8 loads, warp 9
+// multiplies.
 #include <cooperative_groups.h>
 
 #include "cache_row.cuh"
@@ -35,7 +46,8 @@ struct LinearF8Args {
     unsigned *status;
 };
 
-constexpr int kF8Threads = 320, kF8Stages = 24, kF8Ring = 192 * 1024;
+constexpr int kF8Threads = 320, kF8Ring = 192 * 1024;
+constexpr int kF8Stages = 16;  // at most: tiles of 32 rows by 16 tokens
 
 template <int N>
 struct F8Shape {
@@ -441,7 +453,7 @@ static wl_status f8_run(LinearF8Args a, const uint8_t *x, const uint8_t *W, int6
     if (s != WL_OK) return s;
     a.nt = (int)((a.T + N - 1) / N);
     a.rows = p.rows;
-    a.stages = kF8Ring / ((p.rows + N) * 256) < kF8Stages ? kF8Ring / ((p.rows + N) * 256) : kF8Stages;
+    a.stages = kF8Ring / ((p.rows + N) * 256);
     a.tiles = (a.out + p.rows - 1) / p.rows * a.nt;
     const int64_t grid = p.ctas > 1 ? a.tiles * p.ctas : a.tiles < di->sm_count ? a.tiles : di->sm_count;
     const cudaError_t e = p.ctas > 1 ? f8_launch<N, true>(a, wmap, xmap, ydt, p.ctas, (unsigned)grid, st)
@@ -602,22 +614,26 @@ __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUten
     char *stage = ring + S::NST * S::STAGE + warp * 4096;
     uint32_t blk = 0;
     bool good = true;
-    // Scales come four blocks at a time, a group ahead and over the end of a tile (one block ahead, waiting for them was
-    // most of a block's time).
+    // Scales come four blocks at a time, a group ahead (one block ahead, waiting for them was most of a block's time; ahead
+    // over the end of a tile too cost more in registers than the wait at a tile's begin: 351 against 340 us).
     float wn[4], xn[4], f[4];
-    auto fetch = [&](int64_t tile, int kb) {
+    const float *wsp, *xsp;
+    auto place = [&](int64_t tile, const float *&w, const float *&x) {  // of a tile's scales (a division: once a tile)
         const int64_t mt = tile / a.nt, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
-        const float *wsp = a.ws + min(mt * 2 + half, (int64_t)a.ob - 1), *xsp = a.xs + min(t, a.T - 1);
+        w = a.ws + min(mt * 2 + half, (int64_t)a.ob - 1), x = a.xs + min(t, a.T - 1);
+    };
+    auto fetch = [&](const float *w, const float *x, int kb) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t k = min(kb + i, a.nkb - 1);
-            wn[i] = __ldg(wsp + k * a.ob), xn[i] = __ldg(xsp + k * a.T);
+            wn[i] = __ldg(w + k * a.ob), xn[i] = __ldg(x + k * a.T);
         }
     };
-    fetch(first, 0);
     for (int64_t tile = first; tile < a.tiles && good; tile += step) {
         const int64_t mt = tile / a.nt;
         const int64_t o0 = mt * 256 + half * 128, t = (tile - mt * a.nt) * 128 * CTAS + rank * 128 + quarter * 32 + lane;
+        place(tile, wsp, xsp);
+        fetch(wsp, xsp, 0);
         uint64_t acc[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -626,8 +642,7 @@ __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUten
             if ((kb & 3) == 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f[i] = wn[i] * xn[i];
-                const bool here = kb + 4 < a.nkb;
-                fetch(here ? tile : tile + step, here ? kb + 4 : 0);
+                fetch(wsp, xsp, kb + 4);
             }
             const uint64_t s = f8_both(f[0]);
             f[0] = f[1], f[1] = f[2], f[2] = f[3];
@@ -837,7 +852,8 @@ struct F8Few {
     int half;          // columns of a side
 };
 
-constexpr int kFewStages = 16, kFewThreads = 384;
+constexpr int kFewThreads = 384;
+constexpr int kFewStages = 11;  // at most: tiles of 64 rows by 72 tokens
 
 // 32 tokens (t0: the first) by 32 rows of W through the warp's shared memory.
 template <bool F32>
@@ -869,37 +885,12 @@ __device__ __forceinline__ void f8_store_box32(const CUtensorMap *map, char *sta
     }
 }
 
-// The lane's 16 outputs from place `at` of y on, the first n of them in the matrix; vec: 16-byte stores.
-__device__ __forceinline__ void f8_store16(void *y, int ydt, int64_t at, int n, bool vec, const uint64_t acc[8])
+// The lane's 16 outputs from place `at` of y on, the first n of them in the matrix (rows that are not 16 bytes apart).
+__device__ __forceinline__ void f8_store16(void *y, int ydt, int64_t at, int n, const uint64_t acc[8])
 {
-    if (ydt == WL_OUT_F32) {
-        float *p = static_cast<float *>(y) + at;
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-            if (vec && c + 4 <= n) {
-                *reinterpret_cast<float4 *>(p + c) = make_float4(f8_lo(acc[c / 2]), f8_hi(acc[c / 2]), f8_lo(acc[c / 2 + 1]), f8_hi(acc[c / 2 + 1]));
-            } else {
-#pragma unroll
-                for (int i = c; i < c + 4; ++i)
-                    if (i < n) p[i] = i & 1 ? f8_hi(acc[i / 2]) : f8_lo(acc[i / 2]);
-            }
-        }
-    } else {
-        bf16 *p = static_cast<bf16 *>(y) + at;
-#pragma unroll
-        for (int c = 0; c < 16; c += 8) {
-            if (vec && c + 8 <= n) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = bf16x2_bits(f8_lo(acc[c / 2 + i]), f8_hi(acc[c / 2 + i]));
-                *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int i = c; i < c + 8; ++i)
-                    if (i < n) p[i] = __float2bfloat16_rn(i & 1 ? f8_hi(acc[i / 2]) : f8_lo(acc[i / 2]));
-            }
-        }
-    }
+    for (int i = 0; i < 16; ++i)
+        if (i < n) store_out(y, ydt, at + i, i & 1 ? f8_hi(acc[i / 2]) : f8_lo(acc[i / 2]));
 }
 
 __device__ __forceinline__ void f8_scale16(uint64_t *acc, const uint32_t *d, uint64_t s)
@@ -996,8 +987,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __g
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int side = warp / 4, quarter = warp % 4, t = quarter * 32 + lane;
-        const int c0 = side * p.half, chunks = (min(p.rows, c0 + p.half) - c0) / 16;  // columns of the warp, in 16s: 0 .. 8
-        const bool mine = quarter * 32 < a.T && chunks > 0;
+        const int c0 = side * p.half, chunks = p.half / 16;  // columns of the warp, in 16s: 2, 4, 6 or 8
+        const bool mine = quarter * 32 < a.T;
         char *stage = ring + p.stages * p.stage + warp * 4096;
         uint32_t buf = 0, phase = 0;
         bool good = true;
@@ -1038,7 +1029,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __g
                         if (c < chunks) {
                             uint32_t d0[16], d1[16];
                             f8_tmem_ld<16>(at + 16 * c, d0);
-                            if (c + 1 < chunks) f8_tmem_ld<16>(at + 16 * c + 16, d1);
+                            f8_tmem_ld<16>(at + 16 * c + 16, d1);
                             f8_tmem_wait<16>(d0);
                             f8_tmem_wait<16>(d1);
                             f8_scale16(acc + 8 * c, d0, c < cut ? s0 : s1);
@@ -1061,11 +1052,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __g
                         else f8_store_box32<false>(&ymap, stage, quarter * 32, o0 + 32 * b, acc + 16 * b);
                     }
             } else if (t < a.T) {
-                const bool vec = a.out % 8 == 0;
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     if (c < chunks && o0 + 16 * c < a.out)
-                        f8_store16(a.y, ydt, t * a.out + o0 + 16 * c, (int)min((int64_t)16, a.out - o0 - 16 * c), vec, acc + 8 * c);
+                        f8_store16(a.y, ydt, t * a.out + o0 + 16 * c, (int)min((int64_t)16, a.out - o0 - 16 * c), acc + 8 * c);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // before the memory they read goes
@@ -1096,7 +1086,7 @@ static double f8_few_plan(int64_t T, int64_t out, int nkb, int sms, F8Few *p)
     }
     p->half = p->rows / 2;  // a multiple of 32: boxes of 32 rows of W
     p->stage = (p->rows + p->xrows) * 128;
-    p->stages = 192 * 1024 / p->stage < kFewStages ? 192 * 1024 / p->stage : kFewStages;
+    p->stages = kF8Ring / p->stage;
     p->cols = p->rows <= 64 ? 64 : p->rows <= 128 ? 128 : 256;
     p->bufs = 512 / p->cols;
     return best;
@@ -1117,7 +1107,7 @@ static wl_status f8_run_few(LinearF8Args a, const F8Few &p, const uint8_t *x, co
     }
     a.tiles = (a.out + p.rows - 1) / p.rows;
     const int smem = 1024 + p.stages * p.stage + 8 * 4096;
-    cudaError_t e = cudaFuncSetAttribute(linear_f8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + 192 * 1024 + 8 * 4096);
+    cudaError_t e = cudaFuncSetAttribute(linear_f8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kF8Ring + 8 * 4096);
     if (e != cudaSuccess) return cuda_fail(e, "wl_linear_f8 attributes");
     const int64_t grid = a.tiles < di->sm_count ? a.tiles : di->sm_count;
     e = launch_dependent(linear_f8_few_kernel, dim3((unsigned)grid), kFewThreads, (size_t)smem, st, a, p, wmap, xmap, ymap, ydt, (int)boxes);

@@ -735,9 +735,10 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
                 // by the fast sums, where no border is near; the CTA that has the token tells the others
                 if (tid == 0) sh.again = 0;
                 cl.sync();
-                // the draw's target and the sum before its token are each off by at most tol of the sum that they are of
-                const float share = sh.nex > 0 ? 1.0f : fminf(fmaxf(sh.draw[0], 0.0f), 1.0f);
-                choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, true, 2.0f * tol * share * sh.part_sum, a.next + b);
+                // Off are the draw's target, by tol of the part u of the sum that it is, and the sum before its token: no
+                // more than tol of the whole, nor than 5e-6 of itself (|y| up to 32), and 1e-9 for all smaller weights.
+                const float u = fminf(fmaxf(sh.draw[0], 0.0f), 1.0f), off = u * tol + fminf(tol, sh.nex > 0 ? tol : 5e-6f * u) + 1e-9f;
+                choose<L, Q, DRAFT>(sh, rank, ctas, row, qrow, a.vocab, fast_turn, true, off * sh.part_sum, a.next + b);
                 __syncthreads();
                 if (sh.sel >= 0 && !sh.sure && tid < ctas) cl.map_shared_rank(&sh, tid)->again = 1;
                 cl.sync();
