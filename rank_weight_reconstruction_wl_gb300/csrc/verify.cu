@@ -292,8 +292,9 @@ __device__ __forceinline__ VerPart join(const VerPart &a, const VerShared &sh)  
 
 // The lane's share of a row's maximum and its place (greedy) or sum.
 template <typename L>
-__device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, float c)
+__device__ __forceinline__ VerPart row_part(const VerShared &sh, const VerRow<L> &r, bool greedy)
 {
+    const float c = sh.c.h;
     constexpr int E = RowVecs<L>::E, U = 8;
     float m = -CUDART_INF_F, s = 0.0f, sl = 0.0f;
     int best = 0x7fffffff;
@@ -328,17 +329,20 @@ __device__ __forceinline__ VerPart row_part(const VerRow<L> &r, bool greedy, flo
         }
         if (!(top <= m)) {
             const float next = max_nan(m, top);
-            const float f = m > -CUDART_INF_F ? ex2((m - next) * c) : 0.0f;
-            s *= f, sl *= f, m = next;
+            const FF f = m > -CUDART_INF_F ? ff_mul(FF{s, sl}, weight(m, next, sh.c, sh.table)) : FF{0.0f, 0.0f};
+            s = f.h, sl = f.l, m = next;
         }
         if (m == -CUDART_INF_F) continue;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             RowVecs<L>::unpack(now[j], x);
-            float w = 0.0f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) w += ex2((x[i] - m) * c);
-            const float t = s + w, z = t - s;
+            for (int i = 0; i < E; ++i) x[i] = ex2((x[i] - m) * c);
+#pragma unroll
+            for (int d = 1; d < E; d *= 2)
+#pragma unroll
+                for (int i = 0; i < E; i += 2 * d) x[i] += x[i + d];
+            const float w = x[0], t = s + w, z = t - s;
             sl += (s - (t - z)) + (w - z);
             s = t;
         }
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
             const int kid = lo ? __ffs((int)lo) - 1 : hi ? 31 + __ffs((int)hi) : 0;
             if (kid) prefetch_row(static_cast<const L *>(a.logits) + (row0 + kid) * a.logits_stride, row);
         }
-        const VerPart mine = join(row_part(row, greedy, sh.c.h), sh);
+        const VerPart mine = join(row_part(sh, row, greedy), sh);
         if (lane == 0) sh.warp_part[warp] = mine;
         __syncthreads();
         if (warp == 0) {

@@ -200,9 +200,9 @@ class Decoder:
         self._fits(T, None)
         if self.pool is not None and not torch.cuda.is_current_stream_capturing():
             page = self.pool.page_size
-            want = ((self.len + T + page - 1) // page - self.held).clamp(min=0).sum()
-            if int(want - self.pool.top[0]) > 0:
-                raise ValueError(f"the prompt needs {int(want)} pages of {int(self.pool.top)} free ones")
+            need, have = torch.stack((((self.len + T + page - 1) // page).sum(), self.held.sum() + self.pool.top[0])).tolist()
+            if need > have:
+                raise ValueError(f"the sequences would need {need} pages of {have}")
         h = None
         for t in range(0, T, MAX_STEP):
             part = x[:, t:t + MAX_STEP]
