@@ -9,16 +9,16 @@
 // w_scale).  So the block sums are scaled in fp32 whatever the scales are, and the
 // MMAs of the next blocks run meanwhile in other accumulators.  They differ in
 // what is M and what an SM holds:
-//   up to 64 tokens (linear_f8_kernel): W is M, so that one token costs 16
+//   few tokens (linear_f8_kernel): W is M, so that one token costs 16
 //     columns, not 128 padded rows; tiles of a height that fills whole waves of
 //     SMs, or the sum split over a cluster.  Bound by HBM: 1 x 1152 -> 262144
 //     51 us, 0.88 of the copy rate; 1 x 5376 -> 21504 22 us.
-//   65 to 128 tokens (linear_f8_few_kernel): tokens are M; each byte of W is read
+//   up to 128 tokens (linear_f8_few_kernel): tokens are M; each byte of W is read
 //     once.  96 x 1152 -> 262144 59 us, 0.87 of the copy rate.
 //   more (linear_f8_pair_kernel): two SMs share 256 x 256 tiles.  Bound by the
 //     way of a block through its accumulator: 4096 x 5376 -> 21504 340 us, 2.8
 //     PFLOP/s.
-// From 65 tokens on the one that is thought to be the fastest is taken.
+// From 33 tokens on the one that is thought to be the fastest is taken (64 x 1152 -> 262144: the first 65 us, the second 59).
 //
 // linear_f8_kernel: a CTA takes a tile of up to 128 rows of W by N tokens.  Stages
 // and hand-overs are of two blocks: a block alone took 0.36 us however small its
@@ -418,7 +418,7 @@ static cudaError_t f8_launch(const LinearF8Args &a, const CUtensorMap &wmap, con
 }
 
 // A tile's height and the CTAs that share its sum, for tiles of n tokens: the least of waves of CTAs times what a CTA takes.
-// A block takes 0.22 us (n = 16; 0.33 for 64), from about 75 rows on more by its bytes, a tile 0.8 us beside (all measured).
+// A block takes 0.22 us (n = 16; 0.33 for 64), from about 75 rows on more by its bytes, a tile 0.8 us (1.2) beside (all measured).
 // 128 rows of W for 21504 are 168 tiles, two waves in the second of which most SMs have nothing: 1 token, 5376 -> 21504
 // takes 26.7 us with them and 22.1 with 72 rows, which fill both; 5376 -> 5376 11.6 with any height that fits one wave.
 struct F8Tiles {
@@ -436,7 +436,7 @@ static F8Tiles f8_plan(const LinearF8Args &a, int n, int sms)
             const int64_t waves = ((a.out + rows - 1) / rows * nt * ctas + sms - 1) / sms;
             if (ctas > 1 && waves > 1) break;
             const double least = 220 + 2.2 * (n - 16), bytes = 130 + 2.1 * (n - 16) + 1.2 * rows;
-            const double time = (double)waves * (((a.nkb + ctas - 1) / ctas) * (bytes > least ? bytes : least) + 800) + (ctas > 1 ? 3000 : 0);
+            const double time = (double)waves * (((a.nkb + ctas - 1) / ctas) * (bytes > least ? bytes : least) + 800 + 8.3 * (n - 16)) + (ctas > 1 ? 3000 : 0);
             if (time < best.time) best = F8Tiles{rows, ctas, time};
         }
     return best;
@@ -839,7 +839,7 @@ static wl_status f8_run_pair(LinearF8Args a, const uint8_t *x, const uint8_t *W,
     return e == cudaSuccess ? WL_OK : cuda_fail(e, "wl_linear_f8 launch");
 }
 
-// ------------------------------------------------------------- 65 to 128 tokens --
+// ------------------------------------------------------------- 33 to 128 tokens --
 // W's bytes are the time, and each is read once: tokens are M (rows of the tile
 // past them hold whatever the ring holds: their sums are not stored), `rows` rows
 // of W are N, chosen so that the tiles fill whole waves of SMs.  A tile so begins
@@ -853,7 +853,7 @@ struct F8Few {
 };
 
 constexpr int kFewThreads = 384;
-constexpr int kFewStages = 11;  // at most: tiles of 64 rows by 72 tokens
+constexpr int kFewStages = 14;  // at most: tiles of 64 rows by 40 tokens
 
 // 32 tokens (t0: the first) by 32 rows of W through the warp's shared memory.
 template <bool F32>
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __g
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-// The tile height for 65 to 128 tokens and what it is thought to take: waves of tiles, a block's and a tile's time as
+// The tile height for 33 to 128 tokens and what it is thought to take: waves of tiles, a block's and a tile's time as
 // measured (96 tokens, 1152 -> 262144: 58.7 us with 256 rows, 65 with 192; 128 tokens, 5376 -> 21504: 26.5 with 192, 42 with 128).
 static double f8_few_plan(int64_t T, int64_t out, int nkb, int sms, F8Few *p)
 {
@@ -1118,7 +1118,7 @@ wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st)
 {
     const LinearF8Args a{x_scale, w_scale, y, T, out, (int)((in + 127) / 128), (int)((out + 127) / 128), 0, 128, 0, 0, di->status};
-    if (T > 64) {
+    if (T > 32) {
         // The least of what the kernels are thought to take: pairs 0.46 us a block and 2.5 us a tile (measured), the others above.
         F8Few p;
         const int64_t pairs = (out + 255) / 256 * ((T + 255) / 256), at_once = di->sm_count / 2;

@@ -283,11 +283,12 @@ __device__ __forceinline__ FF rescaled(const VerPart &a, float top, const VerSha
     return ff_norm(ff_mul(a.s, weight(a.m, top, sh.c, sh.table)));
 }
 
-__device__ __forceinline__ VerPart join(const VerPart &a, const VerShared &sh)  // over the warp
+// Shares of the warp's lanes together: the maximum with its place (greedy) or with the sum.
+__device__ __forceinline__ VerPart join(const VerPart &a, const VerShared &sh)
 {
     const float top = warp_max_nan(a.m);
-    const int first = (int)__reduce_min_sync(0xffffffffu, (unsigned)(a.m == top ? a.idx : 0x7fffffff));
-    return VerPart{top, ff_norm(ff_warp_sum(rescaled(a, top, sh))), first};
+    if (sh.greedy) return VerPart{top, {0.0f, 0.0f}, (int)__reduce_min_sync(0xffffffffu, (unsigned)(a.m == top ? a.idx : 0x7fffffff))};
+    return VerPart{top, ff_norm(ff_warp_sum(rescaled(a, top, sh))), 0};
 }
 
 // The lane's share of a row's maximum and its place (greedy) or sum.
