@@ -593,16 +593,6 @@ __device__ __forceinline__ void f8_store_boxes(const CUtensorMap *map, char *sta
     }
 }
 
-// A warp's 32 tokens (t: the lane's) by 64 rows of W from o0 on.
-__device__ __forceinline__ void f8_store_part(const LinearF8Args &a, const CUtensorMap *map, char *stage, int ydt, int boxes, int64_t t,
-                                              int64_t o0, const uint64_t acc[32])
-{
-    const int lane = threadIdx.x % 32;
-    if (boxes && ydt == WL_OUT_F32) f8_store_boxes<true>(map, stage, t - lane, o0, a.T, a.out, acc);
-    else if (boxes) f8_store_boxes<false>(map, stage, t - lane, o0, a.T, a.out, acc);
-    else if (t < a.T && o0 < a.out) f8_store_row(a.y, ydt, t * a.out + o0, (int)min((int64_t)64, a.out - o0), acc);
-}
-
 // Scales and stores a pair's tiles, 32 tokens by the 128 rows of W of one of its SMs a warp.
 __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUtensorMap &ymap, int ydt, int boxes, char *ring, uint32_t tmem,
                                               uint64_t *tfull, uint64_t *tempty, int rank, int64_t first, int64_t step)
@@ -671,16 +661,18 @@ __device__ __forceinline__ bool f8_pair_tiles(const LinearF8Args &a, const CUten
             f8_scale32(acc + 48, d1, s);
         }
         if (!good) break;
-        // one branch for both halves: with a branch each (f8_store_part) ptxas gave the loop above other registers and 8 % more time
+        // one branch for both halves: with a branch each ptxas gave the loop above other registers and 8 % more time
         if (boxes && ydt == WL_OUT_F32) {
             f8_store_boxes<true>(&ymap, stage, t - lane, o0, a.T, a.out, acc);
             f8_store_boxes<true>(&ymap, stage, t - lane, o0 + 64, a.T, a.out, acc + 32);
         } else if (boxes) {
             f8_store_boxes<false>(&ymap, stage, t - lane, o0, a.T, a.out, acc);
             f8_store_boxes<false>(&ymap, stage, t - lane, o0 + 64, a.T, a.out, acc + 32);
-        } else {
-            f8_store_part(a, &ymap, stage, ydt, 0, t, o0, acc);
-            f8_store_part(a, &ymap, stage, ydt, 0, t, o0 + 64, acc + 32);
+        } else if (t < a.T) {  // rows that are not 16 bytes apart
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (o0 + 64 * h < a.out)
+                    f8_store_row(a.y, ydt, t * a.out + o0 + 64 * h, (int)min((int64_t)64, a.out - o0 - 64 * h), acc + 32 * h);
         }
     }
     return good;
