@@ -497,7 +497,7 @@ wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const
  * child if it is that one; random numbers and draft are not used.
  *     path[b*n ...]: the accepted nodes, node 0 first, then -1;  accepted[b]:
  *     how many (0 where count[b] is 0, with next[b] = -1).
- * t is temperatures[b] (device) or, where that is NULL, temperature.  Logits of
+ * t is temperatures[b] (device) or, where that is NULL, temperature (64 bits: 0.8 is not rounded).  Logits of
  * -infinity are tokens of no weight.  A row with a NaN or +infinity or with no
  * finite logit, or a t that is NaN, ends the path there with next[b] = -1.  Tokens outside
  * [0, vocab) are rejected.  Decisions are those of exact arithmetic where no
@@ -507,7 +507,7 @@ wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const
  */
 wl_status wl_verify(const void *logits, int64_t logits_stride, wl_out_dtype ldt, const void *draft, int64_t draft_stride,
                     wl_out_dtype ddt, const int32_t *tokens, const float *uniforms, const uint64_t *mask,
-                    const int32_t *count, const float *temperatures, float temperature, int64_t batch, int64_t n,
+                    const int32_t *count, const float *temperatures, double temperature, int64_t batch, int64_t n,
                     int64_t vocab, int32_t *path, int32_t *accepted, int32_t *next, void *stream);
 
 /*

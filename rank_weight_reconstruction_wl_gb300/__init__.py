@@ -154,7 +154,7 @@ def lib():
         L.wl_quant_f8.restype = st
         L.wl_linear_f8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, C.c_int, vp]
         L.wl_linear_f8.restype = st
-        L.wl_verify.argtypes = [vp, i64, C.c_int, vp, i64, C.c_int, vp, vp, vp, vp, vp, f32, i64, i64, i64, vp, vp, vp, vp]
+        L.wl_verify.argtypes = [vp, i64, C.c_int, vp, i64, C.c_int, vp, vp, vp, vp, vp, f64, i64, i64, i64, vp, vp, vp, vp]
         L.wl_verify.restype = st
         L.wl_page_plan.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
         L.wl_page_plan.restype = st

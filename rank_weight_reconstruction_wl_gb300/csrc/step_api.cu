@@ -58,7 +58,7 @@ wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const
 
 wl_status wl_verify(const void *logits, int64_t logits_stride, wl_out_dtype ldt, const void *draft, int64_t draft_stride,
                     wl_out_dtype ddt, const int32_t *tokens, const float *uniforms, const uint64_t *mask,
-                    const int32_t *count, const float *temperatures, float temperature, int64_t batch, int64_t n,
+                    const int32_t *count, const float *temperatures, double temperature, int64_t batch, int64_t n,
                     int64_t vocab, int32_t *path, int32_t *accepted, int32_t *next, void *stream)
 {
     clear_error();
@@ -75,7 +75,7 @@ wl_status wl_verify(const void *logits, int64_t logits_stride, wl_out_dtype ldt,
     if (!aligned(tokens, 4) || !aligned(uniforms, 4) || !aligned(mask, 8) || !aligned(count, 4) || !aligned(temperatures, 4) ||
         !aligned(path, 4) || !aligned(accepted, 4) || !aligned(next, 4))
         return fail(WL_ERR_INVALID_ARG, "mask must be 8-byte aligned, the other small tensors 4-byte");
-    if (!temperatures && (!(temperature >= 0.0f) || !isfinite(temperature)))
+    if (!temperatures && (!(temperature >= 0.0) || !isfinite(temperature)))
         return fail(WL_ERR_INVALID_ARG, "temperature must be finite and >= 0");
     wl_status st = WL_OK;
     const DeviceInfo *di = device_info(&st);

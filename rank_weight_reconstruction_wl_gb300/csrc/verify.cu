@@ -9,7 +9,7 @@
 // down its tree, one pass over a row (split over the cluster's warps) per node.
 // Bound by the chain of passes (load, reductions, cluster barrier): 4 us a node
 // for a vocabulary of 262144, 7 where 32 sequences fill the GPU.  Sampling one
-// such token 11 us, 32 drafted trees of 24 68, 16 chains of 8 with draft rows 96.
+// such token 12 us, 32 drafted trees of 24 72, 16 chains of 8 with draft rows 99.
 // Statistics of all rows first and a walk after would read 4 to 10 times the bytes.
 //
 // Decisions.  A random number closer to a border between two tokens than the
@@ -94,7 +94,7 @@ __device__ __forceinline__ FF ff_of(double d)
 }
 
 // 2^((l - m) c), l <= m, right to about 2^-30 of itself; 0 below 2^-100 and where l is -infinity (rows with a NaN do not
-// come here).  h has the table's bits, l is up to 2^-6 of h.
+// come here).
 __device__ __forceinline__ FF weight(float l, float m, FF c, const float *table)
 {
     const float d = l - m, t = d - l;
@@ -111,7 +111,8 @@ __device__ __forceinline__ FF weight(float l, float m, FF c, const float *table)
     const float Th = table[j], Tl = table[32 + j];
     // 2^k by its bits: z's integer part from bit 5 on
     const float s = __int_as_float(((__float_as_int(z) & ~31) << 18) + 0x3f800000);
-    return y > -100.0f ? FF{Th * s, fmaf(Th, g, Tl) * s} : FF{0.0f, 0.0f};
+    const float low = fmaf(Th, g, Tl), h = Th + low;
+    return y > -100.0f ? FF{h * s, (low - (h - Th)) * s} : FF{0.0f, 0.0f};
 }
 
 // max(R - S q, 0)
@@ -389,15 +390,13 @@ __device__ __forceinline__ void each_R(const VerShared &sh, uint4 w, const float
     }
 }
 
-// The sum of a vector's R: what of them is a multiple of 2^-14 adds up without rounding, the rest is below 2^-14.
+// The sum of a vector's R.  Every addition keeps what it rounds off: many light tokens of equal weight would add up the
+// same rounding each.
 template <typename L, bool DRAFT>
 __device__ __forceinline__ FF vec_sum(const VerShared &sh, const uint4 &w, const float *q, int e0, int rejected, int nex)
 {
     FF s{0.0f, 0.0f};
-    each_R<L, DRAFT>(sh, w, q, e0, rejected, nex, [&](int, FF R) {
-        const float h = (R.h + 768.0f) - 768.0f;  // 1.5 * 2^9: its last place is 2^-14
-        s.h += h, s.l += (R.h - h) + R.l;
-    });
+    each_R<L, DRAFT>(sh, w, q, e0, rejected, nex, [&](int, FF R) { s = ff_add(s, R); });
     return s;
 }
 
@@ -597,11 +596,11 @@ __global__ void __launch_bounds__(kVerThreads, 1) verify_kernel(const __grid_con
         }
         if (tid == kMaxTree) {
             const int count = a.count ? min(max(a.count[b], 0), a.n) : a.n;
-            const float t = a.temperatures ? a.temperatures[b] : a.temperature;
-            const FF c = ff_of(1.4426950408889634 / (double)fminf(t, 1e30f));
+            const double t = a.temperatures ? (double)a.temperatures[b] : a.temperature;
+            const FF c = ff_of(1.4426950408889634 / fmin(t, 1e30));
             for (int r = 0; r < ctas; ++r) {
                 VerShared *p = cl.map_shared_rank(&sh, r);
-                p->count = count, p->greedy = t < 1e-6f, p->valid = t == t, p->c = c;
+                p->count = count, p->greedy = t < 1e-6, p->valid = t == t, p->c = c;
             }
         }
     }

@@ -177,7 +177,7 @@ struct VerifyArgs {
     const uint64_t *mask;
     const int32_t *count;
     const float *temperatures;
-    float temperature;
+    double temperature;
     int batch, n, vocab;
     int32_t *path, *accepted, *next;
 };

@@ -56,7 +56,7 @@ def verify(logits, tokens, uniforms, mask=None, count=None, draft=None, temperat
     tk, un = tokens.cpu().numpy(), uniforms.double().cpu().numpy()
     dr = None if draft is None else draft.double().cpu().numpy()
     mk = None if mask is None else mask.cpu().numpy().view(np.uint64)
-    temps = temperature.double().cpu().numpy() if isinstance(temperature, torch.Tensor) else np.full(B, np.float64(np.float32(temperature)))
+    temps = temperature.double().cpu().numpy() if isinstance(temperature, torch.Tensor) else np.full(B, float(temperature))
     V = lg.shape[1]
     path, acc, nxt = np.full((B, n), -1, np.int32), np.zeros(B, np.int32), np.full(B, -1, np.int32)
     for b in range(B):

@@ -247,6 +247,24 @@ def test_verify_draws_on_borders(wl, gpu, V):
     assert acc.tolist() == [2, 1] * (B // 2)
 
 
+def test_verify_takes_the_temperature_as_given(wl, gpu):
+    """0.3 in 64 bits: rounded to fp32 it would move the border of the first token past the draw."""
+    V, t = 3270000, 0.3
+    low = -15.0 * t
+    a = torch.full((1, V), low)
+    a[0, 0] = 0.0
+    low = float(a[0, 1])
+
+    def first(temp):  # the share of token 0
+        return 1.0 / (1.0 + (V - 1) * math.exp(low / temp))
+
+    lo, hi = sorted((first(t), first(float(np.float32(t)))))
+    u = float(np.float32((lo + hi) / 2))
+    assert lo < u < hi
+    _, _, nxt = _check_verify(wl, gpu, a, torch.zeros(1, 1, dtype=torch.int32), torch.tensor([[u]]), temperature=t)
+    assert (nxt[0] == 0) == (u < first(t))
+
+
 def test_verify_draws_outside_the_range(wl, gpu):
     a, t, u, _ = _drafts(6, 2, 300, 2)
     a[:, 290:] = -math.inf
