@@ -8,7 +8,7 @@
 // Both k run over all sequences in order, so the places are prefix sums and
 // every page is moved by a thread of its own.  One cluster: a CTA owns a run of
 // sequences, the CTAs exchange their totals, and cluster barriers stand between
-// the pages given back and those taken.  Bound by latency: three barriers and
+// the pages given back and those taken.  Bound by latency: the barriers and
 // chains of two or three dependent loads; what scales with the work (page
 // moves, slots) is spread over all threads.
 #include <cooperative_groups.h>
@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
     const int b0 = rank * p.per, nb = max(0, min(p.per, a.batch - b0));
+    cluster_arrive();  // waited for before the first store into a peer: until then it may not have begun
     int *back0 = plan_smem, *want0 = back0 + p.per, *need = want0 + p.per, *have = need + p.per;
     pdl_wait();
     const int top = min(max(__ldg(a.top), 0), a.pool);
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         if (i < nb) back0[i] = backs + sb, want0[i] = wants + sw;
         backs += tb, wants += tw;
     }
+    cluster_wait();
     if (threadIdx.x < ctas) {
         int *peer = cl.map_shared_rank(&sums[0][0], threadIdx.x);
         peer[rank] = backs;
