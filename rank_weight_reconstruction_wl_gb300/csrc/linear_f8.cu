@@ -138,6 +138,19 @@ __device__ __forceinline__ bool f8_wait(uint64_t *bar, unsigned parity, unsigned
     return true;
 }
 
+// Waits until every stage that was filled has been handed back; st and phase as for the next item (of a stage that was
+// never filled the first wait's parity passes).  A commit arrives on its barrier by itself some time after the MMAs, in a
+// pair on the peer's too, and this memory is another CTA's once the kernel has ended.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool f8_ring_tail(uint64_t *empty, int stages, uint32_t st, uint32_t phase, unsigned *status)
+{
+    for (int i = 0; i < stages; ++i) {
+        if (!f8_wait<CLUSTER>(&empty[st], phase, status, kWaitRingEmpty)) return false;
+        if (++st == stages) st = 0, phase ^= 1;
+    }
+    return true;
+}
+
 // acc += d * s for two columns.
 __device__ __forceinline__ void fma2(uint64_t &acc, uint32_t d0, uint32_t d1, uint64_t s)
 {
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) linear_f8_kernel(const __grid_c
                 if (++st == a.stages) st = 0, phase ^= 1;
             }
         }
-        if (!good) gave_up = 1;
+        if (!good || !f8_ring_tail(empty, a.stages, st, phase, a.status)) gave_up = 1;
     } else if (warp == 9) {
         const uint32_t ring0 = s32(ring), issuer = f8_elect();
         uint32_t st = 0, st_phase = 0, buf = 0, buf_phase = 1;
@@ -741,7 +754,7 @@ __global__ void __launch_bounds__(F8Pair::THREADS, 1) linear_f8_pair_kernel(cons
                     if (++st == S::NST) st = 0, phase ^= 1;
                 }
             }
-            if (!good) gave_up = 1;
+            if (!good || !f8_ring_tail<true>(empty, S::NST, st, phase, a.status)) gave_up = 1;
         } else if (warp == 9 && rank == 0) {
             // The whole warp walks and waits, one lane issues: code that the compiler knows to be uniform keeps the
             // descriptors in uniform registers (one lane alone took 630 cycles a block for MMAs of 512).
@@ -946,7 +959,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_f8_few_kernel(const __g
                     if (++st == p.stages) st = 0, phase ^= 1;
                 }
             }
-            if (!good) gave_up = 1;
+            if (!good || !f8_ring_tail(empty, p.stages, st, phase, a.status)) gave_up = 1;
         } else if (warp == 9) {
             const uint32_t ring0 = s32(ring), issuer = f8_elect(), idesc = f8_idesc(128, p.rows);
             uint32_t st = 0, st_phase = 0, buf = 0, buf_phase = 1;
