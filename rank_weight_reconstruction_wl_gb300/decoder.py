@@ -14,10 +14,11 @@ A step takes the newest tokens of every sequence: one each (decoding), a
 drafted tree, or up to 64 of a prompt; ``prompt`` feeds longer ones in chunks.
 ``accept`` keeps a root-to-node path of the tree that a step put into the cache.
 With a head, ``logits`` are the step's and ``verify`` decides which drafted tokens
-hold, keeps them and draws the next:
+hold, keeps them and draws the next (node 0 of the next step is in ``next``):
 
     h = dec.step(x, n, mask, depth)            x: embeddings of the drafted tree
     path, accepted, token = dec.verify(dec.logits(h), tokens, uniforms, mask)
+    tokens[:, 0] = dec.next                    ... and drafts behind it
 
 With pool_pages the sequences share that many cache pages instead of owning
 max_len positions each: a step takes the pages that it needs, gives back what the
@@ -57,7 +58,8 @@ class Decoder:
     head: the vocabulary's projection (F8Weight [vocab, hidden]).  pool_pages: how
     many pages the sequences share (None: enough for max_len each); where they
     run out, sequences in order get all that a step needs or take no token in
-    it, and room (int32 [batch], on the GPU) tells how many each took."""
+    it, and room (int32 [batch], on the GPU) tells how many each took.  next
+    (int32 [batch], on the GPU, after verify()): node 0 of the next step."""
 
     def __init__(self, layers: list[LayerTheta], norms: list[BlockNorms], final: torch.Tensor, kv_heads: int, rope: RopeTable | None,
                  batch: int, max_len: int, page_size: int = 64, cache_dtype=torch.float8_e4m3fn, eps: float = 1e-6,
@@ -78,7 +80,7 @@ class Decoder:
         held = batch * per if pool_pages is None else pool_pages
         self.caches = [KVCache.empty(held, kv_heads, page_size, self.dim, cache_dtype, dev) for _ in layers]
         self.len = torch.zeros(batch, dtype=torch.int32, device=dev)
-        self.head, self.pool, self.held, self.room = head, None, None, None
+        self.head, self.pool, self.held, self.room, self.next = head, None, None, None, None
         if pool_pages is None:
             self.pages = torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per).contiguous()
         else:
@@ -171,7 +173,10 @@ class Decoder:
         """Which of the last step's drafted tokens hold (wl_verify: logits
         [batch * n, vocab], tokens and uniforms [batch, n], mask as given to the
         step), counted into the sequences as accept() does; returns (path,
-        accepted, next): next [batch] is node 0 of the next step."""
+        accepted, token) as wl_verify: token is -1 where none was drawn.  self.next
+        is what the next step begins with: the token drawn, or, for a sequence that
+        took no token in the step (its count or room was 0), its node 0 again, which
+        is not in the cache yet; -1 where the model's row had no distribution."""
         if self._drafted is None:
             raise ValueError("verify() needs a step before it")
         n, had = self._drafted[:2]
@@ -179,6 +184,7 @@ class Decoder:
             raise ValueError(f"tokens must be [{self.batch}, {n}] as the step's, got {tuple(tokens.shape)}")
         path, accepted, token = wl_verify(logits, tokens, uniforms, mask, had, draft, temperature)
         self.accept(None if mask is None else path, accepted)  # a chain's path lies as it is
+        self.next = token if had is None else torch.where(had > 0, token, tokens[:, 0])
         return path, accepted, token
 
     def release(self, done: torch.Tensor):

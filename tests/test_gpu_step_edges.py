@@ -5,6 +5,8 @@ import pytest
 import torch
 
 from tests import step_ref as ref
+from tests.test_gpu_decoder import _x
+from tests.test_gpu_decoder_step import _with_head
 
 pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
@@ -39,3 +41,45 @@ def test_plans_of_clusters_on_a_busy_gpu(wl, gpu, B):
             assert got[k][step][0].tolist() == room and np.array_equal(got[k][step][1].cpu().numpy(), slots)
     for k in range(2):
         assert pages[k].tolist() == table and held[k].tolist() == have and pools[k].free[:top].tolist() == free
+
+
+@pytest.mark.parametrize("temp", [0.0, 0.8])
+def test_a_starved_sequence_keeps_its_token(wl, gpu, temp):
+    """A sequence that waits two steps for pages goes on from the token that it had: states and tokens of a decoder whose
+    sequences have pages of their own and sit the same steps out."""
+    few, embed = _with_head(wl, gpu, 5, max_len=64)  # pages of 16: both prompts and one page
+    own, _ = _with_head(wl, gpu, None, max_len=64)
+    x = _x(gpu, 2, 32)
+    h = few.prompt(x)
+    assert torch.equal(h, own.prompt(x))
+    tok = {d: d.logits(h, F32).argmax(-1).to(torch.int32) for d in (few, own)}
+    first = tok[few].tolist()
+    for k in range(6):
+        if k == 2:
+            done = torch.tensor([True, False], device=gpu)
+            few.release(done), own.release(done)
+        live = [1, 0] if k < 2 else [0, 1]
+        count = torch.tensor(live, dtype=torch.int32, device=gpu)
+        u = torch.rand(2, 1, generator=torch.Generator().manual_seed(k)).to(gpu)
+        for d in (few, own):
+            h = d.step(embed[tok[d].long()], 1, count=None if d is few and k < 2 else count)
+            _, acc, token = d.verify(d.logits(h, F32), tok[d][:, None], u, temperature=temp)
+            assert acc.tolist() == live and [t >= 0 for t in token.tolist()] == [v == 1 for v in live]
+            assert d.next.tolist() == [int(token[b]) if live[b] else int(tok[d][b]) for b in range(2)]
+            tok[d] = d.next
+        if k < 2:
+            assert few.room.tolist() == live and int(tok[few][1]) == first[1]
+        assert torch.equal(tok[few], tok[own])
+    assert few.len.tolist() == own.len.tolist() == [0, 36]
+    assert wl.wl_device_status() == wl.WL_OK
+
+
+def test_next_without_and_with_a_distribution(wl, gpu):
+    """next is the token drawn where all sequences take part, and -1 where a row has no distribution."""
+    dec, embed = _with_head(wl, gpu)
+    h = dec.step(_x(gpu, 2, 1).view(2, -1), 1)
+    logits = dec.logits(h, F32)
+    logits[1, 7] = float("nan")
+    tokens = torch.tensor([[3], [4]], dtype=torch.int32, device=gpu)
+    _, acc, token = dec.verify(logits, tokens, torch.zeros(2, 1, device=gpu), temperature=0.0)
+    assert acc.tolist() == [1, 1] and token.tolist() == dec.next.tolist() == [int(logits[0].argmax()), -1]
