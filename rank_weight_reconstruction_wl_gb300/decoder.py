@@ -57,8 +57,9 @@ class Decoder:
     the GPU) holds the lengths; beside accept(), write to it only to lower them.
     head: the vocabulary's projection (F8Weight [vocab, hidden]).  pool_pages: how
     many pages the sequences share (None: enough for max_len each); where they
-    run out, sequences in order get all that a step needs or take no token in
-    it, and room (int32 [batch], on the GPU) tells how many each took.  next
+    run out, sequences in order get all the pages that a step needs or none, and
+    take the first room[b] tokens (nodes) of the step: those for which there is
+    space, in the last page that they have too; room is int32 [batch], on the GPU.  next
     (int32 [batch], on the GPU, after verify()): node 0 of the next step."""
 
     def __init__(self, layers: list[LayerTheta], norms: list[BlockNorms], final: torch.Tensor, kv_heads: int, rope: RopeTable | None,

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import step_ref as ref
-from tests.test_gpu_decoder import _x
+from tests.test_gpu_decoder import _near, _x
 from tests.test_gpu_decoder_step import _with_head
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +83,40 @@ def test_next_without_and_with_a_distribution(wl, gpu):
     tokens = torch.tensor([[3], [4]], dtype=torch.int32, device=gpu)
     _, acc, token = dec.verify(logits, tokens, torch.zeros(2, 1, device=gpu), temperature=0.0)
     assert acc.tolist() == [1, 1] and token.tolist() == dec.next.tolist() == [int(logits[0].argmax()), -1]
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_step_fills_the_last_page_where_there_are_no_more(wl, gpu, tree):
+    """A sequence of 30 in pages of 16, none left: a step of 5 takes its first two nodes, the next step none; once there is a
+    page the sequence goes on as one that took the same tokens in a prompt."""
+    dec, embed = _with_head(wl, gpu, 3, batch=1, max_len=64)
+    ids = torch.randint(0, 500, (1, 30), generator=torch.Generator().manual_seed(1)).to(gpu)
+    h = dec.prompt(embed[ids])
+    dec.pool.top -= 1  # the last page is somebody else's for now
+    assert int(dec.pool.top) == 0
+    tok = int(dec.logits(h, F32).argmax())
+    mask = depth = None
+    if tree:  # 1, 2 and 3 follow the root, 4 follows 1
+        mask = torch.tensor([[1, 3, 5, 9, 19]], device=gpu)
+        depth = torch.tensor([[0, 1, 1, 1, 2]], dtype=torch.int32, device=gpu)
+    tokens = torch.tensor([[tok, 7, 8, 9, 10]], dtype=torch.int32, device=gpu)
+    h = dec.step(embed[tokens[0].long()], 5, mask, depth)
+    assert dec.room.tolist() == [2]
+    logits = dec.logits(h, F32)
+    logits[0, 7] = 1e4  # node 1 is the likeliest, and so would be nodes 2 and 4 behind it, which are not there
+    logits[1:, 8:11] = 1e4
+    path, acc, token = dec.verify(logits, tokens, torch.zeros(1, 5, device=gpu), mask=mask, temperature=0.0)
+    assert path.tolist() == [[0, 1, -1, -1, -1]] and acc.tolist() == [2] and token.tolist() == dec.next.tolist() == [8]
+    assert dec.len.tolist() == [32] and dec.held.tolist() == [2]
+    h = dec.step(embed[dec.next.long()], 1)
+    assert dec.room.tolist() == [0]
+    _, acc, token = dec.verify(dec.logits(h, F32), dec.next[:, None], torch.zeros(1, 1, device=gpu))
+    assert acc.tolist() == [0] and token.tolist() == [-1] and dec.next.tolist() == [8] and dec.len.tolist() == [32]
+    dec.pool.top += 1
+    h = dec.step(embed[dec.next.long()], 1)
+    assert dec.room.tolist() == [1]
+    whole, _ = _with_head(wl, gpu, None, batch=1)
+    text = ids[0].tolist() + [tok, 7, 8]
+    # the same text, fed in other steps: up to the projections' accumulation order, as the decoder's other tests
+    _near(h[0], whole.prompt(embed[torch.tensor([text], device=gpu)])[0], 0.1, "states")
+    assert wl.wl_device_status() == wl.WL_OK
