@@ -134,7 +134,7 @@ class Decoder:
             m = wl_mlp_geglu_fused(h, th.gate, th.up, th.down)
             pre = self.norms[l + 1].attn_pre if l + 1 < len(self.layers) else self.final
             x, h = wl_norm_residual(m, x, w_post=nm.mlp_post, w_pre=pre, **norm)
-        self._drafted = (n, count, positions, kept)
+        self._drafted = (n, count, positions, kept, mask)
         return h
 
     def accept(self, path: torch.Tensor | None = None, count: torch.Tensor | None = None):
@@ -145,7 +145,7 @@ class Decoder:
         again at the positions that follow len."""
         if self._drafted is None:
             raise ValueError("accept() needs a step before it")
-        n, had, positions, kept = self._drafted
+        n, had, positions, kept, _ = self._drafted
         m = n if path is None else int(path.shape[-1])
         if path is not None and (tuple(path.shape) != (self.batch, m) or not 1 <= m <= n):
             raise ValueError(f"path must be [{self.batch}, 1..{n}], got {tuple(path.shape)}")
@@ -172,8 +172,8 @@ class Decoder:
     def verify(self, logits: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor, mask: torch.Tensor | None = None,
                draft: torch.Tensor | None = None, temperature=1.0):
         """Which of the last step's drafted tokens hold (wl_verify: logits
-        [batch * n, vocab], tokens and uniforms [batch, n], mask as given to the
-        step), counted into the sequences as accept() does; returns (path,
+        [batch * n, vocab], tokens and uniforms [batch, n]; mask: the step's, where
+        it is not given), counted into the sequences as accept() does; returns (path,
         accepted, token) as wl_verify: token is -1 where none was drawn.  self.next
         is what the next step begins with: the token drawn, or, for a sequence that
         took no token in the step (its count or room was 0), its node 0 again, which
@@ -183,6 +183,8 @@ class Decoder:
         n, had = self._drafted[:2]
         if tuple(tokens.shape) != (self.batch, n):
             raise ValueError(f"tokens must be [{self.batch}, {n}] as the step's, got {tuple(tokens.shape)}")
+        if mask is None:
+            mask = self._drafted[4]
         path, accepted, token = wl_verify(logits, tokens, uniforms, mask, had, draft, temperature)
         self.accept(None if mask is None else path, accepted)  # a chain's path lies as it is
         self.next = token if had is None else torch.where(had > 0, token, tokens[:, 0])

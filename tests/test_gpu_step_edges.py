@@ -120,3 +120,19 @@ def test_a_step_fills_the_last_page_where_there_are_no_more(wl, gpu, tree):
     # the same text, fed in other steps: up to the projections' accumulation order, as the decoder's other tests
     _near(h[0], whole.prompt(embed[torch.tensor([text], device=gpu)])[0], 0.1, "states")
     assert wl.wl_device_status() == wl.WL_OK
+
+
+def test_verify_takes_the_mask_of_its_step(wl, gpu):
+    """A tree verified without a mask is the step's tree, not a chain."""
+    mask = torch.tensor([[1, 3, 5]] * 2, device=gpu)  # two children of the root
+    depth = torch.tensor([[0, 1, 1]] * 2, dtype=torch.int32, device=gpu)
+    tokens = torch.tensor([[1, 2, 3]] * 2, dtype=torch.int32, device=gpu)
+    found = []
+    for given in (mask, None):
+        dec, embed = _with_head(wl, gpu)
+        h = dec.step(embed[tokens.view(-1).long()], 3, mask, depth)
+        logits = dec.logits(h, F32)
+        logits[0::3, 3] = 1e4  # the second child
+        got = dec.verify(logits, tokens, torch.zeros(2, 3, device=gpu), mask=given, temperature=0.0)
+        found.append([t.tolist() for t in got] + [dec.len.tolist(), dec.step(embed[got[2].long()], 1).tolist()])
+    assert found[0] == found[1] and found[0][0] == [[0, 2, -1]] * 2
