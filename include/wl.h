@@ -501,7 +501,7 @@ wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const
  * -infinity are tokens of no weight.  A row with a NaN or +infinity or with no
  * finite logit, or a t that is NaN, ends the path there with next[b] = -1.  Tokens outside
  * [0, vocab) are rejected.  Decisions are those of exact arithmetic where no
- * border lies within 2^-29 of the row's sum.
+ * border lies within 2^-29 of the sum of the row's w, after rejections too.
  * Limits: 1 <= batch <= 65536, 1 <= n <= 64, 1 <= vocab <= 2^24; strides at
  * least vocab.
  */

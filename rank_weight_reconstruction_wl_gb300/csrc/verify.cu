@@ -15,8 +15,17 @@
 // Decisions.  A random number closer to a border between two tokens than the
 // sums' rounding would give another token than exact arithmetic does, and a
 // vocabulary has 10^5 borders.  So the sums that decide are made of weights held
-// as two floats (about 2^-30 of each weight), and the sums of the fast pass
-// decide only where their error (a few 10^-6 of the row's sum) cannot matter.
+// as two floats (two_float.h), and the sums of the fast pass decide only where
+// their error (a few 10^-6 of the row's sum) cannot matter.
+//
+// How near a border may be.  Weights and sums are off by e = 2^-36 of themselves
+// (weights below 2^-32 by more, but all of them weigh 2^-8 at most).  A border
+// among plain weights moves by 2 u (1 - u) e of the row's sum S: what is off by
+// the same on both sides cancels.  After j rejections against q a token has
+// w_i - q_i (S_0 + ... + S_{j-1}).  Let A_j be the error of that sum: S_j, the
+// sum over the tokens left, is off by D - Q A_j, |D| <= e S, Q <= 1 their mass in
+// q, so A_{j+1} = (1 - Q) A_j + D, |A_j| <= j e S, and the errors of all R add up
+// to (j + 1) e S at most: 2^-30 of S for 63 rejections.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -24,6 +33,7 @@
 
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
+#include "two_float.h"
 
 namespace cg = cooperative_groups;
 
@@ -36,95 +46,6 @@ constexpr float kTolSum = 6e-7f, kTolBit = 1.3e-7f;
 // A fast sum is right to kTolSum + kTolBit log2(vocab) of the row's sum: 2^-22 for ex2, three roundings of 2^-24 in a
 // vector's sum, and three of y = (l - max) c, each |y| 2^-24 ln2 of the weight, whose sum over the row is at most
 // log2(vocab) 2^-24 ln2 of its sum (the entropy of the weights is at most log2(vocab)).
-
-// 2^(j/32) as two floats, in two tables: 32 entries of 4 bytes are 32 banks, so that lanes never collide (128 pairs of
-// floats took six accesses a warp).
-__constant__ float kExp2High[32] = {
-    0x1.0p+0f, 0x1.059b0ep+0f, 0x1.0b5586p+0f, 0x1.11301ep+0f, 0x1.172b84p+0f, 0x1.1d4874p+0f,
-    0x1.2387a6p+0f, 0x1.29e9ep+0f, 0x1.306fep+0f, 0x1.371a74p+0f, 0x1.3dea64p+0f, 0x1.44e086p+0f,
-    0x1.4bfdaep+0f, 0x1.5342b6p+0f, 0x1.5ab07ep+0f, 0x1.6247ecp+0f, 0x1.6a09e6p+0f, 0x1.71f75ep+0f,
-    0x1.7a1148p+0f, 0x1.82589ap+0f, 0x1.8ace54p+0f, 0x1.93737cp+0f, 0x1.9c4918p+0f, 0x1.a5503cp+0f,
-    0x1.ae89fap+0f, 0x1.b7f77p+0f, 0x1.c199bep+0f, 0x1.cb720ep+0f, 0x1.d5818ep+0f, 0x1.dfc974p+0f,
-    0x1.ea4afap+0f, 0x1.f50766p+0f};
-__constant__ float kExp2Low[32] = {
-    0x0.0p+0f, -0x1.9d4f52p-25f, 0x1.9f3122p-25f, -0x1.fdb496p-25f, -0x1.c15742p-27f, -0x1.d2e8cap-25f,
-    0x1.ceac48p-25f, -0x1.5c0424p-25f, 0x1.4636e2p-25f, -0x1.18aac6p-25f, 0x1.824684p-25f, 0x1.8624b4p-30f,
-    -0x1.593abcp-25f, -0x1.2c561p-25f, -0x1.5bd5ecp-27f, -0x1.f8b55p-25f, 0x1.9fcef4p-26f, 0x1.1d8beep-25f,
-    -0x1.829fdp-25f, -0x1.accc7cp-26f, 0x1.15506ep-27f, -0x1.e64744p-25f, 0x1.51f848p-27f, -0x1.b83b54p-25f,
-    -0x1.a94b14p-26f, -0x1.a09438p-25f, -0x1.3d56b2p-27f, -0x1.8837ccp-27f, -0x1.822dbcp-27f, -0x1.908c94p-25f,
-    0x1.52486cp-27f, -0x1.246ebp-26f};
-
-// ------------------------------------------------------------ two floats --
-struct FF {
-    float h, l;
-};
-
-__device__ __forceinline__ FF ff_add(FF a, FF b)
-{
-    const float s = a.h + b.h, t = s - a.h;
-    const float e = (a.h - (s - t)) + (b.h - t);  // Knuth's two-sum: exact
-    return FF{s, e + (a.l + b.l)};
-}
-
-// The same with l below half a step of h, so that two of them compare by h, then l.
-__device__ __forceinline__ FF ff_norm(FF a)
-{
-    const float s = a.h + a.l;
-    return FF{s, a.l - (s - a.h)};
-}
-__device__ __forceinline__ FF ff_mul(FF a, float f)
-{
-    const float p = a.h * f;
-    return ff_norm(FF{p, fmaf(a.h, f, -p) + a.l * f});
-}
-__device__ __forceinline__ bool ff_less(FF a, FF b)  // false where one is NaN
-{
-    return a.h < b.h || (a.h == b.h && a.l < b.l);
-}
-__device__ __forceinline__ FF ff_mul(FF a, FF b)
-{
-    const float p = a.h * b.h;
-    return FF{p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h)};
-}
-__device__ __forceinline__ double ff_double(FF a) { return (double)a.h + (double)a.l; }
-__device__ __forceinline__ FF ff_of(double d)
-{
-    const float h = (float)d;
-    return FF{h, (float)(d - (double)h)};
-}
-
-// 2^((l - m) c), l <= m, right to about 2^-30 of itself; 0 below 2^-100 and where l is -infinity (rows with a NaN do not
-// come here).
-__device__ __forceinline__ FF weight(float l, float m, FF c, const float *table)
-{
-    const float d = l - m, t = d - l;
-    const float dl = (l - (d - t)) - (m + t);  // what d has lost
-    const float y = fmaxf(d * c.h, -128.0f);
-    const float yl = fmaf(dl, c.h, fmaf(d, c.l, fmaf(d, c.h, -y)));
-    // y + yl = k/32 + f, |f| <= 1/64
-    const float magic = 12582912.0f;  // 1.5 * 2^23
-    const float z = fmaf(y, 32.0f, magic);
-    const float f = fmaf(z - magic, -0.03125f, y) + yl;
-    // 2^f - 1 = f ln2 + (f ln2)^2 / 2 + (f ln2)^3 / 6 + (f ln2)^4 / 24, the next term below 2^-39
-    const float g = f * fmaf(f, fmaf(f, fmaf(f, 0x1.3b2ab6p-7f, 0x1.c6b08ep-5f), 0x1.ebfbep-3f), 0x1.62e43p-1f);
-    const int j = __float_as_int(z) & 31;
-    const float Th = table[j], Tl = table[32 + j];
-    // 2^k by its bits: z's integer part from bit 5 on
-    const float s = __int_as_float(((__float_as_int(z) & ~31) << 18) + 0x3f800000);
-    const float low = fmaf(Th, g, Tl), h = Th + low;
-    return y > -100.0f ? FF{h * s, (low - (h - Th)) * s} : FF{0.0f, 0.0f};
-}
-
-// max(R - S q, 0)
-__device__ __forceinline__ FF residual(FF R, float q, FF S)
-{
-    const float p = q * S.h;
-    const float pl = fmaf(q, S.h, -p) + q * S.l;
-    const float s = R.h - p, t = s - R.h;
-    const float e = (R.h - (s - t)) - (p + t) + (R.l - pl);
-    const float h = s + e;
-    return h > 0.0f ? FF{h, e - (h - s)} : FF{0.0f, 0.0f};
-}
 
 // --------------------------------------------------------------- helpers --
 __device__ __forceinline__ float ex2(float x)
@@ -423,7 +344,7 @@ __device__ __noinline__ void sum_pass(VerShared &sh, cg::cluster_group &cl, cons
             for (int i = 0; i < E; ++i) q[i] = qa[i];
             load_at<Q, E>(qrow, r.vecs.first(v + 32), vocab, qa);
         }
-        acc = ff_add(acc, vec_sum<L, DRAFT>(sh, raw, q, r.vecs.first(v), rejected, nex));
+        acc = ff_sum(acc, vec_sum<L, DRAFT>(sh, raw, q, r.vecs.first(v), rejected, nex));
     }
     acc = ff_norm(ff_warp_sum(acc));
     if (lane == 0) sh.warp_total[warp] = acc;

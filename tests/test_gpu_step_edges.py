@@ -136,3 +136,91 @@ def test_verify_takes_the_mask_of_its_step(wl, gpu):
         got = dec.verify(logits, tokens, torch.zeros(2, 3, device=gpu), mask=given, temperature=0.0)
         found.append([t.tolist() for t in got] + [dec.len.tolist(), dec.step(embed[got[2].long()], 1).tolist()])
     assert found[0] == found[1] and found[0][0] == [[0, 2, -1]] * 2
+
+
+def _near_borders(V, B, seed):
+    """Stars of five children of which the first b % 5 are rejected against a draft distribution; then the next child's draw, or
+    the next token's, lies beside a border, as near as fp32 goes, but 2^-29 of the row's sum at least.  Returns the arguments, what
+    follows in 64 bits (accepted node or 0, next token) and how near each sequence comes to any border."""
+    rs = np.random.RandomState(seed)
+    n, t = 6, 0.8
+    mask = np.array([[1 | 1 << i for i in range(n)]] * B, np.int64)
+    logits = (2 * rs.randn(B * n, V)).astype(np.float32)
+    draft = np.zeros((B * n, V), np.float32)
+    tokens, draws, count = np.zeros((B, n), np.int32), np.full((B, n), 0.5, np.float32), np.zeros(B, np.int32)
+    want, near = [], []
+
+    def beside(x, ok):
+        """An fp32 number in (0, 1) beside x, on a random side, the nearest of a series of growing steps for which ok."""
+        side = 1 if rs.rand() < 0.5 else -1
+        for k in range(120):
+            v = np.float32(x + side * np.spacing(np.float32(x)) * 1.15 ** k)
+            if (float(v) - x) * side > 0 and 0 < v < 1 and ok(float(v)):
+                return v
+        return None
+
+    for b in range(B):
+        z = logits[b * n].astype(np.float64)
+        w = np.exp((z - z.max()) / t)
+        p = np.exp(z + 0.7 * rs.randn(V))
+        q32 = (p / p.sum()).astype(np.float32)
+        draft[b * n] = q32
+        q = q32.astype(np.float64)
+        S0, R, least, got = w.sum(), w.copy(), np.inf, 0
+        test_child = b % 2 == 0
+        c = 1
+        for _ in range(b % 5):
+            S = R.sum()
+            odds = R / (q * S)
+            can = np.nonzero(odds < 0.97)[0]
+            if len(can) == 0 or np.maximum(R - S * q, 0.0).sum() < 1e-3 * S0:
+                break  # none can be rejected, or little would be left
+            k = rs.choice(can)
+            tokens[b, c], draws[b, c] = k, np.float32(0.5 * (odds[k] + 1))
+            least = min(least, abs(float(draws[b, c]) * q[k] * S - R[k]) / S0)
+            R = np.maximum(R - S * q, 0.0)
+            c += 1
+        S = R.sum()
+        odds = R / (q * S)
+        can = np.nonzero((odds > 0.01) & (odds < 0.99))[0]
+        test_child = test_child and len(can) > 0
+        if test_child:
+            k = can[np.argsort(-q[can])[rs.randint(min(5, len(can)))]]  # of the likelier ones: the others' borders are far from fp32's numbers
+            r = beside(odds[k], lambda v: abs(v * q[k] * S - R[k]) >= 2.0 ** -29 * S0)
+            r = np.float32(0.5 * odds[k]) if r is None else r
+            tokens[b, c], draws[b, c] = k, r
+            least = min(least, abs(float(r) * q[k] * S - R[k]) / S0)
+            if float(r) * q[k] * S < R[k]:
+                got = c
+                z = logits[b * n + c].astype(np.float64)
+                R = np.exp((z - z.max()) / t)
+            else:
+                R = np.maximum(R - S * q, 0.0)
+            c += 1
+        P, S = np.cumsum(R), R.sum()
+        scale = P[-1] if got else S0
+        can = np.nonzero((R > 0.1 * S / V) & (P < 0.999 * S))[0]
+        u = None
+        if not test_child and len(can) > 0:
+            u = beside(P[rs.choice(can)] / S, lambda v: np.abs(P - v * S).min() >= 2.0 ** -29 * scale)
+        if u is None:
+            i = int(np.argmax(R))
+            u = np.float32((P[i] - 0.5 * R[i]) / S)
+        draws[b, 0], count[b] = u, c
+        least = min(least, np.abs(P - float(u) * S).min() / scale)
+        want.append((got, int(np.nonzero((R > 0) & (P > float(u) * S))[0][0])))
+        near.append(least)
+    args = [torch.from_numpy(a) for a in (logits, tokens, draws, mask, count, draft)]
+    return args, want, np.array(near)
+
+
+@pytest.mark.parametrize("V,B", [(6, 1000), (40, 2000), (9001, 300)])
+def test_decisions_beside_borders_after_rejections(wl, gpu, V, B):
+    """Decisions are those of exact arithmetic where no border lies within 2^-29 of the row's sum, after rejections too."""
+    (logits, tokens, draws, mask, count, draft), want, near = _near_borders(V, B, V)
+    assert near.min() >= 2.0 ** -29 and (near < 2.0 ** -25).sum() > B // 8
+    path, acc, nxt = wl.wl_verify(logits.to(gpu), tokens.to(gpu), draws.to(gpu), mask=mask.to(gpu), count=count.to(gpu), draft=draft.to(gpu),
+                                  temperature=0.8)
+    got = [(int(p[1]) if a == 2 else 0, t) for p, a, t in zip(path.tolist(), acc.tolist(), nxt.tolist())]
+    wrong = [b for b in range(B) if got[b] != want[b]]
+    assert not wrong, [(b, got[b], want[b], np.log2(near[b])) for b in wrong[:5]]
