@@ -467,7 +467,9 @@ wl_status wl_quant_f8(const void *x, int64_t x_stride, wl_out_dtype xdt, int64_t
  * block b} W[o,i] x[t,i], x [T, in] and W [out, in] e4m3 codes, x_scale
  * [ceil(in/128), T] and w_scale [ceil(in/128), ceil(out/128)] any fp32, y [T,
  * out] of type ydt.  Products of a block are summed by the tensor cores (fp32),
- * blocks are scaled and summed in fp32, and a result is rounded once.
+ * blocks are scaled and summed in fp32, and a result is rounded once.  A block is
+ * scaled by the product of its two scales rounded to fp32: one past fp32's range
+ * is an infinity (a block's sum of 0 times it NaN), one below 2^-126 has fewer bits.
  * Limits: 1 <= T, out <= 2^30; in a multiple of 16, 16 <= in <= 2^20; x, W and
  * y 16-byte aligned.
  */

@@ -7,6 +7,7 @@ import torch
 from tests import step_ref as ref
 from tests.test_gpu_decoder import _near, _x
 from tests.test_gpu_decoder_step import _with_head
+from tests.test_gpu_step_ops import _factors
 
 pytestmark = pytest.mark.gpu
 BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
@@ -224,3 +225,32 @@ def test_decisions_beside_borders_after_rejections(wl, gpu, V, B):
     got = [(int(p[1]) if a == 2 else 0, t) for p, a, t in zip(path.tolist(), acc.tolist(), nxt.tolist())]
     wrong = [b for b in range(B) if got[b] != want[b]]
     assert not wrong, [(b, got[b], want[b], np.log2(near[b])) for b in wrong[:5]]
+
+
+@pytest.mark.parametrize("T,inner,out", [(3, 272, 130), (20, 1152, 9741), (100, 272, 20008), (300, 400, 1000)])
+def test_products_of_scales_at_the_ends_of_fp32(wl, gpu, T, inner, out):
+    """A block is scaled by the product of its scales rounded to fp32: subnormal, zero or infinite where that is."""
+    x, xs, w, ws = _factors(T, inner, out, T)
+    kb = xs.shape[0]
+    xs[:, 0], ws[:, 0] = 2.0 ** -126, 3e-4  # subnormal, 13 bits
+    xs[0, 1] = 2.0 ** -149  # 0 with ws
+    ws[kb - 1] *= 2.0 ** 40
+    xs[kb - 1, 2] = 2.0 ** 120  # infinite
+    y = wl.wl_linear_f8(x.to(gpu), xs.to(gpu), wl.F8Weight(w.to(gpu), ws.to(gpu)), ydt=F32).double().cpu().numpy()
+    want, mag = np.zeros((T, out)), np.zeros((T, out))
+    with np.errstate(over="ignore", invalid="ignore"):
+        for k in range(kb):
+            at = slice(128 * k, 128 * (k + 1))
+            scale = (xs[k].numpy()[:, None] * np.repeat(ws[k].numpy(), 128)[None, :out]).astype(np.float64)  # rounded to fp32
+            a, b = x[:, at].double().numpy(), w[:, at].double().numpy()
+            want += (a @ b.T) * scale
+            mag += (np.abs(a) @ np.abs(b).T) * scale
+    assert np.isinf(mag[2]).all() and np.isfinite(np.delete(mag, 2, 0)).all()
+    assert not np.isfinite(y[2]).any()
+    live = np.ones(T, bool)
+    live[2] = False
+    # as the other products, and fp32's subnormal step for each block and the result
+    tol = (128 * 2.0 ** -23 + (kb + 2) * 2.0 ** -23) * mag + 2.0 ** -24 * np.abs(want) + (kb + 1) * 2.0 ** -149
+    assert (np.abs(y[live] - want[live]) <= tol[live]).all()
+    assert y[0, :128].any()
+    assert wl.wl_device_status() == wl.WL_OK
