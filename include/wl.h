@@ -499,7 +499,8 @@ wl_status wl_linear_f8(const void *x, const float *x_scale, const void *W, const
  * child if it is that one; random numbers and draft are not used.
  *     path[b*n ...]: the accepted nodes, node 0 first, then -1;  accepted[b]:
  *     how many (0 where count[b] is 0, with next[b] = -1).
- * t is temperatures[b] (device) or, where that is NULL, temperature (64 bits: 0.8 is not rounded).  Logits of
+ * t is temperatures[b] (device) or, where that is NULL, temperature (64 bits: 0.8 is not rounded); above 1e30 it counts as
+ * 1e30, so that an infinite one leaves masks of fp32's lowest value masks.  Logits of
  * -infinity are tokens of no weight.  A row with a NaN or +infinity or with no
  * finite logit, or a t that is NaN, ends the path there with next[b] = -1.  Tokens outside
  * [0, vocab) are rejected.  Decisions are those of exact arithmetic where no

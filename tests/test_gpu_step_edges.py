@@ -254,3 +254,15 @@ def test_products_of_scales_at_the_ends_of_fp32(wl, gpu, T, inner, out):
     assert (np.abs(y[live] - want[live]) <= tol[live]).all()
     assert y[0, :128].any()
     assert wl.wl_device_status() == wl.WL_OK
+
+
+def test_an_infinite_temperature_keeps_masks_of_the_lowest_value(wl, gpu):
+    """A temperature counts as 1e30 at most: what is masked by fp32's lowest value has no weight, the rest is as good as equal."""
+    V, B = 300, 16
+    a = torch.full((B, V), torch.finfo(F32).min)
+    a[:, 40:104] = torch.linspace(-3, 3, 64)
+    u = ((torch.arange(B) + 0.5) / B)[:, None].float()
+    temp = torch.full((B,), float("inf"))
+    temp[1::2] = 3e38
+    _, _, nxt = wl.wl_verify(a.to(gpu), torch.zeros(B, 1, dtype=torch.int32, device=gpu), u.to(gpu), temperature=temp.to(gpu))
+    assert nxt.tolist() == [40 + int(64 * (b + 0.5) / B) for b in range(B)]
