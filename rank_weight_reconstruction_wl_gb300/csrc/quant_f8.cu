@@ -126,13 +126,14 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
 }
 
 wl_status launch_quant_f8(const void *x, int64_t x_stride, int xdt, int64_t rows, int64_t in, int64_t group, uint8_t *codes,
-                          float *scales, cudaStream_t st)
+                          float *scales, const DeviceInfo *di, cudaStream_t st)
 {
     QuantArgs a{x, x_stride, rows, codes, scales, (int)in, (int)((in + 127) / 128), 1, fast_div((in + 127) / 128)};
     cudaError_t e;
     if (group == 1) {
         // rows of a CTA: up to 8, so that their scales, neighbours in memory, are written together, while 8 CTAs an SM are left
-        a.rows_per_cta = (int)(rows >= 8 * 1216 ? 8 : rows >= 2432 ? rows / 1216 : 1);
+        const int64_t most = rows / (8 * di->sm_count);
+        a.rows_per_cta = (int)(most < 1 ? 1 : most > 8 ? 8 : most);
         const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta));
         e = xdt == WL_OUT_F32 ? launch_dependent(quant_rows_kernel<float>, grid, 256, 0, st, a)
                               : launch_dependent(quant_rows_kernel<bf16>, grid, 256, 0, st, a);

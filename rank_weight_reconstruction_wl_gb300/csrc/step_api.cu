@@ -32,8 +32,9 @@ wl_status wl_quant_f8(const void *x, int64_t x_stride, wl_out_dtype xdt, int64_t
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
         return fail(WL_ERR_INVALID_ARG, "x and codes must be 16-byte aligned, scales 4-byte");
     wl_status st = WL_OK;
-    if (!device_info(&st)) return st;
-    return launch_quant_f8(x, x_stride, xdt, rows, in, group, static_cast<uint8_t *>(codes), scales,
+    const DeviceInfo *di = device_info(&st);
+    if (!di) return st;
+    return launch_quant_f8(x, x_stride, xdt, rows, in, group, static_cast<uint8_t *>(codes), scales, di,
                            static_cast<cudaStream_t>(stream));
 }
 

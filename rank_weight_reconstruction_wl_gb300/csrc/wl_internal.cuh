@@ -166,7 +166,7 @@ wl_status launch_norm_residual(const void *y, const void *gate, int64_t gate_str
 
 // Operators between a step's last states and the next step (quant_f8.cu, linear_f8.cu, verify.cu, page_plan.cu)
 wl_status launch_quant_f8(const void *x, int64_t x_stride, int xdt, int64_t rows, int64_t in, int64_t group, uint8_t *codes,
-                          float *scales, cudaStream_t st);
+                          float *scales, const DeviceInfo *di, cudaStream_t st);
 wl_status launch_linear_f8(const uint8_t *x, const float *x_scale, const uint8_t *W, const float *w_scale, void *y, int64_t T,
                            int64_t in, int64_t out, int ydt, const DeviceInfo *di, cudaStream_t st);
 struct VerifyArgs {
