@@ -946,7 +946,9 @@ def wl_verify(logits, tokens, uniforms, mask=None, count=None, draft=None, tempe
     token.  draft [batch * n, vocab] bf16 or fp32: row b * n + u is the
     distribution that node u's children were drawn from; None: they are certain
     (a drafter's best tokens).  temperature: a number or fp32 [batch]; below 1e-6
-    the most likely token is taken.  n = 1 is plain sampling."""
+    the most likely token is taken.  n = 1 is plain sampling.  next is -1, no
+    token, where count is 0 (node 0 then still waits, accepted is 0) and where the
+    last accepted node's row has no distribution (a NaN, +infinity, all masked)."""
     if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
         raise ValueError("tokens must be a tensor [batch, n]")
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:

@@ -16,8 +16,8 @@
 //   up to 128 tokens (linear_f8_few_kernel): tokens are M; each byte of W is read
 //     once.  96 x 1152 -> 262144 59 us, 0.87 of the copy rate.
 //   more (linear_f8_pair_kernel): two SMs share 256 x 256 tiles.  Bound by the
-//     way of a block through its accumulator: 4096 x 5376 -> 21504 340 us, 2.8
-//     PFLOP/s.
+//     way of a block through its accumulator: 4096 x 5376 -> 21504 369 us, 2.6
+//     PFLOP/s (340 to 360 in replays of a graph, by the box).
 // From 33 tokens on the one that is thought to be the fastest is taken (64 x 1152 -> 262144: the first 65 us, the second 59).
 //
 // linear_f8_kernel: a CTA takes a tile of up to 128 rows of W by N tokens.  Stages

@@ -3,9 +3,12 @@
 //
 //     e = smallest integer >= -126 with max|block| <= 448 * 2^e,  code = e4m3(x / 2^e)
 //
-// Bound by bytes: x is read once, a code and 1/32 byte of scale written per
-// element; a block is kept in registers between its maximum and its codes.  4096
-// rows of 5376 bf16: 13.7 us, 4.9 TB/s, 0.72 of the copy rate.
+// x is read once, a code and 1/32 byte of scale written per element; a block is
+// kept in registers between its maximum and its codes.  4096 rows of 5376: fp32
+// 17.3 us, 0.94 of the copy rate; bf16 12.9 us, 0.76, as the instructions of an
+// element are the same for half of the bytes.  Blocks of 128 x 128 of 262144 x
+// 1152: fp32 231 us, 0.97; bf16 225 us, 0.59: a CTA's loads, reduction and stores
+// follow one another, and two CTAs an SM (99 registers) hide too little of it.
 #include "cache_row.cuh"
 #include "dec_ptx.cuh"
 

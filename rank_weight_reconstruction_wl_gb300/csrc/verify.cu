@@ -9,8 +9,11 @@
 // down its tree, one pass over a row (split over the cluster's warps) per node.
 // Bound by the chain of passes (load, reductions, cluster barrier): 4 us a node
 // for a vocabulary of 262144, 7 where 32 sequences fill the GPU.  Sampling one
-// such token 12 us, 32 drafted trees of 24 72, 16 chains of 8 with draft rows 99.
-// Statistics of all rows first and a walk after would read 4 to 10 times the bytes.
+// such token 11 us, 32 drafted trees of 24 62 to 68, 16 chains of 8 with draft
+// rows 98.5 (two exact passes after the walk); the trees with draft rows 215 to
+// 273.  Statistics of all rows first and a walk after would read 6 times the bytes
+// for those trees and 20 times for wide greedy ones; for chains, most of whose
+// rows are walked, 1.8 times, which has not been tried.
 //
 // Decisions.  A random number closer to a border between two tokens than the
 // sums' rounding would give another token than exact arithmetic does, and a
